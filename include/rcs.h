@@ -347,6 +347,133 @@ int rcs_ckpt_writer_wait(rcs_ckpt_writer *writer, char *path_out, int64_t path_c
 int rcs_ckpt_writer_destroy(rcs_ckpt_writer *writer);
 
 /*
+ * The update over a list of tensors: what adamw_clip_step does to one flat
+ * float32 vector, done to many tensors at once (one norm over all of them, one
+ * clip factor, one launch for all updates), with weights and gradients in
+ * float32, bfloat16 or float16 and the moments in 32 or in 8 bits. The pages'
+ * update is over a model's parameters ("Training as a Recoverable State
+ * Transition", "The Exact Targets of Clipping and AdamW": g is the
+ * concatenation of all gradients, the clip is global); the step file's arrays
+ * are the list's elements in list order.
+ *
+ * One tensor of a list. Every pointer is device memory of the current device,
+ * caller-owned, contiguous, and aligned to its element (views at any element
+ * offset are fine); nothing written may overlap anything else.
+ *   w, w_type       the weights, n elements of RCS_F32, RCS_BF16 or RCS_F16
+ *   g, g_type       the gradient, n elements; g may be NULL: the tensor then
+ *                   has no gradient, adds nothing to the norm and is left as
+ *                   it is (weights, moments and copy) until one is bound
+ *   m, v            the moments. With state_bits = 32: float32[n] each. With
+ *                   state_bits = 8: uint8 codes, 16-byte aligned, n rounded up
+ *                   to a multiple of RCS_LIST_BLOCK bytes each
+ *   exps            with state_bits = 8: uint16[ceil(n / RCS_LIST_BLOCK)],
+ *                   the blocks' exponents. All three zero is m = v = 0
+ *   copy, copy_type RCS_BF16 or RCS_F16 copy of float32 weights, written with
+ *                   them and never read (NULL: none)
+ *   n               >= 0; 0 is allowed for a tensor, not for the whole list
+ *   wd              the tensor's weight decay
+ */
+#define RCS_F32 0
+#define RCS_BF16 1
+#define RCS_F16 2
+#define RCS_LIST_BLOCK 128
+typedef struct rcs_list_tensor {
+    void *w;
+    const void *g;
+    void *m, *v;
+    void *exps;
+    void *copy;
+    int64_t n;
+    float wd;
+    int32_t w_type, g_type, copy_type;
+} rcs_list_tensor;
+typedef struct rcs_list rcs_list;
+
+/*
+ * rcs_list_create copies the description of `count` tensors to the current
+ * device (about 80 bytes a tensor and 8 for each 1,024 elements) and waits for
+ * that; the arrays stay the caller's and must live as long as the list. It
+ * allocates, so call it before a capture. No later call of the list allocates,
+ * except that grad_global_norm_list uses its stream's workspace (rcs_init).
+ * Calls of one list must not overlap on the device (order them by one stream
+ * or by events): they share the list's buffers, and steps its arrays. A norm
+ * call is an exception: eager ones may run on several streams at once.
+ * rcs_list_destroy waits for the device's work and frees the description; a
+ * captured graph that holds calls of the list must not be replayed after it.
+ * rcs_list_elements: the elements of all tensors.
+ */
+int rcs_list_create(const rcs_list_tensor *tensors, int64_t count, int state_bits,
+                    rcs_list **out);
+int rcs_list_destroy(rcs_list *list);
+int64_t rcs_list_elements(const rcs_list *list);
+
+/*
+ * Binds other gradients of the same types and lengths, count pointers in list
+ * order (NULL: no gradient), in stream order: later calls on the stream use
+ * them.
+ */
+int rcs_list_bind_grads(rcs_list *list, const void *const *g, int64_t count, hipStream_t stream);
+
+/*
+ * The pre-clip global norm of the list's gradients,
+ * sqrt(sum (double)(g * grad_scale)^2) with the product in float32, into
+ * norm_out (device or pinned host memory). The order of the sum depends on the
+ * list's lengths alone. last_grad_norm reports it too, unless the call was
+ * captured.
+ */
+int grad_global_norm_list(const rcs_list *list, float grad_scale, double *norm_out,
+                          hipStream_t stream);
+
+/*
+ * One update of the whole list: the global norm of the gradients times
+ * grad_scale, the clip, and AdamW on every tensor that has a gradient, in
+ * place on w, m, v and copy. Per element, in float32, each operation rounded on
+ * its own: gp = (g * grad_scale) * s, m = b1 m + (1 - b1) gp,
+ * v = b2 v + (1 - b2) (gp gp),
+ * w = w (1 - lr wd) - (lr (m / bc1)) / (sqrt(v / bc2) + eps), with
+ * bc = 1 - beta^t and the constants rounded once from float64; 16-bit weights
+ * and the copy are rounded to nearest even at the end. With moments in 8 bits
+ * the weights see the moments before these are rounded, and the last line is
+ * evaluated to within a few units of float32's last place. If the norm is not
+ * finite nothing is changed.
+ *   t          1-based index of the update
+ *   lr, clip   as for adamw_clip_step; clip = +inf never clips
+ *   grad_scale finite, > 0 (1/n_micro, the inverse of a loss scale, or 1)
+ *   beta1, beta2 in [0, 1); eps a positive normal float
+ *   seed       of the random bits by which 8-bit moments are rounded (they
+ *              are a function of seed, t and the element's place in the list)
+ *   norm_out   NULL, or device or pinned host memory for the pre-clip norm
+ *
+ * 8-bit moments: blocks of RCS_LIST_BLOCK consecutive elements of a tensor
+ * share an exponent for m and one for v (low and high byte of exps). With e
+ * that byte, code k > 0 is the float whose bits are (k + 8 e - 255) << 20 for
+ * v, and with k the low 7 bits and the top bit the sign, (k + 8 e - 127) << 20
+ * for m; k = 0 is zero. e is the biased exponent of the smallest power of two
+ * not below the block's largest magnitude, at least 18 for m and 33 for v and
+ * at most 255; what is not finite is held as an infinity of its sign.
+ */
+int adamw_clip_step_list(rcs_list *list, int32_t t, float lr, float clip, float grad_scale,
+                         double beta1, double beta2, float eps, uint32_t seed, double *norm_out,
+                         hipStream_t stream);
+
+/*
+ * The list's state as flat arrays of rcs_list_elements elements in list order
+ * (a step file's payload: pass them to ckpt_pack or an rcs_ckpt_writer), and
+ * back. Each array is float32 (RCS_F32) or bfloat16 (RCS_BF16), aligned to its
+ * element, apart from the list's own arrays and the others; NULL leaves it
+ * out. Export decodes 8-bit moments exactly. Import rounds weights to their
+ * type, writes the copies too, and rounds 8-bit moments to the nearest value
+ * (ties to even; |m| up to half of the smallest value to zero, v > 0 at least
+ * to the smallest; v below zero to zero), so that what an export gave comes
+ * back exactly; it takes 8-bit moments only together. Tensors without a
+ * gradient are included.
+ */
+int rcs_list_export(const rcs_list *list, void *w, int w_type, void *m, int m_type, void *v,
+                    int v_type, hipStream_t stream);
+int rcs_list_import(rcs_list *list, const void *w, int w_type, const void *m, int m_type,
+                    const void *v, int v_type, hipStream_t stream);
+
+/*
  * Instrumentation: while enabled, adamw_clip_step has its kernel dispatches
  * stamp HIP events (start of grad_norm_partial, end of the last norm kernel
  * -- grad_norm_partial itself when the update kernel does the final

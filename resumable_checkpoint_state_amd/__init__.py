@@ -23,7 +23,7 @@ __all__ = [
     "grad_clip_inplace", "grad_zero", "grad_global_norm", "last_grad_norm", "ckpt_bytes",
     "ckpt_pack", "ckpt_unpack", "init", "profile_enable", "profile_read",
     "strerror", "lib", "LIB_PATH", "build", "step_file_name", "MAX_N",
-    "ckpt_pack_async", "ckpt_pack_wait", "CkptWriter", "StepFileCheckpointer",
+    "ckpt_pack_async", "ckpt_pack_wait", "CkptWriter", "StepFileCheckpointer", "AdamWList",
 ]
 
 OK, EINVAL, ESIZE, EHEADER, EHIP, ENOMEM, EIO, ENOENT = 0, -1, -2, -3, -4, -5, -6, -7
@@ -114,6 +114,23 @@ def lib() -> ctypes.CDLL:
     L.rcs_ckpt_writer_wait.restype = ctypes.c_int
     L.rcs_ckpt_writer_destroy.argtypes = [vp]
     L.rcs_ckpt_writer_destroy.restype = ctypes.c_int
+    L.rcs_list_create.argtypes = [vp, i64, ctypes.c_int, ctypes.POINTER(vp)]
+    L.rcs_list_create.restype = ctypes.c_int
+    L.rcs_list_destroy.argtypes = [vp]
+    L.rcs_list_destroy.restype = ctypes.c_int
+    L.rcs_list_elements.argtypes = [vp]
+    L.rcs_list_elements.restype = i64
+    L.rcs_list_bind_grads.argtypes = [vp, vp, i64, vp]
+    L.rcs_list_bind_grads.restype = ctypes.c_int
+    L.grad_global_norm_list.argtypes = [vp, f32, vp, vp]
+    L.grad_global_norm_list.restype = ctypes.c_int
+    L.adamw_clip_step_list.argtypes = [vp, i32, f32, f32, f32, ctypes.c_double, ctypes.c_double,
+                                       f32, ctypes.c_uint32, vp, vp]
+    L.adamw_clip_step_list.restype = ctypes.c_int
+    for name in ("rcs_list_export", "rcs_list_import"):
+        fn = getattr(L, name)
+        fn.argtypes = [vp, vp, ctypes.c_int, vp, ctypes.c_int, vp, ctypes.c_int, vp]
+        fn.restype = ctypes.c_int
     _lib = L
     return L
 
@@ -388,7 +405,8 @@ class CkptWriter:
 
 class StepFileCheckpointer:
     """Step-file policy around a training loop: call after_step(t, w, m, v)
-    after every completed update. It writes <dir>/step_NNNNNN.bin when t is a
+    after every completed update (or after_step(t, tensors), with an AdamWList
+    in the place of the three arrays, here and in save and resume). It writes <dir>/step_NNNNNN.bin when t is a
     multiple of `every` (0 = never by cadence), when SIGUSR1 arrived (write and
     continue) or when SIGTERM arrived (write, then after_step returns True:
     the caller exits), keeps the newest `keep` files, and resume() loads the
@@ -435,7 +453,9 @@ class StepFileCheckpointer:
             self._writer = None
             self.async_write = False
 
-    def save(self, t: int, w, m, v, wait: bool = False) -> None:
+    def save(self, t: int, w, m=None, v=None, wait: bool = False) -> None:
+        if isinstance(w, AdamWList):
+            w, m, v = w.payload(stream=self.stream)
         if self._writer is None:
             ckpt_pack(t, w, m, v, self.buf, stream=self.stream)
             torch.cuda.synchronize()
@@ -447,14 +467,14 @@ class StepFileCheckpointer:
         if wait:
             self.flush()
 
-    def after_step(self, t: int, w, m, v) -> bool:
+    def after_step(self, t: int, w, m=None, v=None) -> bool:
         sig = signals_poll()
         exiting = bool(sig & SIG_WRITE_EXIT)
         if sig or (self.every > 0 and t % self.every == 0):
             self.save(t, w, m, v, wait=exiting)
         return exiting
 
-    def resume(self, w, m, v) -> int:
+    def resume(self, w, m=None, v=None) -> int:
         """Loads the newest valid step file into w, m, v; returns its step
         (0 when there is none: a fresh run). Continue with t = step + 1."""
         self.flush()
@@ -463,7 +483,12 @@ class StepFileCheckpointer:
             return 0
         _, path = found
         ckpt_file_read(path, self.buf)
+        tensors = w if isinstance(w, AdamWList) else None
+        if tensors is not None:
+            w, m, v = tensors.payload_buffer()
         step = ckpt_unpack(self.buf, w, m, v, stream=self.stream)
+        if tensors is not None:
+            tensors.import_state(w, m, v, stream=self.stream)
         torch.cuda.synchronize()
         return step
 
@@ -479,3 +504,6 @@ def profile_read():
     _check(lib().rcs_profile_read(ctypes.byref(a), ctypes.byref(b), ctypes.byref(k)),
            "rcs_profile_read")
     return a.value, b.value, k.value
+
+
+from .tensor_list import AdamWList  # noqa: E402  (uses the helpers above)

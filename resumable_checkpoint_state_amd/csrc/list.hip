@@ -1,0 +1,1063 @@
+// list.hip -- the clipped AdamW update over a list of tensors: weights and
+// gradients of 32 or 16 bits, moments in 32 or in 8 bits, and the list's state
+// as the flat arrays of a step file. gfx950 kernels and their C ABI.
+//
+// Mathematics. For tensor k of the list, element i, with every float32
+// operation rounded on its own:
+//   norm = sqrt(sum_k sum_i (double)(g_k[i] * gscale)^2), in float64
+//   s    = (float)(clip / norm) if norm > clip else 1
+//   gp   = (g * gscale) * s
+//   m    = b1 m + (1 - b1) gp           v = b2 v + (1 - b2) (gp gp)
+//   w    = w (1 - lr wd_k) - (lr (m / bc1)) / (sqrt(v / bc2) + eps)
+// with bc = 1 - b^t; nothing changes if norm is not finite. With float32
+// weights, gradients and moments and the default betas and eps this is
+// adamw_clip_step's sequence, bit for bit for equal s.
+//
+// Moments in 8 bits. Each tensor is cut into blocks of 128 elements; a block
+// has one exponent byte for m and one for v. A value is a float of 3 mantissa
+// bits, held as its distance, in units of the last of these bits, from the
+// bottom of the block's range: with B = 8 e - 127 (m) or 8 e - 255 (v), e the
+// biased exponent of the smallest power of two not below the block's largest
+// magnitude, code k > 0 stands for the float whose bits are (k + B) << 20 and
+// k = 0 for zero. The range is 15.75 octaves for m and 31.75 for v (as many
+// for sqrt(v)). Decoding is an add and a shift, encoding an add, a shift and a
+// subtraction, all on the float's bits: no table, no division, no product with
+// a scale, and decode(encode(decode(x))) is decode(x) exactly, so a state
+// that went through a step file continues bit-identically.
+//   Rounding: an update adds 20 random bits below the third mantissa bit and
+// cuts (stochastic rounding, which keeps the mean). v changes by at most one
+// part in a thousand per update while its grid's steps are 1/16 to 1/8, so with
+// nearest rounding it would never move again once it is near its scale. The
+// random bits are a hash of (seed, t, element), so an update is a function of
+// its inputs and a resumed run repeats it. Below the smallest value, m goes to
+// the nearer of it and zero (rounding up at random there would now and then
+// make a step of the whole range), and v > 0 goes to the smallest value: v is
+// zero only if it is exactly zero, so that no m is divided by eps alone.
+//
+// Mapping. A table row per tensor (pointers, length, decay, types) and one
+// entry per chunk of 1,024 elements (tensor, chunk within it) live in device
+// memory and are made once, when the list is. One wave takes one chunk: it
+// reads its entry and row through scalar loads and then streams 16 consecutive
+// elements per lane, in two halves of 8, in 16-byte accesses that need only the
+// element's own alignment (so tensors may be views at any offset). The type
+// combination is a uniform branch per wave, so a list of mixed types is one
+// launch. Bound by HBM: see the kernels.
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+#include <new>
+#include <utility>
+#include <vector>
+
+#include "rcs.h"
+#include "rcs_device.h"
+#include "rcs_internal.h"
+
+#pragma clang fp contract(off)
+
+namespace {
+
+constexpr int kBlock = RCS_LIST_BLOCK;  // elements that share a block exponent
+constexpr int kVec = 8;                 // consecutive elements of a lane
+constexpr int kRounds = 2;              // such groups per lane and chunk
+constexpr int kChunk = kWave * kVec * kRounds;
+static_assert(kChunk % kBlock == 0 && kBlock == 16 * kVec, "a block is one 16-lane row");
+constexpr int kListNormThreads = 512;
+// Lowest block exponents (biased): the smallest value and, for m, half of it
+// are then normal floats.
+constexpr int kLowM = 18, kLowV = 33;
+constexpr uint32_t kHashA = 0x9E3779B1u, kHashB = 0xC2A3F1D7u, kHashC = 0x5BD9E4B5u,
+                   kHashK = 0x7F4A7C15u;
+
+// One tensor of the list, in device memory.
+struct Row {
+    void *w;
+    const void *g;  // null: the tensor has no gradient and is left alone
+    void *m, *v;
+    uint16_t *e;  // block exponents of the 8-bit moments: m's low, v's high byte
+    void *c;      // low-precision copy of w, or null
+    int64_t n;
+    int64_t off;  // elements of the list before this tensor
+    float wd;
+    uint8_t wt, gt, ct, pad;  // RCS_F32, RCS_BF16, RCS_F16
+};
+
+struct Chunk {
+    uint32_t row, part;  // elements part * kChunk .. of that tensor
+};
+
+struct ListScalars {
+    float lr, bc1, bc2, b1, c1, b2, c2, eps, gscale;
+    uint32_t key;  // of the update's random bits
+};
+
+// ------------------------------------------------------------- element types
+
+struct F32 {
+    static constexpr int kBytes = 4;
+};
+struct BF16 {
+    static constexpr int kBytes = 2;
+};
+struct F16 {
+    static constexpr int kBytes = 2;
+};
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+// 16 bytes at the alignment of an element: the hardware's vector accesses need
+// no more.
+typedef u32x4 u32x4_by4 __attribute__((aligned(4)));
+typedef u32x4 u32x4_by2 __attribute__((aligned(2)));
+
+// A pointer that came out of a table is one to device memory: said so, its
+// accesses are global ones rather than flat ones, which would wait for LDS too.
+template <class V>
+using Global = __attribute__((address_space(1))) V *;
+template <class V>
+__device__ __forceinline__ Global<V> global(const void *p) {
+    return (Global<V>)reinterpret_cast<uintptr_t>(p);
+}
+
+template <class T>
+struct Raw {  // kVec elements as they lie in memory
+    uint32_t d[kVec * T::kBytes / 4];
+};
+
+__device__ __forceinline__ float elem_f32(uint32_t bits, F32) { return __uint_as_float(bits); }
+__device__ __forceinline__ float elem_f32(uint32_t bits, BF16) {
+    return __uint_as_float(bits << 16);
+}
+__device__ __forceinline__ float elem_f32(uint32_t bits, F16) {
+    return (float)__builtin_bit_cast(_Float16, (uint16_t)bits);
+}
+
+// One rounding to nearest even; a NaN stays one.
+__device__ __forceinline__ uint32_t elem_bits(float x, F32) { return __float_as_uint(x); }
+__device__ __forceinline__ uint32_t elem_bits(float x, BF16) {
+    return __builtin_bit_cast(uint16_t, (__bf16)x);
+}
+__device__ __forceinline__ uint32_t elem_bits(float x, F16) {
+    return __builtin_bit_cast(uint16_t, (_Float16)x);
+}
+
+template <class T>
+__device__ __forceinline__ void unpack(const Raw<T> &r, float (&x)[kVec]) {
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+        if constexpr (T::kBytes == 4) x[i] = elem_f32(r.d[i], T{});
+        else x[i] = elem_f32((r.d[i / 2] >> (16 * (i & 1))) & 0xFFFFu, T{});
+    }
+}
+
+template <class T>
+__device__ __forceinline__ Raw<T> pack(const float (&x)[kVec]) {
+    Raw<T> r;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+        if constexpr (T::kBytes == 4) r.d[i] = elem_bits(x[i], T{});
+        else if (i & 1) r.d[i / 2] |= elem_bits(x[i], T{}) << 16;
+        else r.d[i / 2] = elem_bits(x[i], T{});
+    }
+    return r;
+}
+
+// The kVec elements from element i of p on; cnt of them exist (the others
+// come as zero). Streaming loads unless KEEP.
+template <class T, bool KEEP = false>
+__device__ __forceinline__ Raw<T> load(const void *p, int64_t i, int cnt) {
+    Raw<T> r;
+    const char *a = static_cast<const char *>(p) + i * T::kBytes;
+    if (cnt == kVec) {
+        using V = std::conditional_t<T::kBytes == 4, u32x4_by4, u32x4_by2>;
+        const Global<V> q = global<V>(a);
+#pragma unroll
+        for (int k = 0; k < (int)sizeof(r) / 16; ++k) {
+            const u32x4 x = KEEP ? (u32x4)q[k] : (u32x4)__builtin_nontemporal_load(q + k);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) r.d[4 * k + j] = x[j];
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < (int)sizeof(r) / 4; ++k) r.d[k] = 0;
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) {
+            if (k >= cnt) continue;
+            if constexpr (T::kBytes == 4)
+                r.d[k] = global<uint32_t>(a)[k];
+            else
+                r.d[k / 2] |= (uint32_t)global<uint16_t>(a)[k] << (16 * (k & 1));
+        }
+    }
+    return r;
+}
+
+template <class T>
+__device__ __forceinline__ void store(void *p, int64_t i, int cnt, const Raw<T> &r) {
+    char *a = static_cast<char *>(p) + i * T::kBytes;
+    if (cnt == kVec) {
+        using V = std::conditional_t<T::kBytes == 4, u32x4_by4, u32x4_by2>;
+        const Global<V> q = global<V>(a);
+#pragma unroll
+        for (int k = 0; k < (int)sizeof(r) / 16; ++k) {
+            const u32x4 x = {r.d[4 * k], r.d[4 * k + 1], r.d[4 * k + 2], r.d[4 * k + 3]};
+            __builtin_nontemporal_store((V)x, q + k);
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) {
+            if (k >= cnt) continue;
+            if constexpr (T::kBytes == 4)
+                global<uint32_t>(a)[k] = r.d[k];
+            else
+                global<uint16_t>(a)[k] = (uint16_t)(r.d[k / 2] >> (16 * (k & 1)));
+        }
+    }
+}
+
+// f(T) for the element type t (uniform in the wave).
+template <class F>
+__device__ __forceinline__ void by_type(int t, F f) {
+    if (t == RCS_F32) f(F32{});
+    else if (t == RCS_BF16) f(BF16{});
+    else f(F16{});
+}
+
+// How many of the lane's kVec elements of round j lie in the tensor; left:
+// the tensor's elements from the chunk's first on.
+__device__ __forceinline__ int count_of(int64_t left, int j) {
+    const int64_t r = left - (j * kWave + (int)(threadIdx.x & (kWave - 1))) * kVec;
+    return r >= kVec ? kVec : r > 0 ? (int)r : 0;
+}
+
+// ----------------------------------------------------------- 8-bit moments
+
+// Hash of an element's index and the update: the mixing step of x = index *
+// kHashA + (index >> 32) * kHashB + key.
+__host__ __device__ __forceinline__ uint32_t mixed(uint32_t x) {
+    x = (x ^ (x >> 16)) * kHashC;
+    return x ^ (x >> 15);
+}
+
+// The random bits of elements i .. i + kVec - 1 of the list.
+__device__ __forceinline__ void random_bits(int64_t i, uint32_t key, uint32_t (&r)[kVec]) {
+    const uint32_t x = (uint32_t)i * kHashA + (uint32_t)(i >> 32) * kHashB + key;
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) {
+        // a carry into the index's upper half
+        const uint32_t c = (uint32_t)((i + k) >> 32) - (uint32_t)(i >> 32);
+        r[k] = mixed(x + (uint32_t)k * kHashA + c * kHashB);
+    }
+}
+
+// The largest of a 16-lane row's values, in every lane of the row.
+__device__ __forceinline__ uint32_t row_max(uint32_t x) {
+    auto with = [&](uint32_t y) { x = x > y ? x : y; };
+    with((uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0xB1, 0xF, 0xF, true));   // pairs
+    with((uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x4E, 0xF, 0xF, true));   // quads
+    with((uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x141, 0xF, 0xF, true));  // 8 lanes
+    with((uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x140, 0xF, 0xF, true));  // 16 lanes
+    return x;
+}
+
+__device__ __forceinline__ int base_m(int e) { return 8 * e - 127; }
+__device__ __forceinline__ int base_v(int e) { return 8 * e - 255; }
+
+// Biased exponent of the smallest power of two not below the value with these
+// magnitude bits, at least low; 255 for what is not finite.
+__device__ __forceinline__ int block_exponent(uint32_t bits, int low) {
+    const int e = (int)((bits + 0x7FFFFFu) >> 23);
+    return e < low ? low : e > 255 ? 255 : e;
+}
+
+__device__ __forceinline__ float decode_v(uint32_t k, int base) {
+    return k == 0 ? 0.0f : __uint_as_float((uint32_t)((int)k + base) << 20);
+}
+
+__device__ __forceinline__ float decode_m(uint32_t code, int base) {
+    const uint32_t k = code & 0x7Fu;
+    return k == 0 ? 0.0f
+                  : __uint_as_float(((uint32_t)((int)k + base) << 20) | ((code & 0x80u) << 24));
+}
+
+// Code of the value with magnitude bits `mag`; add is what is added below the
+// third mantissa bit before the rest is cut: 20 random bits, or half a unit
+// (to even) for the nearest value. `low`: magnitude bits above this get at
+// least code 1.
+__device__ __forceinline__ uint32_t encode(uint32_t mag, uint32_t add, int base, uint32_t low,
+                                           int top) {
+    const int k = (int)((mag + add) >> 20) - base;
+    const int least = mag > low ? 1 : 0;
+    const int r = k > least ? k : least;
+    return (uint32_t)(r < top ? r : top);  // beyond the top: only what is not finite
+}
+
+__device__ __forceinline__ uint32_t low_m(int base) {
+    return ((uint32_t)(base + 1) << 20) - 0x800000u;  // half of the smallest value
+}
+
+__device__ __forceinline__ uint32_t encode_m(float m, uint32_t add, int base) {
+    const uint32_t u = __float_as_uint(m);
+    const uint32_t k = encode(u & 0x7FFFFFFFu, add, base, low_m(base), 127);
+    return k == 0 ? 0u : k | ((u >> 24) & 0x80u);
+}
+
+__device__ __forceinline__ uint32_t half_unit(uint32_t mag) { return 0x7FFFFu + ((mag >> 20) & 1u); }
+
+// 8 codes of one byte.
+struct Codes {
+    uint32_t d[kVec / 4];
+    __device__ __forceinline__ uint32_t at(int i) const { return (d[i / 4] >> (8 * (i & 3))) & 0xFFu; }
+    __device__ __forceinline__ void put(int i, uint32_t k) {
+        if ((i & 3) == 0) d[i / 4] = k;
+        else d[i / 4] |= k << (8 * (i & 3));
+    }
+};
+
+__device__ __forceinline__ Codes load_codes(const void *p, int64_t i) {
+    const u32x2 x = __builtin_nontemporal_load(global<u32x2>(static_cast<const char *>(p) + i));
+    return Codes{{x.x, x.y}};
+}
+
+__device__ __forceinline__ void store_codes(void *p, int64_t i, const Codes &c) {
+    __builtin_nontemporal_store(u32x2{c.d[0], c.d[1]},
+                                global<u32x2>(static_cast<char *>(p) + i));
+}
+
+// Block exponents and codes of the lane's m and v (those past the tensor's end
+// are zero), written to the chunk's block; every lane of the row calls this.
+template <class AddM, class AddV>
+__device__ __forceinline__ void store_moments(const Row &t, int64_t i, const float (&m)[kVec],
+                                              const float (&v)[kVec], bool active, AddM add_m,
+                                              AddV add_v) {
+    uint32_t am = 0, av = 0;
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) {
+        const uint32_t um = __float_as_uint(m[k]) & 0x7FFFFFFFu;
+        const uint32_t uv = __float_as_uint(v[k]) & 0x7FFFFFFFu;
+        am = am > um ? am : um;
+        av = av > uv ? av : uv;
+    }
+    const int em = block_exponent(row_max(am), kLowM), ev = block_exponent(row_max(av), kLowV);
+    const int bm = base_m(em), bv = base_v(ev);
+    Codes cm, cv;
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) {
+        cm.put(k, encode_m(m[k], add_m(k), bm));
+        const uint32_t uv = __float_as_uint(v[k]) & 0x7FFFFFFFu;
+        cv.put(k, encode(uv, add_v(k), bv, 0u, 255));
+    }
+    if (!active) return;
+    store_codes(t.m, i, cm);
+    store_codes(t.v, i, cv);
+    if ((threadIdx.x & 15u) == 0) global<uint16_t>(t.e)[i / kBlock] = (uint16_t)(em | (ev << 8));
+}
+
+__device__ __forceinline__ void decode_moments(const Codes &cm, const Codes &cv, uint32_t e,
+                                               float (&m)[kVec], float (&v)[kVec]) {
+    const int bm = base_m((int)(e & 0xFFu)), bv = base_v((int)(e >> 8));
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) {
+        m[k] = decode_m(cm.at(k), bm);
+        v[k] = decode_v(cv.at(k), bv);
+    }
+}
+
+// ------------------------------------------------------------------- kernels
+
+// Per-block float64 partial sums of squares of the list's gradients: wave j
+// of the grid takes chunks j, j + waves, ...; the order depends on the list
+// alone.
+__global__ __launch_bounds__(kListNormThreads) void list_norm_partial(
+    const Row *__restrict__ rows, const Chunk *__restrict__ chunks, int64_t nchunks, float gscale,
+    double *__restrict__ partials) {
+    __shared__ double lds[kListNormThreads / kWave];
+    constexpr int kWaves = kListNormThreads / kWave;
+    double acc[kRounds] = {};
+    const int64_t step = (int64_t)gridDim.x * kWaves;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+    for (int64_t j = (int64_t)blockIdx.x * kWaves + wave; j < nchunks; j += step) {
+        const Chunk c = chunks[j];
+        const Row t = rows[c.row];
+        if (t.g == nullptr) continue;
+        const int64_t first = (int64_t)c.part * kChunk, left = t.n - first;
+        by_type(t.gt, [&](auto T) {
+            using G = decltype(T);
+            Raw<G> r[kRounds];
+#pragma unroll
+            for (int q = 0; q < kRounds; ++q)
+                r[q] = load<G, true>(t.g, first + (q * kWave + (threadIdx.x & (kWave - 1))) * kVec,
+                                     count_of(left, q));
+#pragma unroll
+            for (int q = 0; q < kRounds; ++q) {
+                float x[kVec];
+                unpack(r[q], x);
+#pragma unroll
+                for (int k = 0; k < kVec; ++k) {
+                    const double d = (double)(x[k] * gscale);
+                    acc[q] += d * d;
+                }
+            }
+        });
+    }
+    double sum = 0.0;
+#pragma unroll
+    for (int q = 0; q < kRounds; ++q) sum += acc[q];
+    sum = block_sum<kListNormThreads>(sum, lds);
+    if (threadIdx.x == 0) partials[blockIdx.x] = sum;
+}
+
+__global__ __launch_bounds__(kUpdThreads) void list_norm_final(const double *__restrict__ partials,
+                                                               int nparts, float clip,
+                                                               ClipScalars *__restrict__ record,
+                                                               double *__restrict__ norm_out) {
+    __shared__ double lds[kUpdThreads / kWave];
+    double x[kPartsPerLane];
+    load_partials(partials, nparts, x);
+    const ClipScalars r = final_reduce(x, nparts, clip, lds);
+    if (threadIdx.x == 0) {
+        *record = r;
+        if (norm_out != nullptr) *norm_out = r.norm;
+    }
+}
+
+__device__ __forceinline__ void adamw(float &w, float g, float &m, float &v, float s, float decay,
+                                      const ListScalars &h) {
+    const float ga = g * h.gscale;
+    const float gp = ga * s;
+    const float mi = h.b1 * m + h.c1 * gp;
+    const float vi = h.b2 * v + h.c2 * (gp * gp);
+    const float mh = mi / h.bc1;
+    const float vh = vi / h.bc2;
+    const float den = __builtin_sqrtf(vh) + h.eps;
+    w = w * decay - (h.lr * mh) / den;
+    m = mi;
+    v = vi;
+}
+
+// One chunk of 32-bit moments: W, G the types of weights and gradients.
+template <class W, class G, class Record>
+__device__ __forceinline__ void update32(const Row &t, int64_t first, Record record,
+                                         const ListScalars &h) {
+    const int64_t left = t.n - first;
+    int64_t i[kRounds];
+    int cnt[kRounds];
+    Raw<W> w[kRounds];
+    Raw<G> g[kRounds];
+    Raw<F32> m[kRounds], v[kRounds];
+#pragma unroll
+    for (int q = 0; q < kRounds; ++q) {
+        cnt[q] = count_of(left, q);
+        i[q] = first + (q * kWave + (int)threadIdx.x) * kVec;
+        g[q] = load<G>(t.g, i[q], cnt[q]);
+        w[q] = load<W>(t.w, i[q], cnt[q]);
+        m[q] = load<F32>(t.m, i[q], cnt[q]);
+        v[q] = load<F32>(t.v, i[q], cnt[q]);
+    }
+    const ClipScalars cs = record();
+    if (!cs.apply) return;
+    const float decay = (float)(1.0 - (double)h.lr * (double)t.wd);
+#pragma unroll
+    for (int q = 0; q < kRounds; ++q) {
+        float ww[kVec], gg[kVec], mm[kVec], vv[kVec];
+        unpack(w[q], ww);
+        unpack(g[q], gg);
+        unpack(m[q], mm);
+        unpack(v[q], vv);
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) adamw(ww[k], gg[k], mm[k], vv[k], cs.scale, decay, h);
+        store(t.w, i[q], cnt[q], pack<W>(ww));
+        store(t.m, i[q], cnt[q], pack<F32>(mm));
+        store(t.v, i[q], cnt[q], pack<F32>(vv));
+        if constexpr (W::kBytes == 4) {
+            if (t.c != nullptr) {
+                if (t.ct == RCS_BF16) store(t.c, i[q], cnt[q], pack<BF16>(ww));
+                else store(t.c, i[q], cnt[q], pack<F16>(ww));
+            }
+        }
+    }
+}
+
+// One chunk of 8-bit moments. The code arrays are filled up to whole blocks,
+// so a code access is always a whole vector; a block past the tensor's end is
+// not touched.
+template <class W, class G, class Record>
+__device__ __forceinline__ void update8(const Row &t, int64_t first, Record record,
+                                        const ListScalars &h) {
+    const int64_t left = t.n - first;
+    int64_t i[kRounds];
+    int cnt[kRounds];
+    bool active[kRounds];
+    Raw<W> w[kRounds];
+    Raw<G> g[kRounds];
+    Codes cm[kRounds], cv[kRounds];
+    uint32_t e[kRounds];
+#pragma unroll
+    for (int q = 0; q < kRounds; ++q) {
+        cnt[q] = count_of(left, q);
+        const int at = (q * kWave + (int)threadIdx.x) * kVec;
+        i[q] = first + at;
+        active[q] = (at & ~(kBlock - 1)) < left;
+        g[q] = load<G>(t.g, i[q], cnt[q]);
+        w[q] = load<W>(t.w, i[q], cnt[q]);
+        const int64_t ic = active[q] ? i[q] : 0;
+        cm[q] = load_codes(t.m, ic);
+        cv[q] = load_codes(t.v, ic);
+        e[q] = global<uint16_t>(t.e)[ic / kBlock];
+    }
+    const ClipScalars cs = record();
+    if (!cs.apply) return;
+    const float decay = (float)(1.0 - (double)h.lr * (double)t.wd);
+#pragma unroll
+    for (int q = 0; q < kRounds; ++q) {
+        float ww[kVec], gg[kVec], mm[kVec], vv[kVec];
+        unpack(w[q], ww);
+        unpack(g[q], gg);
+        decode_moments(cm[q], cv[q], e[q], mm, vv);
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) {
+            adamw(ww[k], gg[k], mm[k], vv[k], cs.scale, decay, h);
+            if (k >= cnt[q]) mm[k] = vv[k] = 0.0f;
+        }
+        store(t.w, i[q], cnt[q], pack<W>(ww));
+        if constexpr (W::kBytes == 4) {
+            if (t.c != nullptr) {
+                if (t.ct == RCS_BF16) store(t.c, i[q], cnt[q], pack<BF16>(ww));
+                else store(t.c, i[q], cnt[q], pack<F16>(ww));
+            }
+        }
+        uint32_t r[kVec];
+        random_bits(t.off + i[q], h.key, r);
+        store_moments(t, i[q], mm, vv, active[q], [&](int k) { return r[k] & 0xFFFFFu; },
+                      [&](int k) { return r[k] >> 12; });
+    }
+}
+
+// The update, one wave per chunk. FOLD: every wave does the final reduction of
+// the norm itself (as the flat update does at small n), and the first one
+// writes the record.
+template <bool Q8, bool FOLD>
+__global__ __launch_bounds__(kUpdThreads) void list_update(
+    const Row *__restrict__ rows, const Chunk *__restrict__ chunks,
+    const double *__restrict__ partials, int nparts, float clip, ClipScalars *__restrict__ record,
+    double *__restrict__ norm_out, ListScalars h) {
+    const Chunk c = chunks[chunk_of_block()];
+    const Row t = rows[c.row];
+    double x[kPartsPerLane];
+    if constexpr (FOLD) load_partials(partials, nparts, x);
+    auto get = [&]() -> ClipScalars {
+        if constexpr (FOLD) {
+            const ClipScalars r = final_reduce(x, nparts, clip, nullptr);
+            if (blockIdx.x == 0 && threadIdx.x == 0) {
+                *record = r;
+                if (norm_out != nullptr) *norm_out = r.norm;
+            }
+            return r;
+        } else {
+            return *record;
+        }
+    };
+    if (t.g == nullptr) {
+        (void)get();
+        return;
+    }
+    const int64_t first = (int64_t)c.part * kChunk;
+    by_type(t.wt, [&](auto W) {
+        by_type(t.gt, [&](auto G) {
+            if constexpr (Q8) update8<decltype(W), decltype(G)>(t, first, get, h);
+            else update32<decltype(W), decltype(G)>(t, first, get, h);
+        });
+    });
+}
+
+// Flat arrays of the list's elements, in list order: w, m and v, each float32
+// or bfloat16, or null for one that is left out.
+struct Flat {
+    void *w, *m, *v;
+    int wt, mt, vt;
+};
+
+__device__ __forceinline__ void store_as(int type, void *p, int64_t i, int cnt,
+                                         const float (&x)[kVec]) {
+    if (type == RCS_F32) store(p, i, cnt, pack<F32>(x));
+    else store(p, i, cnt, pack<BF16>(x));
+}
+
+__device__ __forceinline__ void load_as(int type, const void *p, int64_t i, int cnt,
+                                        float (&x)[kVec]) {
+    if (type == RCS_F32) unpack(load<F32>(p, i, cnt), x);
+    else unpack(load<BF16>(p, i, cnt), x);
+}
+
+template <bool Q8>
+__global__ __launch_bounds__(kUpdThreads) void list_export(const Row *__restrict__ rows,
+                                                           const Chunk *__restrict__ chunks,
+                                                           Flat f) {
+    const Chunk c = chunks[blockIdx.x];
+    const Row t = rows[c.row];
+    const int64_t first = (int64_t)c.part * kChunk, left = t.n - first;
+#pragma unroll
+    for (int q = 0; q < kRounds; ++q) {
+        const int cnt = count_of(left, q);
+        const int64_t i = first + (q * kWave + (int)threadIdx.x) * kVec;
+        if (cnt == 0) continue;
+        if (f.w != nullptr)
+            by_type(t.wt, [&](auto W) {
+                float x[kVec];
+                unpack(load<decltype(W)>(t.w, i, cnt), x);
+                store_as(f.wt, f.w, t.off + i, cnt, x);
+            });
+        if (f.m == nullptr && f.v == nullptr) continue;
+        float m[kVec], v[kVec];
+        if constexpr (Q8) {
+            decode_moments(load_codes(t.m, i), load_codes(t.v, i),
+                           global<uint16_t>(t.e)[i / kBlock], m, v);
+        } else {
+            if (f.m != nullptr) unpack(load<F32>(t.m, i, cnt), m);
+            if (f.v != nullptr) unpack(load<F32>(t.v, i, cnt), v);
+        }
+        if (f.m != nullptr) store_as(f.mt, f.m, t.off + i, cnt, m);
+        if (f.v != nullptr) store_as(f.vt, f.v, t.off + i, cnt, v);
+    }
+}
+
+// With 8-bit moments, m and v come together (the host sees to it): a block's
+// two exponents are one store.
+template <bool Q8>
+__global__ __launch_bounds__(kUpdThreads) void list_import(const Row *__restrict__ rows,
+                                                           const Chunk *__restrict__ chunks,
+                                                           Flat f) {
+    const Chunk c = chunks[blockIdx.x];
+    const Row t = rows[c.row];
+    const int64_t first = (int64_t)c.part * kChunk, left = t.n - first;
+#pragma unroll
+    for (int q = 0; q < kRounds; ++q) {
+        const int cnt = count_of(left, q);
+        const int at = (q * kWave + (int)threadIdx.x) * kVec;
+        const int64_t i = first + at;
+        if (f.w != nullptr && cnt > 0) {
+            float x[kVec];
+            load_as(f.wt, f.w, t.off + i, cnt, x);
+            by_type(t.wt, [&](auto W) { store(t.w, i, cnt, pack<decltype(W)>(x)); });
+            if (t.c != nullptr) {
+                if (t.ct == RCS_BF16) store(t.c, i, cnt, pack<BF16>(x));
+                else store(t.c, i, cnt, pack<F16>(x));
+            }
+        }
+        float m[kVec], v[kVec];
+        if constexpr (Q8) {
+            if (f.m == nullptr) continue;
+            load_as(f.mt, f.m, t.off + i, cnt, m);
+            load_as(f.vt, f.v, t.off + i, cnt, v);
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) {  // v below zero is held as zero
+                const uint32_t u = __float_as_uint(v[k]);  // (a NaN is not)
+                v[k] = __uint_as_float((u >> 31) != 0 && u <= 0xFF800000u ? 0u : u & 0x7FFFFFFFu);
+            }
+            store_moments(
+                t, i, m, v, (at & ~(kBlock - 1)) < left,
+                [&](int k) { return half_unit(__float_as_uint(m[k]) & 0x7FFFFFFFu); },
+                [&](int k) { return half_unit(__float_as_uint(v[k])); });
+        } else {
+            if (cnt == 0) continue;
+            if (f.m != nullptr) {
+                load_as(f.mt, f.m, t.off + i, cnt, m);
+                store(t.m, i, cnt, pack<F32>(m));
+            }
+            if (f.v != nullptr) {
+                load_as(f.vt, f.v, t.off + i, cnt, v);
+                store(t.v, i, cnt, pack<F32>(v));
+            }
+        }
+    }
+}
+
+// Other gradients for rows first .. first + count - 1. The pointers travel in
+// the kernel's arguments, so the call is in stream order and needs no staging.
+constexpr int kBind = 256;
+struct Pointers {
+    const void *p[kBind];
+};
+__global__ __launch_bounds__(kBind) void list_bind(Row *__restrict__ rows, int count,
+                                                   Pointers g) {
+    if ((int)threadIdx.x < count) rows[threadIdx.x].g = g.p[threadIdx.x];
+}
+
+// ----------------------------------------------------------------- host side
+
+int type_bytes(int t) { return t == RCS_F32 ? 4 : t == RCS_BF16 || t == RCS_F16 ? 2 : 0; }
+
+struct Span {
+    const char *lo, *hi;
+};
+
+bool by_start(const Span &a, const Span &b) { return a.lo < b.lo; }
+
+}  // namespace
+
+struct rcs_list {
+    int dev = 0;
+    int bits = 32;
+    int64_t n = 0;        // elements of all tensors
+    int64_t nchunks = 0;
+    std::vector<Row> rows;
+    std::vector<Span> written;  // what an update writes, sorted
+    char *mem = nullptr;        // everything below, one allocation
+    Row *d_rows = nullptr;
+    Chunk *d_chunks = nullptr;
+    // norm buffers of the update, and of a norm call that is being captured
+    // (an eager one uses its stream's)
+    double *partials[2] = {nullptr, nullptr};
+    ClipScalars *record[2] = {nullptr, nullptr};
+
+    // Whether [p, p + bytes) shares a byte with what an update writes.
+    bool touches(const void *p, int64_t bytes) const {
+        const Span s{static_cast<const char *>(p), static_cast<const char *>(p) + bytes};
+        auto it = std::upper_bound(written.begin(), written.end(), s, by_start);
+        if (it != written.end() && it->lo < s.hi) return true;
+        return it != written.begin() && (it - 1)->hi > s.lo;
+    }
+
+    int norm_blocks() const {
+        const int64_t b = (nchunks + kListNormThreads / kWave - 1) / (kListNormThreads / kWave);
+        return (int)(b < kNormMaxBlocks ? b : kNormMaxBlocks);
+    }
+};
+
+namespace {
+
+// The largest list whose update folds the final reduction of the norm.
+constexpr int64_t kListFoldMaxN = 8388608;
+// Waves of a launch: the grid's work-items have to fit 32 bits.
+constexpr int64_t kMaxChunks = 0xFFFFFFFFLL / kUpdThreads;
+
+bool aligned(const void *p, int align) {
+    return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(align - 1)) == 0;
+}
+
+// A pointer of the list: aligned to its element and inside one allocation of
+// the current device.
+int check_array(const void *p, int64_t bytes, int align) {
+    return aligned(p, align) ? rcs_check_device_range(p, bytes) : RCS_EINVAL;
+}
+
+int check_list(const rcs_list *list) {
+    if (list == nullptr) return RCS_EINVAL;
+    int dev = -1;
+    if (hipGetDevice(&dev) != hipSuccess) return RCS_EHIP;
+    return dev == list->dev ? RCS_OK : RCS_EINVAL;
+}
+
+// norm_out on the device, where the kernels can write it; null if it is host
+// memory (copied there afterwards) or not wanted.
+bool on_device(const double *p) {
+    hipPointerAttribute_t pa;
+    if (p == nullptr || hipPointerGetAttributes(&pa, p) != hipSuccess) {
+        (void)hipGetLastError();
+        return false;
+    }
+    return pa.type != hipMemoryTypeHost;
+}
+
+bool capturing(hipStream_t stream) {
+    hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
+    if (hipStreamIsCapturing(stream, &st) != hipSuccess) {
+        (void)hipGetLastError();
+        return false;
+    }
+    return st != hipStreamCaptureStatusNone;
+}
+
+void launch_norm(const rcs_list *l, float gscale, double *partials, hipStream_t stream) {
+    hipLaunchKernelGGL(list_norm_partial, dim3(l->norm_blocks()), dim3(kListNormThreads), 0,
+                       stream, (const Row *)l->d_rows, (const Chunk *)l->d_chunks, l->nchunks,
+                       gscale, partials);
+}
+
+int check_flat(const rcs_list *l, const void *p, int type, bool writes) {
+    if (p == nullptr) return RCS_OK;
+    if (type != RCS_F32 && type != RCS_BF16) return RCS_EINVAL;
+    const int64_t bytes = l->n * type_bytes(type);
+    const int rc = check_array(p, bytes, type_bytes(type));
+    if (rc != RCS_OK) return rc;
+    if (l->touches(p, bytes)) return RCS_EINVAL;
+    if (writes)  // an exported array is not a gradient either
+        for (const Row &r : l->rows) {
+            const char *g = static_cast<const char *>(r.g), *q = static_cast<const char *>(p);
+            if (g != nullptr && g < q + bytes && q < g + r.n * type_bytes(r.gt)) return RCS_EINVAL;
+        }
+    return RCS_OK;
+}
+
+bool apart(const void *a, int ta, const void *b, int tb, int64_t n) {
+    const char *x = static_cast<const char *>(a), *y = static_cast<const char *>(b);
+    return a == nullptr || b == nullptr || x + n * type_bytes(ta) <= y ||
+           y + n * type_bytes(tb) <= x;
+}
+
+}  // namespace
+
+extern "C" {
+
+int rcs_list_create(const rcs_list_tensor *tensors, int64_t count, int state_bits,
+                    rcs_list **out) {
+    if (out == nullptr) return RCS_EINVAL;
+    *out = nullptr;
+    if (tensors == nullptr || count < 1 || count > 0x7FFFFFFF ||
+        (state_bits != 32 && state_bits != 8))
+        return RCS_EINVAL;
+    int64_t total = 0, nchunks = 0;
+    for (int64_t k = 0; k < count; ++k) {
+        const rcs_list_tensor &t = tensors[k];
+        if (t.n < 0 || t.n > (1LL << 40)) return RCS_EINVAL;
+        if (type_bytes(t.w_type) == 0 || type_bytes(t.g_type) == 0 || !std::isfinite(t.wd))
+            return RCS_EINVAL;
+        if (t.copy != nullptr &&
+            (t.w_type != RCS_F32 || (t.copy_type != RCS_BF16 && t.copy_type != RCS_F16)))
+            return RCS_EINVAL;
+        const int sa = state_bits == 32 ? 4 : 16;
+        if (t.n > 0 && (!aligned(t.w, type_bytes(t.w_type)) || !aligned(t.m, sa) ||
+                        !aligned(t.v, sa) || (state_bits == 8 && !aligned(t.exps, 2)) ||
+                        (t.g != nullptr && !aligned(t.g, type_bytes(t.g_type))) ||
+                        (t.copy != nullptr && !aligned(t.copy, 2))))
+            return RCS_EINVAL;
+        total += t.n;
+        nchunks += (t.n + kChunk - 1) / kChunk;
+        if (nchunks > kMaxChunks) return RCS_EINVAL;
+    }
+    if (total < 1) return RCS_EINVAL;
+    int rc;
+    try {
+        rcs_list *l = new rcs_list;
+        struct Drop {
+            rcs_list *l;
+            ~Drop() { delete l; }
+        } drop{l};
+        l->bits = state_bits;
+        l->n = total;
+        l->nchunks = nchunks;
+        if (hipGetDevice(&l->dev) != hipSuccess) return RCS_EHIP;
+        std::vector<Chunk> chunks;
+        chunks.reserve((size_t)nchunks);
+        int64_t off = 0;
+        for (int64_t k = 0; k < count; ++k) {
+            const rcs_list_tensor &t = tensors[k];
+            Row r{t.w,  t.g, t.m, t.v, static_cast<uint16_t *>(t.exps), t.copy, t.n, off, t.wd,
+                  (uint8_t)t.w_type, (uint8_t)t.g_type, (uint8_t)t.copy_type, 0};
+            if (t.n == 0) {
+                l->rows.push_back(r);
+                continue;
+            }
+            const int wb = type_bytes(t.w_type), gb = type_bytes(t.g_type);
+            const int64_t blocks = (t.n + kBlock - 1) / kBlock;
+            const int64_t sb = state_bits == 32 ? 4 * t.n : blocks * kBlock;
+            const int sa = state_bits == 32 ? 4 : 16;
+            if ((rc = check_array(t.w, wb * t.n, wb)) != RCS_OK) return rc;
+            if ((rc = check_array(t.m, sb, sa)) != RCS_OK) return rc;
+            if ((rc = check_array(t.v, sb, sa)) != RCS_OK) return rc;
+            if (t.g != nullptr && (rc = check_array(t.g, gb * t.n, gb)) != RCS_OK) return rc;
+            if (t.copy != nullptr && (rc = check_array(t.copy, 2 * t.n, 2)) != RCS_OK) return rc;
+            if (state_bits == 8 && (rc = check_array(t.exps, 2 * blocks, 2)) != RCS_OK) return rc;
+            auto add = [&](const void *p, int64_t bytes) {
+                const char *c = static_cast<const char *>(p);
+                l->written.push_back(Span{c, c + bytes});
+            };
+            add(t.w, wb * t.n);
+            add(t.m, sb);
+            add(t.v, sb);
+            if (t.copy != nullptr) add(t.copy, 2 * t.n);
+            if (state_bits == 8) add(t.exps, 2 * blocks);
+            l->rows.push_back(r);
+            for (int64_t c = 0; c < (t.n + kChunk - 1) / kChunk; ++c)
+                chunks.push_back(Chunk{(uint32_t)k, (uint32_t)c});
+            off += t.n;
+        }
+        std::sort(l->written.begin(), l->written.end(), by_start);
+        for (size_t k = 1; k < l->written.size(); ++k)
+            if (l->written[k].lo < l->written[k - 1].hi) return RCS_EINVAL;
+        for (const Row &r : l->rows)
+            if (r.n > 0 && r.g != nullptr && l->touches(r.g, r.n * type_bytes(r.gt)))
+                return RCS_EINVAL;
+
+        const size_t rows_b = (l->rows.size() * sizeof(Row) + 255) / 256 * 256;
+        const size_t chunks_b = (chunks.size() * sizeof(Chunk) + 255) / 256 * 256;
+        const size_t norm_b = (size_t)kNormMaxBlocks * sizeof(double) + 256;
+        void *p = nullptr;
+        if (hipMalloc(&p, rows_b + chunks_b + 2 * norm_b) != hipSuccess) {
+            (void)hipGetLastError();
+            return RCS_ENOMEM;
+        }
+        l->mem = static_cast<char *>(p);
+        l->d_rows = reinterpret_cast<Row *>(l->mem);
+        l->d_chunks = reinterpret_cast<Chunk *>(l->mem + rows_b);
+        for (int k = 0; k < 2; ++k) {
+            char *q = l->mem + rows_b + chunks_b + (size_t)k * norm_b;
+            l->partials[k] = reinterpret_cast<double *>(q);
+            l->record[k] = reinterpret_cast<ClipScalars *>(q + kNormMaxBlocks * sizeof(double));
+        }
+        if (hipMemcpy(l->d_rows, l->rows.data(), l->rows.size() * sizeof(Row),
+                      hipMemcpyHostToDevice) != hipSuccess ||
+            hipMemcpy(l->d_chunks, chunks.data(), chunks.size() * sizeof(Chunk),
+                      hipMemcpyHostToDevice) != hipSuccess ||
+            hipStreamSynchronize(nullptr) != hipSuccess) {
+            (void)hipGetLastError();
+            (void)hipFree(p);
+            return RCS_EHIP;
+        }
+        drop.l = nullptr;
+        *out = l;
+        return RCS_OK;
+    } catch (const std::bad_alloc &) {
+        return RCS_ENOMEM;
+    }
+}
+
+int rcs_list_destroy(rcs_list *list) {
+    if (list == nullptr) return RCS_OK;
+    // hipFree is not among the calls that a capture under way elsewhere
+    // tolerates by default; this thread's calls are no part of one
+    hipStreamCaptureMode mode = hipStreamCaptureModeRelaxed;
+    const bool swapped = hipThreadExchangeStreamCaptureMode(&mode) == hipSuccess;
+    const hipError_t e = hipFree(list->mem);  // waits for the work that uses it
+    if (swapped) (void)hipThreadExchangeStreamCaptureMode(&mode);
+    delete list;
+    if (e == hipSuccess) return RCS_OK;
+    (void)hipGetLastError();
+    return RCS_EHIP;
+}
+
+int64_t rcs_list_elements(const rcs_list *list) { return list == nullptr ? -1 : list->n; }
+
+int rcs_list_bind_grads(rcs_list *list, const void *const *g, int64_t count, hipStream_t stream) {
+    int rc;
+    if (list == nullptr || g == nullptr || count != (int64_t)list->rows.size()) return RCS_EINVAL;
+    if ((rc = check_list(list)) != RCS_OK) return rc;
+    for (int64_t k = 0; k < count; ++k) {
+        const Row &r = list->rows[(size_t)k];
+        if (r.n == 0 || g[k] == nullptr) continue;
+        const int b = type_bytes(r.gt);
+        if ((rc = check_array(g[k], b * r.n, b)) != RCS_OK) return rc;
+        if (list->touches(g[k], b * r.n)) return RCS_EINVAL;
+    }
+    for (int64_t k = 0; k < count; k += kBind) {
+        const int some = (int)(count - k < kBind ? count - k : kBind);
+        Pointers p;
+        for (int j = 0; j < kBind; ++j) p.p[j] = j < some ? g[k + j] : nullptr;
+        hipLaunchKernelGGL(list_bind, dim3(1), dim3(kBind), 0, stream, list->d_rows + k, some, p);
+        for (int j = 0; j < some; ++j) list->rows[(size_t)(k + j)].g = g[k + j];
+    }
+    return hipGetLastError() == hipSuccess ? RCS_OK : RCS_EHIP;
+}
+
+int grad_global_norm_list(const rcs_list *list, float grad_scale, double *norm_out,
+                          hipStream_t stream) {
+    int rc;
+    if (list == nullptr || norm_out == nullptr) return RCS_EINVAL;
+    if (!std::isfinite(grad_scale) || !(grad_scale > 0.0f)) return RCS_EINVAL;
+    if ((rc = check_list(list)) != RCS_OK) return rc;
+    if ((rc = rcs_check_norm_out(norm_out, list->dev)) != RCS_OK) return rc;
+    double *partials = list->partials[1];
+    ClipScalars *record = list->record[1];
+    std::atomic<bool> *has_norm = nullptr;
+    if (!capturing(stream)) {
+        void *r = nullptr;
+        if ((rc = rcs_norm_buffers(stream, &partials, &r, &has_norm)) != RCS_OK) return rc;
+        record = static_cast<ClipScalars *>(r);
+    }
+    const bool direct = on_device(norm_out);
+    launch_norm(list, grad_scale, partials, stream);
+    hipLaunchKernelGGL(list_norm_final, dim3(1), dim3(kUpdThreads), 0, stream,
+                       (const double *)partials, list->norm_blocks(), INFINITY, record,
+                       direct ? norm_out : nullptr);
+    if (hipGetLastError() != hipSuccess) return RCS_EHIP;
+    if (has_norm != nullptr) *has_norm = true;
+    if (!direct && hipMemcpyAsync(norm_out, &record->norm, sizeof(double), hipMemcpyDefault,
+                                  stream) != hipSuccess)
+        return RCS_EHIP;
+    return RCS_OK;
+}
+
+int adamw_clip_step_list(rcs_list *list, int32_t t, float lr, float clip, float grad_scale,
+                         double beta1, double beta2, float eps, uint32_t seed, double *norm_out,
+                         hipStream_t stream) {
+    int rc;
+    if (list == nullptr || t < 1) return RCS_EINVAL;
+    if (!std::isfinite(lr) || std::isnan(clip) || !(clip > 0.0f)) return RCS_EINVAL;
+    if (!std::isfinite(grad_scale) || !(grad_scale > 0.0f)) return RCS_EINVAL;
+    if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0)) return RCS_EINVAL;
+    if (!std::isnormal(eps) || !(eps > 0.0f)) return RCS_EINVAL;
+    if ((rc = check_list(list)) != RCS_OK) return rc;
+    if (norm_out != nullptr && (rc = rcs_check_norm_out(norm_out, list->dev)) != RCS_OK) return rc;
+    ListScalars h;
+    h.lr = lr;
+    h.bc1 = (float)(1.0 - std::pow(beta1, (double)t));
+    h.bc2 = (float)(1.0 - std::pow(beta2, (double)t));
+    h.b1 = (float)beta1;
+    h.c1 = (float)(1.0 - beta1);
+    h.b2 = (float)beta2;
+    h.c2 = (float)(1.0 - beta2);
+    h.eps = eps;
+    h.gscale = grad_scale;
+    h.key = mixed(mixed(seed * kHashA + (uint32_t)t * kHashB) + kHashK);
+    const bool fold = list->n <= kListFoldMaxN, q8 = list->bits == 8;
+    const bool direct = norm_out != nullptr && on_device(norm_out);
+    double *partials = list->partials[0], *dev_out = direct ? norm_out : nullptr;
+    ClipScalars *record = list->record[0];
+    const int nparts = list->norm_blocks();
+    launch_norm(list, grad_scale, partials, stream);
+    if (!fold)
+        hipLaunchKernelGGL(list_norm_final, dim3(1), dim3(kUpdThreads), 0, stream,
+                           (const double *)partials, nparts, clip, record, dev_out);
+    auto *kernel = q8 ? (fold ? list_update<true, true> : list_update<true, false>)
+                      : (fold ? list_update<false, true> : list_update<false, false>);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)list->nchunks), dim3(kUpdThreads), 0, stream,
+                       (const Row *)list->d_rows, (const Chunk *)list->d_chunks,
+                       (const double *)partials, nparts, clip, record, dev_out, h);
+    if (hipGetLastError() != hipSuccess) return RCS_EHIP;
+    if (norm_out != nullptr && !direct &&
+        hipMemcpyAsync(norm_out, &record->norm, sizeof(double), hipMemcpyDefault, stream) !=
+            hipSuccess)
+        return RCS_EHIP;
+    return RCS_OK;
+}
+
+int rcs_list_export(const rcs_list *list, void *w, int w_type, void *m, int m_type, void *v,
+                    int v_type, hipStream_t stream) {
+    int rc;
+    if (list == nullptr || (w == nullptr && m == nullptr && v == nullptr)) return RCS_EINVAL;
+    if ((rc = check_list(list)) != RCS_OK) return rc;
+    if ((rc = check_flat(list, w, w_type, true)) != RCS_OK) return rc;
+    if ((rc = check_flat(list, m, m_type, true)) != RCS_OK) return rc;
+    if ((rc = check_flat(list, v, v_type, true)) != RCS_OK) return rc;
+    if (!apart(w, w_type, m, m_type, list->n) || !apart(w, w_type, v, v_type, list->n) ||
+        !apart(m, m_type, v, v_type, list->n))
+        return RCS_EINVAL;
+    const Flat f{w, m, v, w_type, m_type, v_type};
+    auto *kernel = list->bits == 8 ? list_export<true> : list_export<false>;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)list->nchunks), dim3(kUpdThreads), 0, stream,
+                       (const Row *)list->d_rows, (const Chunk *)list->d_chunks, f);
+    return hipGetLastError() == hipSuccess ? RCS_OK : RCS_EHIP;
+}
+
+int rcs_list_import(rcs_list *list, const void *w, int w_type, const void *m, int m_type,
+                    const void *v, int v_type, hipStream_t stream) {
+    int rc;
+    if (list == nullptr || (w == nullptr && m == nullptr && v == nullptr)) return RCS_EINVAL;
+    if (list->bits == 8 && (m == nullptr) != (v == nullptr)) return RCS_EINVAL;
+    if ((rc = check_list(list)) != RCS_OK) return rc;
+    if ((rc = check_flat(list, w, w_type, false)) != RCS_OK) return rc;
+    if ((rc = check_flat(list, m, m_type, false)) != RCS_OK) return rc;
+    if ((rc = check_flat(list, v, v_type, false)) != RCS_OK) return rc;
+    const Flat f{const_cast<void *>(w), const_cast<void *>(m), const_cast<void *>(v), w_type,
+                 m_type, v_type};
+    auto *kernel = list->bits == 8 ? list_import<true> : list_import<false>;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)list->nchunks), dim3(kUpdThreads), 0, stream,
+                       (const Row *)list->d_rows, (const Chunk *)list->d_chunks, f);
+    return hipGetLastError() == hipSuccess ? RCS_OK : RCS_EHIP;
+}
+
+}  // extern "C"
