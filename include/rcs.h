@@ -391,7 +391,7 @@ typedef struct rcs_list rcs_list;
 
 /*
  * rcs_list_create copies the description of `count` tensors to the current
- * device (about 80 bytes a tensor and 8 for each 1,024 elements) and waits for
+ * device (about 80 bytes a tensor and 8 for each 512 elements) and waits for
  * that; the arrays stay the caller's and must live as long as the list. It
  * allocates, so call it before a capture. No later call of the list allocates,
  * except that grad_global_norm_list uses its stream's workspace (rcs_init).

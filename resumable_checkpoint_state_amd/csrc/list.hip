@@ -35,13 +35,17 @@
 // zero only if it is exactly zero, so that no m is divided by eps alone.
 //
 // Mapping. A table row per tensor (pointers, length, decay, types) and one
-// entry per chunk of 1,024 elements (tensor, chunk within it) live in device
+// entry per chunk of 512 elements (tensor, chunk within it) live in device
 // memory and are made once, when the list is. One wave takes one chunk: it
-// reads its entry and row through scalar loads and then streams 16 consecutive
-// elements per lane, in two halves of 8, in 16-byte accesses that need only the
-// element's own alignment (so tensors may be views at any offset). The type
+// reads its entry and row through scalar loads and then streams its elements in
+// two rounds of 4 consecutive ones per lane, so that each access of a wave
+// covers whole lines (8 a lane put the halves of a float32 line into two
+// accesses: 802 against 683 us); the accesses need only the element's own
+// alignment, so tensors may be views at any offset. The type
 // combination is a uniform branch per wave, so a list of mixed types is one
-// launch. Bound by HBM: see the kernels.
+// launch. Blocks take chunks in address order (putting each XCD on its own
+// eighth, as the flat update does, was slower here: 651 against 607 us a step
+// of the 124,356,864-element float32 list). Bound by HBM: see the kernels.
 
 #include <hip/hip_runtime.h>
 
@@ -62,11 +66,18 @@
 namespace {
 
 constexpr int kBlock = RCS_LIST_BLOCK;  // elements that share a block exponent
-constexpr int kVec = 8;                 // consecutive elements of a lane
-constexpr int kRounds = 2;              // such groups per lane and chunk
-constexpr int kChunk = kWave * kVec * kRounds;
-static_assert(kChunk % kBlock == 0 && kBlock == 16 * kVec, "a block is one 16-lane row");
-constexpr int kListNormThreads = 512;
+// Elements of one wave. The update of the 124,356,864-element float32 list in
+// one process, same buffers: 607 us a step with 512 elements, 615 with 256,
+// 624 with 1,024 (the flat update: 604).
+constexpr int kChunk = 512;
+static_assert(kChunk % kBlock == 0 && kChunk % (8 * kWave) == 0, "whole blocks and vectors");
+// Norm pass: a block of 16 waves per CU, each with 4 loads of 16 bytes a lane in
+// flight, in runs of 4 chunks (of float32 or bfloat16 gradients of the same
+// list: 86 and 51 us; 8 waves with 8 loads and runs of 8: 89 and 52; runs of
+// one stretch per wave: 97 and 57).
+constexpr int kListNormThreads = 1024;
+constexpr int kRun = 4;
+constexpr int kDeep = 4;
 // Lowest block exponents (biased): the smallest value and, for m, half of it
 // are then normal floats.
 constexpr int kLowM = 18, kLowV = 33;
@@ -92,7 +103,8 @@ struct Chunk {
 
 struct ListScalars {
     float lr, bc1, bc2, b1, c1, b2, c2, eps, gscale;
-    uint32_t key;  // of the update's random bits
+    float lr1, r2;  // lr / bc1 and 1 / bc2, for the free evaluation
+    uint32_t key;   // of the update's random bits
 };
 
 // ------------------------------------------------------------- element types
@@ -111,8 +123,24 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 // 16 bytes at the alignment of an element: the hardware's vector accesses need
 // no more.
-typedef u32x4 u32x4_by4 __attribute__((aligned(4)));
-typedef u32x4 u32x4_by2 __attribute__((aligned(2)));
+template <int DWORDS, int ALIGN>
+struct Vector;
+template <>
+struct Vector<4, 4> {
+    typedef u32x4 type __attribute__((aligned(4)));
+};
+template <>
+struct Vector<4, 2> {
+    typedef u32x4 type __attribute__((aligned(2)));
+};
+template <>
+struct Vector<2, 4> {
+    typedef u32x2 type __attribute__((aligned(4)));
+};
+template <>
+struct Vector<2, 2> {
+    typedef u32x2 type __attribute__((aligned(2)));
+};
 
 // A pointer that came out of a table is one to device memory: said so, its
 // accesses are global ones rather than flat ones, which would wait for LDS too.
@@ -123,9 +151,9 @@ __device__ __forceinline__ Global<V> global(const void *p) {
     return (Global<V>)reinterpret_cast<uintptr_t>(p);
 }
 
-template <class T>
-struct Raw {  // kVec elements as they lie in memory
-    uint32_t d[kVec * T::kBytes / 4];
+template <class T, int V>
+struct Raw {  // V elements as they lie in memory
+    uint32_t d[V * T::kBytes / 4];
 };
 
 __device__ __forceinline__ float elem_f32(uint32_t bits, F32) { return __uint_as_float(bits); }
@@ -136,56 +164,63 @@ __device__ __forceinline__ float elem_f32(uint32_t bits, F16) {
     return (float)__builtin_bit_cast(_Float16, (uint16_t)bits);
 }
 
-// One rounding to nearest even; a NaN stays one.
-__device__ __forceinline__ uint32_t elem_bits(float x, F32) { return __float_as_uint(x); }
-__device__ __forceinline__ uint32_t elem_bits(float x, BF16) {
-    return __builtin_bit_cast(uint16_t, (__bf16)x);
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+
+// One rounding each to nearest even; a NaN stays one.
+__device__ __forceinline__ uint32_t two_bits(float x, float y, BF16) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{x, y}, bf16x2));
 }
-__device__ __forceinline__ uint32_t elem_bits(float x, F16) {
-    return __builtin_bit_cast(uint16_t, (_Float16)x);
+__device__ __forceinline__ uint32_t two_bits(float x, float y, F16) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{x, y}, f16x2));
 }
 
-template <class T>
-__device__ __forceinline__ void unpack(const Raw<T> &r, float (&x)[kVec]) {
+template <class T, int V>
+__device__ __forceinline__ void unpack(const Raw<T, V> &r, float (&x)[V]) {
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
+    for (int i = 0; i < V; ++i) {
         if constexpr (T::kBytes == 4) x[i] = elem_f32(r.d[i], T{});
         else x[i] = elem_f32((r.d[i / 2] >> (16 * (i & 1))) & 0xFFFFu, T{});
     }
 }
 
-template <class T>
-__device__ __forceinline__ Raw<T> pack(const float (&x)[kVec]) {
-    Raw<T> r;
+template <class T, int V>
+__device__ __forceinline__ Raw<T, V> pack(const float (&x)[V]) {
+    Raw<T, V> r;
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-        if constexpr (T::kBytes == 4) r.d[i] = elem_bits(x[i], T{});
-        else if (i & 1) r.d[i / 2] |= elem_bits(x[i], T{}) << 16;
-        else r.d[i / 2] = elem_bits(x[i], T{});
+    for (int i = 0; i < V; i += 2) {
+        if constexpr (T::kBytes == 4) {
+            r.d[i] = __float_as_uint(x[i]);
+            r.d[i + 1] = __float_as_uint(x[i + 1]);
+        } else {
+            r.d[i / 2] = two_bits(x[i], x[i + 1], T{});
+        }
     }
     return r;
 }
 
-// The kVec elements from element i of p on; cnt of them exist (the others
-// come as zero). Streaming loads unless KEEP.
-template <class T, bool KEEP = false>
-__device__ __forceinline__ Raw<T> load(const void *p, int64_t i, int cnt) {
-    Raw<T> r;
+// The V elements from element i of p on; cnt of them exist (the others come as
+// zero), all of them with FULL. Streaming loads unless KEEP.
+template <class T, int V, bool FULL, bool KEEP = false>
+__device__ __forceinline__ Raw<T, V> load(const void *p, int64_t i, int cnt) {
+    Raw<T, V> r;
+    constexpr int kDwords = (int)sizeof(r) / 4, kWide = kDwords < 4 ? kDwords : 4;
     const char *a = static_cast<const char *>(p) + i * T::kBytes;
-    if (cnt == kVec) {
-        using V = std::conditional_t<T::kBytes == 4, u32x4_by4, u32x4_by2>;
-        const Global<V> q = global<V>(a);
+    if (FULL || cnt == V) {
+        using X = typename Vector<kWide, T::kBytes>::type;
+        const Global<X> q = global<X>(a);
 #pragma unroll
-        for (int k = 0; k < (int)sizeof(r) / 16; ++k) {
-            const u32x4 x = KEEP ? (u32x4)q[k] : (u32x4)__builtin_nontemporal_load(q + k);
+        for (int k = 0; k < kDwords / kWide; ++k) {
+            const X x = KEEP ? q[k] : __builtin_nontemporal_load(q + k);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) r.d[4 * k + j] = x[j];
+            for (int j = 0; j < kWide; ++j) r.d[kWide * k + j] = x[j];
         }
     } else {
 #pragma unroll
-        for (int k = 0; k < (int)sizeof(r) / 4; ++k) r.d[k] = 0;
+        for (int k = 0; k < kDwords; ++k) r.d[k] = 0;
 #pragma unroll
-        for (int k = 0; k < kVec; ++k) {
+        for (int k = 0; k < V; ++k) {
             if (k >= cnt) continue;
             if constexpr (T::kBytes == 4)
                 r.d[k] = global<uint32_t>(a)[k];
@@ -196,20 +231,23 @@ __device__ __forceinline__ Raw<T> load(const void *p, int64_t i, int cnt) {
     return r;
 }
 
-template <class T>
-__device__ __forceinline__ void store(void *p, int64_t i, int cnt, const Raw<T> &r) {
+template <bool FULL, class T, int V>
+__device__ __forceinline__ void store(void *p, int64_t i, int cnt, const Raw<T, V> &r) {
+    constexpr int kDwords = (int)sizeof(r) / 4, kWide = kDwords < 4 ? kDwords : 4;
     char *a = static_cast<char *>(p) + i * T::kBytes;
-    if (cnt == kVec) {
-        using V = std::conditional_t<T::kBytes == 4, u32x4_by4, u32x4_by2>;
-        const Global<V> q = global<V>(a);
+    if (FULL || cnt == V) {
+        using X = typename Vector<kWide, T::kBytes>::type;
+        const Global<X> q = global<X>(a);
 #pragma unroll
-        for (int k = 0; k < (int)sizeof(r) / 16; ++k) {
-            const u32x4 x = {r.d[4 * k], r.d[4 * k + 1], r.d[4 * k + 2], r.d[4 * k + 3]};
-            __builtin_nontemporal_store((V)x, q + k);
+        for (int k = 0; k < kDwords / kWide; ++k) {
+            X x;
+#pragma unroll
+            for (int j = 0; j < kWide; ++j) x[j] = r.d[kWide * k + j];
+            __builtin_nontemporal_store(x, q + k);
         }
     } else {
 #pragma unroll
-        for (int k = 0; k < kVec; ++k) {
+        for (int k = 0; k < V; ++k) {
             if (k >= cnt) continue;
             if constexpr (T::kBytes == 4)
                 global<uint32_t>(a)[k] = r.d[k];
@@ -227,11 +265,12 @@ __device__ __forceinline__ void by_type(int t, F f) {
     else f(F16{});
 }
 
-// How many of the lane's kVec elements of round j lie in the tensor; left:
-// the tensor's elements from the chunk's first on.
-__device__ __forceinline__ int count_of(int64_t left, int j) {
-    const int64_t r = left - (j * kWave + (int)(threadIdx.x & (kWave - 1))) * kVec;
-    return r >= kVec ? kVec : r > 0 ? (int)r : 0;
+// How many of the V elements that begin `at` elements after a point lie in the
+// tensor, which has `left` from that point on.
+template <int V>
+__device__ __forceinline__ int count_of(int64_t left, int at) {
+    const int64_t r = left - at;
+    return r >= V ? V : r > 0 ? (int)r : 0;
 }
 
 // ----------------------------------------------------------- 8-bit moments
@@ -243,24 +282,34 @@ __host__ __device__ __forceinline__ uint32_t mixed(uint32_t x) {
     return x ^ (x >> 15);
 }
 
-// The random bits of elements i .. i + kVec - 1 of the list.
-__device__ __forceinline__ void random_bits(int64_t i, uint32_t key, uint32_t (&r)[kVec]) {
+// The random bits of elements i .. i + V - 1 of the list; carry: the upper half
+// of an index may change among them.
+template <int V>
+__device__ __forceinline__ void random_bits(int64_t i, uint32_t key, bool carry,
+                                            uint32_t (&r)[V]) {
     const uint32_t x = (uint32_t)i * kHashA + (uint32_t)(i >> 32) * kHashB + key;
+    if (!carry) {
 #pragma unroll
-    for (int k = 0; k < kVec; ++k) {
-        // a carry into the index's upper half
-        const uint32_t c = (uint32_t)((i + k) >> 32) - (uint32_t)(i >> 32);
-        r[k] = mixed(x + (uint32_t)k * kHashA + c * kHashB);
+        for (int k = 0; k < V; ++k) r[k] = mixed(x + (uint32_t)k * kHashA);
+    } else {
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const uint32_t up = (uint32_t)((i + k) >> 32) - (uint32_t)(i >> 32);
+            r[k] = mixed(x + (uint32_t)k * kHashA + up * kHashB);
+        }
     }
 }
 
-// The largest of a 16-lane row's values, in every lane of the row.
-__device__ __forceinline__ uint32_t row_max(uint32_t x) {
+// The largest of the values of the lanes that share a block of V elements
+// each, in every one of them.
+template <int V>
+__device__ __forceinline__ uint32_t block_max(uint32_t x) {
     auto with = [&](uint32_t y) { x = x > y ? x : y; };
     with((uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0xB1, 0xF, 0xF, true));   // pairs
     with((uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x4E, 0xF, 0xF, true));   // quads
     with((uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x141, 0xF, 0xF, true));  // 8 lanes
     with((uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x140, 0xF, 0xF, true));  // 16 lanes
+    if constexpr (V == 4) with((uint32_t)__shfl_xor((int)x, 16, kWave));
     return x;
 }
 
@@ -308,9 +357,10 @@ __device__ __forceinline__ uint32_t encode_m(float m, uint32_t add, int base) {
 
 __device__ __forceinline__ uint32_t half_unit(uint32_t mag) { return 0x7FFFFu + ((mag >> 20) & 1u); }
 
-// 8 codes of one byte.
+// V codes of one byte.
+template <int V>
 struct Codes {
-    uint32_t d[kVec / 4];
+    uint32_t d[V / 4];
     __device__ __forceinline__ uint32_t at(int i) const { return (d[i / 4] >> (8 * (i & 3))) & 0xFFu; }
     __device__ __forceinline__ void put(int i, uint32_t k) {
         if ((i & 3) == 0) d[i / 4] = k;
@@ -318,35 +368,47 @@ struct Codes {
     }
 };
 
-__device__ __forceinline__ Codes load_codes(const void *p, int64_t i) {
-    const u32x2 x = __builtin_nontemporal_load(global<u32x2>(static_cast<const char *>(p) + i));
-    return Codes{{x.x, x.y}};
+template <int V>
+__device__ __forceinline__ Codes<V> load_codes(const void *p, int64_t i) {
+    Codes<V> c;
+    const char *a = static_cast<const char *>(p) + i;
+    if constexpr (V == 8) {
+        const u32x2 x = __builtin_nontemporal_load(global<u32x2>(a));
+        c.d[0] = x.x;
+        c.d[1] = x.y;
+    } else {
+        c.d[0] = __builtin_nontemporal_load(global<uint32_t>(a));
+    }
+    return c;
 }
 
-__device__ __forceinline__ void store_codes(void *p, int64_t i, const Codes &c) {
-    __builtin_nontemporal_store(u32x2{c.d[0], c.d[1]},
-                                global<u32x2>(static_cast<char *>(p) + i));
+template <int V>
+__device__ __forceinline__ void store_codes(void *p, int64_t i, const Codes<V> &c) {
+    char *a = static_cast<char *>(p) + i;
+    if constexpr (V == 8) __builtin_nontemporal_store(u32x2{c.d[0], c.d[1]}, global<u32x2>(a));
+    else __builtin_nontemporal_store(c.d[0], global<uint32_t>(a));
 }
 
 // Block exponents and codes of the lane's m and v (those past the tensor's end
-// are zero), written to the chunk's block; every lane of the row calls this.
-template <class AddM, class AddV>
-__device__ __forceinline__ void store_moments(const Row &t, int64_t i, const float (&m)[kVec],
-                                              const float (&v)[kVec], bool active, AddM add_m,
+// are zero), written to their block; every lane of the block calls this.
+template <int V, class AddM, class AddV>
+__device__ __forceinline__ void store_moments(const Row &t, int64_t i, const float (&m)[V],
+                                              const float (&v)[V], bool active, AddM add_m,
                                               AddV add_v) {
     uint32_t am = 0, av = 0;
 #pragma unroll
-    for (int k = 0; k < kVec; ++k) {
+    for (int k = 0; k < V; ++k) {
         const uint32_t um = __float_as_uint(m[k]) & 0x7FFFFFFFu;
         const uint32_t uv = __float_as_uint(v[k]) & 0x7FFFFFFFu;
         am = am > um ? am : um;
         av = av > uv ? av : uv;
     }
-    const int em = block_exponent(row_max(am), kLowM), ev = block_exponent(row_max(av), kLowV);
+    const int em = block_exponent(block_max<V>(am), kLowM);
+    const int ev = block_exponent(block_max<V>(av), kLowV);
     const int bm = base_m(em), bv = base_v(ev);
-    Codes cm, cv;
+    Codes<V> cm, cv;
 #pragma unroll
-    for (int k = 0; k < kVec; ++k) {
+    for (int k = 0; k < V; ++k) {
         cm.put(k, encode_m(m[k], add_m(k), bm));
         const uint32_t uv = __float_as_uint(v[k]) & 0x7FFFFFFFu;
         cv.put(k, encode(uv, add_v(k), bv, 0u, 255));
@@ -354,14 +416,16 @@ __device__ __forceinline__ void store_moments(const Row &t, int64_t i, const flo
     if (!active) return;
     store_codes(t.m, i, cm);
     store_codes(t.v, i, cv);
-    if ((threadIdx.x & 15u) == 0) global<uint16_t>(t.e)[i / kBlock] = (uint16_t)(em | (ev << 8));
+    if ((threadIdx.x & (kBlock / V - 1)) == 0)
+        global<uint16_t>(t.e)[i / kBlock] = (uint16_t)(em | (ev << 8));
 }
 
-__device__ __forceinline__ void decode_moments(const Codes &cm, const Codes &cv, uint32_t e,
-                                               float (&m)[kVec], float (&v)[kVec]) {
+template <int V>
+__device__ __forceinline__ void decode_moments(const Codes<V> &cm, const Codes<V> &cv, uint32_t e,
+                                               float (&m)[V], float (&v)[V]) {
     const int bm = base_m((int)(e & 0xFFu)), bv = base_v((int)(e >> 8));
 #pragma unroll
-    for (int k = 0; k < kVec; ++k) {
+    for (int k = 0; k < V; ++k) {
         m[k] = decode_m(cm.at(k), bm);
         v[k] = decode_v(cv.at(k), bv);
     }
@@ -369,44 +433,83 @@ __device__ __forceinline__ void decode_moments(const Codes &cm, const Codes &cv,
 
 // ------------------------------------------------------------------- kernels
 
-// Per-block float64 partial sums of squares of the list's gradients: wave j
-// of the grid takes chunks j, j + waves, ...; the order depends on the list
-// alone.
+template <class G, int V>
+__device__ __forceinline__ void add_squares(const Raw<G, V> &r, float gscale, double &acc) {
+    float x[V];
+    unpack(r, x);
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        const double d = (double)(x[k] * gscale);
+        acc = __builtin_fma(d, d, acc);  // the square of a float is exact in float64
+    }
+}
+
+// Sum of squares of elements first .. stop - 1 of a gradient, this lane's part.
+template <class G, bool KEEP>
+__device__ __forceinline__ double squares_of(const void *g, int64_t first, int64_t stop,
+                                             float gscale) {
+    constexpr int V = 16 / G::kBytes;  // one 16-byte vector
+    constexpr int kStep = kWave * V;
+    const int lane = (int)threadIdx.x & (kWave - 1);
+    double acc[4] = {};
+    int64_t i = first + lane * V;
+    int64_t at = first;
+    for (; at + kDeep * kStep <= stop; at += kDeep * kStep, i += kDeep * kStep) {
+        Raw<G, V> r[kDeep];
+#pragma unroll
+        for (int q = 0; q < kDeep; ++q) r[q] = load<G, V, true, KEEP>(g, i + q * kStep, V);
+#pragma unroll
+        for (int q = 0; q < kDeep; ++q) add_squares(r[q], gscale, acc[q & 3]);
+    }
+    for (; at < stop; at += kStep, i += kStep)
+        add_squares(load<G, V, false, KEEP>(g, i, count_of<V>(stop - i, 0)), gscale, acc[0]);
+    return (acc[0] + acc[1]) + (acc[2] + acc[3]);
+}
+
+// Per-block float64 partial sums of squares of the list's gradients. The waves
+// of the grid take runs of kRun consecutive chunks in turn, and go through a run
+// one stretch of a tensor at a time; the order depends on the list's lengths
+// alone. The table entries of a run are fetched while the one before it is
+// summed.
 __global__ __launch_bounds__(kListNormThreads) void list_norm_partial(
-    const Row *__restrict__ rows, const Chunk *__restrict__ chunks, int64_t nchunks, float gscale,
-    double *__restrict__ partials) {
+    const Row *__restrict__ rows, const Chunk *__restrict__ chunks, int64_t nchunks,
+    int64_t keep_from, float gscale, double *__restrict__ partials) {
     __shared__ double lds[kListNormThreads / kWave];
     constexpr int kWaves = kListNormThreads / kWave;
-    double acc[kRounds] = {};
-    const int64_t step = (int64_t)gridDim.x * kWaves;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
-    for (int64_t j = (int64_t)blockIdx.x * kWaves + wave; j < nchunks; j += step) {
-        const Chunk c = chunks[j];
-        const Row t = rows[c.row];
-        if (t.g == nullptr) continue;
-        const int64_t first = (int64_t)c.part * kChunk, left = t.n - first;
-        by_type(t.gt, [&](auto T) {
-            using G = decltype(T);
-            Raw<G> r[kRounds];
-#pragma unroll
-            for (int q = 0; q < kRounds; ++q)
-                r[q] = load<G, true>(t.g, first + (q * kWave + (threadIdx.x & (kWave - 1))) * kVec,
-                                     count_of(left, q));
-#pragma unroll
-            for (int q = 0; q < kRounds; ++q) {
-                float x[kVec];
-                unpack(r[q], x);
-#pragma unroll
-                for (int k = 0; k < kVec; ++k) {
-                    const double d = (double)(x[k] * gscale);
-                    acc[q] += d * d;
-                }
-            }
-        });
-    }
+    const int64_t step = (int64_t)gridDim.x * kWaves * kRun;
+    int64_t run = ((int64_t)blockIdx.x * kWaves + wave) * kRun;
     double sum = 0.0;
-#pragma unroll
-    for (int q = 0; q < kRounds; ++q) sum += acc[q];
+    if (run < nchunks) {
+        Chunk c = chunks[run];
+        Chunk next = chunks[run + step < nchunks ? run + step : run];
+        Row t = rows[c.row];
+        for (; run < nchunks; run += step) {
+            const Chunk after = chunks[run + 2 * step < nchunks ? run + 2 * step : run];
+            const Row next_row = rows[next.row];
+            const int64_t end = run + kRun < nchunks ? run + kRun : nchunks;
+            for (int64_t j = run;;) {
+                const int64_t first = (int64_t)c.part * kChunk;
+                const int64_t whole = (t.n - first + kChunk - 1) / kChunk;
+                const int64_t mine = whole < end - j ? whole : end - j;
+                int64_t stop = first + mine * kChunk;
+                if (stop > t.n) stop = t.n;
+                if (t.g != nullptr)
+                    by_type(t.gt, [&](auto G) {
+                        using T = decltype(G);
+                        sum += run < keep_from ? squares_of<T, false>(t.g, first, stop, gscale)
+                                               : squares_of<T, true>(t.g, first, stop, gscale);
+                    });
+                j += mine;
+                if (j >= end) break;
+                c = chunks[j];
+                t = rows[c.row];
+            }
+            c = next;
+            t = next_row;
+            next = after;
+        }
+    }
     sum = block_sum<kListNormThreads>(sum, lds);
     if (threadIdx.x == 0) partials[blockIdx.x] = sum;
 }
@@ -425,113 +528,137 @@ __global__ __launch_bounds__(kUpdThreads) void list_norm_final(const double *__r
     }
 }
 
-__device__ __forceinline__ void adamw(float &w, float g, float &m, float &v, float s, float decay,
-                                      const ListScalars &h) {
+// New moments of one element; the operations and their roundings are part of
+// the definition (8-bit moments are rounded from exactly these).
+__device__ __forceinline__ void moments(float g, float &m, float &v, float s,
+                                        const ListScalars &h) {
     const float ga = g * h.gscale;
     const float gp = ga * s;
-    const float mi = h.b1 * m + h.c1 * gp;
-    const float vi = h.b2 * v + h.c2 * (gp * gp);
-    const float mh = mi / h.bc1;
-    const float vh = vi / h.bc2;
-    const float den = __builtin_sqrtf(vh) + h.eps;
-    w = w * decay - (h.lr * mh) / den;
-    m = mi;
-    v = vi;
+    m = h.b1 * m + h.c1 * gp;
+    v = h.b2 * v + h.c2 * (gp * gp);
 }
 
-// One chunk of 32-bit moments: W, G the types of weights and gradients.
-template <class W, class G, class Record>
+// The weight in the flat update's operation sequence: divisions and root
+// correctly rounded (beside 32-bit moments, where memory hides them).
+__device__ __forceinline__ float weight(float w, float m, float v, float decay,
+                                        const ListScalars &h) {
+    const float mh = m / h.bc1;
+    const float vh = v / h.bc2;
+    const float den = __builtin_sqrtf(vh) + h.eps;
+    return w * decay - (h.lr * mh) / den;
+}
+
+// The weight beside 8-bit moments, where the arithmetic is what counts: the
+// two divisions by constants are products, root and reciprocal the hardware's
+// (1 ulp each; v below float32's normal range only shows next to an eps of
+// its size).
+__device__ __forceinline__ float weight_free(float w, float m, float v, float decay,
+                                             const ListScalars &h) {
+    const float den = __builtin_amdgcn_sqrtf(v * h.r2) + h.eps;
+    return __builtin_fmaf(w, decay, -(m * h.lr1 * __builtin_amdgcn_rcpf(den)));
+}
+
+// R groups of 32-bit moments from element `first` on: W, G the types of weights
+// and gradients; FULL: all of them lie in the tensor.
+template <class W, class G, int V, int R, bool FULL, class Record>
 __device__ __forceinline__ void update32(const Row &t, int64_t first, Record record,
                                          const ListScalars &h) {
     const int64_t left = t.n - first;
-    int64_t i[kRounds];
-    int cnt[kRounds];
-    Raw<W> w[kRounds];
-    Raw<G> g[kRounds];
-    Raw<F32> m[kRounds], v[kRounds];
+    int64_t i[R];
+    int cnt[R];
+    Raw<W, V> w[R];
+    Raw<G, V> g[R];
+    Raw<F32, V> m[R], v[R];
 #pragma unroll
-    for (int q = 0; q < kRounds; ++q) {
-        cnt[q] = count_of(left, q);
-        i[q] = first + (q * kWave + (int)threadIdx.x) * kVec;
-        g[q] = load<G>(t.g, i[q], cnt[q]);
-        w[q] = load<W>(t.w, i[q], cnt[q]);
-        m[q] = load<F32>(t.m, i[q], cnt[q]);
-        v[q] = load<F32>(t.v, i[q], cnt[q]);
+    for (int q = 0; q < R; ++q) {
+        const int at = (q * kWave + (int)threadIdx.x) * V;
+        cnt[q] = FULL ? V : count_of<V>(left, at);
+        i[q] = first + at;
+        g[q] = load<G, V, FULL>(t.g, i[q], cnt[q]);
+        w[q] = load<W, V, FULL>(t.w, i[q], cnt[q]);
+        m[q] = load<F32, V, FULL>(t.m, i[q], cnt[q]);
+        v[q] = load<F32, V, FULL>(t.v, i[q], cnt[q]);
     }
     const ClipScalars cs = record();
     if (!cs.apply) return;
     const float decay = (float)(1.0 - (double)h.lr * (double)t.wd);
 #pragma unroll
-    for (int q = 0; q < kRounds; ++q) {
-        float ww[kVec], gg[kVec], mm[kVec], vv[kVec];
+    for (int q = 0; q < R; ++q) {
+        float ww[V], gg[V], mm[V], vv[V];
         unpack(w[q], ww);
         unpack(g[q], gg);
         unpack(m[q], mm);
         unpack(v[q], vv);
 #pragma unroll
-        for (int k = 0; k < kVec; ++k) adamw(ww[k], gg[k], mm[k], vv[k], cs.scale, decay, h);
-        store(t.w, i[q], cnt[q], pack<W>(ww));
-        store(t.m, i[q], cnt[q], pack<F32>(mm));
-        store(t.v, i[q], cnt[q], pack<F32>(vv));
+        for (int k = 0; k < V; ++k) {
+            moments(gg[k], mm[k], vv[k], cs.scale, h);
+            ww[k] = weight(ww[k], mm[k], vv[k], decay, h);
+        }
+        store<FULL>(t.w, i[q], cnt[q], pack<W>(ww));
+        store<FULL>(t.m, i[q], cnt[q], pack<F32>(mm));
+        store<FULL>(t.v, i[q], cnt[q], pack<F32>(vv));
         if constexpr (W::kBytes == 4) {
             if (t.c != nullptr) {
-                if (t.ct == RCS_BF16) store(t.c, i[q], cnt[q], pack<BF16>(ww));
-                else store(t.c, i[q], cnt[q], pack<F16>(ww));
+                if (t.ct == RCS_BF16) store<FULL>(t.c, i[q], cnt[q], pack<BF16>(ww));
+                else store<FULL>(t.c, i[q], cnt[q], pack<F16>(ww));
             }
         }
     }
 }
 
-// One chunk of 8-bit moments. The code arrays are filled up to whole blocks,
+// The same with 8-bit moments. The code arrays are filled up to whole blocks,
 // so a code access is always a whole vector; a block past the tensor's end is
 // not touched.
-template <class W, class G, class Record>
+template <class W, class G, int V, int R, bool FULL, class Record>
 __device__ __forceinline__ void update8(const Row &t, int64_t first, Record record,
                                         const ListScalars &h) {
     const int64_t left = t.n - first;
-    int64_t i[kRounds];
-    int cnt[kRounds];
-    bool active[kRounds];
-    Raw<W> w[kRounds];
-    Raw<G> g[kRounds];
-    Codes cm[kRounds], cv[kRounds];
-    uint32_t e[kRounds];
+    // (uniform: the group's first and last element of the list)
+    const bool carry = ((t.off + first) >> 32) != ((t.off + first + R * kWave * V - 1) >> 32);
+    int64_t i[R];
+    int cnt[R];
+    bool active[R];
+    Raw<W, V> w[R];
+    Raw<G, V> g[R];
+    Codes<V> cm[R], cv[R];
+    uint32_t e[R];
 #pragma unroll
-    for (int q = 0; q < kRounds; ++q) {
-        cnt[q] = count_of(left, q);
-        const int at = (q * kWave + (int)threadIdx.x) * kVec;
+    for (int q = 0; q < R; ++q) {
+        const int at = (q * kWave + (int)threadIdx.x) * V;
+        cnt[q] = FULL ? V : count_of<V>(left, at);
         i[q] = first + at;
-        active[q] = (at & ~(kBlock - 1)) < left;
-        g[q] = load<G>(t.g, i[q], cnt[q]);
-        w[q] = load<W>(t.w, i[q], cnt[q]);
+        active[q] = FULL || (at & ~(kBlock - 1)) < left;
+        g[q] = load<G, V, FULL>(t.g, i[q], cnt[q]);
+        w[q] = load<W, V, FULL>(t.w, i[q], cnt[q]);
         const int64_t ic = active[q] ? i[q] : 0;
-        cm[q] = load_codes(t.m, ic);
-        cv[q] = load_codes(t.v, ic);
+        cm[q] = load_codes<V>(t.m, ic);
+        cv[q] = load_codes<V>(t.v, ic);
         e[q] = global<uint16_t>(t.e)[ic / kBlock];
     }
     const ClipScalars cs = record();
     if (!cs.apply) return;
     const float decay = (float)(1.0 - (double)h.lr * (double)t.wd);
 #pragma unroll
-    for (int q = 0; q < kRounds; ++q) {
-        float ww[kVec], gg[kVec], mm[kVec], vv[kVec];
+    for (int q = 0; q < R; ++q) {
+        float ww[V], gg[V], mm[V], vv[V];
         unpack(w[q], ww);
         unpack(g[q], gg);
         decode_moments(cm[q], cv[q], e[q], mm, vv);
 #pragma unroll
-        for (int k = 0; k < kVec; ++k) {
-            adamw(ww[k], gg[k], mm[k], vv[k], cs.scale, decay, h);
-            if (k >= cnt[q]) mm[k] = vv[k] = 0.0f;
+        for (int k = 0; k < V; ++k) {
+            moments(gg[k], mm[k], vv[k], cs.scale, h);
+            ww[k] = weight_free(ww[k], mm[k], vv[k], decay, h);
+            if (!FULL && k >= cnt[q]) mm[k] = vv[k] = 0.0f;
         }
-        store(t.w, i[q], cnt[q], pack<W>(ww));
+        store<FULL>(t.w, i[q], cnt[q], pack<W>(ww));
         if constexpr (W::kBytes == 4) {
             if (t.c != nullptr) {
-                if (t.ct == RCS_BF16) store(t.c, i[q], cnt[q], pack<BF16>(ww));
-                else store(t.c, i[q], cnt[q], pack<F16>(ww));
+                if (t.ct == RCS_BF16) store<FULL>(t.c, i[q], cnt[q], pack<BF16>(ww));
+                else store<FULL>(t.c, i[q], cnt[q], pack<F16>(ww));
             }
         }
-        uint32_t r[kVec];
-        random_bits(t.off + i[q], h.key, r);
+        uint32_t r[V];
+        random_bits(t.off + i[q], h.key, carry, r);
         store_moments(t, i[q], mm, vv, active[q], [&](int k) { return r[k] & 0xFFFFFu; },
                       [&](int k) { return r[k] >> 12; });
     }
@@ -545,7 +672,7 @@ __global__ __launch_bounds__(kUpdThreads) void list_update(
     const Row *__restrict__ rows, const Chunk *__restrict__ chunks,
     const double *__restrict__ partials, int nparts, float clip, ClipScalars *__restrict__ record,
     double *__restrict__ norm_out, ListScalars h) {
-    const Chunk c = chunks[chunk_of_block()];
+    const Chunk c = chunks[blockIdx.x];
     const Row t = rows[c.row];
     double x[kPartsPerLane];
     if constexpr (FOLD) load_partials(partials, nparts, x);
@@ -568,8 +695,21 @@ __global__ __launch_bounds__(kUpdThreads) void list_update(
     const int64_t first = (int64_t)c.part * kChunk;
     by_type(t.wt, [&](auto W) {
         by_type(t.gt, [&](auto G) {
-            if constexpr (Q8) update8<decltype(W), decltype(G)>(t, first, get, h);
-            else update32<decltype(W), decltype(G)>(t, first, get, h);
+            using WT = decltype(W);
+            using GT = decltype(G);
+            constexpr int V = 4, R = kChunk / (kWave * V);
+            if (t.n - first >= kChunk) {
+                if constexpr (Q8) update8<WT, GT, V, R, true>(t, first, get, h);
+                else update32<WT, GT, V, R, true>(t, first, get, h);
+                return;
+            }
+            const ClipScalars r = get();  // the tensor's last chunk: one group at a time
+            auto same = [&] { return r; };
+#pragma unroll 1
+            for (int64_t at = first; at < t.n; at += kWave * V) {
+                if constexpr (Q8) update8<WT, GT, V, 1, false>(t, at, same, h);
+                else update32<WT, GT, V, 1, false>(t, at, same, h);
+            }
         });
     });
 }
@@ -581,99 +721,116 @@ struct Flat {
     int wt, mt, vt;
 };
 
+template <bool FULL, int V>
 __device__ __forceinline__ void store_as(int type, void *p, int64_t i, int cnt,
-                                         const float (&x)[kVec]) {
-    if (type == RCS_F32) store(p, i, cnt, pack<F32>(x));
-    else store(p, i, cnt, pack<BF16>(x));
+                                         const float (&x)[V]) {
+    if (type == RCS_F32) store<FULL>(p, i, cnt, pack<F32>(x));
+    else store<FULL>(p, i, cnt, pack<BF16>(x));
 }
 
+template <bool FULL, int V>
 __device__ __forceinline__ void load_as(int type, const void *p, int64_t i, int cnt,
-                                        float (&x)[kVec]) {
-    if (type == RCS_F32) unpack(load<F32>(p, i, cnt), x);
-    else unpack(load<BF16>(p, i, cnt), x);
+                                        float (&x)[V]) {
+    if (type == RCS_F32) unpack(load<F32, V, FULL>(p, i, cnt), x);
+    else unpack(load<BF16, V, FULL>(p, i, cnt), x);
 }
 
-template <bool Q8>
+// One group of V elements a lane from element `first` of t on.
+template <bool Q8, int V, bool FULL>
+__device__ __forceinline__ void export_group(const Row &t, int64_t first, const Flat &f) {
+    const int at = (int)threadIdx.x * V;
+    const int cnt = FULL ? V : count_of<V>(t.n - first, at);
+    const int64_t i = first + at;
+    if (cnt == 0) return;
+    float m[V], v[V];
+    if (f.m != nullptr || f.v != nullptr) {
+        if constexpr (Q8) {
+            decode_moments(load_codes<V>(t.m, i), load_codes<V>(t.v, i),
+                           global<uint16_t>(t.e)[i / kBlock], m, v);
+        } else {
+            if (f.m != nullptr) unpack(load<F32, V, FULL>(t.m, i, cnt), m);
+            if (f.v != nullptr) unpack(load<F32, V, FULL>(t.v, i, cnt), v);
+        }
+    }
+    if (f.w != nullptr)
+        by_type(t.wt, [&](auto W) {
+            float x[V];
+            unpack(load<decltype(W), V, FULL>(t.w, i, cnt), x);
+            store_as<FULL>(f.wt, f.w, t.off + i, cnt, x);
+        });
+    if (f.m != nullptr) store_as<FULL>(f.mt, f.m, t.off + i, cnt, m);
+    if (f.v != nullptr) store_as<FULL>(f.vt, f.v, t.off + i, cnt, v);
+}
+
+template <bool Q8, int V>
 __global__ __launch_bounds__(kUpdThreads) void list_export(const Row *__restrict__ rows,
                                                            const Chunk *__restrict__ chunks,
                                                            Flat f) {
     const Chunk c = chunks[blockIdx.x];
     const Row t = rows[c.row];
-    const int64_t first = (int64_t)c.part * kChunk, left = t.n - first;
+    const int64_t first = (int64_t)c.part * kChunk;
+    if (t.n - first >= kChunk) {
 #pragma unroll
-    for (int q = 0; q < kRounds; ++q) {
-        const int cnt = count_of(left, q);
-        const int64_t i = first + (q * kWave + (int)threadIdx.x) * kVec;
-        if (cnt == 0) continue;
-        if (f.w != nullptr)
-            by_type(t.wt, [&](auto W) {
-                float x[kVec];
-                unpack(load<decltype(W)>(t.w, i, cnt), x);
-                store_as(f.wt, f.w, t.off + i, cnt, x);
-            });
-        if (f.m == nullptr && f.v == nullptr) continue;
-        float m[kVec], v[kVec];
-        if constexpr (Q8) {
-            decode_moments(load_codes(t.m, i), load_codes(t.v, i),
-                           global<uint16_t>(t.e)[i / kBlock], m, v);
-        } else {
-            if (f.m != nullptr) unpack(load<F32>(t.m, i, cnt), m);
-            if (f.v != nullptr) unpack(load<F32>(t.v, i, cnt), v);
-        }
-        if (f.m != nullptr) store_as(f.mt, f.m, t.off + i, cnt, m);
-        if (f.v != nullptr) store_as(f.vt, f.v, t.off + i, cnt, v);
+        for (int q = 0; q < kChunk / (kWave * V); ++q)
+            export_group<Q8, V, true>(t, first + q * kWave * V, f);
+        return;
     }
+#pragma unroll 1
+    for (int64_t at = first; at < t.n; at += kWave * V) export_group<Q8, V, false>(t, at, f);
 }
 
 // With 8-bit moments, m and v come together (the host sees to it): a block's
 // two exponents are one store.
-template <bool Q8>
+template <bool Q8, int V, bool FULL>
+__device__ __forceinline__ void import_group(const Row &t, int64_t first, const Flat &f) {
+    const int at = (int)threadIdx.x * V;
+    const int64_t left = t.n - first;
+    const int cnt = FULL ? V : count_of<V>(left, at);
+    const int64_t i = first + at;
+    float m[V], v[V];
+    if (f.m != nullptr) load_as<FULL>(f.mt, f.m, t.off + i, cnt, m);
+    if (f.v != nullptr) load_as<FULL>(f.vt, f.v, t.off + i, cnt, v);
+    if (f.w != nullptr && cnt > 0) {
+        float x[V];
+        load_as<FULL>(f.wt, f.w, t.off + i, cnt, x);
+        by_type(t.wt, [&](auto W) { store<FULL>(t.w, i, cnt, pack<decltype(W)>(x)); });
+        if (t.c != nullptr) {
+            if (t.ct == RCS_BF16) store<FULL>(t.c, i, cnt, pack<BF16>(x));
+            else store<FULL>(t.c, i, cnt, pack<F16>(x));
+        }
+    }
+    if constexpr (Q8) {
+        if (f.m == nullptr) return;
+#pragma unroll
+        for (int k = 0; k < V; ++k) {  // v below zero is held as zero (a NaN is not)
+            const uint32_t u = __float_as_uint(v[k]);
+            v[k] = __uint_as_float((u >> 31) != 0 && u <= 0xFF800000u ? 0u : u & 0x7FFFFFFFu);
+        }
+        store_moments(
+            t, i, m, v, FULL || (at & ~(kBlock - 1)) < left,
+            [&](int k) { return half_unit(__float_as_uint(m[k]) & 0x7FFFFFFFu); },
+            [&](int k) { return half_unit(__float_as_uint(v[k])); });
+    } else {
+        if (f.m != nullptr && cnt > 0) store<FULL>(t.m, i, cnt, pack<F32>(m));
+        if (f.v != nullptr && cnt > 0) store<FULL>(t.v, i, cnt, pack<F32>(v));
+    }
+}
+
+template <bool Q8, int V>
 __global__ __launch_bounds__(kUpdThreads) void list_import(const Row *__restrict__ rows,
                                                            const Chunk *__restrict__ chunks,
                                                            Flat f) {
     const Chunk c = chunks[blockIdx.x];
     const Row t = rows[c.row];
-    const int64_t first = (int64_t)c.part * kChunk, left = t.n - first;
+    const int64_t first = (int64_t)c.part * kChunk;
+    if (t.n - first >= kChunk) {
 #pragma unroll
-    for (int q = 0; q < kRounds; ++q) {
-        const int cnt = count_of(left, q);
-        const int at = (q * kWave + (int)threadIdx.x) * kVec;
-        const int64_t i = first + at;
-        if (f.w != nullptr && cnt > 0) {
-            float x[kVec];
-            load_as(f.wt, f.w, t.off + i, cnt, x);
-            by_type(t.wt, [&](auto W) { store(t.w, i, cnt, pack<decltype(W)>(x)); });
-            if (t.c != nullptr) {
-                if (t.ct == RCS_BF16) store(t.c, i, cnt, pack<BF16>(x));
-                else store(t.c, i, cnt, pack<F16>(x));
-            }
-        }
-        float m[kVec], v[kVec];
-        if constexpr (Q8) {
-            if (f.m == nullptr) continue;
-            load_as(f.mt, f.m, t.off + i, cnt, m);
-            load_as(f.vt, f.v, t.off + i, cnt, v);
-#pragma unroll
-            for (int k = 0; k < kVec; ++k) {  // v below zero is held as zero
-                const uint32_t u = __float_as_uint(v[k]);  // (a NaN is not)
-                v[k] = __uint_as_float((u >> 31) != 0 && u <= 0xFF800000u ? 0u : u & 0x7FFFFFFFu);
-            }
-            store_moments(
-                t, i, m, v, (at & ~(kBlock - 1)) < left,
-                [&](int k) { return half_unit(__float_as_uint(m[k]) & 0x7FFFFFFFu); },
-                [&](int k) { return half_unit(__float_as_uint(v[k])); });
-        } else {
-            if (cnt == 0) continue;
-            if (f.m != nullptr) {
-                load_as(f.mt, f.m, t.off + i, cnt, m);
-                store(t.m, i, cnt, pack<F32>(m));
-            }
-            if (f.v != nullptr) {
-                load_as(f.vt, f.v, t.off + i, cnt, v);
-                store(t.v, i, cnt, pack<F32>(v));
-            }
-        }
+        for (int q = 0; q < kChunk / (kWave * V); ++q)
+            import_group<Q8, V, true>(t, first + q * kWave * V, f);
+        return;
     }
+#pragma unroll 1
+    for (int64_t at = first; at < t.n; at += kWave * V) import_group<Q8, V, false>(t, at, f);
 }
 
 // Other gradients for rows first .. first + count - 1. The pointers travel in
@@ -704,6 +861,7 @@ struct rcs_list {
     int bits = 32;
     int64_t n = 0;        // elements of all tensors
     int64_t nchunks = 0;
+    int64_t keep_from = 0;  // first chunk whose gradient the norm pass leaves in the cache
     std::vector<Row> rows;
     std::vector<Span> written;  // what an update writes, sorted
     char *mem = nullptr;        // everything below, one allocation
@@ -732,6 +890,9 @@ namespace {
 
 // The largest list whose update folds the final reduction of the norm.
 constexpr int64_t kListFoldMaxN = 8388608;
+// Bytes at the end of the gradients that the norm pass reads with cache-
+// allocating loads, so that the update finds them in the last-level cache.
+constexpr int64_t kCachedTailBytes = 320LL << 20;
 // Waves of a launch: the grid's work-items have to fit 32 bits.
 constexpr int64_t kMaxChunks = 0xFFFFFFFFLL / kUpdThreads;
 
@@ -775,7 +936,7 @@ bool capturing(hipStream_t stream) {
 void launch_norm(const rcs_list *l, float gscale, double *partials, hipStream_t stream) {
     hipLaunchKernelGGL(list_norm_partial, dim3(l->norm_blocks()), dim3(kListNormThreads), 0,
                        stream, (const Row *)l->d_rows, (const Chunk *)l->d_chunks, l->nchunks,
-                       gscale, partials);
+                       l->keep_from, gscale, partials);
 }
 
 int check_flat(const rcs_list *l, const void *p, int type, bool writes) {
@@ -840,6 +1001,16 @@ int rcs_list_create(const rcs_list_tensor *tensors, int64_t count, int state_bit
         l->bits = state_bits;
         l->n = total;
         l->nchunks = nchunks;
+        int64_t from = nchunks, tail = 0;
+        for (int64_t k = count - 1; k >= 0 && tail < kCachedTailBytes; --k) {
+            const int64_t c = (tensors[k].n + kChunk - 1) / kChunk;
+            const int64_t per = (int64_t)kChunk * type_bytes(tensors[k].g_type);
+            const int64_t want = (kCachedTailBytes - tail + per - 1) / per;
+            const int64_t take = c < want ? c : want;
+            from -= take;
+            tail += take * per;
+        }
+        l->keep_from = from;
         if (hipGetDevice(&l->dev) != hipSuccess) return RCS_EHIP;
         std::vector<Chunk> chunks;
         chunks.reserve((size_t)nchunks);
@@ -1002,6 +1173,8 @@ int adamw_clip_step_list(rcs_list *list, int32_t t, float lr, float clip, float 
     h.c2 = (float)(1.0 - beta2);
     h.eps = eps;
     h.gscale = grad_scale;
+    h.lr1 = (float)((double)lr / (1.0 - std::pow(beta1, (double)t)));
+    h.r2 = (float)(1.0 / (1.0 - std::pow(beta2, (double)t)));
     h.key = mixed(mixed(seed * kHashA + (uint32_t)t * kHashB) + kHashK);
     const bool fold = list->n <= kListFoldMaxN, q8 = list->bits == 8;
     const bool direct = norm_out != nullptr && on_device(norm_out);
@@ -1037,7 +1210,10 @@ int rcs_list_export(const rcs_list *list, void *w, int w_type, void *m, int m_ty
         !apart(m, m_type, v, v_type, list->n))
         return RCS_EINVAL;
     const Flat f{w, m, v, w_type, m_type, v_type};
-    auto *kernel = list->bits == 8 ? list_export<true> : list_export<false>;
+    const bool wide = (w == nullptr || w_type == RCS_BF16) && (m == nullptr || m_type == RCS_BF16) &&
+                      (v == nullptr || v_type == RCS_BF16);
+    auto *kernel = list->bits == 8 ? (wide ? list_export<true, 8> : list_export<true, 4>)
+                                   : list_export<false, 4>;
     hipLaunchKernelGGL(kernel, dim3((unsigned)list->nchunks), dim3(kUpdThreads), 0, stream,
                        (const Row *)list->d_rows, (const Chunk *)list->d_chunks, f);
     return hipGetLastError() == hipSuccess ? RCS_OK : RCS_EHIP;
@@ -1054,7 +1230,9 @@ int rcs_list_import(rcs_list *list, const void *w, int w_type, const void *m, in
     if ((rc = check_flat(list, v, v_type, false)) != RCS_OK) return rc;
     const Flat f{const_cast<void *>(w), const_cast<void *>(m), const_cast<void *>(v), w_type,
                  m_type, v_type};
-    auto *kernel = list->bits == 8 ? list_import<true> : list_import<false>;
+    const bool wide = (w == nullptr || w_type == RCS_BF16) && (m == nullptr || m_type == RCS_BF16);
+    auto *kernel = list->bits == 8 ? (wide ? list_import<true, 8> : list_import<true, 4>)
+                                   : list_import<false, 4>;
     hipLaunchKernelGGL(kernel, dim3((unsigned)list->nchunks), dim3(kUpdThreads), 0, stream,
                        (const Row *)list->d_rows, (const Chunk *)list->d_chunks, f);
     return hipGetLastError() == hipSuccess ? RCS_OK : RCS_EHIP;

@@ -73,6 +73,14 @@
 
 namespace {
 
+// Contiguous regions of the vectors the update streams at once: block b
+// works in region b % kRegions. Blocks are dispatched round-robin over the
+// chip's 8 XCDs, so with 8 regions each XCD streams its own contiguous eighth
+// of w, g, m, v. With one-wave blocks, over 14 buffer placements on one box
+// the step took 605.0-619.3 us (mean 611.0) with 8 regions against
+// 612.9-631.1 (617.5) with 4 (6 placements on another box: means 609.9 and
+// 608.0; 2, 1, 16 and 32 regions were slower).
+constexpr int64_t kRegions = 8;
 // Largest n whose step folds the final norm reduction into the update kernel
 // (measured: folding saves 1.7-2.4 us per step up to 8,388,608 elements and
 // costs 4.8 us at 16,777,216 and 23 us at 124,356,864).
@@ -334,6 +342,18 @@ __device__ __forceinline__ void st_shifted(float *__restrict__ xb, int q, int64_
         }
         p[3] = r.w;
     }
+}
+
+// The chunk of the vectors block blockIdx.x works on: a bijection of
+// [0, gridDim.x) that puts block b in contiguous region b % kRegions, at
+// position b / kRegions. Blocks are dispatched round-robin over the XCDs, so
+// each XCD streams its own regions, and neighbouring chunks (which share a
+// cache line at their common edge when an array is off the body's phase) run
+// on the same XCD and its L2.
+__device__ __forceinline__ int64_t chunk_of_block() {
+    const int64_t nblk = gridDim.x, b = blockIdx.x;
+    const int64_t k = kRegions, q = nblk / k, r = nblk % k, x = b % k, j = b / k;
+    return (x < r) ? x * (q + 1) + j : r * (q + 1) + (x - r) * q + j;
 }
 
 // Phases of w, g, m, v relative to the 16-byte aligned body, in floats

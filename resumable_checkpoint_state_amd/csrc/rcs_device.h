@@ -1,7 +1,7 @@
 // rcs_device.h -- device code that the library's kernels share: the wave and
-// block sums, the final reduction of the norm pass with the clip record, the
-// streaming accesses and the mapping of blocks to chunks. Everything has
-// internal linkage (each source file compiles its own copy).
+// block sums, the final reduction of the norm pass with the clip record and the
+// streaming accesses. Everything has internal linkage (each source file
+// compiles its own copy).
 #ifndef RCS_DEVICE_H
 #define RCS_DEVICE_H
 
@@ -14,14 +14,6 @@
 namespace {
 
 constexpr int kWave = 64;
-// Contiguous regions of the vectors the update streams at once: block b
-// works in region b % kRegions. Blocks are dispatched round-robin over the
-// chip's 8 XCDs, so with 8 regions each XCD streams its own contiguous eighth
-// of w, g, m, v. With one-wave blocks, over 14 buffer placements on one box
-// the step took 605.0-619.3 us (mean 611.0) with 8 regions against
-// 612.9-631.1 (617.5) with 4 (6 placements on another box: means 609.9 and
-// 608.0; 2, 1, 16 and 32 regions were slower).
-constexpr int64_t kRegions = 8;
 // The norm pass never has more blocks, and so partial sums, than this.
 constexpr int kNormMaxBlocks = 256;
 // At most this many partials reach the final reduction.
@@ -134,18 +126,6 @@ __device__ __forceinline__ T ld_stream(const T *p) {
 template <typename T>
 __device__ __forceinline__ void st_stream(T *p, T x) {
     __builtin_nontemporal_store(x, p);
-}
-
-// The chunk of the vectors block blockIdx.x works on: a bijection of
-// [0, gridDim.x) that puts block b in contiguous region b % kRegions, at
-// position b / kRegions. Blocks are dispatched round-robin over the XCDs, so
-// each XCD streams its own regions, and neighbouring chunks (which share a
-// cache line at their common edge when an array is off the body's phase) run
-// on the same XCD and its L2.
-__device__ __forceinline__ int64_t chunk_of_block() {
-    const int64_t nblk = gridDim.x, b = blockIdx.x;
-    const int64_t k = kRegions, q = nblk / k, r = nblk % k, x = b % k, j = b / k;
-    return (x < r) ? x * (q + 1) + j : r * (q + 1) + (x - r) * q + j;
 }
 
 }  // namespace
