@@ -437,9 +437,13 @@ int grad_global_norm_list(const rcs_list *list, float grad_scale, double *norm_o
  * evaluated to within a few units of float32's last place. If the norm is not
  * finite nothing is changed.
  *   t          1-based index of the update
- *   lr, clip   as for adamw_clip_step; clip = +inf never clips
+ *   lr, clip   as for adamw_clip_step; clip = +inf never clips. With moments in
+ *              8 bits, (1 - beta1^t) eps / lr must not fall below the normal
+ *              floats (for the default eps: lr below 1e29), and an lr whose
+ *              inverse overflows counts as zero
  *   grad_scale finite, > 0 (1/n_micro, the inverse of a loss scale, or 1)
- *   beta1, beta2 in [0, 1); eps a positive normal float
+ *   beta1, beta2 in [0, 1); eps a positive normal float. A beta of 0 forgets
+ *              an 8-bit moment that is infinite, too
  *   seed       of the random bits by which 8-bit moments are rounded (they
  *              are a function of seed, t and the element's place in the list)
  *   norm_out   NULL, or device or pinned host memory for the pre-clip norm
@@ -448,7 +452,7 @@ int grad_global_norm_list(const rcs_list *list, float grad_scale, double *norm_o
  * share an exponent for m and one for v (low and high byte of exps). With e
  * that byte, code k > 0 is the float whose bits are (k + 8 e - 255) << 20 for
  * v, and with k the low 7 bits and the top bit the sign, (k + 8 e - 127) << 20
- * for m; k = 0 is zero. e is the biased exponent of the smallest power of two
+ * for m; k = 0 is zero, with either sign. e is the biased exponent of the smallest power of two
  * not below the block's largest magnitude, at least 18 for m and 33 for v and
  * at most 255; what is not finite is held as an infinity of its sign.
  */

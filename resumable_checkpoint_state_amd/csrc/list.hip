@@ -103,7 +103,7 @@ struct Chunk {
 
 struct ListScalars {
     float lr, bc1, bc2, b1, c1, b2, c2, eps, gscale;
-    float lr1, r2;  // lr / bc1 and 1 / bc2, for the free evaluation
+    float da, db;   // for the free evaluation of the weight: weight_free
     uint32_t key;   // of the update's random bits
 };
 
@@ -200,16 +200,18 @@ __device__ __forceinline__ Raw<T, V> pack(const float (&x)[V]) {
     return r;
 }
 
-// The V elements from element i of p on; cnt of them exist (the others come as
-// zero), all of them with FULL. Streaming loads unless KEEP.
+// The V elements from element first + at of p on, `first` uniform in the wave;
+// cnt of them exist (the others come as zero), all of them with FULL. Streaming
+// loads unless KEEP.
 template <class T, int V, bool FULL, bool KEEP = false>
-__device__ __forceinline__ Raw<T, V> load(const void *p, int64_t i, int cnt) {
+__device__ __forceinline__ Raw<T, V> load(const void *p, int64_t first, uint32_t at, int cnt) {
     Raw<T, V> r;
     constexpr int kDwords = (int)sizeof(r) / 4, kWide = kDwords < 4 ? kDwords : 4;
-    const char *a = static_cast<const char *>(p) + i * T::kBytes;
+    const Global<char> a =
+        global<char>(static_cast<const char *>(p) + first * T::kBytes) + at * T::kBytes;
     if (FULL || cnt == V) {
         using X = typename Vector<kWide, T::kBytes>::type;
-        const Global<X> q = global<X>(a);
+        const Global<X> q = (Global<X>)a;
 #pragma unroll
         for (int k = 0; k < kDwords / kWide; ++k) {
             const X x = KEEP ? q[k] : __builtin_nontemporal_load(q + k);
@@ -223,21 +225,23 @@ __device__ __forceinline__ Raw<T, V> load(const void *p, int64_t i, int cnt) {
         for (int k = 0; k < V; ++k) {
             if (k >= cnt) continue;
             if constexpr (T::kBytes == 4)
-                r.d[k] = global<uint32_t>(a)[k];
+                r.d[k] = ((Global<uint32_t>)a)[k];
             else
-                r.d[k / 2] |= (uint32_t)global<uint16_t>(a)[k] << (16 * (k & 1));
+                r.d[k / 2] |= (uint32_t)((Global<uint16_t>)a)[k] << (16 * (k & 1));
         }
     }
     return r;
 }
 
 template <bool FULL, class T, int V>
-__device__ __forceinline__ void store(void *p, int64_t i, int cnt, const Raw<T, V> &r) {
+__device__ __forceinline__ void store(void *p, int64_t first, uint32_t at, int cnt,
+                                      const Raw<T, V> &r) {
     constexpr int kDwords = (int)sizeof(r) / 4, kWide = kDwords < 4 ? kDwords : 4;
-    char *a = static_cast<char *>(p) + i * T::kBytes;
+    const Global<char> a =
+        global<char>(static_cast<char *>(p) + first * T::kBytes) + at * T::kBytes;
     if (FULL || cnt == V) {
         using X = typename Vector<kWide, T::kBytes>::type;
-        const Global<X> q = global<X>(a);
+        const Global<X> q = (Global<X>)a;
 #pragma unroll
         for (int k = 0; k < kDwords / kWide; ++k) {
             X x;
@@ -250,9 +254,9 @@ __device__ __forceinline__ void store(void *p, int64_t i, int cnt, const Raw<T, 
         for (int k = 0; k < V; ++k) {
             if (k >= cnt) continue;
             if constexpr (T::kBytes == 4)
-                global<uint32_t>(a)[k] = r.d[k];
+                ((Global<uint32_t>)a)[k] = r.d[k];
             else
-                global<uint16_t>(a)[k] = (uint16_t)(r.d[k / 2] >> (16 * (k & 1)));
+                ((Global<uint16_t>)a)[k] = (uint16_t)(r.d[k / 2] >> (16 * (k & 1)));
         }
     }
 }
@@ -282,22 +286,30 @@ __host__ __device__ __forceinline__ uint32_t mixed(uint32_t x) {
     return x ^ (x >> 15);
 }
 
-// The random bits of elements i .. i + V - 1 of the list; carry: the upper half
-// of an index may change among them.
+// The random bits of elements first + at .. first + at + V - 1 of the list,
+// `first` uniform; carry: the upper half of an index may change among the
+// wave's.
 template <int V>
-__device__ __forceinline__ void random_bits(int64_t i, uint32_t key, bool carry,
+__device__ __forceinline__ void random_bits(int64_t first, uint32_t at, uint32_t key, bool carry,
                                             uint32_t (&r)[V]) {
-    const uint32_t x = (uint32_t)i * kHashA + (uint32_t)(i >> 32) * kHashB + key;
+    const uint32_t x =
+        (uint32_t)first * kHashA + (uint32_t)(first >> 32) * kHashB + key + at * kHashA;
     if (!carry) {
 #pragma unroll
         for (int k = 0; k < V; ++k) r[k] = mixed(x + (uint32_t)k * kHashA);
     } else {
 #pragma unroll
         for (int k = 0; k < V; ++k) {
-            const uint32_t up = (uint32_t)((i + k) >> 32) - (uint32_t)(i >> 32);
+            const uint32_t up = (uint32_t)((first + at + k) >> 32) - (uint32_t)(first >> 32);
             r[k] = mixed(x + (uint32_t)k * kHashA + up * kHashB);
         }
     }
+}
+
+// The larger of each pair of 16-lane rows' values, in every lane of the pair.
+__device__ __forceinline__ uint32_t row_pair_max(uint32_t x) {
+    const auto y = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    return y[0] > y[1] ? y[0] : y[1];
 }
 
 // The largest of the values of the lanes that share a block of V elements
@@ -309,126 +321,168 @@ __device__ __forceinline__ uint32_t block_max(uint32_t x) {
     with((uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x4E, 0xF, 0xF, true));   // quads
     with((uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x141, 0xF, 0xF, true));  // 8 lanes
     with((uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x140, 0xF, 0xF, true));  // 16 lanes
-    if constexpr (V == 4) with((uint32_t)__shfl_xor((int)x, 16, kWave));
+    return V == 8 ? x : row_pair_max(x);
+}
+
+// The codes' arithmetic runs on two elements at once, in the upper 16 bits of
+// their floats: sign, exponent and 7 mantissa bits, of which the format keeps 3.
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ u16x2 both(uint32_t x) { return u16x2{(uint16_t)x, (uint16_t)x}; }
+__device__ __forceinline__ u16x2 halves(uint32_t x) { return __builtin_bit_cast(u16x2, x); }
+// A 1 that the compiler does not see through: it would turn min(k, 1) * x, one
+// instruction each for two elements, into a comparison and a selection for each.
+__device__ __forceinline__ uint32_t hidden_one(uint32_t x) {
+    asm("" : "+v"(x));
     return x;
+}
+__device__ __forceinline__ uint32_t word(u16x2 x) { return __builtin_bit_cast(uint32_t, x); }
+
+// Upper halves of two words.
+__device__ __forceinline__ u16x2 upper(uint32_t x0, uint32_t x1) {
+    return halves(__builtin_amdgcn_perm(x1, x0, 0x07060302u));
 }
 
 __device__ __forceinline__ int base_m(int e) { return 8 * e - 127; }
 __device__ __forceinline__ int base_v(int e) { return 8 * e - 255; }
 
-// Biased exponent of the smallest power of two not below the value with these
-// magnitude bits, at least low; 255 for what is not finite.
-__device__ __forceinline__ int block_exponent(uint32_t bits, int low) {
-    const int e = (int)((bits + 0x7FFFFFu) >> 23);
+// Biased exponent of the smallest power of two not below a block's largest
+// magnitude, given the upper half of that magnitude's bits plus 0x7FFFFF; at
+// least low, and 255 for what is not finite.
+__device__ __forceinline__ int block_exponent(uint32_t half, int low) {
+    const int e = (int)(half >> 7);
     return e < low ? low : e > 255 ? 255 : e;
 }
-
-__device__ __forceinline__ float decode_v(uint32_t k, int base) {
-    return k == 0 ? 0.0f : __uint_as_float((uint32_t)((int)k + base) << 20);
-}
-
-__device__ __forceinline__ float decode_m(uint32_t code, int base) {
-    const uint32_t k = code & 0x7Fu;
-    return k == 0 ? 0.0f
-                  : __uint_as_float(((uint32_t)((int)k + base) << 20) | ((code & 0x80u) << 24));
-}
-
-// Code of the value with magnitude bits `mag`; add is what is added below the
-// third mantissa bit before the rest is cut: 20 random bits, or half a unit
-// (to even) for the nearest value. `low`: magnitude bits above this get at
-// least code 1.
-__device__ __forceinline__ uint32_t encode(uint32_t mag, uint32_t add, int base, uint32_t low,
-                                           int top) {
-    const int k = (int)((mag + add) >> 20) - base;
-    const int least = mag > low ? 1 : 0;
-    const int r = k > least ? k : least;
-    return (uint32_t)(r < top ? r : top);  // beyond the top: only what is not finite
-}
-
-__device__ __forceinline__ uint32_t low_m(int base) {
-    return ((uint32_t)(base + 1) << 20) - 0x800000u;  // half of the smallest value
-}
-
-__device__ __forceinline__ uint32_t encode_m(float m, uint32_t add, int base) {
-    const uint32_t u = __float_as_uint(m);
-    const uint32_t k = encode(u & 0x7FFFFFFFu, add, base, low_m(base), 127);
-    return k == 0 ? 0u : k | ((u >> 24) & 0x80u);
-}
-
-__device__ __forceinline__ uint32_t half_unit(uint32_t mag) { return 0x7FFFFu + ((mag >> 20) & 1u); }
 
 // V codes of one byte.
 template <int V>
 struct Codes {
     uint32_t d[V / 4];
-    __device__ __forceinline__ uint32_t at(int i) const { return (d[i / 4] >> (8 * (i & 3))) & 0xFFu; }
-    __device__ __forceinline__ void put(int i, uint32_t k) {
-        if ((i & 3) == 0) d[i / 4] = k;
-        else d[i / 4] |= k << (8 * (i & 3));
+    // codes 2 j and 2 j + 1, each in 16 bits
+    __device__ __forceinline__ u16x2 pair(int j) const {
+        return halves(__builtin_amdgcn_perm(0u, d[j / 2], j & 1 ? 0x0C030C02u : 0x0C010C00u));
+    }
+    __device__ __forceinline__ void four(int j, u16x2 k01, u16x2 k23) {
+        d[j] = __builtin_amdgcn_perm(word(k23), word(k01), 0x06040200u);
     }
 };
 
 template <int V>
-__device__ __forceinline__ Codes<V> load_codes(const void *p, int64_t i) {
+__device__ __forceinline__ Codes<V> load_codes(const void *p, int64_t first, uint32_t at) {
     Codes<V> c;
-    const char *a = static_cast<const char *>(p) + i;
+    const Global<char> a = global<char>(static_cast<const char *>(p) + first) + at;
     if constexpr (V == 8) {
-        const u32x2 x = __builtin_nontemporal_load(global<u32x2>(a));
+        const u32x2 x = __builtin_nontemporal_load((Global<u32x2>)a);
         c.d[0] = x.x;
         c.d[1] = x.y;
     } else {
-        c.d[0] = __builtin_nontemporal_load(global<uint32_t>(a));
+        c.d[0] = __builtin_nontemporal_load((Global<uint32_t>)a);
     }
     return c;
 }
 
 template <int V>
-__device__ __forceinline__ void store_codes(void *p, int64_t i, const Codes<V> &c) {
-    char *a = static_cast<char *>(p) + i;
-    if constexpr (V == 8) __builtin_nontemporal_store(u32x2{c.d[0], c.d[1]}, global<u32x2>(a));
-    else __builtin_nontemporal_store(c.d[0], global<uint32_t>(a));
+__device__ __forceinline__ void store_codes(void *p, int64_t first, uint32_t at,
+                                            const Codes<V> &c) {
+    const Global<char> a = global<char>(static_cast<char *>(p) + first) + at;
+    if constexpr (V == 8)
+        __builtin_nontemporal_store(u32x2{c.d[0], c.d[1]}, (Global<u32x2>)a);
+    else
+        __builtin_nontemporal_store(c.d[0], (Global<uint32_t>)a);
 }
 
-// Block exponents and codes of the lane's m and v (those past the tensor's end
-// are zero), written to their block; every lane of the block calls this.
-template <int V, class AddM, class AddV>
-__device__ __forceinline__ void store_moments(const Row &t, int64_t i, const float (&m)[V],
-                                              const float (&v)[V], bool active, AddM add_m,
-                                              AddV add_v) {
-    uint32_t am = 0, av = 0;
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-        const uint32_t um = __float_as_uint(m[k]) & 0x7FFFFFFFu;
-        const uint32_t uv = __float_as_uint(v[k]) & 0x7FFFFFFFu;
-        am = am > um ? am : um;
-        av = av > uv ? av : uv;
-    }
-    const int em = block_exponent(block_max<V>(am), kLowM);
-    const int ev = block_exponent(block_max<V>(av), kLowV);
-    const int bm = base_m(em), bv = base_v(ev);
-    Codes<V> cm, cv;
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-        cm.put(k, encode_m(m[k], add_m(k), bm));
-        const uint32_t uv = __float_as_uint(v[k]) & 0x7FFFFFFFu;
-        cv.put(k, encode(uv, add_v(k), bv, 0u, 255));
-    }
-    if (!active) return;
-    store_codes(t.m, i, cm);
-    store_codes(t.v, i, cv);
-    if ((threadIdx.x & (kBlock / V - 1)) == 0)
-        global<uint16_t>(t.e)[i / kBlock] = (uint16_t)(em | (ev << 8));
+// The exponents of the block that holds element first + at (first begins one).
+__device__ __forceinline__ Global<uint16_t> exponents_at(const Row &t, int64_t first,
+                                                         uint32_t at) {
+    return global<uint16_t>(t.e + first / kBlock) + at / kBlock;
 }
 
+// A float's upper half is 16 (k + B), plus the sign for m, and 0 for k = 0; its
+// lower half is zero.
 template <int V>
 __device__ __forceinline__ void decode_moments(const Codes<V> &cm, const Codes<V> &cv, uint32_t e,
                                                float (&m)[V], float (&v)[V]) {
-    const int bm = base_m((int)(e & 0xFFu)), bv = base_v((int)(e >> 8));
+    const uint32_t bm = 16u * (uint32_t)base_m((int)(e & 0xFFu));
+    const u16x2 bv = both(16u * (uint32_t)base_v((int)(e >> 8)));
+    const uint32_t bm2 = bm | (bm << 16);
+    const u16x2 one = halves(hidden_one(0x00010001u));
 #pragma unroll
-    for (int k = 0; k < V; ++k) {
-        m[k] = decode_m(cm.at(k), bm);
-        v[k] = decode_v(cv.at(k), bv);
+    for (int j = 0; j < V / 2; ++j) {
+        const u16x2 c = cm.pair(j), k = halves(word(c) & 0x007F007Fu);
+        const u16x2 signed_base = halves(((word(c) << 8) & 0x80008000u) | (bm2 & 0x7FFF7FFFu));
+        const uint32_t x = word(k * both(16) + __builtin_elementwise_min(k, one) * signed_base);
+        m[2 * j] = __uint_as_float(x << 16);
+        m[2 * j + 1] = __uint_as_float(x & 0xFFFF0000u);
+        const u16x2 l = cv.pair(j);
+        const uint32_t y = word(l * both(16) + __builtin_elementwise_min(l, one) * bv);
+        v[2 * j] = __uint_as_float(y << 16);
+        v[2 * j + 1] = __uint_as_float(y & 0xFFFF0000u);
     }
+}
+
+// What is added below the third mantissa bit before the rest is cut off, for
+// the nearest value (ties to even).
+__device__ __forceinline__ uint32_t half_unit(uint32_t bits) { return 0x7FFFFu + ((bits >> 20) & 1u); }
+
+// Block exponents and codes of the lane's m and v (those past the tensor's end
+// are zero), written to their block; every lane of the block calls this.
+// add_m, add_v: below 2^20, what is added to the bits of element k before they
+// are cut (random bits, or half a unit). v is not below zero, and neither is a
+// NaN.
+template <int V, class AddM, class AddV>
+__device__ __forceinline__ void store_moments(const Row &t, int64_t first, uint32_t at,
+                                              const float (&m)[V], const float (&v)[V],
+                                              bool active, AddM add_m, AddV add_v) {
+    // ym: upper halves of |m|'s bits plus 0x7FFFFF. Their largest gives the
+    // block's exponent; and as the smallest value L and half of it are a power
+    // of two apart and end in 20 zero bits, ym >= L exactly where |m| > L / 2.
+    // The sum saturates, so a NaN stays above every number.
+    u16x2 ym[V / 2], big = both(0);
+    uint32_t av = 0;
+#pragma unroll
+    for (int j = 0; j < V / 2; ++j) {
+        const uint32_t y0 = __float_as_uint(m[2 * j]) + 0x7FFFFFu;
+        const uint32_t y1 = __float_as_uint(m[2 * j + 1]) + 0x7FFFFFu;
+        ym[j] = halves(word(upper(y0, y1)) & 0x7FFF7FFFu);
+        big = __builtin_elementwise_max(big, ym[j]);
+        const uint32_t u0 = __float_as_uint(v[2 * j]), u1 = __float_as_uint(v[2 * j + 1]);
+        av = av > u0 ? av : u0;
+        av = av > u1 ? av : u1;
+    }
+    const uint32_t one = hidden_one(1u);
+    const uint32_t am = big.x > big.y ? big.x : big.y;
+    const int em = block_exponent(block_max<V>(am), kLowM);
+    const int ev = block_exponent((block_max<V>(av) + 0x7FFFFFu) >> 16, kLowV);
+    const u16x2 bm = both((uint32_t)base_m(em)), bv = both((uint32_t)base_v(ev));
+    const u16x2 least = both(16u * (uint32_t)(base_m(em) + 1));
+    u16x2 km[V / 2], kv[V / 2];
+#pragma unroll
+    for (int j = 0; j < V / 2; ++j) {
+        const uint32_t u0 = __float_as_uint(m[2 * j]), u1 = __float_as_uint(m[2 * j + 1]);
+        const u16x2 x = upper(u0 + add_m(2 * j), u1 + add_m(2 * j + 1));
+        u16x2 y = __builtin_elementwise_max(halves(word(x) & 0x7FFF7FFFu),
+                                            __builtin_elementwise_min(ym[j], least));
+        y = __builtin_elementwise_sub_sat(y >> both(4), bm);
+        y = __builtin_elementwise_min(y, both(127));
+        km[j] = halves(((word(x) >> 8) & 0x00800080u) | word(y));
+        const uint32_t s0 = __float_as_uint(v[2 * j]), s1 = __float_as_uint(v[2 * j + 1]);
+        const u16x2 z = upper(s0 + add_v(2 * j), s1 + add_v(2 * j + 1));
+        const u16x2 some = halves((s0 < one ? s0 : one) | ((s1 < one ? s1 : one) << 16));
+        kv[j] = __builtin_elementwise_min(
+            __builtin_elementwise_max(__builtin_elementwise_sub_sat(z >> both(4), bv), some),
+            both(255));
+    }
+    Codes<V> cm, cv;
+#pragma unroll
+    for (int j = 0; j < V / 4; ++j) {
+        cm.four(j, km[2 * j], km[2 * j + 1]);
+        cv.four(j, kv[2 * j], kv[2 * j + 1]);
+    }
+    if (!active) return;
+    store_codes(t.m, first, at, cm);
+    store_codes(t.v, first, at, cv);
+    if ((threadIdx.x & (kBlock / V - 1)) == 0)
+        *exponents_at(t, first, at) = (uint16_t)(em | (ev << 8));
 }
 
 // ------------------------------------------------------------------- kernels
@@ -450,19 +504,19 @@ __device__ __forceinline__ double squares_of(const void *g, int64_t first, int64
                                              float gscale) {
     constexpr int V = 16 / G::kBytes;  // one 16-byte vector
     constexpr int kStep = kWave * V;
-    const int lane = (int)threadIdx.x & (kWave - 1);
+    const int lane = ((int)threadIdx.x & (kWave - 1)) * V;
     double acc[4] = {};
-    int64_t i = first + lane * V;
-    int64_t at = first;
-    for (; at + kDeep * kStep <= stop; at += kDeep * kStep, i += kDeep * kStep) {
+    int64_t i = first;
+    for (; i + kDeep * kStep <= stop; i += kDeep * kStep) {
         Raw<G, V> r[kDeep];
 #pragma unroll
-        for (int q = 0; q < kDeep; ++q) r[q] = load<G, V, true, KEEP>(g, i + q * kStep, V);
+        for (int q = 0; q < kDeep; ++q) r[q] = load<G, V, true, KEEP>(g, i, lane + q * kStep, V);
 #pragma unroll
         for (int q = 0; q < kDeep; ++q) add_squares(r[q], gscale, acc[q & 3]);
     }
-    for (; at < stop; at += kStep, i += kStep)
-        add_squares(load<G, V, false, KEEP>(g, i, count_of<V>(stop - i, 0)), gscale, acc[0]);
+    for (; i < stop; i += kStep)
+        add_squares(load<G, V, false, KEEP>(g, i, lane, count_of<V>(stop - i, lane)), gscale,
+                    acc[0]);
     return (acc[0] + acc[1]) + (acc[2] + acc[3]);
 }
 
@@ -528,14 +582,31 @@ __global__ __launch_bounds__(kUpdThreads) void list_norm_final(const double *__r
     }
 }
 
-// New moments of one element; the operations and their roundings are part of
-// the definition (8-bit moments are rounded from exactly these).
-__device__ __forceinline__ void moments(float g, float &m, float &v, float s,
+// New moments of one element from its scaled gradient; the operations and their
+// roundings are part of the definition (8-bit moments are rounded from exactly
+// these).
+__device__ __forceinline__ void moments(float ga, float &m, float &v, float s,
                                         const ListScalars &h) {
-    const float ga = g * h.gscale;
     const float gp = ga * s;
     m = h.b1 * m + h.c1 * gp;
     v = h.b2 * v + h.c2 * (gp * gp);
+}
+
+// g * gscale, which a uniform branch leaves out where it changes nothing.
+template <int V>
+__device__ __forceinline__ void scale(float (&g)[V], const ListScalars &h) {
+    if (h.gscale == 1.0f) return;
+#pragma unroll
+    for (int k = 0; k < V; ++k) g[k] = g[k] * h.gscale;
+}
+
+// A beta of zero forgets the moment, an infinite one too: 0 times that would be
+// a NaN, and with this no moment is ever one.
+template <int V>
+__device__ __forceinline__ void forget(float (&x)[V], float beta) {
+    if (beta != 0.0f) return;
+#pragma unroll
+    for (int k = 0; k < V; ++k) x[k] = 0.0f;
 }
 
 // The weight in the flat update's operation sequence: divisions and root
@@ -548,14 +619,15 @@ __device__ __forceinline__ float weight(float w, float m, float v, float decay,
     return w * decay - (h.lr * mh) / den;
 }
 
-// The weight beside 8-bit moments, where the arithmetic is what counts: the
-// two divisions by constants are products, root and reciprocal the hardware's
-// (1 ulp each; v below float32's normal range only shows next to an eps of
-// its size).
+// The weight beside 8-bit moments, where the arithmetic is what counts:
+//   w decay - lr (m / bc1) / (sqrt(v / bc2) + eps) = w decay - m / (da sqrt(v) + db)
+// with da = bc1 / (lr sqrt(bc2)), db = bc1 eps / lr; root and reciprocal are the
+// hardware's (1 ulp each; v below float32's normal range would only show next
+// to an eps of its size).
 __device__ __forceinline__ float weight_free(float w, float m, float v, float decay,
                                              const ListScalars &h) {
-    const float den = __builtin_amdgcn_sqrtf(v * h.r2) + h.eps;
-    return __builtin_fmaf(w, decay, -(m * h.lr1 * __builtin_amdgcn_rcpf(den)));
+    const float den = __builtin_fmaf(__builtin_amdgcn_sqrtf(v), h.da, h.db);
+    return __builtin_fmaf(-m, __builtin_amdgcn_rcpf(den), w * decay);
 }
 
 // R groups of 32-bit moments from element `first` on: W, G the types of weights
@@ -564,20 +636,18 @@ template <class W, class G, int V, int R, bool FULL, class Record>
 __device__ __forceinline__ void update32(const Row &t, int64_t first, Record record,
                                          const ListScalars &h) {
     const int64_t left = t.n - first;
-    int64_t i[R];
-    int cnt[R];
+    int at[R], cnt[R];
     Raw<W, V> w[R];
     Raw<G, V> g[R];
     Raw<F32, V> m[R], v[R];
 #pragma unroll
     for (int q = 0; q < R; ++q) {
-        const int at = (q * kWave + (int)threadIdx.x) * V;
-        cnt[q] = FULL ? V : count_of<V>(left, at);
-        i[q] = first + at;
-        g[q] = load<G, V, FULL>(t.g, i[q], cnt[q]);
-        w[q] = load<W, V, FULL>(t.w, i[q], cnt[q]);
-        m[q] = load<F32, V, FULL>(t.m, i[q], cnt[q]);
-        v[q] = load<F32, V, FULL>(t.v, i[q], cnt[q]);
+        at[q] = (q * kWave + (int)threadIdx.x) * V;
+        cnt[q] = FULL ? V : count_of<V>(left, at[q]);
+        g[q] = load<G, V, FULL>(t.g, first, at[q], cnt[q]);
+        w[q] = load<W, V, FULL>(t.w, first, at[q], cnt[q]);
+        m[q] = load<F32, V, FULL>(t.m, first, at[q], cnt[q]);
+        v[q] = load<F32, V, FULL>(t.v, first, at[q], cnt[q]);
     }
     const ClipScalars cs = record();
     if (!cs.apply) return;
@@ -589,18 +659,19 @@ __device__ __forceinline__ void update32(const Row &t, int64_t first, Record rec
         unpack(g[q], gg);
         unpack(m[q], mm);
         unpack(v[q], vv);
+        scale(gg, h);
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             moments(gg[k], mm[k], vv[k], cs.scale, h);
             ww[k] = weight(ww[k], mm[k], vv[k], decay, h);
         }
-        store<FULL>(t.w, i[q], cnt[q], pack<W>(ww));
-        store<FULL>(t.m, i[q], cnt[q], pack<F32>(mm));
-        store<FULL>(t.v, i[q], cnt[q], pack<F32>(vv));
+        store<FULL>(t.w, first, at[q], cnt[q], pack<W>(ww));
+        store<FULL>(t.m, first, at[q], cnt[q], pack<F32>(mm));
+        store<FULL>(t.v, first, at[q], cnt[q], pack<F32>(vv));
         if constexpr (W::kBytes == 4) {
             if (t.c != nullptr) {
-                if (t.ct == RCS_BF16) store<FULL>(t.c, i[q], cnt[q], pack<BF16>(ww));
-                else store<FULL>(t.c, i[q], cnt[q], pack<F16>(ww));
+                if (t.ct == RCS_BF16) store<FULL>(t.c, first, at[q], cnt[q], pack<BF16>(ww));
+                else store<FULL>(t.c, first, at[q], cnt[q], pack<F16>(ww));
             }
         }
     }
@@ -615,8 +686,7 @@ __device__ __forceinline__ void update8(const Row &t, int64_t first, Record reco
     const int64_t left = t.n - first;
     // (uniform: the group's first and last element of the list)
     const bool carry = ((t.off + first) >> 32) != ((t.off + first + R * kWave * V - 1) >> 32);
-    int64_t i[R];
-    int cnt[R];
+    int at[R], cnt[R];
     bool active[R];
     Raw<W, V> w[R];
     Raw<G, V> g[R];
@@ -624,16 +694,15 @@ __device__ __forceinline__ void update8(const Row &t, int64_t first, Record reco
     uint32_t e[R];
 #pragma unroll
     for (int q = 0; q < R; ++q) {
-        const int at = (q * kWave + (int)threadIdx.x) * V;
-        cnt[q] = FULL ? V : count_of<V>(left, at);
-        i[q] = first + at;
-        active[q] = FULL || (at & ~(kBlock - 1)) < left;
-        g[q] = load<G, V, FULL>(t.g, i[q], cnt[q]);
-        w[q] = load<W, V, FULL>(t.w, i[q], cnt[q]);
-        const int64_t ic = active[q] ? i[q] : 0;
-        cm[q] = load_codes<V>(t.m, ic);
-        cv[q] = load_codes<V>(t.v, ic);
-        e[q] = global<uint16_t>(t.e)[ic / kBlock];
+        at[q] = (q * kWave + (int)threadIdx.x) * V;
+        cnt[q] = FULL ? V : count_of<V>(left, at[q]);
+        active[q] = FULL || (at[q] & ~(kBlock - 1)) < left;
+        g[q] = load<G, V, FULL>(t.g, first, at[q], cnt[q]);
+        w[q] = load<W, V, FULL>(t.w, first, at[q], cnt[q]);
+        const int there = active[q] ? at[q] : 0;
+        cm[q] = load_codes<V>(t.m, first, there);
+        cv[q] = load_codes<V>(t.v, first, there);
+        e[q] = *exponents_at(t, first, there);
     }
     const ClipScalars cs = record();
     if (!cs.apply) return;
@@ -644,22 +713,25 @@ __device__ __forceinline__ void update8(const Row &t, int64_t first, Record reco
         unpack(w[q], ww);
         unpack(g[q], gg);
         decode_moments(cm[q], cv[q], e[q], mm, vv);
+        forget(mm, h.b1);
+        forget(vv, h.b2);
+        scale(gg, h);
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             moments(gg[k], mm[k], vv[k], cs.scale, h);
             ww[k] = weight_free(ww[k], mm[k], vv[k], decay, h);
             if (!FULL && k >= cnt[q]) mm[k] = vv[k] = 0.0f;
         }
-        store<FULL>(t.w, i[q], cnt[q], pack<W>(ww));
+        store<FULL>(t.w, first, at[q], cnt[q], pack<W>(ww));
         if constexpr (W::kBytes == 4) {
             if (t.c != nullptr) {
-                if (t.ct == RCS_BF16) store<FULL>(t.c, i[q], cnt[q], pack<BF16>(ww));
-                else store<FULL>(t.c, i[q], cnt[q], pack<F16>(ww));
+                if (t.ct == RCS_BF16) store<FULL>(t.c, first, at[q], cnt[q], pack<BF16>(ww));
+                else store<FULL>(t.c, first, at[q], cnt[q], pack<F16>(ww));
             }
         }
         uint32_t r[V];
-        random_bits(t.off + i[q], h.key, carry, r);
-        store_moments(t, i[q], mm, vv, active[q], [&](int k) { return r[k] & 0xFFFFFu; },
+        random_bits(t.off + first, at[q], h.key, carry, r);
+        store_moments(t, first, at[q], mm, vv, active[q], [&](int k) { return r[k] & 0xFFFFFu; },
                       [&](int k) { return r[k] >> 12; });
     }
 }
@@ -697,7 +769,10 @@ __global__ __launch_bounds__(kUpdThreads) void list_update(
         by_type(t.gt, [&](auto G) {
             using WT = decltype(W);
             using GT = decltype(G);
-            constexpr int V = 4, R = kChunk / (kWave * V);
+            // 16-bit weights and gradients beside 8-bit moments: 8 elements a lane
+            // still cover whole lines and halve the work per block exponent
+            constexpr int V = Q8 && WT::kBytes == 2 && GT::kBytes == 2 ? 8 : 4;
+            constexpr int R = kChunk / (kWave * V);
             if (t.n - first >= kChunk) {
                 if constexpr (Q8) update8<WT, GT, V, R, true>(t, first, get, h);
                 else update32<WT, GT, V, R, true>(t, first, get, h);
@@ -722,17 +797,17 @@ struct Flat {
 };
 
 template <bool FULL, int V>
-__device__ __forceinline__ void store_as(int type, void *p, int64_t i, int cnt,
+__device__ __forceinline__ void store_as(int type, void *p, int64_t first, uint32_t at, int cnt,
                                          const float (&x)[V]) {
-    if (type == RCS_F32) store<FULL>(p, i, cnt, pack<F32>(x));
-    else store<FULL>(p, i, cnt, pack<BF16>(x));
+    if (type == RCS_F32) store<FULL>(p, first, at, cnt, pack<F32>(x));
+    else store<FULL>(p, first, at, cnt, pack<BF16>(x));
 }
 
 template <bool FULL, int V>
-__device__ __forceinline__ void load_as(int type, const void *p, int64_t i, int cnt,
-                                        float (&x)[V]) {
-    if (type == RCS_F32) unpack(load<F32, V, FULL>(p, i, cnt), x);
-    else unpack(load<BF16, V, FULL>(p, i, cnt), x);
+__device__ __forceinline__ void load_as(int type, const void *p, int64_t first, uint32_t at,
+                                        int cnt, float (&x)[V]) {
+    if (type == RCS_F32) unpack(load<F32, V, FULL>(p, first, at, cnt), x);
+    else unpack(load<BF16, V, FULL>(p, first, at, cnt), x);
 }
 
 // One group of V elements a lane from element `first` of t on.
@@ -740,26 +815,25 @@ template <bool Q8, int V, bool FULL>
 __device__ __forceinline__ void export_group(const Row &t, int64_t first, const Flat &f) {
     const int at = (int)threadIdx.x * V;
     const int cnt = FULL ? V : count_of<V>(t.n - first, at);
-    const int64_t i = first + at;
     if (cnt == 0) return;
     float m[V], v[V];
     if (f.m != nullptr || f.v != nullptr) {
         if constexpr (Q8) {
-            decode_moments(load_codes<V>(t.m, i), load_codes<V>(t.v, i),
-                           global<uint16_t>(t.e)[i / kBlock], m, v);
+            decode_moments(load_codes<V>(t.m, first, at), load_codes<V>(t.v, first, at),
+                           *exponents_at(t, first, at), m, v);
         } else {
-            if (f.m != nullptr) unpack(load<F32, V, FULL>(t.m, i, cnt), m);
-            if (f.v != nullptr) unpack(load<F32, V, FULL>(t.v, i, cnt), v);
+            if (f.m != nullptr) unpack(load<F32, V, FULL>(t.m, first, at, cnt), m);
+            if (f.v != nullptr) unpack(load<F32, V, FULL>(t.v, first, at, cnt), v);
         }
     }
     if (f.w != nullptr)
         by_type(t.wt, [&](auto W) {
             float x[V];
-            unpack(load<decltype(W), V, FULL>(t.w, i, cnt), x);
-            store_as<FULL>(f.wt, f.w, t.off + i, cnt, x);
+            unpack(load<decltype(W), V, FULL>(t.w, first, at, cnt), x);
+            store_as<FULL>(f.wt, f.w, t.off + first, at, cnt, x);
         });
-    if (f.m != nullptr) store_as<FULL>(f.mt, f.m, t.off + i, cnt, m);
-    if (f.v != nullptr) store_as<FULL>(f.vt, f.v, t.off + i, cnt, v);
+    if (f.m != nullptr) store_as<FULL>(f.mt, f.m, t.off + first, at, cnt, m);
+    if (f.v != nullptr) store_as<FULL>(f.vt, f.v, t.off + first, at, cnt, v);
 }
 
 template <bool Q8, int V>
@@ -786,33 +860,33 @@ __device__ __forceinline__ void import_group(const Row &t, int64_t first, const 
     const int at = (int)threadIdx.x * V;
     const int64_t left = t.n - first;
     const int cnt = FULL ? V : count_of<V>(left, at);
-    const int64_t i = first + at;
     float m[V], v[V];
-    if (f.m != nullptr) load_as<FULL>(f.mt, f.m, t.off + i, cnt, m);
-    if (f.v != nullptr) load_as<FULL>(f.vt, f.v, t.off + i, cnt, v);
+    if (f.m != nullptr) load_as<FULL>(f.mt, f.m, t.off + first, at, cnt, m);
+    if (f.v != nullptr) load_as<FULL>(f.vt, f.v, t.off + first, at, cnt, v);
     if (f.w != nullptr && cnt > 0) {
         float x[V];
-        load_as<FULL>(f.wt, f.w, t.off + i, cnt, x);
-        by_type(t.wt, [&](auto W) { store<FULL>(t.w, i, cnt, pack<decltype(W)>(x)); });
+        load_as<FULL>(f.wt, f.w, t.off + first, at, cnt, x);
+        by_type(t.wt, [&](auto W) { store<FULL>(t.w, first, at, cnt, pack<decltype(W)>(x)); });
         if (t.c != nullptr) {
-            if (t.ct == RCS_BF16) store<FULL>(t.c, i, cnt, pack<BF16>(x));
-            else store<FULL>(t.c, i, cnt, pack<F16>(x));
+            if (t.ct == RCS_BF16) store<FULL>(t.c, first, at, cnt, pack<BF16>(x));
+            else store<FULL>(t.c, first, at, cnt, pack<F16>(x));
         }
     }
     if constexpr (Q8) {
         if (f.m == nullptr) return;
 #pragma unroll
-        for (int k = 0; k < V; ++k) {  // v below zero is held as zero (a NaN is not)
-            const uint32_t u = __float_as_uint(v[k]);
-            v[k] = __uint_as_float((u >> 31) != 0 && u <= 0xFF800000u ? 0u : u & 0x7FFFFFFFu);
+        for (int k = 0; k < V; ++k) {  // a NaN becomes an infinity, v below zero zero
+            const uint32_t a = __float_as_uint(m[k]), u = __float_as_uint(v[k]);
+            const uint32_t a1 = a & 0x7FFFFFFFu, u1 = u & 0x7FFFFFFFu;
+            m[k] = __uint_as_float((a1 < 0x7F800000u ? a1 : 0x7F800000u) | (a & 0x80000000u));
+            v[k] = __uint_as_float(u1 > 0x7F800000u ? 0x7F800000u : u == u1 ? u : 0u);
         }
-        store_moments(
-            t, i, m, v, FULL || (at & ~(kBlock - 1)) < left,
-            [&](int k) { return half_unit(__float_as_uint(m[k]) & 0x7FFFFFFFu); },
-            [&](int k) { return half_unit(__float_as_uint(v[k])); });
+        store_moments(t, first, at, m, v, FULL || (at & ~(kBlock - 1)) < left,
+                      [&](int k) { return half_unit(__float_as_uint(m[k])); },
+                      [&](int k) { return half_unit(__float_as_uint(v[k])); });
     } else {
-        if (f.m != nullptr && cnt > 0) store<FULL>(t.m, i, cnt, pack<F32>(m));
-        if (f.v != nullptr && cnt > 0) store<FULL>(t.v, i, cnt, pack<F32>(v));
+        if (f.m != nullptr && cnt > 0) store<FULL>(t.m, first, at, cnt, pack<F32>(m));
+        if (f.v != nullptr && cnt > 0) store<FULL>(t.v, first, at, cnt, pack<F32>(v));
     }
 }
 
@@ -1173,8 +1247,17 @@ int adamw_clip_step_list(rcs_list *list, int32_t t, float lr, float clip, float 
     h.c2 = (float)(1.0 - beta2);
     h.eps = eps;
     h.gscale = grad_scale;
-    h.lr1 = (float)((double)lr / (1.0 - std::pow(beta1, (double)t)));
-    h.r2 = (float)(1.0 / (1.0 - std::pow(beta2, (double)t)));
+    // weight_free's constants; a learning rate of zero, or whose inverse
+    // overflows, divides by infinity
+    const double over = (1.0 - std::pow(beta1, (double)t)) / (double)lr;
+    h.da = (float)(over / std::sqrt(1.0 - std::pow(beta2, (double)t)));
+    h.db = (float)(over * (double)eps);
+    if (lr == 0.0f || !std::isfinite(h.da) || !std::isfinite(h.db)) {
+        h.da = 1.0f;
+        h.db = INFINITY;
+    } else if (list->bits == 8 && !std::isnormal(h.db)) {
+        return RCS_EINVAL;  // lr so large that v = 0 would divide by nothing
+    }
     h.key = mixed(mixed(seed * kHashA + (uint32_t)t * kHashB) + kHashK);
     const bool fold = list->n <= kListFoldMaxN, q8 = list->bits == 8;
     const bool direct = norm_out != nullptr && on_device(norm_out);

@@ -45,7 +45,7 @@ def encode(x, which, add=None):
     k = np.clip(np.maximum(((mag + add) >> 20) - base, (mag > low).astype(np.int64)), 0,
                 UNITS[which])
     if which == "m":
-        k |= ((x.view(np.uint32) >> 24) & np.where(k > 0, 0x80, 0)).astype(np.int64)
+        k |= ((x.view(np.uint32) >> 24) & 0x80).astype(np.int64)
     out = np.zeros(e.size * BLOCK, np.uint8)
     out[:x.size] = k
     return out, e.astype(np.uint8)

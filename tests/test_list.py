@@ -27,15 +27,14 @@ F32, BF16, F16 = torch.float32, torch.bfloat16, torch.float16
 # 1,024, several of them
 SIZES = [0, 1, 7, 8, 9, 127, 128, 129, 130, 1023, 1024, 1025, 2048, 5003]
 
-# Rounding steps of float32 (2^-24 of the larger of the two terms each) in
-# w * decay - (lr * m_hat) / (sqrt(v_hat) + eps) as adamw_clip_step_list gives
-# it beside 8-bit moments: one half step each for w * decay, m_hat's factor
-# (lr / bc1) and its product, v_hat's factor and the root's (sqrt halves the
-# relative error of its operand), the sum with eps, and the final difference
-# (7 x 1/2); a whole step each (1 ulp) for the hardware's square root and
-# reciprocal, one half for the product with the reciprocal: 6 steps of 2^-23,
-# so 12 of 2^-24.
-WEIGHT_ULPS = 12
+# Steps of 2^-24 (half a unit in float32's last place, relative to the larger of
+# the two terms) by which w * decay - m / (da * sqrt(v) + db), as
+# adamw_clip_step_list gives the weight beside 8-bit moments, may be off
+# weights64: w * decay 1; the denominator's da 1, the hardware's root 2 (a whole
+# unit), their sum with db 1; the hardware's reciprocal 2; the difference 2 (it
+# may be twice the larger term); and weights64 takes bc1 and bc2 rounded to
+# float32, 1 and (under the root) 1/2. 10.5 in all.
+WEIGHT_ULPS = 10.5
 
 
 # --------------------------------------------------------------- the reference
@@ -426,6 +425,37 @@ def test_zero_gradients(dev, bits):
     check_step(case, 1, 1e-2, 1.0)
     m, v = case.moments()
     assert not m.any() and not v.any()
+
+
+@gpu
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("lr", [0.0, 1e-44, 1e-12, -1e-3, 1e6, 1e20])
+def test_extreme_learning_rates(dev, bits, lr):
+    case = Case(dev, [2000, 515], bits=bits)
+    case.g[0][::7] = 0
+    check_step(case, 1, lr, 1.0)
+    check_step(case, 50, lr, float("inf"), eps=1e-16)
+    if bits == 8:  # nothing would be left of eps
+        with pytest.raises(rcs.RcsError):
+            case.list.step(1, 1e30, 1.0)
+
+
+@gpu
+def test_infinite_moments(dev):
+    """An infinite 8-bit moment stays infinite, alone in its block; a beta of
+    zero forgets it."""
+    case = Case(dev, [256], bits=8, state=False)
+    v = torch.ones(256, device=dev)
+    m = torch.ones(256, device=dev)
+    v[5], m[7], m[8] = float("inf"), float("inf"), float("-inf")
+    case.list.import_state(m=m, v=v)
+    case.list.step(1, 1e-3, 1.0)
+    gm, gv = case.moments()
+    assert gv[5] == np.inf and gm[7] == np.inf and gm[8] == -np.inf
+    assert np.isfinite(np.delete(gm, [7, 8])).all() and np.isfinite(np.delete(gv, 5)).all()
+    case.list.step(2, 1e-3, 1.0, beta1=0.0, beta2=0.0)
+    gm, gv = case.moments()
+    assert np.isfinite(gm).all() and np.isfinite(gv).all()
 
 
 @gpu
