@@ -418,7 +418,8 @@ int rcs_list_bind_grads(rcs_list *list, const void *const *g, int64_t count, hip
  * The pre-clip global norm of the list's gradients,
  * sqrt(sum (double)(g * grad_scale)^2) with the product in float32, into
  * norm_out (device or pinned host memory). The order of the sum depends on the
- * list's lengths alone. last_grad_norm reports it too, unless the call was
+ * list's lengths and, with 32-bit moments, on the addresses of m modulo 256,
+ * so results are deterministic for a given list. last_grad_norm reports it too, unless the call was
  * captured.
  */
 int grad_global_norm_list(const rcs_list *list, float grad_scale, double *norm_out,

@@ -84,27 +84,53 @@ constexpr int kLowM = 18, kLowV = 33;
 constexpr uint32_t kHashA = 0x9E3779B1u, kHashB = 0xC2A3F1D7u, kHashC = 0x5BD9E4B5u,
                    kHashK = 0x7F4A7C15u;
 
-// One tensor of the list, in device memory.
+// One tensor of the list, in device memory. All but c is one scalar load of 64
+// bytes.
 struct Row {
     void *w;
     const void *g;  // null: the tensor has no gradient and is left alone
     void *m, *v;
-    uint16_t *e;  // block exponents of the 8-bit moments: m's low, v's high byte
-    void *c;      // low-precision copy of w, or null
+    union {
+        uint16_t *e;    // block exponents of the 8-bit moments: m's low, v's high byte
+        int64_t shift;  // 32-bit moments: chunks begin this many elements early
+    };
     int64_t n;
     int64_t off;  // elements of the list before this tensor
     float wd;
-    uint8_t wt, gt, ct, pad;  // RCS_F32, RCS_BF16, RCS_F16
+    uint32_t types;  // RCS_F32, RCS_BF16, RCS_F16 of w, of g and of c, a byte each
+    void *c;         // low-precision copy of w, or null
+    __host__ __device__ int wt() const { return (int)(types & 0xFFu); }
+    __host__ __device__ int gt() const { return (int)((types >> 8) & 0xFFu); }
+    __host__ __device__ int ct() const { return (int)((types >> 16) & 0xFFu); }
 };
 
-struct Chunk {
-    uint32_t row, part;  // elements part * kChunk .. of that tensor
+// A chunk: the row of its tensor in the lower half, its number there in the
+// upper one. With 8-bit moments chunk k begins at element k * kChunk. With
+// 32-bit ones the boundaries lie where m's address is a multiple of 256 bytes
+// (as far as arrays share their phase, whole lines then belong to one wave:
+// 65 -> 58 us a step of a 12.7M-element bfloat16 list of odd sizes), so the
+// first chunk may be short: chunk k begins `shift` elements before that.
+typedef uint64_t Chunk;
+__device__ __forceinline__ uint32_t row_of(Chunk c) { return (uint32_t)c; }
+
+// Elements first .. end - 1 of a tensor; a chunk's are whole if it lies inside.
+struct Range {
+    int64_t first, end;
+    bool whole;
 };
+template <bool Q8>
+__device__ __forceinline__ Range range_of(Chunk c, const Row &t) {
+    const int64_t a = (int64_t)(c >> 32) * kChunk - (Q8 ? 0 : t.shift), b = a + kChunk;
+    return Range{Q8 || a >= 0 ? a : 0, b <= t.n ? b : t.n, (Q8 || a >= 0) && b <= t.n};
+}
 
 struct ListScalars {
     float lr, bc1, bc2, b1, c1, b2, c2, eps, gscale;
     float da, db;   // for the free evaluation of the weight: weight_free
     uint32_t key;   // of the update's random bits
+    // 0 for a beta of 0, which forgets the 8-bit moment, an infinite one too (0
+    // times that would be a NaN; with this no moment is ever one); else all ones
+    uint32_t keep_m, keep_v;
 };
 
 // ------------------------------------------------------------- element types
@@ -462,15 +488,12 @@ __device__ __forceinline__ void store_moments(const Row &t, int64_t first, uint3
         const u16x2 x = upper(u0 + add_m(2 * j), u1 + add_m(2 * j + 1));
         u16x2 y = __builtin_elementwise_max(halves(word(x) & 0x7FFF7FFFu),
                                             __builtin_elementwise_min(ym[j], least));
-        y = __builtin_elementwise_sub_sat(y >> both(4), bm);
-        y = __builtin_elementwise_min(y, both(127));
+        y = __builtin_elementwise_sub_sat(y >> both(4), bm);  // (infinity comes to the top code)
         km[j] = halves(((word(x) >> 8) & 0x00800080u) | word(y));
         const uint32_t s0 = __float_as_uint(v[2 * j]), s1 = __float_as_uint(v[2 * j + 1]);
         const u16x2 z = upper(s0 + add_v(2 * j), s1 + add_v(2 * j + 1));
         const u16x2 some = halves((s0 < one ? s0 : one) | ((s1 < one ? s1 : one) << 16));
-        kv[j] = __builtin_elementwise_min(
-            __builtin_elementwise_max(__builtin_elementwise_sub_sat(z >> both(4), bv), some),
-            both(255));
+        kv[j] = __builtin_elementwise_max(__builtin_elementwise_sub_sat(z >> both(4), bv), some);
     }
     Codes<V> cm, cv;
 #pragma unroll
@@ -505,26 +528,38 @@ __device__ __forceinline__ double squares_of(const void *g, int64_t first, int64
     constexpr int V = 16 / G::kBytes;  // one 16-byte vector
     constexpr int kStep = kWave * V;
     const int lane = ((int)threadIdx.x & (kWave - 1)) * V;
-    double acc[4] = {};
+    double acc[kDeep] = {};
     int64_t i = first;
     for (; i + kDeep * kStep <= stop; i += kDeep * kStep) {
         Raw<G, V> r[kDeep];
 #pragma unroll
         for (int q = 0; q < kDeep; ++q) r[q] = load<G, V, true, KEEP>(g, i, lane + q * kStep, V);
 #pragma unroll
-        for (int q = 0; q < kDeep; ++q) add_squares(r[q], gscale, acc[q & 3]);
+        for (int q = 0; q < kDeep; ++q) add_squares(r[q], gscale, acc[q]);
     }
-    for (; i < stop; i += kStep)
-        add_squares(load<G, V, false, KEEP>(g, i, lane, count_of<V>(stop - i, lane)), gscale,
-                    acc[0]);
+    if (i < stop) {  // the rest, also in flight at once: whole steps, then lane by lane
+        const int steps = (int)((stop - i) / kStep);
+        const int64_t last = i + steps * kStep;
+        Raw<G, V> r[kDeep - 1], z = {};
+#pragma unroll
+        for (int q = 0; q < kDeep - 1; ++q)
+            if (q < steps) r[q] = load<G, V, true, KEEP>(g, i, lane + q * kStep, V);
+        if (last < stop)
+            z = load<G, V, false, KEEP>(g, last, lane, count_of<V>(stop - last, lane));
+#pragma unroll
+        for (int q = 0; q < kDeep - 1; ++q)
+            if (q < steps) add_squares(r[q], gscale, acc[q]);
+        if (last < stop) add_squares(z, gscale, acc[kDeep - 1]);
+    }
     return (acc[0] + acc[1]) + (acc[2] + acc[3]);
 }
 
 // Per-block float64 partial sums of squares of the list's gradients. The waves
 // of the grid take runs of kRun consecutive chunks in turn, and go through a run
-// one stretch of a tensor at a time; the order depends on the list's lengths
-// alone. The table entries of a run are fetched while the one before it is
+// one stretch of a tensor at a time; the order depends on the list's chunks alone.
+// The table entries of a run are fetched while the one before it is
 // summed.
+template <bool Q8>
 __global__ __launch_bounds__(kListNormThreads) void list_norm_partial(
     const Row *__restrict__ rows, const Chunk *__restrict__ chunks, int64_t nchunks,
     int64_t keep_from, float gscale, double *__restrict__ partials) {
@@ -537,19 +572,20 @@ __global__ __launch_bounds__(kListNormThreads) void list_norm_partial(
     if (run < nchunks) {
         Chunk c = chunks[run];
         Chunk next = chunks[run + step < nchunks ? run + step : run];
-        Row t = rows[c.row];
+        Row t = rows[row_of(c)];
         for (; run < nchunks; run += step) {
             const Chunk after = chunks[run + 2 * step < nchunks ? run + 2 * step : run];
-            const Row next_row = rows[next.row];
+            const Row next_row = rows[row_of(next)];
             const int64_t end = run + kRun < nchunks ? run + kRun : nchunks;
             for (int64_t j = run;;) {
-                const int64_t first = (int64_t)c.part * kChunk;
-                const int64_t whole = (t.n - first + kChunk - 1) / kChunk;
-                const int64_t mine = whole < end - j ? whole : end - j;
-                int64_t stop = first + mine * kChunk;
+                const int64_t shift = Q8 ? 0 : t.shift, k = (int64_t)(c >> 32);
+                const int64_t rest = (t.n + shift + kChunk - 1) / kChunk - k;
+                const int64_t mine = rest < end - j ? rest : end - j;
+                int64_t first = k * kChunk - shift, stop = first + mine * kChunk;
+                if (first < 0) first = 0;
                 if (stop > t.n) stop = t.n;
                 if (t.g != nullptr)
-                    by_type(t.gt, [&](auto G) {
+                    by_type(t.gt(), [&](auto G) {
                         using T = decltype(G);
                         sum += run < keep_from ? squares_of<T, false>(t.g, first, stop, gscale)
                                                : squares_of<T, true>(t.g, first, stop, gscale);
@@ -557,7 +593,7 @@ __global__ __launch_bounds__(kListNormThreads) void list_norm_partial(
                 j += mine;
                 if (j >= end) break;
                 c = chunks[j];
-                t = rows[c.row];
+                t = rows[row_of(c)];
             }
             c = next;
             t = next_row;
@@ -600,15 +636,6 @@ __device__ __forceinline__ void scale(float (&g)[V], const ListScalars &h) {
     for (int k = 0; k < V; ++k) g[k] = g[k] * h.gscale;
 }
 
-// A beta of zero forgets the moment, an infinite one too: 0 times that would be
-// a NaN, and with this no moment is ever one.
-template <int V>
-__device__ __forceinline__ void forget(float (&x)[V], float beta) {
-    if (beta != 0.0f) return;
-#pragma unroll
-    for (int k = 0; k < V; ++k) x[k] = 0.0f;
-}
-
 // The weight in the flat update's operation sequence: divisions and root
 // correctly rounded (beside 32-bit moments, where memory hides them).
 __device__ __forceinline__ float weight(float w, float m, float v, float decay,
@@ -632,10 +659,10 @@ __device__ __forceinline__ float weight_free(float w, float m, float v, float de
 
 // R groups of 32-bit moments from element `first` on: W, G the types of weights
 // and gradients; FULL: all of them lie in the tensor.
-template <class W, class G, int V, int R, bool FULL, class Record>
-__device__ __forceinline__ void update32(const Row &t, int64_t first, Record record,
-                                         const ListScalars &h) {
-    const int64_t left = t.n - first;
+template <class W, class G, int V, int R, bool FULL, class Factor>
+__device__ __forceinline__ void update32(const Row &t, int64_t first, int64_t end,
+                                         Factor clip_factor, const ListScalars &h) {
+    const int64_t left = end - first;
     int at[R], cnt[R];
     Raw<W, V> w[R];
     Raw<G, V> g[R];
@@ -649,8 +676,8 @@ __device__ __forceinline__ void update32(const Row &t, int64_t first, Record rec
         m[q] = load<F32, V, FULL>(t.m, first, at[q], cnt[q]);
         v[q] = load<F32, V, FULL>(t.v, first, at[q], cnt[q]);
     }
-    const ClipScalars cs = record();
-    if (!cs.apply) return;
+    float s;
+    if (!clip_factor(s)) return;
     const float decay = (float)(1.0 - (double)h.lr * (double)t.wd);
 #pragma unroll
     for (int q = 0; q < R; ++q) {
@@ -662,7 +689,7 @@ __device__ __forceinline__ void update32(const Row &t, int64_t first, Record rec
         scale(gg, h);
 #pragma unroll
         for (int k = 0; k < V; ++k) {
-            moments(gg[k], mm[k], vv[k], cs.scale, h);
+            moments(gg[k], mm[k], vv[k], s, h);
             ww[k] = weight(ww[k], mm[k], vv[k], decay, h);
         }
         store<FULL>(t.w, first, at[q], cnt[q], pack<W>(ww));
@@ -670,7 +697,7 @@ __device__ __forceinline__ void update32(const Row &t, int64_t first, Record rec
         store<FULL>(t.v, first, at[q], cnt[q], pack<F32>(vv));
         if constexpr (W::kBytes == 4) {
             if (t.c != nullptr) {
-                if (t.ct == RCS_BF16) store<FULL>(t.c, first, at[q], cnt[q], pack<BF16>(ww));
+                if (t.ct() == RCS_BF16) store<FULL>(t.c, first, at[q], cnt[q], pack<BF16>(ww));
                 else store<FULL>(t.c, first, at[q], cnt[q], pack<F16>(ww));
             }
         }
@@ -680,10 +707,10 @@ __device__ __forceinline__ void update32(const Row &t, int64_t first, Record rec
 // The same with 8-bit moments. The code arrays are filled up to whole blocks,
 // so a code access is always a whole vector; a block past the tensor's end is
 // not touched.
-template <class W, class G, int V, int R, bool FULL, class Record>
-__device__ __forceinline__ void update8(const Row &t, int64_t first, Record record,
-                                        const ListScalars &h) {
-    const int64_t left = t.n - first;
+template <class W, class G, int V, int R, bool FULL, class Factor>
+__device__ __forceinline__ void update8(const Row &t, int64_t first, int64_t end,
+                                        Factor clip_factor, const ListScalars &h) {
+    const int64_t left = end - first;
     // (uniform: the group's first and last element of the list)
     const bool carry = ((t.off + first) >> 32) != ((t.off + first + R * kWave * V - 1) >> 32);
     int at[R], cnt[R];
@@ -704,28 +731,31 @@ __device__ __forceinline__ void update8(const Row &t, int64_t first, Record reco
         cv[q] = load_codes<V>(t.v, first, there);
         e[q] = *exponents_at(t, first, there);
     }
-    const ClipScalars cs = record();
-    if (!cs.apply) return;
+    float s;
+    if (!clip_factor(s)) return;
     const float decay = (float)(1.0 - (double)h.lr * (double)t.wd);
 #pragma unroll
     for (int q = 0; q < R; ++q) {
         float ww[V], gg[V], mm[V], vv[V];
         unpack(w[q], ww);
         unpack(g[q], gg);
+#pragma unroll
+        for (int k = 0; k < V / 4; ++k) {
+            cm[q].d[k] &= h.keep_m;
+            cv[q].d[k] &= h.keep_v;
+        }
         decode_moments(cm[q], cv[q], e[q], mm, vv);
-        forget(mm, h.b1);
-        forget(vv, h.b2);
         scale(gg, h);
 #pragma unroll
         for (int k = 0; k < V; ++k) {
-            moments(gg[k], mm[k], vv[k], cs.scale, h);
+            moments(gg[k], mm[k], vv[k], s, h);
             ww[k] = weight_free(ww[k], mm[k], vv[k], decay, h);
             if (!FULL && k >= cnt[q]) mm[k] = vv[k] = 0.0f;
         }
         store<FULL>(t.w, first, at[q], cnt[q], pack<W>(ww));
         if constexpr (W::kBytes == 4) {
             if (t.c != nullptr) {
-                if (t.ct == RCS_BF16) store<FULL>(t.c, first, at[q], cnt[q], pack<BF16>(ww));
+                if (t.ct() == RCS_BF16) store<FULL>(t.c, first, at[q], cnt[q], pack<BF16>(ww));
                 else store<FULL>(t.c, first, at[q], cnt[q], pack<F16>(ww));
             }
         }
@@ -736,54 +766,62 @@ __device__ __forceinline__ void update8(const Row &t, int64_t first, Record reco
     }
 }
 
-// The update, one wave per chunk. FOLD: every wave does the final reduction of
-// the norm itself (as the flat update does at small n), and the first one
-// writes the record.
+// The update, one wave per chunk. The clip record was written by
+// list_norm_final; it is read beside the table. FOLD: every wave does the final
+// reduction of the norm itself (as the flat update does at small n), behind its
+// loads, and the first one writes the record.
 template <bool Q8, bool FOLD>
 __global__ __launch_bounds__(kUpdThreads) void list_update(
     const Row *__restrict__ rows, const Chunk *__restrict__ chunks,
     const double *__restrict__ partials, int nparts, float clip, ClipScalars *__restrict__ record,
     double *__restrict__ norm_out, ListScalars h) {
     const Chunk c = chunks[blockIdx.x];
-    const Row t = rows[c.row];
     double x[kPartsPerLane];
+    ClipScalars cs = {};
     if constexpr (FOLD) load_partials(partials, nparts, x);
-    auto get = [&]() -> ClipScalars {
+    else cs = *record;
+    const Row t = rows[row_of(c)];
+    auto factor = [&](float &s) -> bool {
         if constexpr (FOLD) {
-            const ClipScalars r = final_reduce(x, nparts, clip, nullptr);
+            asm volatile("" ::: "memory");  // the loads before this stay before it
+            cs = final_reduce(x, nparts, clip, nullptr);
             if (blockIdx.x == 0 && threadIdx.x == 0) {
-                *record = r;
-                if (norm_out != nullptr) *norm_out = r.norm;
+                *record = cs;
+                if (norm_out != nullptr) *norm_out = cs.norm;
             }
-            return r;
-        } else {
-            return *record;
         }
+        s = cs.scale;
+        return cs.apply != 0;
     };
-    if (t.g == nullptr) {
-        (void)get();
+    if (t.g == nullptr || (!FOLD && !cs.apply)) {
+        float s;
+        if constexpr (FOLD) (void)factor(s);
         return;
     }
-    const int64_t first = (int64_t)c.part * kChunk;
-    by_type(t.wt, [&](auto W) {
-        by_type(t.gt, [&](auto G) {
+    const Range r = range_of<Q8>(c, t);
+    by_type(t.wt(), [&](auto W) {
+        by_type(t.gt(), [&](auto G) {
             using WT = decltype(W);
             using GT = decltype(G);
             // 16-bit weights and gradients beside 8-bit moments: 8 elements a lane
             // still cover whole lines and halve the work per block exponent
             constexpr int V = Q8 && WT::kBytes == 2 && GT::kBytes == 2 ? 8 : 4;
             constexpr int R = kChunk / (kWave * V);
-            if (t.n - first >= kChunk) {
-                if constexpr (Q8) update8<WT, GT, V, R, true>(t, first, get, h);
-                else update32<WT, GT, V, R, true>(t, first, get, h);
+            if (r.whole) {
+                if constexpr (Q8) update8<WT, GT, V, R, true>(t, r.first, r.end, factor, h);
+                else update32<WT, GT, V, R, true>(t, r.first, r.end, factor, h);
                 return;
             }
-            const ClipScalars r = get();  // the tensor's last chunk: one group at a time
-            auto same = [&] { return r; };
+            float s;  // a tensor's first or last chunk: one group at a time
+            if (!factor(s)) return;
+            auto same = [s](float &y) {
+                y = s;
+                return true;
+            };
 #pragma unroll 1
-            for (int64_t at = first; at < t.n; at += kWave * V) {
-                if constexpr (Q8) update8<WT, GT, V, 1, false>(t, at, same, h);
-                else update32<WT, GT, V, 1, false>(t, at, same, h);
+            for (int64_t at = r.first; at < r.end; at += kWave * V) {
+                if constexpr (Q8) update8<WT, GT, V, 1, false>(t, at, r.end, same, h);
+                else update32<WT, GT, V, 1, false>(t, at, r.end, same, h);
             }
         });
     });
@@ -812,9 +850,10 @@ __device__ __forceinline__ void load_as(int type, const void *p, int64_t first, 
 
 // One group of V elements a lane from element `first` of t on.
 template <bool Q8, int V, bool FULL>
-__device__ __forceinline__ void export_group(const Row &t, int64_t first, const Flat &f) {
+__device__ __forceinline__ void export_group(const Row &t, int64_t first, int64_t end,
+                                             const Flat &f) {
     const int at = (int)threadIdx.x * V;
-    const int cnt = FULL ? V : count_of<V>(t.n - first, at);
+    const int cnt = FULL ? V : count_of<V>(end - first, at);
     if (cnt == 0) return;
     float m[V], v[V];
     if (f.m != nullptr || f.v != nullptr) {
@@ -827,7 +866,7 @@ __device__ __forceinline__ void export_group(const Row &t, int64_t first, const 
         }
     }
     if (f.w != nullptr)
-        by_type(t.wt, [&](auto W) {
+        by_type(t.wt(), [&](auto W) {
             float x[V];
             unpack(load<decltype(W), V, FULL>(t.w, first, at, cnt), x);
             store_as<FULL>(f.wt, f.w, t.off + first, at, cnt, x);
@@ -841,24 +880,26 @@ __global__ __launch_bounds__(kUpdThreads) void list_export(const Row *__restrict
                                                            const Chunk *__restrict__ chunks,
                                                            Flat f) {
     const Chunk c = chunks[blockIdx.x];
-    const Row t = rows[c.row];
-    const int64_t first = (int64_t)c.part * kChunk;
-    if (t.n - first >= kChunk) {
+    const Row t = rows[row_of(c)];
+    const Range r = range_of<Q8>(c, t);
+    if (r.whole) {
 #pragma unroll
         for (int q = 0; q < kChunk / (kWave * V); ++q)
-            export_group<Q8, V, true>(t, first + q * kWave * V, f);
+            export_group<Q8, V, true>(t, r.first + q * kWave * V, r.end, f);
         return;
     }
 #pragma unroll 1
-    for (int64_t at = first; at < t.n; at += kWave * V) export_group<Q8, V, false>(t, at, f);
+    for (int64_t at = r.first; at < r.end; at += kWave * V)
+        export_group<Q8, V, false>(t, at, r.end, f);
 }
 
 // With 8-bit moments, m and v come together (the host sees to it): a block's
 // two exponents are one store.
 template <bool Q8, int V, bool FULL>
-__device__ __forceinline__ void import_group(const Row &t, int64_t first, const Flat &f) {
+__device__ __forceinline__ void import_group(const Row &t, int64_t first, int64_t end,
+                                             const Flat &f) {
     const int at = (int)threadIdx.x * V;
-    const int64_t left = t.n - first;
+    const int64_t left = end - first;
     const int cnt = FULL ? V : count_of<V>(left, at);
     float m[V], v[V];
     if (f.m != nullptr) load_as<FULL>(f.mt, f.m, t.off + first, at, cnt, m);
@@ -866,9 +907,9 @@ __device__ __forceinline__ void import_group(const Row &t, int64_t first, const 
     if (f.w != nullptr && cnt > 0) {
         float x[V];
         load_as<FULL>(f.wt, f.w, t.off + first, at, cnt, x);
-        by_type(t.wt, [&](auto W) { store<FULL>(t.w, first, at, cnt, pack<decltype(W)>(x)); });
+        by_type(t.wt(), [&](auto W) { store<FULL>(t.w, first, at, cnt, pack<decltype(W)>(x)); });
         if (t.c != nullptr) {
-            if (t.ct == RCS_BF16) store<FULL>(t.c, first, at, cnt, pack<BF16>(x));
+            if (t.ct() == RCS_BF16) store<FULL>(t.c, first, at, cnt, pack<BF16>(x));
             else store<FULL>(t.c, first, at, cnt, pack<F16>(x));
         }
     }
@@ -895,16 +936,17 @@ __global__ __launch_bounds__(kUpdThreads) void list_import(const Row *__restrict
                                                            const Chunk *__restrict__ chunks,
                                                            Flat f) {
     const Chunk c = chunks[blockIdx.x];
-    const Row t = rows[c.row];
-    const int64_t first = (int64_t)c.part * kChunk;
-    if (t.n - first >= kChunk) {
+    const Row t = rows[row_of(c)];
+    const Range r = range_of<Q8>(c, t);
+    if (r.whole) {
 #pragma unroll
         for (int q = 0; q < kChunk / (kWave * V); ++q)
-            import_group<Q8, V, true>(t, first + q * kWave * V, f);
+            import_group<Q8, V, true>(t, r.first + q * kWave * V, r.end, f);
         return;
     }
 #pragma unroll 1
-    for (int64_t at = first; at < t.n; at += kWave * V) import_group<Q8, V, false>(t, at, f);
+    for (int64_t at = r.first; at < r.end; at += kWave * V)
+        import_group<Q8, V, false>(t, at, r.end, f);
 }
 
 // Other gradients for rows first .. first + count - 1. The pointers travel in
@@ -919,6 +961,16 @@ __global__ __launch_bounds__(kBind) void list_bind(Row *__restrict__ rows, int c
 }
 
 // ----------------------------------------------------------------- host side
+
+// The shift of a tensor whose m begins at p (32-bit moments).
+int64_t shift_of(const void *p, int64_t n) {
+    const int64_t head = (int64_t)((256u - (reinterpret_cast<uintptr_t>(p) & 255u)) & 255u) / 4;
+    return head == 0 || n <= kChunk ? 0 : kChunk - head;
+}
+
+int64_t chunks_of(const rcs_list_tensor &t, int bits) {
+    return (t.n + (bits == 8 ? 0 : shift_of(t.m, t.n)) + kChunk - 1) / kChunk;
+}
 
 int type_bytes(int t) { return t == RCS_F32 ? 4 : t == RCS_BF16 || t == RCS_F16 ? 2 : 0; }
 
@@ -1008,7 +1060,8 @@ bool capturing(hipStream_t stream) {
 }
 
 void launch_norm(const rcs_list *l, float gscale, double *partials, hipStream_t stream) {
-    hipLaunchKernelGGL(list_norm_partial, dim3(l->norm_blocks()), dim3(kListNormThreads), 0,
+    auto *kernel = l->bits == 8 ? list_norm_partial<true> : list_norm_partial<false>;
+    hipLaunchKernelGGL(kernel, dim3(l->norm_blocks()), dim3(kListNormThreads), 0,
                        stream, (const Row *)l->d_rows, (const Chunk *)l->d_chunks, l->nchunks,
                        l->keep_from, gscale, partials);
 }
@@ -1023,7 +1076,7 @@ int check_flat(const rcs_list *l, const void *p, int type, bool writes) {
     if (writes)  // an exported array is not a gradient either
         for (const Row &r : l->rows) {
             const char *g = static_cast<const char *>(r.g), *q = static_cast<const char *>(p);
-            if (g != nullptr && g < q + bytes && q < g + r.n * type_bytes(r.gt)) return RCS_EINVAL;
+            if (g != nullptr && g < q + bytes && q < g + r.n * type_bytes(r.gt())) return RCS_EINVAL;
         }
     return RCS_OK;
 }
@@ -1061,7 +1114,7 @@ int rcs_list_create(const rcs_list_tensor *tensors, int64_t count, int state_bit
                         (t.copy != nullptr && !aligned(t.copy, 2))))
             return RCS_EINVAL;
         total += t.n;
-        nchunks += (t.n + kChunk - 1) / kChunk;
+        nchunks += chunks_of(t, state_bits);
         if (nchunks > kMaxChunks) return RCS_EINVAL;
     }
     if (total < 1) return RCS_EINVAL;
@@ -1077,7 +1130,7 @@ int rcs_list_create(const rcs_list_tensor *tensors, int64_t count, int state_bit
         l->nchunks = nchunks;
         int64_t from = nchunks, tail = 0;
         for (int64_t k = count - 1; k >= 0 && tail < kCachedTailBytes; --k) {
-            const int64_t c = (tensors[k].n + kChunk - 1) / kChunk;
+            const int64_t c = chunks_of(tensors[k], state_bits);
             const int64_t per = (int64_t)kChunk * type_bytes(tensors[k].g_type);
             const int64_t want = (kCachedTailBytes - tail + per - 1) / per;
             const int64_t take = c < want ? c : want;
@@ -1091,8 +1144,11 @@ int rcs_list_create(const rcs_list_tensor *tensors, int64_t count, int state_bit
         int64_t off = 0;
         for (int64_t k = 0; k < count; ++k) {
             const rcs_list_tensor &t = tensors[k];
-            Row r{t.w,  t.g, t.m, t.v, static_cast<uint16_t *>(t.exps), t.copy, t.n, off, t.wd,
-                  (uint8_t)t.w_type, (uint8_t)t.g_type, (uint8_t)t.copy_type, 0};
+            const uint32_t types = (uint32_t)t.w_type | (uint32_t)t.g_type << 8 |
+                                   (t.copy != nullptr ? (uint32_t)t.copy_type << 16 : 0u);
+            Row r{t.w, t.g, t.m, t.v, {}, t.n, off, t.wd, types, t.copy};
+            if (state_bits == 8) r.e = static_cast<uint16_t *>(t.exps);
+            else r.shift = shift_of(t.m, t.n);
             if (t.n == 0) {
                 l->rows.push_back(r);
                 continue;
@@ -1117,15 +1173,15 @@ int rcs_list_create(const rcs_list_tensor *tensors, int64_t count, int state_bit
             if (t.copy != nullptr) add(t.copy, 2 * t.n);
             if (state_bits == 8) add(t.exps, 2 * blocks);
             l->rows.push_back(r);
-            for (int64_t c = 0; c < (t.n + kChunk - 1) / kChunk; ++c)
-                chunks.push_back(Chunk{(uint32_t)k, (uint32_t)c});
+            for (int64_t c = 0; c < chunks_of(t, state_bits); ++c)
+                chunks.push_back((Chunk)c << 32 | (Chunk)k);
             off += t.n;
         }
         std::sort(l->written.begin(), l->written.end(), by_start);
         for (size_t k = 1; k < l->written.size(); ++k)
             if (l->written[k].lo < l->written[k - 1].hi) return RCS_EINVAL;
         for (const Row &r : l->rows)
-            if (r.n > 0 && r.g != nullptr && l->touches(r.g, r.n * type_bytes(r.gt)))
+            if (r.n > 0 && r.g != nullptr && l->touches(r.g, r.n * type_bytes(r.gt())))
                 return RCS_EINVAL;
 
         const size_t rows_b = (l->rows.size() * sizeof(Row) + 255) / 256 * 256;
@@ -1184,7 +1240,7 @@ int rcs_list_bind_grads(rcs_list *list, const void *const *g, int64_t count, hip
     for (int64_t k = 0; k < count; ++k) {
         const Row &r = list->rows[(size_t)k];
         if (r.n == 0 || g[k] == nullptr) continue;
-        const int b = type_bytes(r.gt);
+        const int b = type_bytes(r.gt());
         if ((rc = check_array(g[k], b * r.n, b)) != RCS_OK) return rc;
         if (list->touches(g[k], b * r.n)) return RCS_EINVAL;
     }
@@ -1247,6 +1303,8 @@ int adamw_clip_step_list(rcs_list *list, int32_t t, float lr, float clip, float 
     h.c2 = (float)(1.0 - beta2);
     h.eps = eps;
     h.gscale = grad_scale;
+    h.keep_m = h.b1 == 0.0f ? 0u : ~0u;
+    h.keep_v = h.b2 == 0.0f ? 0u : ~0u;
     // weight_free's constants; a learning rate of zero, or whose inverse
     // overflows, divides by infinity
     const double over = (1.0 - std::pow(beta1, (double)t)) / (double)lr;
