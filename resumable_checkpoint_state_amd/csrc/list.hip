@@ -54,7 +54,7 @@
 #include <cmath>
 #include <cstdint>
 #include <new>
-#include <utility>
+#include <type_traits>
 #include <vector>
 
 #include "rcs.h"
@@ -131,9 +131,15 @@ struct ListScalars {
     // 0 for a beta of 0, which forgets the 8-bit moment, an infinite one too (0
     // times that would be a NaN; with this no moment is ever one); else all ones
     uint32_t keep_m, keep_v;
+    int32_t fits;  // the update's arrays fit the last-level cache
 };
 
 // ------------------------------------------------------------- element types
+
+// Bytes of an element type; 0 if there is no such type.
+__host__ __device__ constexpr int type_bytes(int t) {
+    return t == RCS_F32 ? 4 : t == RCS_BF16 || t == RCS_F16 ? 2 : 0;
+}
 
 struct F32 {
     static constexpr int kBytes = 4;
@@ -286,6 +292,31 @@ __device__ __forceinline__ void store(void *p, int64_t first, uint32_t at, int c
         }
     }
 }
+
+// Whether an array's chunks begin off a line boundary, and its waves so share
+// lines with their neighbours: its loads are then left in the cache for them
+// (KEEP) rather than streamed, which would fetch those lines twice. The two
+// cases are told apart by f(true) or f(false), each behind a barrier of its own:
+// the compiler would merge loads that only differ in this.
+template <class F>
+__device__ __forceinline__ void by_lines(bool shared, F f) {
+    if (shared) {
+        asm volatile("; shared lines" ::: "memory");
+        f(std::true_type{});
+    } else {
+        asm volatile("; whole lines" ::: "memory");
+        f(std::false_type{});
+    }
+}
+__device__ __forceinline__ bool off_line(const void *p, int64_t bytes) {
+    return ((reinterpret_cast<uintptr_t>(p) + (uintptr_t)bytes) & 127u) != 0;
+}
+
+// (Update beside 8-bit moments, float32 weights at odd offsets, bfloat16
+// gradients and copies, streamed against kept: 51.6 and 48.1 us at 12.7M
+// elements, 89.5 and 87.1 at 24.7M, 129 and 130 at 36.7M, 164 and 171 at 50M:
+// kept while all its arrays fit the cache. Export 49.7 and 44.6 us at 12.7M,
+// 488 and 476 at 124.6M, import 421 and 395: kept always.)
 
 // f(T) for the element type t (uniform in the wave).
 template <class F>
@@ -707,7 +738,7 @@ __device__ __forceinline__ void update32(const Row &t, int64_t first, int64_t en
 // The same with 8-bit moments. The code arrays are filled up to whole blocks,
 // so a code access is always a whole vector; a block past the tensor's end is
 // not touched.
-template <class W, class G, int V, int R, bool FULL, class Factor>
+template <class W, class G, int V, int R, bool FULL, bool KEEP, class Factor>
 __device__ __forceinline__ void update8(const Row &t, int64_t first, int64_t end,
                                         Factor clip_factor, const ListScalars &h) {
     const int64_t left = end - first;
@@ -724,8 +755,8 @@ __device__ __forceinline__ void update8(const Row &t, int64_t first, int64_t end
         at[q] = (q * kWave + (int)threadIdx.x) * V;
         cnt[q] = FULL ? V : count_of<V>(left, at[q]);
         active[q] = FULL || (at[q] & ~(kBlock - 1)) < left;
-        g[q] = load<G, V, FULL>(t.g, first, at[q], cnt[q]);
-        w[q] = load<W, V, FULL>(t.w, first, at[q], cnt[q]);
+        g[q] = load<G, V, FULL, KEEP>(t.g, first, at[q], cnt[q]);
+        w[q] = load<W, V, FULL, KEEP>(t.w, first, at[q], cnt[q]);
         const int there = active[q] ? at[q] : 0;
         cm[q] = load_codes<V>(t.m, first, there);
         cv[q] = load_codes<V>(t.v, first, there);
@@ -769,8 +800,11 @@ __device__ __forceinline__ void update8(const Row &t, int64_t first, int64_t end
 // The update, one wave per chunk. The clip record was written by
 // list_norm_final; it is read beside the table. FOLD: every wave does the final
 // reduction of the norm itself (as the flat update does at small n), behind its
-// loads, and the first one writes the record.
-template <bool Q8, bool FOLD>
+// loads, and the first one writes the record. W, G: the types of weights and
+// gradients; a list with several pairs of types has a launch for each (one
+// kernel that branched on them held 92 vector registers for every pair and
+// spilled scalar ones).
+template <class W, class G, bool Q8, bool FOLD>
 __global__ __launch_bounds__(kUpdThreads) void list_update(
     const Row *__restrict__ rows, const Chunk *__restrict__ chunks,
     const double *__restrict__ partials, int nparts, float clip, ClipScalars *__restrict__ record,
@@ -799,32 +833,30 @@ __global__ __launch_bounds__(kUpdThreads) void list_update(
         return;
     }
     const Range r = range_of<Q8>(c, t);
-    by_type(t.wt(), [&](auto W) {
-        by_type(t.gt(), [&](auto G) {
-            using WT = decltype(W);
-            using GT = decltype(G);
-            // 16-bit weights and gradients beside 8-bit moments: 8 elements a lane
-            // still cover whole lines and halve the work per block exponent
-            constexpr int V = Q8 && WT::kBytes == 2 && GT::kBytes == 2 ? 8 : 4;
-            constexpr int R = kChunk / (kWave * V);
-            if (r.whole) {
-                if constexpr (Q8) update8<WT, GT, V, R, true>(t, r.first, r.end, factor, h);
-                else update32<WT, GT, V, R, true>(t, r.first, r.end, factor, h);
-                return;
-            }
-            float s;  // a tensor's first or last chunk: one group at a time
-            if (!factor(s)) return;
-            auto same = [s](float &y) {
-                y = s;
-                return true;
-            };
+    // 16-bit weights and gradients beside 8-bit moments: 8 elements a lane still
+    // cover whole lines and halve the work per block exponent
+    constexpr int V = Q8 && W::kBytes == 2 && G::kBytes == 2 ? 8 : 4;
+    constexpr int R = kChunk / (kWave * V);
+    if (r.whole) {
+        if constexpr (Q8)
+            by_lines(h.fits != 0 && off_line(t.w, 0), [&](auto K) {
+                update8<W, G, V, R, true, K.value>(t, r.first, r.end, factor, h);
+            });
+        else
+            update32<W, G, V, R, true>(t, r.first, r.end, factor, h);
+        return;
+    }
+    float s;  // a tensor's first or last chunk: one group at a time
+    if (!factor(s)) return;
+    auto same = [s](float &y) {
+        y = s;
+        return true;
+    };
 #pragma unroll 1
-            for (int64_t at = r.first; at < r.end; at += kWave * V) {
-                if constexpr (Q8) update8<WT, GT, V, 1, false>(t, at, r.end, same, h);
-                else update32<WT, GT, V, 1, false>(t, at, r.end, same, h);
-            }
-        });
-    });
+    for (int64_t at = r.first; at < r.end; at += kWave * V) {
+        if constexpr (Q8) update8<W, G, V, 1, false, true>(t, at, r.end, same, h);
+        else update32<W, G, V, 1, false>(t, at, r.end, same, h);
+    }
 }
 
 // Flat arrays of the list's elements, in list order: w, m and v, each float32
@@ -841,15 +873,15 @@ __device__ __forceinline__ void store_as(int type, void *p, int64_t first, uint3
     else store<FULL>(p, first, at, cnt, pack<BF16>(x));
 }
 
-template <bool FULL, int V>
+template <bool FULL, bool KEEP, int V>
 __device__ __forceinline__ void load_as(int type, const void *p, int64_t first, uint32_t at,
                                         int cnt, float (&x)[V]) {
-    if (type == RCS_F32) unpack(load<F32, V, FULL>(p, first, at, cnt), x);
-    else unpack(load<BF16, V, FULL>(p, first, at, cnt), x);
+    if (type == RCS_F32) unpack(load<F32, V, FULL, KEEP>(p, first, at, cnt), x);
+    else unpack(load<BF16, V, FULL, KEEP>(p, first, at, cnt), x);
 }
 
 // One group of V elements a lane from element `first` of t on.
-template <bool Q8, int V, bool FULL>
+template <bool Q8, int V, bool FULL, bool KEEP>
 __device__ __forceinline__ void export_group(const Row &t, int64_t first, int64_t end,
                                              const Flat &f) {
     const int at = (int)threadIdx.x * V;
@@ -868,7 +900,7 @@ __device__ __forceinline__ void export_group(const Row &t, int64_t first, int64_
     if (f.w != nullptr)
         by_type(t.wt(), [&](auto W) {
             float x[V];
-            unpack(load<decltype(W), V, FULL>(t.w, first, at, cnt), x);
+            unpack(load<decltype(W), V, FULL, KEEP>(t.w, first, at, cnt), x);
             store_as<FULL>(f.wt, f.w, t.off + first, at, cnt, x);
         });
     if (f.m != nullptr) store_as<FULL>(f.mt, f.m, t.off + first, at, cnt, m);
@@ -883,30 +915,32 @@ __global__ __launch_bounds__(kUpdThreads) void list_export(const Row *__restrict
     const Row t = rows[row_of(c)];
     const Range r = range_of<Q8>(c, t);
     if (r.whole) {
+        by_lines(off_line(t.w, r.first * type_bytes(t.wt())), [&](auto K) {
 #pragma unroll
-        for (int q = 0; q < kChunk / (kWave * V); ++q)
-            export_group<Q8, V, true>(t, r.first + q * kWave * V, r.end, f);
+            for (int q = 0; q < kChunk / (kWave * V); ++q)
+                export_group<Q8, V, true, K.value>(t, r.first + q * kWave * V, r.end, f);
+        });
         return;
     }
 #pragma unroll 1
     for (int64_t at = r.first; at < r.end; at += kWave * V)
-        export_group<Q8, V, false>(t, at, r.end, f);
+        export_group<Q8, V, false, true>(t, at, r.end, f);
 }
 
 // With 8-bit moments, m and v come together (the host sees to it): a block's
 // two exponents are one store.
-template <bool Q8, int V, bool FULL>
+template <bool Q8, int V, bool FULL, bool KEEP>
 __device__ __forceinline__ void import_group(const Row &t, int64_t first, int64_t end,
                                              const Flat &f) {
     const int at = (int)threadIdx.x * V;
     const int64_t left = end - first;
     const int cnt = FULL ? V : count_of<V>(left, at);
     float m[V], v[V];
-    if (f.m != nullptr) load_as<FULL>(f.mt, f.m, t.off + first, at, cnt, m);
-    if (f.v != nullptr) load_as<FULL>(f.vt, f.v, t.off + first, at, cnt, v);
+    if (f.m != nullptr) load_as<FULL, KEEP>(f.mt, f.m, t.off + first, at, cnt, m);
+    if (f.v != nullptr) load_as<FULL, KEEP>(f.vt, f.v, t.off + first, at, cnt, v);
     if (f.w != nullptr && cnt > 0) {
         float x[V];
-        load_as<FULL>(f.wt, f.w, t.off + first, at, cnt, x);
+        load_as<FULL, KEEP>(f.wt, f.w, t.off + first, at, cnt, x);
         by_type(t.wt(), [&](auto W) { store<FULL>(t.w, first, at, cnt, pack<decltype(W)>(x)); });
         if (t.c != nullptr) {
             if (t.ct() == RCS_BF16) store<FULL>(t.c, first, at, cnt, pack<BF16>(x));
@@ -939,14 +973,16 @@ __global__ __launch_bounds__(kUpdThreads) void list_import(const Row *__restrict
     const Row t = rows[row_of(c)];
     const Range r = range_of<Q8>(c, t);
     if (r.whole) {
+        by_lines(off_line(f.m, (t.off + r.first) * type_bytes(f.mt)), [&](auto K) {
 #pragma unroll
-        for (int q = 0; q < kChunk / (kWave * V); ++q)
-            import_group<Q8, V, true>(t, r.first + q * kWave * V, r.end, f);
+            for (int q = 0; q < kChunk / (kWave * V); ++q)
+                import_group<Q8, V, true, K.value>(t, r.first + q * kWave * V, r.end, f);
+        });
         return;
     }
 #pragma unroll 1
     for (int64_t at = r.first; at < r.end; at += kWave * V)
-        import_group<Q8, V, false>(t, at, r.end, f);
+        import_group<Q8, V, false, true>(t, at, r.end, f);
 }
 
 // Other gradients for rows first .. first + count - 1. The pointers travel in
@@ -972,10 +1008,14 @@ int64_t chunks_of(const rcs_list_tensor &t, int bits) {
     return (t.n + (bits == 8 ? 0 : shift_of(t.m, t.n)) + kChunk - 1) / kChunk;
 }
 
-int type_bytes(int t) { return t == RCS_F32 ? 4 : t == RCS_BF16 || t == RCS_F16 ? 2 : 0; }
-
 struct Span {
     const char *lo, *hi;
+};
+
+// The chunks whose weights and gradients are of one pair of types.
+struct Group {
+    int wt, gt;
+    int64_t first, count;
 };
 
 bool by_start(const Span &a, const Span &b) { return a.lo < b.lo; }
@@ -987,8 +1027,10 @@ struct rcs_list {
     int bits = 32;
     int64_t n = 0;        // elements of all tensors
     int64_t nchunks = 0;
+    int64_t bytes = 0;     // of weights, gradients, copies and 8-bit moments
     int64_t keep_from = 0;  // first chunk whose gradient the norm pass leaves in the cache
     std::vector<Row> rows;
+    std::vector<Group> groups;
     std::vector<Span> written;  // what an update writes, sorted
     char *mem = nullptr;        // everything below, one allocation
     Row *d_rows = nullptr;
@@ -1019,6 +1061,7 @@ constexpr int64_t kListFoldMaxN = 8388608;
 // Bytes at the end of the gradients that the norm pass reads with cache-
 // allocating loads, so that the update finds them in the last-level cache.
 constexpr int64_t kCachedTailBytes = 320LL << 20;
+constexpr int64_t kCacheBytes = 256LL << 20;  // the last-level cache
 // Waves of a launch: the grid's work-items have to fit 32 bits.
 constexpr int64_t kMaxChunks = 0xFFFFFFFFLL / kUpdThreads;
 
@@ -1066,6 +1109,21 @@ void launch_norm(const rcs_list *l, float gscale, double *partials, hipStream_t 
                        l->keep_from, gscale, partials);
 }
 
+template <bool Q8, bool FOLD>
+auto *update_kernel(const Group &g) {
+    auto *kernel = list_update<F32, F32, Q8, FOLD>;
+    auto with = [&](auto W) {
+        using WT = decltype(W);
+        kernel = g.gt == RCS_F32    ? list_update<WT, F32, Q8, FOLD>
+                 : g.gt == RCS_BF16 ? list_update<WT, BF16, Q8, FOLD>
+                                    : list_update<WT, F16, Q8, FOLD>;
+    };
+    if (g.wt == RCS_F32) with(F32{});
+    else if (g.wt == RCS_BF16) with(BF16{});
+    else with(F16{});
+    return kernel;
+}
+
 int check_flat(const rcs_list *l, const void *p, int type, bool writes) {
     if (p == nullptr) return RCS_OK;
     if (type != RCS_F32 && type != RCS_BF16) return RCS_EINVAL;
@@ -1098,7 +1156,7 @@ int rcs_list_create(const rcs_list_tensor *tensors, int64_t count, int state_bit
     if (tensors == nullptr || count < 1 || count > 0x7FFFFFFF ||
         (state_bits != 32 && state_bits != 8))
         return RCS_EINVAL;
-    int64_t total = 0, nchunks = 0;
+    int64_t total = 0, nchunks = 0, bytes = 0;
     for (int64_t k = 0; k < count; ++k) {
         const rcs_list_tensor &t = tensors[k];
         if (t.n < 0 || t.n > (1LL << 40)) return RCS_EINVAL;
@@ -1115,6 +1173,8 @@ int rcs_list_create(const rcs_list_tensor *tensors, int64_t count, int state_bit
             return RCS_EINVAL;
         total += t.n;
         nchunks += chunks_of(t, state_bits);
+        bytes += t.n * (type_bytes(t.w_type) + type_bytes(t.g_type) +
+                        (t.copy != nullptr ? 2 : 0) + 2);
         if (nchunks > kMaxChunks) return RCS_EINVAL;
     }
     if (total < 1) return RCS_EINVAL;
@@ -1128,16 +1188,7 @@ int rcs_list_create(const rcs_list_tensor *tensors, int64_t count, int state_bit
         l->bits = state_bits;
         l->n = total;
         l->nchunks = nchunks;
-        int64_t from = nchunks, tail = 0;
-        for (int64_t k = count - 1; k >= 0 && tail < kCachedTailBytes; --k) {
-            const int64_t c = chunks_of(tensors[k], state_bits);
-            const int64_t per = (int64_t)kChunk * type_bytes(tensors[k].g_type);
-            const int64_t want = (kCachedTailBytes - tail + per - 1) / per;
-            const int64_t take = c < want ? c : want;
-            from -= take;
-            tail += take * per;
-        }
-        l->keep_from = from;
+        l->bytes = bytes;
         if (hipGetDevice(&l->dev) != hipSuccess) return RCS_EHIP;
         std::vector<Chunk> chunks;
         chunks.reserve((size_t)nchunks);
@@ -1173,9 +1224,28 @@ int rcs_list_create(const rcs_list_tensor *tensors, int64_t count, int state_bit
             if (t.copy != nullptr) add(t.copy, 2 * t.n);
             if (state_bits == 8) add(t.exps, 2 * blocks);
             l->rows.push_back(r);
-            for (int64_t c = 0; c < chunks_of(t, state_bits); ++c)
-                chunks.push_back((Chunk)c << 32 | (Chunk)k);
             off += t.n;
+        }
+        for (int pair = 0; pair < 9; ++pair) {
+            const Group g{pair / 3, pair % 3, (int64_t)chunks.size(), 0};
+            for (int64_t k = 0; k < count; ++k)
+                if (tensors[k].w_type == g.wt && tensors[k].g_type == g.gt)
+                    for (int64_t c = 0; c < chunks_of(tensors[k], state_bits); ++c)
+                        chunks.push_back((Chunk)c << 32 | (Chunk)k);
+            if ((int64_t)chunks.size() > g.first)
+                l->groups.push_back(
+                    Group{g.wt, g.gt, g.first, (int64_t)chunks.size() - g.first});
+        }
+        // the last chunks, as many as hold kCachedTailBytes of gradients
+        l->keep_from = nchunks;
+        int64_t tail = 0;
+        for (size_t k = l->groups.size(); k-- > 0 && tail < kCachedTailBytes;) {
+            const Group &g = l->groups[k];
+            const int64_t per = (int64_t)kChunk * type_bytes(g.gt);
+            const int64_t want = (kCachedTailBytes - tail + per - 1) / per;
+            const int64_t take = g.count < want ? g.count : want;
+            l->keep_from -= take;
+            tail += take * per;
         }
         std::sort(l->written.begin(), l->written.end(), by_start);
         for (size_t k = 1; k < l->written.size(); ++k)
@@ -1303,6 +1373,7 @@ int adamw_clip_step_list(rcs_list *list, int32_t t, float lr, float clip, float 
     h.c2 = (float)(1.0 - beta2);
     h.eps = eps;
     h.gscale = grad_scale;
+    h.fits = list->bytes <= kCacheBytes;
     h.keep_m = h.b1 == 0.0f ? 0u : ~0u;
     h.keep_v = h.b2 == 0.0f ? 0u : ~0u;
     // weight_free's constants; a learning rate of zero, or whose inverse
@@ -1326,11 +1397,13 @@ int adamw_clip_step_list(rcs_list *list, int32_t t, float lr, float clip, float 
     if (!fold)
         hipLaunchKernelGGL(list_norm_final, dim3(1), dim3(kUpdThreads), 0, stream,
                            (const double *)partials, nparts, clip, record, dev_out);
-    auto *kernel = q8 ? (fold ? list_update<true, true> : list_update<true, false>)
-                      : (fold ? list_update<false, true> : list_update<false, false>);
-    hipLaunchKernelGGL(kernel, dim3((unsigned)list->nchunks), dim3(kUpdThreads), 0, stream,
-                       (const Row *)list->d_rows, (const Chunk *)list->d_chunks,
-                       (const double *)partials, nparts, clip, record, dev_out, h);
+    for (const Group &g : list->groups) {
+        auto *kernel = q8 ? (fold ? update_kernel<true, true>(g) : update_kernel<true, false>(g))
+                          : (fold ? update_kernel<false, true>(g) : update_kernel<false, false>(g));
+        hipLaunchKernelGGL(kernel, dim3((unsigned)g.count), dim3(kUpdThreads), 0, stream,
+                           (const Row *)list->d_rows, (const Chunk *)list->d_chunks + g.first,
+                           (const double *)partials, nparts, clip, record, dev_out, h);
+    }
     if (hipGetLastError() != hipSuccess) return RCS_EHIP;
     if (norm_out != nullptr && !direct &&
         hipMemcpyAsync(norm_out, &record->norm, sizeof(double), hipMemcpyDefault, stream) !=
