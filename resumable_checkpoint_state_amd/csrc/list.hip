@@ -41,11 +41,10 @@
 // two rounds of 4 consecutive ones per lane, so that each access of a wave
 // covers whole lines (8 a lane put the halves of a float32 line into two
 // accesses: 802 against 683 us); the accesses need only the element's own
-// alignment, so tensors may be views at any offset. The type
-// combination is a uniform branch per wave, so a list of mixed types is one
-// launch. Blocks take chunks in address order (putting each XCD on its own
-// eighth, as the flat update does, was slower here: 651 against 607 us a step
-// of the 124,356,864-element float32 list). Bound by HBM: see the kernels.
+// alignment, so tensors may be views at any offset. Chunks
+// are sorted by the types of weights and gradients; each pair of them has a
+// kernel and a launch of its own. Bound by HBM, beside 8-bit moments of 16-bit
+// weights nearly as much by the vector instructions.
 
 #include <hip/hip_runtime.h>
 
@@ -112,6 +111,29 @@ struct Row {
 // first chunk may be short: chunk k begins `shift` elements before that.
 typedef uint64_t Chunk;
 __device__ __forceinline__ uint32_t row_of(Chunk c) { return (uint32_t)c; }
+
+// The chunk of block blockIdx.x: a permutation of [0, gridDim.x). Blocks are
+// dispatched round-robin over the 8 XCDs, so taken in order, neighbouring
+// chunks run on different ones, and each fetches the lines they share on its
+// own (of arrays off a line boundary, of the block exponents, of the table).
+// Within each window of 8 * kNear chunks an XCD here gets kNear neighbours.
+// us with chunks in order and so: 8-bit moments, float32 weights with bfloat16
+// gradients and copies, 348 and 338 at 124,356,864 elements, 47.7 and 45.0 at
+// 12.7M of odd sizes; export 328 and 319, import 432 and 426; 32-bit moments
+// 60.6 and 57.5 (12.7M bfloat16, odd sizes), 187 and 185 (37M float32), 247
+// and 245 (50M), but 607 and 624 at 124,356,864 float32: there they stay in
+// order. (16 neighbours: 343 for export; 128 or 256: as 64. Each XCD on an
+// eighth of the list, as in the flat update: 651 for 607.)
+constexpr uint32_t kNear = 64;
+constexpr int64_t kNearMaxN = 1LL << 26;  // beside 32-bit moments
+constexpr uint32_t kWindow = 8 * kNear;
+// in_windows: the blocks of whole windows, 0 to take all chunks in order (a
+// kernel argument: the grid's size would be a load of its own).
+__device__ __forceinline__ uint32_t near_chunk(uint32_t in_windows) {
+    const uint32_t b = blockIdx.x, i = b % kWindow;
+    const uint32_t near = b - i + (i % 8) * kNear + i / 8;
+    return b < in_windows ? near : b;
+}
 
 // Elements first .. end - 1 of a tensor; a chunk's are whole if it lies inside.
 struct Range {
@@ -806,10 +828,10 @@ __device__ __forceinline__ void update8(const Row &t, int64_t first, int64_t end
 // spilled scalar ones).
 template <class W, class G, bool Q8, bool FOLD>
 __global__ __launch_bounds__(kUpdThreads) void list_update(
-    const Row *__restrict__ rows, const Chunk *__restrict__ chunks,
-    const double *__restrict__ partials, int nparts, float clip, ClipScalars *__restrict__ record,
+    const Row *__restrict__ rows, const Chunk *__restrict__ chunks, uint32_t in_windows,
+    int nparts, const double *__restrict__ partials, float clip, ClipScalars *__restrict__ record,
     double *__restrict__ norm_out, ListScalars h) {
-    const Chunk c = chunks[blockIdx.x];
+    const Chunk c = chunks[near_chunk(in_windows)];
     double x[kPartsPerLane];
     ClipScalars cs = {};
     if constexpr (FOLD) load_partials(partials, nparts, x);
@@ -827,6 +849,8 @@ __global__ __launch_bounds__(kUpdThreads) void list_update(
         s = cs.scale;
         return cs.apply != 0;
     };
+    // all of the row before the branch, in one trip
+    asm volatile("" ::"s"(t.n), "s"(t.off), "s"(t.types), "s"(h.lr), "s"(h.eps), "s"(h.key));
     if (t.g == nullptr || (!FOLD && !cs.apply)) {
         float s;
         if constexpr (FOLD) (void)factor(s);
@@ -910,8 +934,8 @@ __device__ __forceinline__ void export_group(const Row &t, int64_t first, int64_
 template <bool Q8, int V>
 __global__ __launch_bounds__(kUpdThreads) void list_export(const Row *__restrict__ rows,
                                                            const Chunk *__restrict__ chunks,
-                                                           Flat f) {
-    const Chunk c = chunks[blockIdx.x];
+                                                           uint32_t in_windows, Flat f) {
+    const Chunk c = chunks[near_chunk(in_windows)];
     const Row t = rows[row_of(c)];
     const Range r = range_of<Q8>(c, t);
     if (r.whole) {
@@ -968,8 +992,8 @@ __device__ __forceinline__ void import_group(const Row &t, int64_t first, int64_
 template <bool Q8, int V>
 __global__ __launch_bounds__(kUpdThreads) void list_import(const Row *__restrict__ rows,
                                                            const Chunk *__restrict__ chunks,
-                                                           Flat f) {
-    const Chunk c = chunks[blockIdx.x];
+                                                           uint32_t in_windows, Flat f) {
+    const Chunk c = chunks[near_chunk(in_windows)];
     const Row t = rows[row_of(c)];
     const Range r = range_of<Q8>(c, t);
     if (r.whole) {
@@ -1108,6 +1132,8 @@ void launch_norm(const rcs_list *l, float gscale, double *partials, hipStream_t 
                        stream, (const Row *)l->d_rows, (const Chunk *)l->d_chunks, l->nchunks,
                        l->keep_from, gscale, partials);
 }
+
+uint32_t in_windows(int64_t blocks) { return (uint32_t)(blocks - blocks % kWindow); }
 
 template <bool Q8, bool FOLD>
 auto *update_kernel(const Group &g) {
@@ -1397,12 +1423,14 @@ int adamw_clip_step_list(rcs_list *list, int32_t t, float lr, float clip, float 
     if (!fold)
         hipLaunchKernelGGL(list_norm_final, dim3(1), dim3(kUpdThreads), 0, stream,
                            (const double *)partials, nparts, clip, record, dev_out);
+    const bool near = q8 || list->n <= kNearMaxN;
     for (const Group &g : list->groups) {
         auto *kernel = q8 ? (fold ? update_kernel<true, true>(g) : update_kernel<true, false>(g))
                           : (fold ? update_kernel<false, true>(g) : update_kernel<false, false>(g));
         hipLaunchKernelGGL(kernel, dim3((unsigned)g.count), dim3(kUpdThreads), 0, stream,
                            (const Row *)list->d_rows, (const Chunk *)list->d_chunks + g.first,
-                           (const double *)partials, nparts, clip, record, dev_out, h);
+                           near ? in_windows(g.count) : 0u, nparts, (const double *)partials,
+                           clip, record, dev_out, h);
     }
     if (hipGetLastError() != hipSuccess) return RCS_EHIP;
     if (norm_out != nullptr && !direct &&
@@ -1429,7 +1457,8 @@ int rcs_list_export(const rcs_list *list, void *w, int w_type, void *m, int m_ty
     auto *kernel = list->bits == 8 ? (wide ? list_export<true, 8> : list_export<true, 4>)
                                    : list_export<false, 4>;
     hipLaunchKernelGGL(kernel, dim3((unsigned)list->nchunks), dim3(kUpdThreads), 0, stream,
-                       (const Row *)list->d_rows, (const Chunk *)list->d_chunks, f);
+                       (const Row *)list->d_rows, (const Chunk *)list->d_chunks,
+                       in_windows(list->nchunks), f);
     return hipGetLastError() == hipSuccess ? RCS_OK : RCS_EHIP;
 }
 
@@ -1448,7 +1477,8 @@ int rcs_list_import(rcs_list *list, const void *w, int w_type, const void *m, in
     auto *kernel = list->bits == 8 ? (wide ? list_import<true, 8> : list_import<true, 4>)
                                    : list_import<false, 4>;
     hipLaunchKernelGGL(kernel, dim3((unsigned)list->nchunks), dim3(kUpdThreads), 0, stream,
-                       (const Row *)list->d_rows, (const Chunk *)list->d_chunks, f);
+                       (const Row *)list->d_rows, (const Chunk *)list->d_chunks,
+                       in_windows(list->nchunks), f);
     return hipGetLastError() == hipSuccess ? RCS_OK : RCS_EHIP;
 }
 
