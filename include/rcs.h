@@ -1,6 +1,7 @@
 /*
  * rcs.h -- C ABI of the MI355X (gfx950) library for one clipped AdamW update
- * over a flat float32 parameter vector and for the step_NNNNNN.bin state.
+ * over a flat float32 parameter vector, or over a list of tensors, and for the
+ * step_NNNNNN.bin state.
  *
  * All entry points are extern "C", take plain pointers and sizes, and only
  * enqueue work on the given HIP stream (0 = the null stream of the current
@@ -17,7 +18,8 @@
  * calling thread gets its own workspace (rcs_init from that thread). (The
  * asynchronous pack also keeps two HIP events per snapshot buffer, and the
  * instrumentation its events while enabled. An rcs_ckpt_writer, created and
- * destroyed explicitly, owns its snapshot, host buffer, stream and thread.)
+ * destroyed explicitly, owns its snapshot, host buffer, stream and thread; an
+ * rcs_list, likewise, its description of the tensors and its norm buffers.)
  *
  * Every call validates its arguments on the host before enqueuing anything and
  * returns one of the status codes below; a negative return means nothing was
@@ -453,9 +455,10 @@ int grad_global_norm_list(const rcs_list *list, float grad_scale, double *norm_o
  * share an exponent for m and one for v (low and high byte of exps). With e
  * that byte, code k > 0 is the float whose bits are (k + 8 e - 255) << 20 for
  * v, and with k the low 7 bits and the top bit the sign, (k + 8 e - 127) << 20
- * for m; k = 0 is zero, with either sign. e is the biased exponent of the smallest power of two
- * not below the block's largest magnitude, at least 18 for m and 33 for v and
- * at most 255; what is not finite is held as an infinity of its sign.
+ * for m; k = 0 is zero, with either sign. e is the biased exponent of the
+ * smallest power of two not below the block's largest magnitude, at least 18
+ * for m and 33 for v and at most 255; what is not finite, or rounds beyond the
+ * largest float, is held as an infinity of its sign.
  */
 int adamw_clip_step_list(rcs_list *list, int32_t t, float lr, float clip, float grad_scale,
                          double beta1, double beta2, float eps, uint32_t seed, double *norm_out,

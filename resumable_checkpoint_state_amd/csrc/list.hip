@@ -515,7 +515,6 @@ __device__ __forceinline__ void store_moments(const Row &t, int64_t first, uint3
     // ym: upper halves of |m|'s bits plus 0x7FFFFF. Their largest gives the
     // block's exponent; and as the smallest value L and half of it are a power
     // of two apart and end in 20 zero bits, ym >= L exactly where |m| > L / 2.
-    // The sum saturates, so a NaN stays above every number.
     u16x2 ym[V / 2], big = both(0);
     uint32_t av = 0;
 #pragma unroll
@@ -609,8 +608,8 @@ __device__ __forceinline__ double squares_of(const void *g, int64_t first, int64
 
 // Per-block float64 partial sums of squares of the list's gradients. The waves
 // of the grid take runs of kRun consecutive chunks in turn, and go through a run
-// one stretch of a tensor at a time; the order depends on the list's chunks alone.
-// The table entries of a run are fetched while the one before it is
+// one stretch of a tensor at a time; the order depends on the list's chunks
+// alone. The table entries of a run are fetched while the one before it is
 // summed.
 template <bool Q8>
 __global__ __launch_bounds__(kListNormThreads) void list_norm_partial(

@@ -529,6 +529,35 @@ def test_import_of_what_is_not_finite(dev):
 
 
 @gpu
+def test_import_of_the_largest_floats(dev):
+    """What rounds beyond the largest float becomes an infinity, as the
+    reference has it; half a step below does not."""
+    m = torch.full((128,), 3.0e38, device=dev)
+    m[1], m[2], m[3] = 3.4e38, -3.4e38, 3.25e38
+    v = m.abs()
+    case = Case(dev, [128], bits=8, state=False)
+    case.list.import_state(m=m, v=v)
+    for got, x, which in zip(case.moments(), (host(m), host(v)), "mv"):
+        want = ref.decode(*ref.encode(x, which), which, 128)
+        assert (got.view(np.uint32) == want.view(np.uint32)).all()
+        assert np.isinf(got[1]) and np.isfinite(got[0])
+
+
+@gpu
+def test_many_chunks_of_unaligned_tensors(dev):
+    """Whole windows of chunks, both with loads kept in the cache and without,
+    on tensors off every line boundary; export and import of the same."""
+    for n, w in ((1_500_007, BF16), (1_500_007, F32)):
+        case = Case(dev, [n, 3, n], bits=8, w=w, g=BF16, gap=3, copy=BF16 if w == F32 else None,
+                    sigma=1e-3)
+        if case.c is not None:
+            case.list.import_state(w=torch.cat([x.float() for x in case.w]))
+        check_step(case, 7, 1e-3, 1.0)
+    case = Case(dev, [n, 3, n], bits=32, w=BF16, g=BF16, gap=5, sigma=1e-3)
+    check_step(case, 7, 1e-3, 1.0)
+
+
+@gpu
 def test_import_and_export_of_32_bits(dev):
     case = Case(dev, SIZES, w=BF16, bits=32, state=False)
     m, v, w = (torch.randn(case.n + 1, device=dev)[1:] for _ in range(3))
