@@ -52,6 +52,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <cstring>
 #include <new>
 #include <type_traits>
 #include <vector>
@@ -1092,11 +1093,29 @@ bool aligned(const void *p, int align) {
     return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(align - 1)) == 0;
 }
 
-// A pointer of the list: aligned to its element and inside one allocation of
-// the current device.
-int check_array(const void *p, int64_t bytes, int align) {
-    return aligned(p, align) ? rcs_check_device_range(p, bytes) : RCS_EINVAL;
-}
+// Checks pointers of one call: aligned to their element and, as for the other
+// entry points, inside one allocation of the current device. The allocations
+// seen are remembered for the call: a list's arrays mostly lie in few of them,
+// and each question to the runtime costs more than the rest of the check.
+class Arrays {
+public:
+    int check(const void *p, int64_t bytes, int align) {
+        if (!aligned(p, align)) return RCS_EINVAL;
+        const char *q = static_cast<const char *>(p);
+        for (const Span &s : seen_)
+            if (s.lo <= q && q < s.hi) return bytes <= s.hi - q ? RCS_OK : RCS_ESIZE;
+        Span s{nullptr, nullptr};
+        const int rc = rcs_device_allocation(p, &s.lo, &s.hi);
+        if (rc != RCS_OK || s.lo == nullptr) return rc;
+        seen_[next_++ % kSeen] = s;
+        return bytes <= s.hi - q ? RCS_OK : RCS_ESIZE;
+    }
+
+private:
+    static constexpr unsigned kSeen = 16;
+    Span seen_[kSeen] = {};
+    unsigned next_ = 0;
+};
 
 int check_list(const rcs_list *list) {
     if (list == nullptr) return RCS_EINVAL;
@@ -1149,11 +1168,11 @@ auto *update_kernel(const Group &g) {
     return kernel;
 }
 
-int check_flat(const rcs_list *l, const void *p, int type, bool writes) {
+int check_flat(Arrays &arrays, const rcs_list *l, const void *p, int type, bool writes) {
     if (p == nullptr) return RCS_OK;
     if (type != RCS_F32 && type != RCS_BF16) return RCS_EINVAL;
     const int64_t bytes = l->n * type_bytes(type);
-    const int rc = check_array(p, bytes, type_bytes(type));
+    const int rc = arrays.check(p, bytes, type_bytes(type));
     if (rc != RCS_OK) return rc;
     if (l->touches(p, bytes)) return RCS_EINVAL;
     if (writes)  // an exported array is not a gradient either
@@ -1210,6 +1229,7 @@ int rcs_list_create(const rcs_list_tensor *tensors, int64_t count, int state_bit
             rcs_list *l;
             ~Drop() { delete l; }
         } drop{l};
+        Arrays arrays;
         l->bits = state_bits;
         l->n = total;
         l->nchunks = nchunks;
@@ -1233,12 +1253,12 @@ int rcs_list_create(const rcs_list_tensor *tensors, int64_t count, int state_bit
             const int64_t blocks = (t.n + kBlock - 1) / kBlock;
             const int64_t sb = state_bits == 32 ? 4 * t.n : blocks * kBlock;
             const int sa = state_bits == 32 ? 4 : 16;
-            if ((rc = check_array(t.w, wb * t.n, wb)) != RCS_OK) return rc;
-            if ((rc = check_array(t.m, sb, sa)) != RCS_OK) return rc;
-            if ((rc = check_array(t.v, sb, sa)) != RCS_OK) return rc;
-            if (t.g != nullptr && (rc = check_array(t.g, gb * t.n, gb)) != RCS_OK) return rc;
-            if (t.copy != nullptr && (rc = check_array(t.copy, 2 * t.n, 2)) != RCS_OK) return rc;
-            if (state_bits == 8 && (rc = check_array(t.exps, 2 * blocks, 2)) != RCS_OK) return rc;
+            if ((rc = arrays.check(t.w, wb * t.n, wb)) != RCS_OK) return rc;
+            if ((rc = arrays.check(t.m, sb, sa)) != RCS_OK) return rc;
+            if ((rc = arrays.check(t.v, sb, sa)) != RCS_OK) return rc;
+            if (t.g != nullptr && (rc = arrays.check(t.g, gb * t.n, gb)) != RCS_OK) return rc;
+            if (t.copy != nullptr && (rc = arrays.check(t.copy, 2 * t.n, 2)) != RCS_OK) return rc;
+            if (state_bits == 8 && (rc = arrays.check(t.exps, 2 * blocks, 2)) != RCS_OK) return rc;
             auto add = [&](const void *p, int64_t bytes) {
                 const char *c = static_cast<const char *>(p);
                 l->written.push_back(Span{c, c + bytes});
@@ -1281,6 +1301,9 @@ int rcs_list_create(const rcs_list_tensor *tensors, int64_t count, int state_bit
 
         const size_t rows_b = (l->rows.size() * sizeof(Row) + 255) / 256 * 256;
         const size_t chunks_b = (chunks.size() * sizeof(Chunk) + 255) / 256 * 256;
+        std::vector<char> tables(rows_b + chunks_b);
+        std::memcpy(tables.data(), l->rows.data(), l->rows.size() * sizeof(Row));
+        std::memcpy(tables.data() + rows_b, chunks.data(), chunks.size() * sizeof(Chunk));
         const size_t norm_b = (size_t)kNormMaxBlocks * sizeof(double) + 256;
         void *p = nullptr;
         if (hipMalloc(&p, rows_b + chunks_b + 2 * norm_b) != hipSuccess) {
@@ -1295,10 +1318,8 @@ int rcs_list_create(const rcs_list_tensor *tensors, int64_t count, int state_bit
             l->partials[k] = reinterpret_cast<double *>(q);
             l->record[k] = reinterpret_cast<ClipScalars *>(q + kNormMaxBlocks * sizeof(double));
         }
-        if (hipMemcpy(l->d_rows, l->rows.data(), l->rows.size() * sizeof(Row),
-                      hipMemcpyHostToDevice) != hipSuccess ||
-            hipMemcpy(l->d_chunks, chunks.data(), chunks.size() * sizeof(Chunk),
-                      hipMemcpyHostToDevice) != hipSuccess ||
+        if (hipMemcpy(l->mem, tables.data(), tables.size(), hipMemcpyHostToDevice) !=
+                hipSuccess ||
             hipStreamSynchronize(nullptr) != hipSuccess) {
             (void)hipGetLastError();
             (void)hipFree(p);
@@ -1330,13 +1351,14 @@ int64_t rcs_list_elements(const rcs_list *list) { return list == nullptr ? -1 : 
 
 int rcs_list_bind_grads(rcs_list *list, const void *const *g, int64_t count, hipStream_t stream) {
     int rc;
+    Arrays arrays;
     if (list == nullptr || g == nullptr || count != (int64_t)list->rows.size()) return RCS_EINVAL;
     if ((rc = check_list(list)) != RCS_OK) return rc;
     for (int64_t k = 0; k < count; ++k) {
         const Row &r = list->rows[(size_t)k];
         if (r.n == 0 || g[k] == nullptr) continue;
         const int b = type_bytes(r.gt());
-        if ((rc = check_array(g[k], b * r.n, b)) != RCS_OK) return rc;
+        if ((rc = arrays.check(g[k], b * r.n, b)) != RCS_OK) return rc;
         if (list->touches(g[k], b * r.n)) return RCS_EINVAL;
     }
     for (int64_t k = 0; k < count; k += kBind) {
@@ -1444,9 +1466,10 @@ int rcs_list_export(const rcs_list *list, void *w, int w_type, void *m, int m_ty
     int rc;
     if (list == nullptr || (w == nullptr && m == nullptr && v == nullptr)) return RCS_EINVAL;
     if ((rc = check_list(list)) != RCS_OK) return rc;
-    if ((rc = check_flat(list, w, w_type, true)) != RCS_OK) return rc;
-    if ((rc = check_flat(list, m, m_type, true)) != RCS_OK) return rc;
-    if ((rc = check_flat(list, v, v_type, true)) != RCS_OK) return rc;
+    Arrays arrays;
+    if ((rc = check_flat(arrays, list, w, w_type, true)) != RCS_OK) return rc;
+    if ((rc = check_flat(arrays, list, m, m_type, true)) != RCS_OK) return rc;
+    if ((rc = check_flat(arrays, list, v, v_type, true)) != RCS_OK) return rc;
     if (!apart(w, w_type, m, m_type, list->n) || !apart(w, w_type, v, v_type, list->n) ||
         !apart(m, m_type, v, v_type, list->n))
         return RCS_EINVAL;
@@ -1467,9 +1490,10 @@ int rcs_list_import(rcs_list *list, const void *w, int w_type, const void *m, in
     if (list == nullptr || (w == nullptr && m == nullptr && v == nullptr)) return RCS_EINVAL;
     if (list->bits == 8 && (m == nullptr) != (v == nullptr)) return RCS_EINVAL;
     if ((rc = check_list(list)) != RCS_OK) return rc;
-    if ((rc = check_flat(list, w, w_type, false)) != RCS_OK) return rc;
-    if ((rc = check_flat(list, m, m_type, false)) != RCS_OK) return rc;
-    if ((rc = check_flat(list, v, v_type, false)) != RCS_OK) return rc;
+    Arrays arrays;
+    if ((rc = check_flat(arrays, list, w, w_type, false)) != RCS_OK) return rc;
+    if ((rc = check_flat(arrays, list, m, m_type, false)) != RCS_OK) return rc;
+    if ((rc = check_flat(arrays, list, v, v_type, false)) != RCS_OK) return rc;
     const Flat f{const_cast<void *>(w), const_cast<void *>(m), const_cast<void *>(v), w_type,
                  m_type, v_type};
     const bool wide = (w == nullptr || w_type == RCS_BF16) && (m == nullptr || m_type == RCS_BF16);

@@ -1129,7 +1129,20 @@ int32_t get_le32(const unsigned char *p) {
 
 }  // namespace
 
-int rcs_check_device_range(const void *p, int64_t bytes) { return check_device_range(p, bytes); }
+int rcs_device_allocation(const void *p, const char **lo, const char **hi) {
+    *lo = *hi = nullptr;
+    const int rc = check_device_range(p, 0);
+    if (rc != RCS_OK) return rc;
+    hipDeviceptr_t base = nullptr;
+    size_t size = 0;
+    if (hipMemGetAddressRange(&base, &size, const_cast<void *>(p)) == hipSuccess && base) {
+        *lo = static_cast<const char *>(base);
+        *hi = *lo + size;
+    } else {
+        (void)hipGetLastError();
+    }
+    return RCS_OK;
+}
 
 int rcs_check_norm_out(const double *p, int dev) { return check_norm_out(p, dev); }
 

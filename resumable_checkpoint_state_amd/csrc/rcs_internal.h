@@ -12,8 +12,11 @@
 // (call before freeing the buffer; no copy out of it may still be pending).
 void rcs_snapshot_forget(int dev, const void *snapshot);
 
-// The device-array and norm-destination checks of the C ABI (a status code).
-int rcs_check_device_range(const void *p, int64_t bytes);
+// The C ABI's check that p is memory of the current device, and the bounds of
+// the allocation it lies in (both null where the runtime reports none).
+int rcs_device_allocation(const void *p, const char **lo, const char **hi);
+
+// The check of a norm destination (a status code).
 int rcs_check_norm_out(const double *p, int dev);
 
 // The (current device, stream) workspace of the norm kernels: the partial
