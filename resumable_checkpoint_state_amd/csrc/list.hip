@@ -151,9 +151,9 @@ struct ListScalars {
     float lr, bc1, bc2, b1, c1, b2, c2, eps, gscale;
     float da, db;   // for the free evaluation of the weight: weight_free
     uint32_t key;   // of the update's random bits
-    // 0 for a beta of 0, which forgets the 8-bit moment, an infinite one too (0
-    // times that would be a NaN; with this no moment is ever one); else all ones
-    uint32_t keep_m, keep_v;
+    // of decode_moments; 0 for a beta of 0, which forgets the 8-bit moment, an
+    // infinite one too (0 times that would be a NaN; so no moment is ever one)
+    uint32_t mask_m, mask_v;
     int32_t fits;  // the update's arrays fit the last-level cache
 };
 
@@ -434,18 +434,16 @@ __device__ __forceinline__ int block_exponent(uint32_t half, int low) {
     return e < low ? low : e > 255 ? 255 : e;
 }
 
-// V codes of one byte.
+// V codes of one byte. The arithmetic takes codes j and j + 2 of a word
+// together, j = 0 or 1: a mask puts them into 16 bits each.
 template <int V>
 struct Codes {
     uint32_t d[V / 4];
-    // codes 2 j and 2 j + 1, each in 16 bits
-    __device__ __forceinline__ u16x2 pair(int j) const {
-        return halves(__builtin_amdgcn_perm(0u, d[j / 2], j & 1 ? 0x0C030C02u : 0x0C010C00u));
-    }
-    __device__ __forceinline__ void four(int j, u16x2 k01, u16x2 k23) {
-        d[j] = __builtin_amdgcn_perm(word(k23), word(k01), 0x06040200u);
-    }
 };
+template <int V>
+__device__ __forceinline__ constexpr int first_of_pair(int p) {  // of the V / 2 pairs
+    return 4 * (p / 2) + (p & 1);
+}
 
 template <int V>
 __device__ __forceinline__ Codes<V> load_codes(const void *p, int64_t first, uint32_t at) {
@@ -478,25 +476,30 @@ __device__ __forceinline__ Global<uint16_t> exponents_at(const Row &t, int64_t f
 }
 
 // A float's upper half is 16 (k + B), plus the sign for m, and 0 for k = 0; its
-// lower half is zero.
+// lower half is zero. mask_m, mask_v: kMaskM and kMaskV, or 0 to take all codes
+// as 0.
+constexpr uint32_t kMaskM = 0x07F007F0u, kMaskV = 0x0FF00FF0u;  // 16 k of two codes
 template <int V>
 __device__ __forceinline__ void decode_moments(const Codes<V> &cm, const Codes<V> &cv, uint32_t e,
-                                               float (&m)[V], float (&v)[V]) {
+                                               uint32_t mask_m, uint32_t mask_v, float (&m)[V],
+                                               float (&v)[V]) {
     const uint32_t bm = 16u * (uint32_t)base_m((int)(e & 0xFFu));
     const u16x2 bv = both(16u * (uint32_t)base_v((int)(e >> 8)));
-    const uint32_t bm2 = bm | (bm << 16);
+    const uint32_t bm2 = (bm | (bm << 16)) & 0x7FFF7FFFu;
     const u16x2 one = halves(hidden_one(0x00010001u));
 #pragma unroll
-    for (int j = 0; j < V / 2; ++j) {
-        const u16x2 c = cm.pair(j), k = halves(word(c) & 0x007F007Fu);
-        const u16x2 signed_base = halves(((word(c) << 8) & 0x80008000u) | (bm2 & 0x7FFF7FFFu));
-        const uint32_t x = word(k * both(16) + __builtin_elementwise_min(k, one) * signed_base);
-        m[2 * j] = __uint_as_float(x << 16);
-        m[2 * j + 1] = __uint_as_float(x & 0xFFFF0000u);
-        const u16x2 l = cv.pair(j);
-        const uint32_t y = word(l * both(16) + __builtin_elementwise_min(l, one) * bv);
-        v[2 * j] = __uint_as_float(y << 16);
-        v[2 * j + 1] = __uint_as_float(y & 0xFFFF0000u);
+    for (int p = 0; p < V / 2; ++p) {
+        const int i = first_of_pair<V>(p);
+        const uint32_t c = cm.d[p / 2], l = cv.d[p / 2];
+        const u16x2 k = halves((p & 1 ? c >> 4 : c << 4) & mask_m);
+        const u16x2 signed_base = halves(((p & 1 ? c : c << 8) & 0x80008000u) | bm2);
+        const uint32_t x = word(k + __builtin_elementwise_min(k, one) * signed_base);
+        m[i] = __uint_as_float(x << 16);
+        m[i + 2] = __uint_as_float(x & 0xFFFF0000u);
+        const u16x2 n = halves((p & 1 ? l >> 4 : l << 4) & mask_v);
+        const uint32_t y = word(n + __builtin_elementwise_min(n, one) * bv);
+        v[i] = __uint_as_float(y << 16);
+        v[i + 2] = __uint_as_float(y & 0xFFFF0000u);
     }
 }
 
@@ -519,12 +522,13 @@ __device__ __forceinline__ void store_moments(const Row &t, int64_t first, uint3
     u16x2 ym[V / 2], big = both(0);
     uint32_t av = 0;
 #pragma unroll
-    for (int j = 0; j < V / 2; ++j) {
-        const uint32_t y0 = __float_as_uint(m[2 * j]) + 0x7FFFFFu;
-        const uint32_t y1 = __float_as_uint(m[2 * j + 1]) + 0x7FFFFFu;
-        ym[j] = halves(word(upper(y0, y1)) & 0x7FFF7FFFu);
-        big = __builtin_elementwise_max(big, ym[j]);
-        const uint32_t u0 = __float_as_uint(v[2 * j]), u1 = __float_as_uint(v[2 * j + 1]);
+    for (int p = 0; p < V / 2; ++p) {
+        const int i = first_of_pair<V>(p);
+        const uint32_t y0 = __float_as_uint(m[i]) + 0x7FFFFFu;
+        const uint32_t y1 = __float_as_uint(m[i + 2]) + 0x7FFFFFu;
+        ym[p] = halves(word(upper(y0, y1)) & 0x7FFF7FFFu);
+        big = __builtin_elementwise_max(big, ym[p]);
+        const uint32_t u0 = __float_as_uint(v[i]), u1 = __float_as_uint(v[i + 2]);
         av = av > u0 ? av : u0;
         av = av > u1 ? av : u1;
     }
@@ -534,25 +538,27 @@ __device__ __forceinline__ void store_moments(const Row &t, int64_t first, uint3
     const int ev = block_exponent((block_max<V>(av) + 0x7FFFFFu) >> 16, kLowV);
     const u16x2 bm = both((uint32_t)base_m(em)), bv = both((uint32_t)base_v(ev));
     const u16x2 least = both(16u * (uint32_t)(base_m(em) + 1));
-    u16x2 km[V / 2], kv[V / 2];
-#pragma unroll
-    for (int j = 0; j < V / 2; ++j) {
-        const uint32_t u0 = __float_as_uint(m[2 * j]), u1 = __float_as_uint(m[2 * j + 1]);
-        const u16x2 x = upper(u0 + add_m(2 * j), u1 + add_m(2 * j + 1));
-        u16x2 y = __builtin_elementwise_max(halves(word(x) & 0x7FFF7FFFu),
-                                            __builtin_elementwise_min(ym[j], least));
-        y = __builtin_elementwise_sub_sat(y >> both(4), bm);  // (infinity comes to the top code)
-        km[j] = halves(((word(x) >> 8) & 0x00800080u) | word(y));
-        const uint32_t s0 = __float_as_uint(v[2 * j]), s1 = __float_as_uint(v[2 * j + 1]);
-        const u16x2 z = upper(s0 + add_v(2 * j), s1 + add_v(2 * j + 1));
-        const u16x2 some = halves((s0 < one ? s0 : one) | ((s1 < one ? s1 : one) << 16));
-        kv[j] = __builtin_elementwise_max(__builtin_elementwise_sub_sat(z >> both(4), bv), some);
-    }
     Codes<V> cm, cv;
 #pragma unroll
-    for (int j = 0; j < V / 4; ++j) {
-        cm.four(j, km[2 * j], km[2 * j + 1]);
-        cv.four(j, kv[2 * j], kv[2 * j + 1]);
+    for (int p = 0; p < V / 2; ++p) {
+        const int i = first_of_pair<V>(p);
+        const uint32_t u0 = __float_as_uint(m[i]), u1 = __float_as_uint(m[i + 2]);
+        const u16x2 x = upper(u0 + add_m(i), u1 + add_m(i + 2));
+        u16x2 y = __builtin_elementwise_max(halves(word(x) & 0x7FFF7FFFu),
+                                            __builtin_elementwise_min(ym[p], least));
+        y = __builtin_elementwise_sub_sat(y >> both(4), bm);  // (infinity comes to the top code)
+        const uint32_t s0 = __float_as_uint(v[i]), s1 = __float_as_uint(v[i + 2]);
+        const u16x2 z = upper(s0 + add_v(i), s1 + add_v(i + 2));
+        const u16x2 some = halves((s0 < one ? s0 : one) | ((s1 < one ? s1 : one) << 16));
+        const u16x2 k =
+            __builtin_elementwise_max(__builtin_elementwise_sub_sat(z >> both(4), bv), some);
+        if (p & 1) {
+            cm.d[p / 2] |= (word(y) << 8) | (word(x) & 0x80008000u);
+            cv.d[p / 2] |= word(k) << 8;
+        } else {
+            cm.d[p / 2] = ((word(x) >> 8) & 0x00800080u) | word(y);
+            cv.d[p / 2] = word(k);
+        }
     }
     if (!active) return;
     store_codes(t.m, first, at, cm);
@@ -792,12 +798,7 @@ __device__ __forceinline__ void update8(const Row &t, int64_t first, int64_t end
         float ww[V], gg[V], mm[V], vv[V];
         unpack(w[q], ww);
         unpack(g[q], gg);
-#pragma unroll
-        for (int k = 0; k < V / 4; ++k) {
-            cm[q].d[k] &= h.keep_m;
-            cv[q].d[k] &= h.keep_v;
-        }
-        decode_moments(cm[q], cv[q], e[q], mm, vv);
+        decode_moments(cm[q], cv[q], e[q], h.mask_m, h.mask_v, mm, vv);
         scale(gg, h);
 #pragma unroll
         for (int k = 0; k < V; ++k) {
@@ -915,7 +916,7 @@ __device__ __forceinline__ void export_group(const Row &t, int64_t first, int64_
     if (f.m != nullptr || f.v != nullptr) {
         if constexpr (Q8) {
             decode_moments(load_codes<V>(t.m, first, at), load_codes<V>(t.v, first, at),
-                           *exponents_at(t, first, at), m, v);
+                           *exponents_at(t, first, at), kMaskM, kMaskV, m, v);
         } else {
             if (f.m != nullptr) unpack(load<F32, V, FULL>(t.m, first, at, cnt), m);
             if (f.v != nullptr) unpack(load<F32, V, FULL>(t.v, first, at, cnt), v);
@@ -1421,8 +1422,8 @@ int adamw_clip_step_list(rcs_list *list, int32_t t, float lr, float clip, float 
     h.eps = eps;
     h.gscale = grad_scale;
     h.fits = list->bytes <= kCacheBytes;
-    h.keep_m = h.b1 == 0.0f ? 0u : ~0u;
-    h.keep_v = h.b2 == 0.0f ? 0u : ~0u;
+    h.mask_m = h.b1 == 0.0f ? 0u : kMaskM;
+    h.mask_v = h.b2 == 0.0f ? 0u : kMaskV;
     // weight_free's constants; a learning rate of zero, or whose inverse
     // overflows, divides by infinity
     const double over = (1.0 - std::pow(beta1, (double)t)) / (double)lr;
