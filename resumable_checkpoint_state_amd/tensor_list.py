@@ -14,6 +14,7 @@ from . import _check, _norm_out, _stream, lib
 
 BLOCK = 128  # elements that share a block exponent (RCS_LIST_BLOCK)
 _TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_FLAT_TYPES = (torch.float32, torch.bfloat16)
 
 
 class _Tensor(ctypes.Structure):
@@ -23,8 +24,7 @@ class _Tensor(ctypes.Structure):
                 ("g_type", ctypes.c_int32), ("copy_type", ctypes.c_int32)]
 
 
-def _checked(t, name: str, dev: int, types=_TYPES) -> torch.Tensor:
-    """A detached alias of t (it keeps the memory alive, whatever becomes of t)."""
+def _check_tensor(t, name: str, dev: int, types) -> None:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) tensor")
     if t.dtype not in types or not t.is_contiguous():
@@ -33,6 +33,11 @@ def _checked(t, name: str, dev: int, types=_TYPES) -> torch.Tensor:
     if t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}; the library works on the current device "
                          f"(cuda:{dev}): use torch.cuda.device(...)")
+
+
+def _checked(t, name: str, dev: int, types=_TYPES) -> torch.Tensor:
+    """A detached alias of t (it keeps the memory alive, whatever becomes of t)."""
+    _check_tensor(t, name, dev, types)
     return t.detach()
 
 
@@ -177,27 +182,32 @@ class AdamWList:
                                            _stream(stream)), "grad_global_norm_list")
         return out
 
-    def _flat(self, x, name: str):
-        if x is None:
-            return None, 0
-        x = _checked(x, name, torch.cuda.current_device(), (torch.float32, torch.bfloat16))
-        if x.numel() != self.n:
-            raise ValueError(f"{name} has {x.numel()} elements, expected {self.n}")
-        return x.data_ptr(), _TYPES[x.dtype]
+    def _flat(self, w, m, v) -> list:
+        """Pointer and type of each of three flat arrays (or None)."""
+        dev, out = torch.cuda.current_device(), []
+        for name, x in (("w", w), ("m", m), ("v", v)):
+            if x is None:
+                out += (None, 0)
+                continue
+            _check_tensor(x, name, dev, _FLAT_TYPES)
+            if x.numel() != self.n:
+                raise ValueError(f"{name} has {x.numel()} elements, expected {self.n}")
+            out += (x.data_ptr(), _TYPES[x.dtype])
+        return out
 
     def export_state(self, w=None, m=None, v=None, stream=None) -> None:
         """Writes the weights and moments, in list order, to flat float32 or
         bfloat16 tensors of n elements (None: left out). What 8 bits hold is
         exact in either type."""
-        args = (*self._flat(w, "w"), *self._flat(m, "m"), *self._flat(v, "v"))
-        _check(lib().rcs_list_export(self.handle, *args, _stream(stream)), "rcs_list_export")
+        _check(lib().rcs_list_export(self.handle, *self._flat(w, m, v), _stream(stream)),
+               "rcs_list_export")
 
     def import_state(self, w=None, m=None, v=None, stream=None) -> None:
         """Reads them back: weights rounded to their types (copies written
         too), 8-bit moments to the nearest value they can hold (m and v then
         come together)."""
-        args = (*self._flat(w, "w"), *self._flat(m, "m"), *self._flat(v, "v"))
-        _check(lib().rcs_list_import(self.handle, *args, _stream(stream)), "rcs_list_import")
+        _check(lib().rcs_list_import(self.handle, *self._flat(w, m, v), _stream(stream)),
+               "rcs_list_import")
 
     def payload_buffer(self) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
         """Flat float32 w, m and v, one allocation made at the first call: the
