@@ -1,4 +1,4 @@
-"""Builds librcs.so in-tree from csrc/ with hipcc for gfx950."""
+"""Builds librcs.so in-tree from csrc/rcs.hip with hipcc for gfx950."""
 from __future__ import annotations
 
 import os
@@ -7,7 +7,6 @@ import subprocess
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SRC = os.path.join(PKG, "csrc", "rcs.hip")
-SRC_LIST = os.path.join(PKG, "csrc", "list.hip")
 SRC_IO = os.path.join(PKG, "csrc", "ckpt_io.cpp")
 SRC_WRITER = os.path.join(PKG, "csrc", "ckpt_writer.cpp")
 LIB = os.path.join(PKG, "librcs.so")
@@ -50,7 +49,7 @@ def hipcc_shared(sources: list[str], out: str, extra_flags: list[str] | None = N
 
 
 def build(extra_flags: list[str] | None = None, out: str | None = None) -> str:
-    return hipcc_shared([SRC, SRC_LIST, SRC_IO, SRC_WRITER], out or LIB, extra_flags)
+    return hipcc_shared([SRC, SRC_IO, SRC_WRITER], out or LIB, extra_flags)
 
 
 def build_ceilings() -> str:

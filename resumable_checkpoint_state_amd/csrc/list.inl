@@ -1,6 +1,7 @@
-// list.hip -- the clipped AdamW update over a list of tensors: weights and
+// list.inl -- the clipped AdamW update over a list of tensors: weights and
 // gradients of 32 or 16 bits, moments in 32 or in 8 bits, and the list's state
-// as the flat arrays of a step file. gfx950 kernels and their C ABI.
+// as the flat arrays of a step file. gfx950 kernels and their C ABI; the last
+// part of rcs.hip, whose final reduction, workspaces and checks it uses.
 //
 // Mathematics. For tensor k of the list, element i, with every float32
 // operation rounded on its own:
@@ -46,22 +47,9 @@
 // kernel and a launch of its own. Bound by HBM, beside 8-bit moments of 16-bit
 // weights nearly as much by the vector instructions.
 
-#include <hip/hip_runtime.h>
-
 #include <algorithm>
-#include <atomic>
-#include <cmath>
-#include <cstdint>
-#include <cstring>
 #include <new>
 #include <type_traits>
-#include <vector>
-
-#include "rcs.h"
-#include "rcs_device.h"
-#include "rcs_internal.h"
-
-#pragma clang fp contract(off)
 
 namespace {
 
@@ -1105,11 +1093,17 @@ public:
         const char *q = static_cast<const char *>(p);
         for (const Span &s : seen_)
             if (s.lo <= q && q < s.hi) return bytes <= s.hi - q ? RCS_OK : RCS_ESIZE;
-        Span s{nullptr, nullptr};
-        const int rc = rcs_device_allocation(p, &s.lo, &s.hi);
-        if (rc != RCS_OK || s.lo == nullptr) return rc;
-        seen_[next_++ % kSeen] = s;
-        return bytes <= s.hi - q ? RCS_OK : RCS_ESIZE;
+        const int rc = check_device_range(p, bytes);
+        if (rc != RCS_OK) return rc;
+        hipDeviceptr_t base = nullptr;
+        size_t size = 0;
+        if (hipMemGetAddressRange(&base, &size, const_cast<void *>(p)) == hipSuccess && base) {
+            const char *lo = static_cast<const char *>(base);
+            seen_[next_++ % kSeen] = Span{lo, lo + size};
+        } else {
+            (void)hipGetLastError();
+        }
+        return RCS_OK;
     }
 
 private:
@@ -1378,14 +1372,14 @@ int grad_global_norm_list(const rcs_list *list, float grad_scale, double *norm_o
     if (list == nullptr || norm_out == nullptr) return RCS_EINVAL;
     if (!std::isfinite(grad_scale) || !(grad_scale > 0.0f)) return RCS_EINVAL;
     if ((rc = check_list(list)) != RCS_OK) return rc;
-    if ((rc = rcs_check_norm_out(norm_out, list->dev)) != RCS_OK) return rc;
+    if ((rc = check_norm_out(norm_out, list->dev)) != RCS_OK) return rc;
     double *partials = list->partials[1];
     ClipScalars *record = list->record[1];
-    std::atomic<bool> *has_norm = nullptr;
+    Workspace *ws = nullptr;
     if (!capturing(stream)) {
-        void *r = nullptr;
-        if ((rc = rcs_norm_buffers(stream, &partials, &r, &has_norm)) != RCS_OK) return rc;
-        record = static_cast<ClipScalars *>(r);
+        if ((rc = get_workspace(stream, &ws)) != RCS_OK) return rc;
+        partials = ws->partials;
+        record = ws->scalars;
     }
     const bool direct = on_device(norm_out);
     launch_norm(list, grad_scale, partials, stream);
@@ -1393,7 +1387,7 @@ int grad_global_norm_list(const rcs_list *list, float grad_scale, double *norm_o
                        (const double *)partials, list->norm_blocks(), INFINITY, record,
                        direct ? norm_out : nullptr);
     if (hipGetLastError() != hipSuccess) return RCS_EHIP;
-    if (has_norm != nullptr) *has_norm = true;
+    if (ws != nullptr) ws->has_norm = true;
     if (!direct && hipMemcpyAsync(norm_out, &record->norm, sizeof(double), hipMemcpyDefault,
                                   stream) != hipSuccess)
         return RCS_EHIP;
@@ -1410,7 +1404,7 @@ int adamw_clip_step_list(rcs_list *list, int32_t t, float lr, float clip, float 
     if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0)) return RCS_EINVAL;
     if (!std::isnormal(eps) || !(eps > 0.0f)) return RCS_EINVAL;
     if ((rc = check_list(list)) != RCS_OK) return rc;
-    if (norm_out != nullptr && (rc = rcs_check_norm_out(norm_out, list->dev)) != RCS_OK) return rc;
+    if (norm_out != nullptr && (rc = check_norm_out(norm_out, list->dev)) != RCS_OK) return rc;
     ListScalars h;
     h.lr = lr;
     h.bc1 = (float)(1.0 - std::pow(beta1, (double)t));

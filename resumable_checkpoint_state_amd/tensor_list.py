@@ -1,7 +1,7 @@
 """The update over a list of tensors: a thin binding of the rcs_list calls.
 
 Argument marshalling only, as in the rest of the package: the norm, the update
-and the conversions run in the HIP kernels of csrc/list.hip.
+and the conversions run in the HIP kernels of csrc/list.inl.
 """
 from __future__ import annotations
 
