@@ -66,6 +66,12 @@ static_assert(kChunk % kBlock == 0 && kChunk % (8 * kWave) == 0, "whole blocks a
 constexpr int kListNormThreads = 1024;
 constexpr int kRun = 4;
 constexpr int kDeep = 4;
+// The norm's buffers: partial sums, record, and the count of blocks that have
+// left theirs. A stream's workspace has the same layout.
+constexpr size_t kNormRecordAt = (size_t)kNormMaxBlocks * sizeof(double);
+constexpr size_t kNormArrivedAt = kNormRecordAt + 128;
+constexpr size_t kNormBytes = kNormRecordAt + 256;
+static_assert(sizeof(ClipScalars) <= 128, "the record ends before the count");
 // Lowest block exponents (biased): the smallest value and, for m, half of it
 // are then normal floats.
 constexpr int kLowM = 18, kLowV = 33;
@@ -605,11 +611,24 @@ __device__ __forceinline__ double squares_of(const void *g, int64_t first, int64
 // of the grid take runs of kRun consecutive chunks in turn, and go through a run
 // one stretch of a tensor at a time; the order depends on the list's chunks
 // alone. The table entries of a run are fetched while the one before it is
-// summed.
+// summed. Bound by HBM; of 16-bit gradients, by the start and end of so short a
+// pass too: 124,356,864 float32 gradients 75.3 us = 6.6 TB/s, bfloat16 ones
+// 37.4 us = 6.6 TB/s out of the last-level cache, 47.1 us = 5.3 TB/s behind an
+// update that left other things there.
+//   The end (unless arrived is null: the update then reduces the partials): the
+// block that finds itself the last to leave its partial reduces them all, in
+// their order, whichever it is. A partial goes out as an exchange whose answer
+// is waited for: it then has been performed where the atomics of all XCDs meet,
+// before the block counts itself; the last block's loads, issued after its own
+// count came back, are device-scope ones that no cache answers. (With a plain
+// store and fences, which write back and drop whole caches, 54.5 us for 48.5 at
+// 124,356,864 bfloat16 gradients; a kernel of its own 50.1, and 6.5 for 4.8 at
+// 262,144.) The count wraps to zero by itself.
 template <bool Q8>
-__global__ __launch_bounds__(kListNormThreads) void list_norm_partial(
+__global__ __launch_bounds__(kListNormThreads) void list_norm(
     const Row *__restrict__ rows, const Chunk *__restrict__ chunks, int64_t nchunks,
-    int64_t keep_from, float gscale, double *__restrict__ partials) {
+    int64_t keep_from, float gscale, double *partials, uint32_t *arrived, float clip,
+    ClipScalars *__restrict__ record, double *__restrict__ norm_out) {
     __shared__ double lds[kListNormThreads / kWave];
     constexpr int kWaves = kListNormThreads / kWave;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
@@ -648,22 +667,37 @@ __global__ __launch_bounds__(kListNormThreads) void list_norm_partial(
         }
     }
     sum = block_sum<kListNormThreads>(sum, lds);
-    if (threadIdx.x == 0) partials[blockIdx.x] = sum;
-}
-
-__global__ __launch_bounds__(kUpdThreads) void list_norm_final(const double *__restrict__ partials,
-                                                               int nparts, float clip,
-                                                               ClipScalars *__restrict__ record,
-                                                               double *__restrict__ norm_out) {
-    __shared__ double lds[kUpdThreads / kWave];
+    if (arrived == nullptr) {
+        if (threadIdx.x == 0) partials[blockIdx.x] = sum;
+        return;
+    }
+    if (threadIdx.x >= kWave) return;
+    uint32_t before = 0;
+    if (threadIdx.x == 0) {
+        const unsigned long long old = __hip_atomic_exchange(
+            reinterpret_cast<unsigned long long *>(partials + blockIdx.x),
+            (unsigned long long)__double_as_longlong(sum), __ATOMIC_RELAXED,
+            __HIP_MEMORY_SCOPE_AGENT);
+        asm volatile("; the partial has arrived" ::"v"(old) : "memory");
+        before = atomicInc(arrived, gridDim.x - 1);
+    }
+    if ((uint32_t)__builtin_amdgcn_readfirstlane((int)before) != gridDim.x - 1) return;
     double x[kPartsPerLane];
-    load_partials(partials, nparts, x);
-    const ClipScalars r = final_reduce(x, nparts, clip, lds);
+#pragma unroll
+    for (int k = 0; k < kPartsPerLane; ++k) {
+        const int j = (int)threadIdx.x + k * kUpdThreads, last = (int)gridDim.x - 1;
+        x[k] = __hip_atomic_load(partials + (j < last ? j : last), __ATOMIC_RELAXED,
+                                 __HIP_MEMORY_SCOPE_AGENT);
+    }
+    const ClipScalars r = final_reduce(x, (int)gridDim.x, clip, nullptr);
     if (threadIdx.x == 0) {
         *record = r;
         if (norm_out != nullptr) *norm_out = r.norm;
     }
 }
+
+// Sets a workspace's count of arrived blocks to zero, once.
+__global__ void list_norm_init(uint32_t *arrived) { *arrived = 0; }
 
 // New moments of one element from its scaled gradient; the operations and their
 // roundings are part of the definition (8-bit moments are rounded from exactly
@@ -808,13 +842,18 @@ __device__ __forceinline__ void update8(const Row &t, int64_t first, int64_t end
     }
 }
 
-// The update, one wave per chunk. The clip record was written by
-// list_norm_final; it is read beside the table. FOLD: every wave does the final
-// reduction of the norm itself (as the flat update does at small n), behind its
-// loads, and the first one writes the record. W, G: the types of weights and
-// gradients; a list with several pairs of types has a launch for each (one
-// kernel that branched on them held 92 vector registers for every pair and
-// spilled scalar ones).
+// The update, one wave per chunk. The clip record was written by list_norm; it
+// is read beside the table. FOLD: every wave does the final reduction of the
+// norm itself (as the flat update does at small n), behind its loads, and the
+// first one writes the record. W, G: the types of weights and gradients; a list
+// with several pairs of types has a launch for each (one kernel that branched on
+// them held 92 vector registers for every pair and spilled scalar ones).
+//   At 124,356,864 elements, each pass once over its bytes: float32 weights and
+// gradients with 32-bit moments 527 us = 6.6 TB/s, bfloat16 ones 413 us =
+// 6.6 TB/s; with 8-bit moments, float32 weights, bfloat16 gradients and copies
+// 293 us = 6.8 TB/s, bfloat16 weights and gradients 195 us = 6.4 TB/s. Bound by
+// HBM; the last one, at 397 vector instructions a chunk (49.6 an element), by
+// them as well: 230 us in a run at a lower clock.
 template <class W, class G, bool Q8, bool FOLD>
 __global__ __launch_bounds__(kUpdThreads) void list_update(
     const Row *__restrict__ rows, const Chunk *__restrict__ chunks, uint32_t in_windows,
@@ -873,7 +912,11 @@ __global__ __launch_bounds__(kUpdThreads) void list_update(
 }
 
 // Flat arrays of the list's elements, in list order: w, m and v, each float32
-// or bfloat16, or null for one that is left out.
+// or bfloat16, or null for one that is left out. Bound by HBM: at 124,356,864
+// elements with bfloat16 weights and 8-bit moments, export to float32 takes
+// 328 us = 6.1 TB/s (three quarters of it written), of the moments alone to
+// bfloat16 119 us = 6.3 TB/s (8 elements a lane there, whole lines of it), import
+// from float32 313 us = 6.4 TB/s.
 struct Flat {
     void *w, *m, *v;
     int wt, mt, vt;
@@ -1050,8 +1093,7 @@ struct rcs_list {
     Chunk *d_chunks = nullptr;
     // norm buffers of the update, and of a norm call that is being captured
     // (an eager one uses its stream's)
-    double *partials[2] = {nullptr, nullptr};
-    ClipScalars *record[2] = {nullptr, nullptr};
+    NormBuffers norm[2];
 
     // Whether [p, p + bytes) shares a byte with what an update writes.
     bool touches(const void *p, int64_t bytes) const {
@@ -1069,7 +1111,10 @@ struct rcs_list {
 
 namespace {
 
-// The largest list whose update folds the final reduction of the norm.
+// The largest list whose update folds the final reduction of the norm; above it
+// the norm pass ends with it. us a step with and without: 7.4 and 8.4 at 262,144
+// float32 elements, 10.6 and 12.0 at 1M, 25.2 and 26.8 at 4M, 44.1 and 47.2 at
+// 8.4M; 8-bit moments at 8.0M 33.0 and 32.6.
 constexpr int64_t kListFoldMaxN = 8388608;
 // Bytes at the end of the gradients that the norm pass reads with cache-
 // allocating loads, so that the update finds them in the last-level cache.
@@ -1139,11 +1184,18 @@ bool capturing(hipStream_t stream) {
     return st != hipStreamCaptureStatusNone;
 }
 
-void launch_norm(const rcs_list *l, float gscale, double *partials, hipStream_t stream) {
-    auto *kernel = l->bits == 8 ? list_norm_partial<true> : list_norm_partial<false>;
+uint32_t *arrived(const NormBuffers &nb) {
+    return reinterpret_cast<uint32_t *>(reinterpret_cast<char *>(nb.partials) + kNormArrivedAt);
+}
+
+// fold: the update will reduce the partials itself.
+void launch_norm(const rcs_list *l, float gscale, const NormBuffers &nb, bool fold, float clip,
+                 double *dev_out, hipStream_t stream) {
+    auto *kernel = l->bits == 8 ? list_norm<true> : list_norm<false>;
     hipLaunchKernelGGL(kernel, dim3(l->norm_blocks()), dim3(kListNormThreads), 0,
                        stream, (const Row *)l->d_rows, (const Chunk *)l->d_chunks, l->nchunks,
-                       l->keep_from, gscale, partials);
+                       l->keep_from, gscale, nb.partials, fold ? nullptr : arrived(nb), clip,
+                       nb.scalars, dev_out);
 }
 
 uint32_t in_windows(int64_t blocks) { return (uint32_t)(blocks - blocks % kWindow); }
@@ -1296,12 +1348,11 @@ int rcs_list_create(const rcs_list_tensor *tensors, int64_t count, int state_bit
 
         const size_t rows_b = (l->rows.size() * sizeof(Row) + 255) / 256 * 256;
         const size_t chunks_b = (chunks.size() * sizeof(Chunk) + 255) / 256 * 256;
-        std::vector<char> tables(rows_b + chunks_b);
+        std::vector<char> tables(rows_b + chunks_b + 2 * kNormBytes);
         std::memcpy(tables.data(), l->rows.data(), l->rows.size() * sizeof(Row));
         std::memcpy(tables.data() + rows_b, chunks.data(), chunks.size() * sizeof(Chunk));
-        const size_t norm_b = (size_t)kNormMaxBlocks * sizeof(double) + 256;
         void *p = nullptr;
-        if (hipMalloc(&p, rows_b + chunks_b + 2 * norm_b) != hipSuccess) {
+        if (hipMalloc(&p, tables.size()) != hipSuccess) {
             (void)hipGetLastError();
             return RCS_ENOMEM;
         }
@@ -1309,9 +1360,9 @@ int rcs_list_create(const rcs_list_tensor *tensors, int64_t count, int state_bit
         l->d_rows = reinterpret_cast<Row *>(l->mem);
         l->d_chunks = reinterpret_cast<Chunk *>(l->mem + rows_b);
         for (int k = 0; k < 2; ++k) {
-            char *q = l->mem + rows_b + chunks_b + (size_t)k * norm_b;
-            l->partials[k] = reinterpret_cast<double *>(q);
-            l->record[k] = reinterpret_cast<ClipScalars *>(q + kNormMaxBlocks * sizeof(double));
+            char *q = l->mem + rows_b + chunks_b + (size_t)k * kNormBytes;
+            l->norm[k].partials = reinterpret_cast<double *>(q);
+            l->norm[k].scalars = reinterpret_cast<ClipScalars *>(q + kNormRecordAt);
         }
         if (hipMemcpy(l->mem, tables.data(), tables.size(), hipMemcpyHostToDevice) !=
                 hipSuccess ||
@@ -1373,22 +1424,23 @@ int grad_global_norm_list(const rcs_list *list, float grad_scale, double *norm_o
     if (!std::isfinite(grad_scale) || !(grad_scale > 0.0f)) return RCS_EINVAL;
     if ((rc = check_list(list)) != RCS_OK) return rc;
     if ((rc = check_norm_out(norm_out, list->dev)) != RCS_OK) return rc;
-    double *partials = list->partials[1];
-    ClipScalars *record = list->record[1];
+    NormBuffers nb = list->norm[1];
     Workspace *ws = nullptr;
     if (!capturing(stream)) {
         if ((rc = get_workspace(stream, &ws)) != RCS_OK) return rc;
-        partials = ws->partials;
-        record = ws->scalars;
+        nb = *ws;
+        std::lock_guard<std::mutex> lk(g_mu);
+        if (!ws->counts) {  // in stream order before the first pass that counts there
+            hipLaunchKernelGGL(list_norm_init, dim3(1), dim3(1), 0, stream, arrived(nb));
+            if (hipGetLastError() != hipSuccess) return RCS_EHIP;
+            ws->counts = true;
+        }
     }
     const bool direct = on_device(norm_out);
-    launch_norm(list, grad_scale, partials, stream);
-    hipLaunchKernelGGL(list_norm_final, dim3(1), dim3(kUpdThreads), 0, stream,
-                       (const double *)partials, list->norm_blocks(), INFINITY, record,
-                       direct ? norm_out : nullptr);
+    launch_norm(list, grad_scale, nb, false, INFINITY, direct ? norm_out : nullptr, stream);
     if (hipGetLastError() != hipSuccess) return RCS_EHIP;
     if (ws != nullptr) ws->has_norm = true;
-    if (!direct && hipMemcpyAsync(norm_out, &record->norm, sizeof(double), hipMemcpyDefault,
+    if (!direct && hipMemcpyAsync(norm_out, &nb.scalars->norm, sizeof(double), hipMemcpyDefault,
                                   stream) != hipSuccess)
         return RCS_EHIP;
     return RCS_OK;
@@ -1432,25 +1484,21 @@ int adamw_clip_step_list(rcs_list *list, int32_t t, float lr, float clip, float 
     h.key = mixed(mixed(seed * kHashA + (uint32_t)t * kHashB) + kHashK);
     const bool fold = list->n <= kListFoldMaxN, q8 = list->bits == 8;
     const bool direct = norm_out != nullptr && on_device(norm_out);
-    double *partials = list->partials[0], *dev_out = direct ? norm_out : nullptr;
-    ClipScalars *record = list->record[0];
-    const int nparts = list->norm_blocks();
-    launch_norm(list, grad_scale, partials, stream);
-    if (!fold)
-        hipLaunchKernelGGL(list_norm_final, dim3(1), dim3(kUpdThreads), 0, stream,
-                           (const double *)partials, nparts, clip, record, dev_out);
+    double *dev_out = direct ? norm_out : nullptr;
+    const NormBuffers &nb = list->norm[0];
+    launch_norm(list, grad_scale, nb, fold, clip, dev_out, stream);
     const bool near = q8 || list->n <= kNearMaxN;
     for (const Group &g : list->groups) {
         auto *kernel = q8 ? (fold ? update_kernel<true, true>(g) : update_kernel<true, false>(g))
                           : (fold ? update_kernel<false, true>(g) : update_kernel<false, false>(g));
         hipLaunchKernelGGL(kernel, dim3((unsigned)g.count), dim3(kUpdThreads), 0, stream,
                            (const Row *)list->d_rows, (const Chunk *)list->d_chunks + g.first,
-                           near ? in_windows(g.count) : 0u, nparts, (const double *)partials,
-                           clip, record, dev_out, h);
+                           near ? in_windows(g.count) : 0u, list->norm_blocks(),
+                           (const double *)nb.partials, clip, nb.scalars, dev_out, h);
     }
     if (hipGetLastError() != hipSuccess) return RCS_EHIP;
     if (norm_out != nullptr && !direct &&
-        hipMemcpyAsync(norm_out, &record->norm, sizeof(double), hipMemcpyDefault, stream) !=
+        hipMemcpyAsync(norm_out, &nb.scalars->norm, sizeof(double), hipMemcpyDefault, stream) !=
             hipSuccess)
         return RCS_EHIP;
     return RCS_OK;

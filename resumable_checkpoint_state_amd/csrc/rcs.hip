@@ -835,6 +835,7 @@ struct NormBuffers {
 
 struct Workspace : NormBuffers {
     std::atomic<bool> has_norm{false};
+    bool counts = false;  // list_norm's count is there (set under g_mu)
 };
 
 std::mutex g_mu;

@@ -669,6 +669,37 @@ def test_streams(dev):
 
 
 @gpu
+def test_norms_of_several_lists_in_turn_on_one_stream(dev):
+    """Norms of 1, 37 and 256 blocks and the flat norm take turns in one
+    workspace, steps and a graph between them."""
+    cases = [Case(dev, sizes, g=BF16, w=BF16) for sizes in ([7], [300_001, 9], [9_000_001])]
+    flat = torch.randn(100_003, device=dev)
+    want = [norm_of(c) for c in cases]
+    stream = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    held = torch.zeros(1, dtype=torch.float64, device=dev)
+    with torch.cuda.graph(graph):
+        cases[1].list.grad_norm(out=held)
+    outs = [torch.zeros(1, dtype=torch.float64, device=dev) for _ in range(4)]
+    first = None
+    with torch.cuda.stream(stream):
+        for k in range(25):
+            for c, o in zip(cases, outs):
+                o.zero_()
+                c.list.grad_norm(out=o)
+            rcs.grad_global_norm(flat, out=outs[3])
+            graph.replay()
+            cases[2].list.step(k + 1, 0.0, 1.0)  # its own count, on the same list
+            stream.synchronize()
+            now = [float(x.cpu()) for x in (*outs, held)]
+            first = first or now
+            assert now == first
+    for c, x, y in zip(cases, first, want):
+        assert abs(x - y) <= 2 * max(c.n, 16) * 2.0 ** -53 * y
+    assert first[4] == first[1]
+
+
+@gpu
 def test_determinism(dev):
     """The same list and inputs give the same bits, wherever the gradients lie."""
     a, b = Case(dev, [1_000_003, 17], bits=8), Case(dev, [1_000_003, 17], bits=8, gap=1)
