@@ -351,8 +351,9 @@ int rcs_ckpt_writer_destroy(rcs_ckpt_writer *writer);
 /*
  * The update over a list of tensors: what adamw_clip_step does to one flat
  * float32 vector, done to many tensors at once (one norm over all of them, one
- * clip factor, one launch for all updates), with weights and gradients in
- * float32, bfloat16 or float16 and the moments in 32 or in 8 bits. The pages'
+ * clip factor, one launch for the updates of all tensors whose weights and
+ * gradients have the same types), with weights and gradients in float32,
+ * bfloat16 or float16 and the moments in 32 or in 8 bits. The pages'
  * update is over a model's parameters ("Training as a Recoverable State
  * Transition", "The Exact Targets of Clipping and AdamW": g is the
  * concatenation of all gradients, the clip is global); the step file's arrays
@@ -412,7 +413,9 @@ int64_t rcs_list_elements(const rcs_list *list);
 /*
  * Binds other gradients of the same types and lengths, count pointers in list
  * order (NULL: no gradient), in stream order: later calls on the stream use
- * them.
+ * them. (A captured call binds at each replay; until then nothing has changed
+ * on the device. A captured step or norm uses what is bound when it is
+ * replayed.)
  */
 int rcs_list_bind_grads(rcs_list *list, const void *const *g, int64_t count, hipStream_t stream);
 
@@ -420,9 +423,9 @@ int rcs_list_bind_grads(rcs_list *list, const void *const *g, int64_t count, hip
  * The pre-clip global norm of the list's gradients,
  * sqrt(sum (double)(g * grad_scale)^2) with the product in float32, into
  * norm_out (device or pinned host memory). The order of the sum depends on the
- * list's lengths and, with 32-bit moments, on the addresses of m modulo 256,
- * so results are deterministic for a given list. last_grad_norm reports it too, unless the call was
- * captured.
+ * list's lengths and types and, with 32-bit moments, on the addresses of m
+ * modulo 256, so results are deterministic for a given list. last_grad_norm
+ * reports it too, unless the call was captured.
  */
 int grad_global_norm_list(const rcs_list *list, float grad_scale, double *norm_out,
                           hipStream_t stream);

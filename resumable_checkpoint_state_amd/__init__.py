@@ -406,11 +406,11 @@ class CkptWriter:
 class StepFileCheckpointer:
     """Step-file policy around a training loop: call after_step(t, w, m, v)
     after every completed update (or after_step(t, tensors), with an AdamWList
-    in the place of the three arrays, here and in save and resume). It writes <dir>/step_NNNNNN.bin when t is a
-    multiple of `every` (0 = never by cadence), when SIGUSR1 arrived (write and
-    continue) or when SIGTERM arrived (write, then after_step returns True:
-    the caller exits), keeps the newest `keep` files, and resume() loads the
-    newest valid one.
+    in the place of the three arrays, here and in save and resume). It writes
+    <dir>/step_NNNNNN.bin when t is a multiple of `every` (0 = never by
+    cadence), when SIGUSR1 arrived (write and continue) or when SIGTERM arrived
+    (write, then after_step returns True: the caller exits), keeps the newest
+    `keep` files, and resume() loads the newest valid one.
 
     async_write=True hands each save to the library's CkptWriter (a device
     snapshot on the training stream, the copy on its own stream, the atomic

@@ -150,7 +150,9 @@ class AdamWList:
 
     def bind_grads(self, grads: Sequence[torch.Tensor | None], stream=None) -> None:
         """Other gradients of the same shapes and types (None: the tensor has
-        none), from the stream's next call on."""
+        none), from the stream's next call on. The list lets go of those before:
+        keep them while work that uses them is under way on another stream
+        than their own, or a captured graph will bind them again."""
         h, grads = self.handle, list(grads)
         if len(grads) != len(self._params):
             raise ValueError(f"grads has {len(grads)} entries, expected {len(self._params)}")
