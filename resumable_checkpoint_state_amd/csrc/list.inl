@@ -612,8 +612,8 @@ __device__ __forceinline__ double squares_of(const void *g, int64_t first, int64
 // one stretch of a tensor at a time; the order depends on the list's chunks
 // alone. The table entries of a run are fetched while the one before it is
 // summed. Bound by HBM; of 16-bit gradients, by the start and end of so short a
-// pass too: 124,356,864 float32 gradients 75.3 us = 6.6 TB/s, bfloat16 ones
-// 37.4 us = 6.6 TB/s out of the last-level cache, 47.1 us = 5.3 TB/s behind an
+// pass too: 124,356,864 float32 gradients 80 us = 6.2 TB/s, bfloat16 ones 39 us =
+// 6.3 TB/s where the last-level cache holds them, 48 us = 5.2 TB/s behind an
 // update that left other things there.
 //   The end (unless arrived is null: the update then reduces the partials): the
 // block that finds itself the last to leave its partial reduces them all, in
@@ -849,9 +849,9 @@ __device__ __forceinline__ void update8(const Row &t, int64_t first, int64_t end
 // with several pairs of types has a launch for each (one kernel that branched on
 // them held 92 vector registers for every pair and spilled scalar ones).
 //   At 124,356,864 elements, each pass once over its bytes: float32 weights and
-// gradients with 32-bit moments 527 us = 6.6 TB/s, bfloat16 ones 413 us =
-// 6.6 TB/s; with 8-bit moments, float32 weights, bfloat16 gradients and copies
-// 293 us = 6.8 TB/s, bfloat16 weights and gradients 195 us = 6.4 TB/s. Bound by
+// gradients with 32-bit moments 527 us = 6.6 TB/s, bfloat16 ones 410 us =
+// 6.7 TB/s; with 8-bit moments, float32 weights, bfloat16 gradients and copies
+// 291 us = 6.9 TB/s, bfloat16 weights and gradients 197 us = 6.3 TB/s. Bound by
 // HBM; the last one, at 397 vector instructions a chunk (49.6 an element), by
 // them as well: 230 us in a run at a lower clock.
 template <class W, class G, bool Q8, bool FOLD>
@@ -915,8 +915,8 @@ __global__ __launch_bounds__(kUpdThreads) void list_update(
 // or bfloat16, or null for one that is left out. Bound by HBM: at 124,356,864
 // elements with bfloat16 weights and 8-bit moments, export to float32 takes
 // 328 us = 6.1 TB/s (three quarters of it written), of the moments alone to
-// bfloat16 119 us = 6.3 TB/s (8 elements a lane there, whole lines of it), import
-// from float32 313 us = 6.4 TB/s.
+// bfloat16 120 us = 6.3 TB/s (8 elements a lane there, whole lines of it), import
+// from float32 311 us = 6.4 TB/s.
 struct Flat {
     void *w, *m, *v;
     int wt, mt, vt;
