@@ -669,6 +669,34 @@ def test_streams(dev):
 
 
 @gpu
+def test_a_captured_binding_binds_at_each_replay(dev):
+    """And a captured step without one uses what is bound when it is replayed."""
+    case = Case(dev, [3001, 700], bits=8)
+    mine = case.g
+    twice, four = ([g * k for g in mine] for k in (2.0, 4.0))
+    norms = [torch.zeros(1, dtype=torch.float64, device=dev) for _ in range(2)]
+    binds, plain = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(binds):
+        case.list.bind_grads(twice)
+        case.list.step(1, 1e-3, 1.0, norm_out=norms[0])
+    with torch.cuda.graph(plain):
+        case.list.step(2, 1e-3, 1.0, norm_out=norms[1])
+    one = norm_of(case)
+    for _ in range(3):
+        for grads, factor in ((mine, 1), (four, 4)):
+            case.list.bind_grads(grads)
+            plain.replay()
+            torch.cuda.synchronize()
+            assert abs(float(norms[1].cpu()) - factor * one) <= 1e-11 * factor * one
+        binds.replay()
+        plain.replay()
+        torch.cuda.synchronize()
+        for x in norms:
+            assert abs(float(x.cpu()) - 2 * one) <= 1e-11 * 2 * one
+
+
+@gpu
 def test_norms_of_several_lists_in_turn_on_one_stream(dev):
     """Norms of 1, 37 and 256 blocks and the flat norm take turns in one
     workspace, steps and a graph between them."""
