@@ -730,11 +730,29 @@ __device__ __forceinline__ float weight(float w, float m, float v, float decay,
 // The weight beside 8-bit moments, where the arithmetic is what counts:
 //   w decay - lr (m / bc1) / (sqrt(v / bc2) + eps) = w decay - m / (da sqrt(v) + db)
 // with da = bc1 / (lr sqrt(bc2)), db = bc1 eps / lr; root and reciprocal are the
-// hardware's (1 ulp each; v below float32's normal range would only show next
-// to an eps of its size).
+// hardware's, 1 ulp each over the normal floats. The root of a subnormal v comes
+// out as zero: da sqrt(v) then lacks up to 2^-63 da of a denominator of at least
+// db = sqrt(bc2) eps da, which is for the caller to weigh (kWideEps).
 __device__ __forceinline__ float weight_free(float w, float m, float v, float decay,
                                              const ListScalars &h) {
     const float den = __builtin_fmaf(__builtin_amdgcn_sqrtf(v), h.da, h.db);
+    return __builtin_fmaf(-m, __builtin_amdgcn_rcpf(den), w * decay);
+}
+
+// Below this sqrt(bc2) eps, weight_wide takes the place of weight_free: from it
+// on what the root of a subnormal v lacks is at most 2^-27 of the denominator, an
+// eighth of a rounding. (us a step in either form: 218 and 223 at 124,356,864
+// bfloat16 elements, 19.5 and 20.6 at 8.0M; float32 weights 372 and 373, 25.8
+// and 26.0.)
+constexpr double kWideEps = 0x1p-36;
+
+// weight_free with the root right for every v: a small one is scaled by 2^64 and
+// its root by 2^-32, both exactly.
+__device__ __forceinline__ float weight_wide(float w, float m, float v, float decay,
+                                             const ListScalars &h) {
+    const bool small = v < 0x1p-64f;
+    const float root = __builtin_amdgcn_sqrtf(small ? v * 0x1p64f : v);
+    const float den = __builtin_fmaf(small ? root * 0x1p-32f : root, h.da, h.db);
     return __builtin_fmaf(-m, __builtin_amdgcn_rcpf(den), w * decay);
 }
 
@@ -787,8 +805,8 @@ __device__ __forceinline__ void update32(const Row &t, int64_t first, int64_t en
 
 // The same with 8-bit moments. The code arrays are filled up to whole blocks,
 // so a code access is always a whole vector; a block past the tensor's end is
-// not touched.
-template <class W, class G, int V, int R, bool FULL, bool KEEP, class Factor>
+// not touched. WIDE: the weight's form.
+template <class W, class G, int V, int R, bool FULL, bool KEEP, bool WIDE, class Factor>
 __device__ __forceinline__ void update8(const Row &t, int64_t first, int64_t end,
                                         Factor clip_factor, const ListScalars &h) {
     const int64_t left = end - first;
@@ -825,7 +843,8 @@ __device__ __forceinline__ void update8(const Row &t, int64_t first, int64_t end
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             moments(gg[k], mm[k], vv[k], s, h);
-            ww[k] = weight_free(ww[k], mm[k], vv[k], decay, h);
+            ww[k] = WIDE ? weight_wide(ww[k], mm[k], vv[k], decay, h)
+                         : weight_free(ww[k], mm[k], vv[k], decay, h);
             if (!FULL && k >= cnt[q]) mm[k] = vv[k] = 0.0f;
         }
         store<FULL>(t.w, first, at[q], cnt[q], pack<W>(ww));
@@ -847,14 +866,17 @@ __device__ __forceinline__ void update8(const Row &t, int64_t first, int64_t end
 // norm itself (as the flat update does at small n), behind its loads, and the
 // first one writes the record. W, G: the types of weights and gradients; a list
 // with several pairs of types has a launch for each (one kernel that branched on
-// them held 92 vector registers for every pair and spilled scalar ones).
+// them held 92 vector registers for every pair and spilled scalar ones). WIDE:
+// the weight beside 8-bit moments in weight_wide's form, kernels of their own
+// too (a branch in update8 that left the compiler one order of instructions for
+// both forms: 24.8 and 25.3 us at 8.0M float32 elements).
 //   At 124,356,864 elements, each pass once over its bytes: float32 weights and
 // gradients with 32-bit moments 527 us = 6.6 TB/s, bfloat16 ones 410 us =
 // 6.7 TB/s; with 8-bit moments, float32 weights, bfloat16 gradients and copies
 // 291 us = 6.9 TB/s, bfloat16 weights and gradients 197 us = 6.3 TB/s. Bound by
 // HBM; the last one, at 397 vector instructions a chunk (49.6 an element), by
 // them as well: 230 us in a run at a lower clock.
-template <class W, class G, bool Q8, bool FOLD>
+template <class W, class G, bool Q8, bool FOLD, bool WIDE = false>
 __global__ __launch_bounds__(kUpdThreads) void list_update(
     const Row *__restrict__ rows, const Chunk *__restrict__ chunks, uint32_t in_windows,
     int nparts, const double *__restrict__ partials, float clip, ClipScalars *__restrict__ record,
@@ -892,7 +914,7 @@ __global__ __launch_bounds__(kUpdThreads) void list_update(
     if (r.whole) {
         if constexpr (Q8)
             by_lines(h.fits != 0 && off_line(t.w, 0), [&](auto K) {
-                update8<W, G, V, R, true, K.value>(t, r.first, r.end, factor, h);
+                update8<W, G, V, R, true, K.value, WIDE>(t, r.first, r.end, factor, h);
             });
         else
             update32<W, G, V, R, true>(t, r.first, r.end, factor, h);
@@ -906,7 +928,7 @@ __global__ __launch_bounds__(kUpdThreads) void list_update(
     };
 #pragma unroll 1
     for (int64_t at = r.first; at < r.end; at += kWave * V) {
-        if constexpr (Q8) update8<W, G, V, 1, false, true>(t, at, r.end, same, h);
+        if constexpr (Q8) update8<W, G, V, 1, false, true, WIDE>(t, at, r.end, same, h);
         else update32<W, G, V, 1, false>(t, at, r.end, same, h);
     }
 }
@@ -1200,14 +1222,14 @@ void launch_norm(const rcs_list *l, float gscale, const NormBuffers &nb, bool fo
 
 uint32_t in_windows(int64_t blocks) { return (uint32_t)(blocks - blocks % kWindow); }
 
-template <bool Q8, bool FOLD>
+template <bool Q8, bool FOLD, bool WIDE>
 auto *update_kernel(const Group &g) {
-    auto *kernel = list_update<F32, F32, Q8, FOLD>;
+    auto *kernel = list_update<F32, F32, Q8, FOLD, WIDE>;
     auto with = [&](auto W) {
         using WT = decltype(W);
-        kernel = g.gt == RCS_F32    ? list_update<WT, F32, Q8, FOLD>
-                 : g.gt == RCS_BF16 ? list_update<WT, BF16, Q8, FOLD>
-                                    : list_update<WT, F16, Q8, FOLD>;
+        kernel = g.gt == RCS_F32    ? list_update<WT, F32, Q8, FOLD, WIDE>
+                 : g.gt == RCS_BF16 ? list_update<WT, BF16, Q8, FOLD, WIDE>
+                                    : list_update<WT, F16, Q8, FOLD, WIDE>;
     };
     if (g.wt == RCS_F32) with(F32{});
     else if (g.wt == RCS_BF16) with(BF16{});
@@ -1473,8 +1495,10 @@ int adamw_clip_step_list(rcs_list *list, int32_t t, float lr, float clip, float 
     // weight_free's constants; a learning rate of zero, or whose inverse
     // overflows, divides by infinity
     const double over = (1.0 - std::pow(beta1, (double)t)) / (double)lr;
-    h.da = (float)(over / std::sqrt(1.0 - std::pow(beta2, (double)t)));
+    const double root2 = std::sqrt(1.0 - std::pow(beta2, (double)t));
+    h.da = (float)(over / root2);
     h.db = (float)(over * (double)eps);
+    const bool wide = root2 * (double)eps < kWideEps;
     if (lr == 0.0f || !std::isfinite(h.da) || !std::isfinite(h.db)) {
         h.da = 1.0f;
         h.db = INFINITY;
@@ -1489,8 +1513,13 @@ int adamw_clip_step_list(rcs_list *list, int32_t t, float lr, float clip, float 
     launch_norm(list, grad_scale, nb, fold, clip, dev_out, stream);
     const bool near = q8 || list->n <= kNearMaxN;
     for (const Group &g : list->groups) {
-        auto *kernel = q8 ? (fold ? update_kernel<true, true>(g) : update_kernel<true, false>(g))
-                          : (fold ? update_kernel<false, true>(g) : update_kernel<false, false>(g));
+        auto *kernel = fold ? update_kernel<false, true, false>(g)
+                            : update_kernel<false, false, false>(g);
+        if (q8 && wide)
+            kernel = fold ? update_kernel<true, true, true>(g) : update_kernel<true, false, true>(g);
+        else if (q8)
+            kernel = fold ? update_kernel<true, true, false>(g)
+                          : update_kernel<true, false, false>(g);
         hipLaunchKernelGGL(kernel, dim3((unsigned)g.count), dim3(kUpdThreads), 0, stream,
                            (const Row *)list->d_rows, (const Chunk *)list->d_chunks + g.first,
                            near ? in_windows(g.count) : 0u, list->norm_blocks(),

@@ -441,6 +441,23 @@ def test_extreme_learning_rates(dev, bits, lr):
 
 
 @gpu
+@pytest.mark.parametrize("t", [1, 50])
+@pytest.mark.parametrize("eps", [1e-12, 1e-15, 1e-20, 1e-30])
+@pytest.mark.parametrize("w,g", [(F32, F32), (BF16, BF16)])
+def test_second_moments_below_the_normal_floats(dev, w, g, eps, t):
+    """Gradients whose squares are subnormal floats or nothing, beside an eps
+    that the square root of such a float (up to 1e-19) stands out from: with
+    weights of zero the step is all there is to see."""
+    case = Case(dev, [4096, 515], w=w, g=g, bits=8, state=False, wd=[0.0, 0.0])
+    for x, y in zip(case.g, case.w):
+        tiny = torch.logspace(-22.5, -12, x.numel(), device=dev, dtype=torch.float64)
+        tiny[::3] *= -1
+        x.copy_(tiny)
+        y[::2] = 0
+    check_step(case, t, 1e-3, 1.0, eps=eps)
+
+
+@gpu
 def test_infinite_moments(dev):
     """An infinite 8-bit moment stays infinite, alone in its block; a beta of
     zero forgets it."""
