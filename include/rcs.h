@@ -445,8 +445,7 @@ int grad_global_norm_list(const rcs_list *list, float grad_scale, double *norm_o
  *   t          1-based index of the update
  *   lr, clip   as for adamw_clip_step; clip = +inf never clips. With moments in
  *              8 bits, (1 - beta1^t) eps / lr must not fall below the normal
- *              floats (for the default eps: lr below 1e29), and an lr whose
- *              inverse overflows counts as zero
+ *              floats (for the default eps: lr below 1e29)
  *   grad_scale finite, > 0 (1/n_micro, the inverse of a loss scale, or 1)
  *   beta1, beta2 in [0, 1); eps a positive normal float. A beta of 0 forgets
  *              an 8-bit moment that is infinite, too

@@ -48,6 +48,7 @@
 // weights nearly as much by the vector instructions.
 
 #include <algorithm>
+#include <cfloat>
 #include <new>
 #include <type_traits>
 
@@ -143,7 +144,7 @@ __device__ __forceinline__ Range range_of(Chunk c, const Row &t) {
 
 struct ListScalars {
     float lr, bc1, bc2, b1, c1, b2, c2, eps, gscale;
-    float da, db;   // for the free evaluation of the weight: weight_free
+    float da, db, sc;  // for the free evaluation of the weight: weight_free, weight_wide
     uint32_t key;   // of the update's random bits
     // of decode_moments; 0 for a beta of 0, which forgets the 8-bit moment, an
     // infinite one too (0 times that would be a NaN; so no moment is ever one)
@@ -732,7 +733,8 @@ __device__ __forceinline__ float weight(float w, float m, float v, float decay,
 // with da = bc1 / (lr sqrt(bc2)), db = bc1 eps / lr; root and reciprocal are the
 // hardware's, 1 ulp each over the normal floats. The root of a subnormal v comes
 // out as zero: da sqrt(v) then lacks up to 2^-63 da of a denominator of at least
-// db = sqrt(bc2) eps da, which is for the caller to weigh (kWideEps).
+// db = sqrt(bc2) eps da, which is for the caller to weigh (kWideEps), and so is
+// a denominator whose reciprocal is no normal float (kWideDen).
 __device__ __forceinline__ float weight_free(float w, float m, float v, float decay,
                                              const ListScalars &h) {
     const float den = __builtin_fmaf(__builtin_amdgcn_sqrtf(v), h.da, h.db);
@@ -746,14 +748,22 @@ __device__ __forceinline__ float weight_free(float w, float m, float v, float de
 // and 26.0.)
 constexpr double kWideEps = 0x1p-36;
 
-// weight_free with the root right for every v: a small one is scaled by 2^64 and
-// its root by 2^-32, both exactly.
+// And where the largest denominator, da sqrt(2^128) + db, passes this one (an lr
+// below about 1e-18, or eps / lr beyond 1e37): da and db are then scaled down to
+// it by a power of two, sc, and so is the quotient.
+constexpr double kWideDen = 0x1p125;
+
+// weight_free with the root right for every v (a small one is scaled by 2^64 and
+// its root by 2^-32, both exactly) and the quotient scaled by sc (one rounding
+// more, so not for an sc of 1).
 __device__ __forceinline__ float weight_wide(float w, float m, float v, float decay,
                                              const ListScalars &h) {
     const bool small = v < 0x1p-64f;
     const float root = __builtin_amdgcn_sqrtf(small ? v * 0x1p64f : v);
     const float den = __builtin_fmaf(small ? root * 0x1p-32f : root, h.da, h.db);
-    return __builtin_fmaf(-m, __builtin_amdgcn_rcpf(den), w * decay);
+    const float over = __builtin_amdgcn_rcpf(den);
+    return h.sc == 1.0f ? __builtin_fmaf(-m, over, w * decay)
+                        : __builtin_fmaf(-(m * over), h.sc, w * decay);
 }
 
 // R groups of 32-bit moments from element `first` on: W, G the types of weights
@@ -1492,18 +1502,26 @@ int adamw_clip_step_list(rcs_list *list, int32_t t, float lr, float clip, float 
     h.fits = list->bytes <= kCacheBytes;
     h.mask_m = h.b1 == 0.0f ? 0u : kMaskM;
     h.mask_v = h.b2 == 0.0f ? 0u : kMaskV;
-    // weight_free's constants; a learning rate of zero, or whose inverse
-    // overflows, divides by infinity
+    // weight_free's constants; a learning rate of zero divides by infinity
     const double over = (1.0 - std::pow(beta1, (double)t)) / (double)lr;
     const double root2 = std::sqrt(1.0 - std::pow(beta2, (double)t));
-    h.da = (float)(over / root2);
-    h.db = (float)(over * (double)eps);
-    const bool wide = root2 * (double)eps < kWideEps;
-    if (lr == 0.0f || !std::isfinite(h.da) || !std::isfinite(h.db)) {
+    const double da = over / root2, db = over * (double)eps;
+    const double most = std::fabs(da) * 0x1p64 + std::fabs(db);
+    bool wide = root2 * (double)eps < kWideEps;
+    h.da = (float)da;
+    h.db = (float)db;
+    h.sc = 1.0f;
+    if (lr == 0.0f) {
         h.da = 1.0f;
         h.db = INFINITY;
-    } else if (list->bits == 8 && !std::isnormal(h.db)) {
+    } else if (list->bits == 8 && std::fabs(db) < (double)FLT_MIN) {
         return RCS_EINVAL;  // lr so large that v = 0 would divide by nothing
+    } else if (most > kWideDen) {
+        const int k = std::ilogb(most / kWideDen) + 1;
+        h.da = (float)std::ldexp(da, -k);
+        h.db = (float)std::ldexp(db, -k);
+        h.sc = (float)std::ldexp(1.0, -k);
+        wide = true;
     }
     h.key = mixed(mixed(seed * kHashA + (uint32_t)t * kHashB) + kHashK);
     const bool fold = list->n <= kListFoldMaxN, q8 = list->bits == 8;

@@ -457,6 +457,42 @@ def test_second_moments_below_the_normal_floats(dev, w, g, eps, t):
     check_step(case, t, 1e-3, 1.0, eps=eps)
 
 
+# One rounding more than WEIGHT_ULPS: where the denominator does not fit the
+# floats whose reciprocal is a normal one, the quotient is rounded before it is
+# scaled (by a power of two).
+SCALED_ULPS = WEIGHT_ULPS + 1
+
+
+@gpu
+@pytest.mark.parametrize("w,g", [(F32, F32), (BF16, BF16)])
+@pytest.mark.parametrize("lr,eps", [(1e-18, 1e-8), (1e-20, 1e-8), (-1e-30, 1e-8), (1e-38, 1e-8),
+                                    (1e-42, 1e-8), (1e-30, 1e-30), (1e-3, 1e37), (1e-8, 1e33)])
+def test_denominators_beyond_the_normal_reciprocals(dev, w, g, lr, eps):
+    """lr so small, or eps so large, that (sqrt(v / bc2) + eps) bc1 / lr passes
+    2^126, whose reciprocal is no normal float. Weights of zero show the step
+    alone; where it is subnormal, one unit of 2^-149 for its two roundings."""
+    case = Case(dev, [4096, 515], w=w, g=g, bits=8, state=False, wd=[0.0, 0.0])
+    for x, y in zip(case.g, case.w):
+        wide = torch.logspace(-10, 18.5, x.numel(), device=dev, dtype=torch.float64)
+        wide[::3] *= -1
+        x.copy_(wide)
+        y.zero_()
+    norm = torch.zeros(1, dtype=torch.float64, device=dev)
+    case.list.step(1, lr, float("inf"), eps=eps, norm_out=norm)
+    torch.cuda.synchronize()
+    for x, y in zip(case.g, case.w):
+        z = np.zeros(x.numel(), np.float32)
+        _, rm, rv = ref.update32(z, host(x), z, z, float(norm.cpu()), 1, lr, 0.0, float("inf"),
+                                 eps=eps)
+        w64, size = ref.weights64(z, rm, rv, 1, lr, 0.0, eps=eps)
+        assert (np.abs(w64) > 0).all()
+        tol = SCALED_ULPS * 2.0 ** -24 * size + 2.0 ** -149
+        if w != F32:
+            tol = tol + np.abs(w64) * 2.0 ** -8 + 2.0 ** -134
+        got = host(y).astype(np.float64)
+        assert (np.abs(got - w64) <= tol).all(), np.max(np.abs(got - w64) / tol)
+
+
 @gpu
 def test_infinite_moments(dev):
     """An infinite 8-bit moment stays infinite, alone in its block; a beta of
