@@ -413,11 +413,13 @@ int64_t rcs_list_elements(const rcs_list *list);
 /*
  * Binds other gradients of the same types and lengths, count pointers in list
  * order (NULL: no gradient), in stream order: later calls on the stream use
- * them. (A captured call binds at each replay; until then nothing has changed
- * on the device. A captured step or norm uses what is bound when it is
- * replayed.)
+ * them. (A captured call binds at each replay; until the first one nothing has
+ * changed on the device, and the gradients from before it must stay. A captured
+ * step or norm uses what is bound when it is replayed.) rcs_stream_capturing
+ * tells the two apart: 1 while the stream is being captured, else 0.
  */
 int rcs_list_bind_grads(rcs_list *list, const void *const *g, int64_t count, hipStream_t stream);
+int rcs_stream_capturing(hipStream_t stream);
 
 /*
  * The pre-clip global norm of the list's gradients,

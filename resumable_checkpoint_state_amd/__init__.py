@@ -122,6 +122,8 @@ def lib() -> ctypes.CDLL:
     L.rcs_list_elements.restype = i64
     L.rcs_list_bind_grads.argtypes = [vp, vp, i64, vp]
     L.rcs_list_bind_grads.restype = ctypes.c_int
+    L.rcs_stream_capturing.argtypes = [vp]
+    L.rcs_stream_capturing.restype = ctypes.c_int
     L.grad_global_norm_list.argtypes = [vp, f32, vp, vp]
     L.grad_global_norm_list.restype = ctypes.c_int
     L.adamw_clip_step_list.argtypes = [vp, i32, f32, f32, f32, ctypes.c_double, ctypes.c_double,

@@ -1449,6 +1449,8 @@ int rcs_list_bind_grads(rcs_list *list, const void *const *g, int64_t count, hip
     return hipGetLastError() == hipSuccess ? RCS_OK : RCS_EHIP;
 }
 
+int rcs_stream_capturing(hipStream_t stream) { return capturing(stream) ? 1 : 0; }
+
 int grad_global_norm_list(const rcs_list *list, float grad_scale, double *norm_out,
                           hipStream_t stream) {
     int rc;

@@ -61,7 +61,8 @@ class AdamWList:
     place in the list.
 
     Calls of one list must not overlap on the device. A captured graph that
-    holds calls of a list must not be replayed after its close().
+    holds calls of a list must not be replayed after its close(), which is also
+    what becomes of a list that nothing refers to any more.
     """
 
     def __init__(self, params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor | None],
@@ -87,6 +88,7 @@ class AdamWList:
         self._gtypes = [grad_dtype or p.dtype if g is None else getattr(g, "dtype", None)
                         for p, g in zip(self._params, grads)]
         self._grads = self._checked_grads(grads, dev)
+        self._captured: list[list[torch.Tensor | None]] = []  # bound by graphs
         self._copies = []
         for k, (c, p) in enumerate(zip(copies, self._params)):
             if c is not None:
@@ -152,15 +154,21 @@ class AdamWList:
         """Other gradients of the same shapes and types (None: the tensor has
         none), from the stream's next call on. The list lets go of those before:
         keep them while work that uses them is under way on another stream
-        than their own, or a captured graph will bind them again."""
+        than their own. A captured call binds at each replay of its graph, and
+        until the first one nothing has changed: the list keeps both the
+        gradients from before it and, until close(), those of the graph."""
         h, grads = self.handle, list(grads)
         if len(grads) != len(self._params):
             raise ValueError(f"grads has {len(grads)} entries, expected {len(self._params)}")
         new = self._checked_grads(grads, torch.cuda.current_device())
         ptrs = (ctypes.c_void_p * len(new))(*[None if g is None else g.data_ptr() for g in new])
-        _check(lib().rcs_list_bind_grads(h, ptrs, len(new), _stream(stream)),
-               "rcs_list_bind_grads")
-        self._grads = new
+        s = _stream(stream)
+        captured = lib().rcs_stream_capturing(s)
+        _check(lib().rcs_list_bind_grads(h, ptrs, len(new), s), "rcs_list_bind_grads")
+        if captured:
+            self._captured.append(new)
+        else:
+            self._grads = new
 
     def step(self, t: int, lr: float, clip: float, grad_scale: float = 1.0, beta1: float = 0.9,
              beta2: float = 0.999, eps: float = 1e-8, norm_out: torch.Tensor | None = None,
@@ -232,6 +240,7 @@ class AdamWList:
         if self._h is not None:
             h, self._h = self._h, None
             _check(lib().rcs_list_destroy(h), "rcs_list_destroy")
+            self._captured.clear()
 
     def __del__(self):
         try:

@@ -16,6 +16,7 @@ import os
 import numpy as np
 import pytest
 import torch
+from torch.multiprocessing.reductions import StorageWeakRef
 
 import list_reference as ref
 import resumable_checkpoint_state_amd as rcs
@@ -148,6 +149,48 @@ def test_binding_refuses_before_the_device():
         rcs.AdamWList([a], [a], wd=[0.1, 0.2])
     with pytest.raises(TypeError):
         rcs.AdamWList([a], [a])  # host memory
+
+
+class _Binds:
+    """A library whose rcs_list_bind_grads succeeds, on a stream that is being
+    captured or not."""
+
+    capturing = False
+
+    def rcs_stream_capturing(self, stream):
+        return int(self.capturing)
+
+    def rcs_list_bind_grads(self, handle, ptrs, count, stream):
+        return rcs.OK
+
+
+def test_what_a_binding_keeps_alive(monkeypatch):
+    """Until the replay of a captured binding the device has the gradients from
+    before it, and at each replay again those of the call: both stay. An eager
+    binding lets go of the ones it replaces, but not of a graph's."""
+    stub = _Binds()
+    monkeypatch.setattr(tensor_list, "lib", lambda: stub)
+    monkeypatch.setattr(tensor_list, "_checked", lambda t, *args: t.detach())
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    lst = rcs.AdamWList.__new__(rcs.AdamWList)
+    lst._h, lst._captured = ctypes.c_void_p(1), []
+    lst._params, lst._gtypes = [torch.zeros(8)], [F32]
+    first, captured, later, last = (torch.zeros(8) for _ in range(4))
+    held = {k: StorageWeakRef(x.untyped_storage()) for k, x in
+            dict(first=first, captured=captured, later=later, last=last).items()}
+    lst._grads = [first.detach()]
+    stub.capturing = True
+    lst.bind_grads([captured], stream=0)
+    del first, captured
+    assert not held["first"].expired() and not held["captured"].expired()
+    stub.capturing = False
+    lst.bind_grads([later], stream=0)
+    del later
+    assert held["first"].expired()
+    assert not held["captured"].expired() and not held["later"].expired()
+    lst.bind_grads([last], stream=0)
+    assert held["later"].expired() and not held["captured"].expired()
+    lst._h = None  # nothing to destroy
 
 
 # --------------------------------------------------------------------- the GPU
@@ -747,6 +790,33 @@ def test_a_captured_binding_binds_at_each_replay(dev):
         torch.cuda.synchronize()
         for x in norms:
             assert abs(float(x.cpu()) - 2 * one) <= 1e-11 * 2 * one
+
+
+@gpu
+def test_gradients_from_before_a_captured_binding_stay(dev):
+    """The caller drops the gradients bound before the capture, then those that
+    the graph binds: eager calls before the first replay still have the former
+    ones, the replays the latter."""
+    case = Case(dev, [300_001, 700], bits=8)
+    one = norm_of(case)
+    twice = [g * 2 for g in case.g]
+    norms = [torch.zeros(1, dtype=torch.float64, device=dev) for _ in range(2)]
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        case.list.bind_grads(twice)
+        case.list.grad_norm(out=norms[0])
+    del case.g, case.fg, twice
+    torch.cuda.empty_cache()
+    junk = [torch.full((300_701,), 9.0, device=dev) for _ in range(8)]
+    case.list.grad_norm(out=norms[1])
+    torch.cuda.synchronize()
+    assert abs(float(norms[1].cpu()) - one) <= 1e-11 * one
+    for _ in range(3):
+        graph.replay()
+        float(junk[0].sum())
+        torch.cuda.synchronize()
+        assert abs(float(norms[0].cpu()) - 2 * one) <= 1e-11 * 2 * one
 
 
 @gpu
