@@ -472,7 +472,8 @@ int adamw_clip_step_list(rcs_list *list, int32_t t, float lr, float clip, float 
  * The list's state as flat arrays of rcs_list_elements elements in list order
  * (a step file's payload: pass them to ckpt_pack or an rcs_ckpt_writer), and
  * back. Each array is float32 (RCS_F32) or bfloat16 (RCS_BF16), aligned to its
- * element, apart from the list's own arrays and the others; NULL leaves it
+ * element, apart from the list's own arrays and the others, and in an export
+ * from the gradients bound and those of captured bindings since; NULL leaves it
  * out. Export decodes 8-bit moments exactly. Import rounds weights to their
  * type, writes the copies too, and rounds 8-bit moments to the nearest value
  * (ties to even; |m| up to half of the smallest value to zero, v > 0 at least

@@ -1120,6 +1120,9 @@ struct rcs_list {
     std::vector<Row> rows;
     std::vector<Group> groups;
     std::vector<Span> written;  // what an update writes, sorted
+    // gradients of captured bindings, which a replay may put in the place of the
+    // rows', up to the next eager binding
+    std::vector<Span> captured;
     char *mem = nullptr;        // everything below, one allocation
     Row *d_rows = nullptr;
     Chunk *d_chunks = nullptr;
@@ -1258,6 +1261,11 @@ int check_flat(Arrays &arrays, const rcs_list *l, const void *p, int type, bool 
         for (const Row &r : l->rows) {
             const char *g = static_cast<const char *>(r.g), *q = static_cast<const char *>(p);
             if (g != nullptr && g < q + bytes && q < g + r.n * type_bytes(r.gt())) return RCS_EINVAL;
+        }
+    if (writes)
+        for (const Span &g : l->captured) {
+            const char *q = static_cast<const char *>(p);
+            if (g.lo < q + bytes && q < g.hi) return RCS_EINVAL;
         }
     return RCS_OK;
 }
@@ -1439,12 +1447,29 @@ int rcs_list_bind_grads(rcs_list *list, const void *const *g, int64_t count, hip
         if ((rc = arrays.check(g[k], b * r.n, b)) != RCS_OK) return rc;
         if (list->touches(g[k], b * r.n)) return RCS_EINVAL;
     }
+    const bool later = capturing(stream);
+    if (later) {
+        const size_t before = list->captured.size();
+        try {
+            for (int64_t k = 0; k < count; ++k) {
+                const Row &r = list->rows[(size_t)k];
+                const char *p = static_cast<const char *>(g[k]);
+                if (r.n > 0 && p != nullptr)
+                    list->captured.push_back(Span{p, p + r.n * type_bytes(r.gt())});
+            }
+        } catch (const std::bad_alloc &) {
+            list->captured.resize(before);
+            return RCS_ENOMEM;
+        }
+    } else {
+        list->captured.clear();
+    }
     for (int64_t k = 0; k < count; k += kBind) {
         const int some = (int)(count - k < kBind ? count - k : kBind);
         Pointers p;
         for (int j = 0; j < kBind; ++j) p.p[j] = j < some ? g[k + j] : nullptr;
         hipLaunchKernelGGL(list_bind, dim3(1), dim3(kBind), 0, stream, list->d_rows + k, some, p);
-        for (int j = 0; j < some; ++j) list->rows[(size_t)(k + j)].g = g[k + j];
+        for (int j = 0; !later && j < some; ++j) list->rows[(size_t)(k + j)].g = g[k + j];
     }
     return hipGetLastError() == hipSuccess ? RCS_OK : RCS_EHIP;
 }

@@ -820,6 +820,32 @@ def test_gradients_from_before_a_captured_binding_stay(dev):
 
 
 @gpu
+def test_an_export_spares_the_gradients_of_a_captured_binding(dev):
+    """Both sets may be what the device has bound: neither is exported over."""
+    case = Case(dev, [600, 400], gap=0)
+    other, third = torch.randn(1000, device=dev), torch.randn(1000, device=dev)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        case.list.bind_grads(case.cut(other))
+    kept = [raw(x).copy() for x in (case.fg, other)]
+    for _ in range(2):
+        for x in (case.fg, other):
+            with pytest.raises(rcs.RcsError):
+                case.list.export_state(w=x)
+        case.list.export_state(w=third)
+        graph.replay()
+        torch.cuda.synchronize()
+    assert all((raw(x) == k).all() for x, k in zip((case.fg, other), kept))
+    assert (raw(third) == raw(case.fw)).all()
+    case.list.bind_grads(case.cut(third))
+    case.list.export_state(w=other)
+    with pytest.raises(rcs.RcsError):
+        case.list.export_state(w=third)
+    torch.cuda.synchronize()
+
+
+@gpu
 def test_norms_of_several_lists_in_turn_on_one_stream(dev):
     """Norms of 1, 37 and 256 blocks and the flat norm take turns in one
     workspace, steps and a graph between them."""
