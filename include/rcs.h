@@ -197,9 +197,11 @@ int grad_zero(float *g, int64_t n, hipStream_t stream);
 
 /*
  * Copies the pre-clip norm computed by the most recent adamw_clip_step,
- * adamw_clip_step_accum, grad_clip_inplace or grad_global_norm on this stream
- * into norm_out (device or pinned host float64), in stream order. The resume
- * lesson records this norm before the clip to detect numerical faults.
+ * adamw_clip_step_accum, grad_clip_inplace or grad_global_norm on this stream,
+ * or by the most recent adamw_clip_step_list or grad_global_norm_list (unless
+ * that call was captured), into norm_out (device or pinned host float64), in
+ * stream order. The resume lesson records this norm before the clip to detect
+ * numerical faults.
  * RCS_EINVAL if nothing ran on the stream.
  */
 int last_grad_norm(hipStream_t stream, double *norm_out);
@@ -397,7 +399,8 @@ typedef struct rcs_list rcs_list;
  * device (about 80 bytes a tensor and 8 for each 512 elements) and waits for
  * that; the arrays stay the caller's and must live as long as the list. It
  * allocates, so call it before a capture. No later call of the list allocates,
- * except that grad_global_norm_list uses its stream's workspace (rcs_init).
+ * except that grad_global_norm_list and adamw_clip_step_list use their stream's
+ * workspace (rcs_init) unless they are captured.
  * Calls of one list must not overlap on the device (order them by one stream
  * or by events): they share the list's buffers, and steps its arrays. A norm
  * call is an exception: eager ones may run on several streams at once.
@@ -454,6 +457,7 @@ int grad_global_norm_list(const rcs_list *list, float grad_scale, double *norm_o
  *   seed       of the random bits by which 8-bit moments are rounded (they
  *              are a function of seed, t and the element's place in the list)
  *   norm_out   NULL, or device or pinned host memory for the pre-clip norm
+ *              (which last_grad_norm reports too, unless the call was captured)
  *
  * 8-bit moments: blocks of RCS_LIST_BLOCK consecutive elements of a tensor
  * share an exponent for m and one for v (low and high byte of exps). With e

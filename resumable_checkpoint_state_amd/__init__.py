@@ -252,7 +252,8 @@ def grad_global_norm(g, out: torch.Tensor | None = None, stream=None) -> torch.T
 
 
 def last_grad_norm(out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-    """The pre-clip norm of the last update enqueued on the stream."""
+    """The pre-clip norm of the last update or norm enqueued on the stream
+    (captured calls of an AdamWList excepted: they report in norm_out alone)."""
     out = _norm_out(out)
     _check(lib().last_grad_norm(_stream(stream), out.data_ptr()), "last_grad_norm")
     return out

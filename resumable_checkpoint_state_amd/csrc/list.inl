@@ -67,10 +67,12 @@ static_assert(kChunk % kBlock == 0 && kChunk % (8 * kWave) == 0, "whole blocks a
 constexpr int kListNormThreads = 1024;
 constexpr int kRun = 4;
 constexpr int kDeep = 4;
-// The norm's buffers: partial sums, record, and the count of blocks that have
-// left theirs. A stream's workspace has the same layout.
+// The norm's buffers: partial sums, record, the count of blocks that have left
+// theirs, and, in a stream's workspace, which has the same layout, the norm of
+// its last update over a list (whose record is the list's own).
 constexpr size_t kNormRecordAt = (size_t)kNormMaxBlocks * sizeof(double);
 constexpr size_t kNormArrivedAt = kNormRecordAt + 128;
+constexpr size_t kNormLastAt = kNormRecordAt + 192;
 constexpr size_t kNormBytes = kNormRecordAt + 256;
 static_assert(sizeof(ClipScalars) <= 128, "the record ends before the count");
 // Lowest block exponents (biased): the smallest value and, for m, half of it
@@ -629,7 +631,7 @@ template <bool Q8>
 __global__ __launch_bounds__(kListNormThreads) void list_norm(
     const Row *__restrict__ rows, const Chunk *__restrict__ chunks, int64_t nchunks,
     int64_t keep_from, float gscale, double *partials, uint32_t *arrived, float clip,
-    ClipScalars *__restrict__ record, double *__restrict__ norm_out) {
+    ClipScalars *__restrict__ record, double *__restrict__ norm_out, double *__restrict__ last) {
     __shared__ double lds[kListNormThreads / kWave];
     constexpr int kWaves = kListNormThreads / kWave;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
@@ -686,14 +688,15 @@ __global__ __launch_bounds__(kListNormThreads) void list_norm(
     double x[kPartsPerLane];
 #pragma unroll
     for (int k = 0; k < kPartsPerLane; ++k) {
-        const int j = (int)threadIdx.x + k * kUpdThreads, last = (int)gridDim.x - 1;
-        x[k] = __hip_atomic_load(partials + (j < last ? j : last), __ATOMIC_RELAXED,
+        const int j = (int)threadIdx.x + k * kUpdThreads, end = (int)gridDim.x - 1;
+        x[k] = __hip_atomic_load(partials + (j < end ? j : end), __ATOMIC_RELAXED,
                                  __HIP_MEMORY_SCOPE_AGENT);
     }
     const ClipScalars r = final_reduce(x, (int)gridDim.x, clip, nullptr);
     if (threadIdx.x == 0) {
         *record = r;
         if (norm_out != nullptr) *norm_out = r.norm;
+        if (last != nullptr) *last = r.norm;
     }
 }
 
@@ -890,7 +893,7 @@ template <class W, class G, bool Q8, bool FOLD, bool WIDE = false>
 __global__ __launch_bounds__(kUpdThreads) void list_update(
     const Row *__restrict__ rows, const Chunk *__restrict__ chunks, uint32_t in_windows,
     int nparts, const double *__restrict__ partials, float clip, ClipScalars *__restrict__ record,
-    double *__restrict__ norm_out, ListScalars h) {
+    double *__restrict__ norm_out, double *__restrict__ last, ListScalars h) {
     const Chunk c = chunks[near_chunk(in_windows)];
     double x[kPartsPerLane];
     ClipScalars cs = {};
@@ -904,6 +907,7 @@ __global__ __launch_bounds__(kUpdThreads) void list_update(
             if (blockIdx.x == 0 && threadIdx.x == 0) {
                 *record = cs;
                 if (norm_out != nullptr) *norm_out = cs.norm;
+                if (last != nullptr) *last = cs.norm;
             }
         }
         s = cs.scale;
@@ -1219,18 +1223,37 @@ bool capturing(hipStream_t stream) {
     return st != hipStreamCaptureStatusNone;
 }
 
+// The workspace of a stream that is not being captured. It may be made while
+// another stream is: an allocation of this thread is no part of that capture.
+int list_workspace(int dev, hipStream_t stream, Workspace **out) {
+    if (t_ws.ws != nullptr && t_ws.dev == dev && t_ws.stream == stream) {
+        *out = t_ws.ws;
+        return RCS_OK;
+    }
+    hipStreamCaptureMode mode = hipStreamCaptureModeRelaxed;
+    const bool swapped = hipThreadExchangeStreamCaptureMode(&mode) == hipSuccess;
+    const int rc = get_workspace(stream, out);
+    if (swapped) (void)hipThreadExchangeStreamCaptureMode(&mode);
+    return rc;
+}
+
+double *last_norm(const NormBuffers &nb) {
+    return reinterpret_cast<double *>(reinterpret_cast<char *>(nb.partials) + kNormLastAt);
+}
+
 uint32_t *arrived(const NormBuffers &nb) {
     return reinterpret_cast<uint32_t *>(reinterpret_cast<char *>(nb.partials) + kNormArrivedAt);
 }
 
-// fold: the update will reduce the partials itself.
+// fold: the update will reduce the partials itself. dev_out, last: further places
+// for the norm, or null.
 void launch_norm(const rcs_list *l, float gscale, const NormBuffers &nb, bool fold, float clip,
-                 double *dev_out, hipStream_t stream) {
+                 double *dev_out, double *last, hipStream_t stream) {
     auto *kernel = l->bits == 8 ? list_norm<true> : list_norm<false>;
     hipLaunchKernelGGL(kernel, dim3(l->norm_blocks()), dim3(kListNormThreads), 0,
                        stream, (const Row *)l->d_rows, (const Chunk *)l->d_chunks, l->nchunks,
                        l->keep_from, gscale, nb.partials, fold ? nullptr : arrived(nb), clip,
-                       nb.scalars, dev_out);
+                       nb.scalars, dev_out, last);
 }
 
 uint32_t in_windows(int64_t blocks) { return (uint32_t)(blocks - blocks % kWindow); }
@@ -1486,7 +1509,7 @@ int grad_global_norm_list(const rcs_list *list, float grad_scale, double *norm_o
     NormBuffers nb = list->norm[1];
     Workspace *ws = nullptr;
     if (!capturing(stream)) {
-        if ((rc = get_workspace(stream, &ws)) != RCS_OK) return rc;
+        if ((rc = list_workspace(list->dev, stream, &ws)) != RCS_OK) return rc;
         nb = *ws;
         std::lock_guard<std::mutex> lk(g_mu);
         if (!ws->counts) {  // in stream order before the first pass that counts there
@@ -1496,9 +1519,10 @@ int grad_global_norm_list(const rcs_list *list, float grad_scale, double *norm_o
         }
     }
     const bool direct = on_device(norm_out);
-    launch_norm(list, grad_scale, nb, false, INFINITY, direct ? norm_out : nullptr, stream);
+    launch_norm(list, grad_scale, nb, false, INFINITY, direct ? norm_out : nullptr, nullptr,
+                stream);
     if (hipGetLastError() != hipSuccess) return RCS_EHIP;
-    if (ws != nullptr) ws->has_norm = true;
+    if (ws != nullptr) ws->last = &ws->scalars->norm;
     if (!direct && hipMemcpyAsync(norm_out, &nb.scalars->norm, sizeof(double), hipMemcpyDefault,
                                   stream) != hipSuccess)
         return RCS_EHIP;
@@ -1555,7 +1579,11 @@ int adamw_clip_step_list(rcs_list *list, int32_t t, float lr, float clip, float 
     const bool direct = norm_out != nullptr && on_device(norm_out);
     double *dev_out = direct ? norm_out : nullptr;
     const NormBuffers &nb = list->norm[0];
-    launch_norm(list, grad_scale, nb, fold, clip, dev_out, stream);
+    // for last_grad_norm; a replay reports only where norm_out says
+    Workspace *ws = nullptr;
+    if (!capturing(stream) && (rc = list_workspace(list->dev, stream, &ws)) != RCS_OK) return rc;
+    double *last = ws != nullptr ? last_norm(*ws) : nullptr;
+    launch_norm(list, grad_scale, nb, fold, clip, dev_out, last, stream);
     const bool near = q8 || list->n <= kNearMaxN;
     for (const Group &g : list->groups) {
         auto *kernel = fold ? update_kernel<false, true, false>(g)
@@ -1568,9 +1596,10 @@ int adamw_clip_step_list(rcs_list *list, int32_t t, float lr, float clip, float 
         hipLaunchKernelGGL(kernel, dim3((unsigned)g.count), dim3(kUpdThreads), 0, stream,
                            (const Row *)list->d_rows, (const Chunk *)list->d_chunks + g.first,
                            near ? in_windows(g.count) : 0u, list->norm_blocks(),
-                           (const double *)nb.partials, clip, nb.scalars, dev_out, h);
+                           (const double *)nb.partials, clip, nb.scalars, dev_out, last, h);
     }
     if (hipGetLastError() != hipSuccess) return RCS_EHIP;
+    if (ws != nullptr) ws->last = last;
     if (norm_out != nullptr && !direct &&
         hipMemcpyAsync(norm_out, &nb.scalars->norm, sizeof(double), hipMemcpyDefault, stream) !=
             hipSuccess)

@@ -834,7 +834,9 @@ struct NormBuffers {
 };
 
 struct Workspace : NormBuffers {
-    std::atomic<bool> has_norm{false};
+    // where the norm of the stream's last call is: in the record, or beside it
+    // for an update over a list (null: nothing has run)
+    std::atomic<const double *> last{nullptr};
     bool counts = false;  // list_norm's count is there (set under g_mu)
 };
 
@@ -1303,7 +1305,7 @@ int adamw_clip_step_accum(float *w, const float *g, float *m, float *v, int64_t 
             ev = &g_prof.ev[4 * g_prof.next++];
     }
     rc = launch_step(w, g, m, v, n, clip, h, ws, stream, ev);
-    if (rc == RCS_OK) ws->has_norm = true;
+    if (rc == RCS_OK) ws->last = &ws->scalars->norm;
     return rc;
 }
 
@@ -1339,7 +1341,7 @@ int grad_global_norm(const float *g, int64_t n, double *norm_out, hipStream_t st
     Workspace *ws = nullptr;
     if ((rc = get_workspace(stream, &ws)) != RCS_OK) return rc;
     if ((rc = launch_norm(g, n, 1.0f, INFINITY, ws, stream)) != RCS_OK) return rc;
-    ws->has_norm = true;
+    ws->last = &ws->scalars->norm;
     if (hipMemcpyAsync(norm_out, &ws->scalars->norm, sizeof(double), hipMemcpyDefault, stream) !=
         hipSuccess)
         return RCS_EHIP;
@@ -1376,7 +1378,7 @@ int grad_clip_inplace(float *g, int64_t n, float clip, hipStream_t stream) {
                            n, (const ClipScalars *)ws->scalars);
     }
     if (hipGetLastError() != hipSuccess) return RCS_EHIP;
-    ws->has_norm = true;
+    ws->last = &ws->scalars->norm;
     return RCS_OK;
 }
 
@@ -1403,9 +1405,9 @@ int last_grad_norm(hipStream_t stream, double *norm_out) {
     Workspace *ws = nullptr;
     int rc;
     if ((rc = get_workspace(stream, &ws)) != RCS_OK) return rc;
-    if (!ws->has_norm) return RCS_EINVAL;
-    if (hipMemcpyAsync(norm_out, &ws->scalars->norm, sizeof(double), hipMemcpyDefault, stream) !=
-        hipSuccess)
+    const double *last = ws->last;
+    if (last == nullptr) return RCS_EINVAL;
+    if (hipMemcpyAsync(norm_out, last, sizeof(double), hipMemcpyDefault, stream) != hipSuccess)
         return RCS_EHIP;
     return RCS_OK;
 }

@@ -846,6 +846,69 @@ def test_an_export_spares_the_gradients_of_a_captured_binding(dev):
 
 
 @gpu
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("n", [5000, 8_400_000])
+def test_last_grad_norm_reports_a_step(dev, bits, n):
+    """Whatever ran on the stream before, wherever else the norm goes, and for a
+    step that is skipped too; each stream has its own, and a captured step
+    leaves it."""
+    case = Case(dev, [n, 77], bits=bits)
+    flat = torch.ones(1000, device=dev)
+    want = float(case.list.grad_norm().cpu())
+    outs = (None, torch.zeros(1, dtype=torch.float64, device=dev),
+            torch.zeros(1, dtype=torch.float64, pin_memory=True))
+
+    def last(**kw):
+        x = rcs.last_grad_norm(**kw)
+        torch.cuda.synchronize()
+        return float(x.cpu())
+
+    rcs.grad_global_norm(flat)
+    ones = last()
+    for out in outs:
+        rcs.grad_global_norm(flat)
+        assert last() == ones != want
+        case.list.step(1, 0.0, 1.0, norm_out=out)
+        assert last() == want
+        assert out is None or float(out.cpu()) == want
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    case.list.step(2, 0.0, 1.0, grad_scale=0.5, stream=side)
+    assert last(stream=side) == want / 2 and last() == want
+    rcs.grad_global_norm(flat)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        case.list.step(3, 0.0, 1.0, norm_out=outs[1])
+    graph.replay()
+    assert last() == ones and float(outs[1].cpu()) == want
+    case.g[1][3] = float("inf")
+    case.list.step(4, 0.0, 1.0)
+    assert last() == float("inf")
+
+
+@gpu
+def test_a_step_on_a_fresh_stream_while_another_is_captured(dev):
+    """The stream's workspace is made on the way; the capture goes on."""
+    case, other = Case(dev, [3000]), Case(dev, [3000], bits=8)
+    want, mine = norm_of(case), float(other.list.grad_norm().cpu())
+    side, norm_side = torch.cuda.Stream(), torch.cuda.Stream()
+    outs = [torch.zeros(1, dtype=torch.float64, device=dev) for _ in range(3)]
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        case.list.grad_norm(out=outs[0])
+        other.list.step(1, 0.0, 1.0, norm_out=outs[1], stream=side)
+        other.list.grad_norm(out=outs[2], stream=norm_side)
+    torch.cuda.synchronize()
+    assert float(outs[1].cpu()) == float(outs[2].cpu()) == mine
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert abs(float(outs[0].cpu()) - want) <= 1e-11 * want
+
+
+@gpu
 def test_norms_of_several_lists_in_turn_on_one_stream(dev):
     """Norms of 1, 37 and 256 blocks and the flat norm take turns in one
     workspace, steps and a graph between them."""
