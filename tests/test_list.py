@@ -24,8 +24,8 @@ from resumable_checkpoint_state_amd import tensor_list
 
 gpu = pytest.mark.gpu
 F32, BF16, F16 = torch.float32, torch.bfloat16, torch.float16
-# 0: no chunk at all; around one lane's 8 elements, a block of 128, a chunk of
-# 1,024, several of them
+# 0: no chunk at all; around one lane's 8 elements, a block of 128, two chunks of
+# 512, several of them (CHUNK_SIZES: around one)
 SIZES = [0, 1, 7, 8, 9, 127, 128, 129, 130, 1023, 1024, 1025, 2048, 5003]
 
 # Steps of 2^-24 (half a unit in float32's last place, relative to the larger of
@@ -361,6 +361,42 @@ def test_step(dev, bits, w, g, gap):
     assert check_step(case, 1, 3e-3, 1.0) > 1.0
     check_step(case, 2, 3e-3, float("inf"), scale=0.25)
     check_step(case, 1000, 1e-2, 0.5, b1=0.8, b2=0.95, eps=1e-6)
+
+
+# Around the kernels' chunk, 512 elements, and around one and a fraction: with
+# 32-bit moments the chunks of a tensor of more than 512 begin where its m lies on
+# a 256-byte boundary, so what matters there is where the tensor begins in the
+# list, too. The single elements move what follows them.
+CHUNK_SIZES = [511, 512, 513, 1, 512, 513, 575, 1, 576, 577, 62, 639, 640, 641, 3, 1023, 1,
+               1087, 1088, 1089, 1536, 1537]
+
+
+@gpu
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("w,g", [(F32, F32), (F32, BF16), (BF16, BF16)])
+@pytest.mark.parametrize("gap", [0, 1])
+def test_step_around_a_chunk(dev, bits, w, g, gap):
+    case = Case(dev, CHUNK_SIZES, w=w, g=g, bits=bits, gap=gap)
+    check_step(case, 3, 3e-3, 1.0)
+    check_step(case, 4, 3e-3, float("inf"))
+    n = case.n
+    got = [torch.full((n + 1,), 3.0, device=dev) for _ in range(3)]
+    case.list.export_state(*(x[:n] for x in got))
+    m, v = case.moments()
+    assert (host(got[0])[:n] == host(torch.cat(case.w))).all()
+    assert (host(got[1])[:n] == m).all() and (host(got[2])[:n] == v).all()
+    assert all(float(x[n].cpu()) == 3.0 for x in got)
+    other = Case(dev, CHUNK_SIZES, w=w, g=g, bits=bits, gap=gap, seed=2)
+    gaps = other.gaps(other.fw)
+    other.list.import_state(*(x[:n] for x in got))
+    torch.cuda.synchronize()
+    assert (raw(torch.cat(other.w)) == raw(torch.cat(case.w))).all()
+    # the values, that is: where an update rounded a block's largest down to the
+    # next power of two, and for a zero, the codes of the same values differ
+    om, ov = other.moments()
+    assert (om.view(np.uint32) == m.view(np.uint32)).all()
+    assert (ov.view(np.uint32) == v.view(np.uint32)).all()
+    assert (other.gaps(other.fw) == gaps).all()
 
 
 @gpu
