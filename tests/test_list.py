@@ -748,6 +748,45 @@ def test_a_run_continues_bit_identically_from_its_step_file(dev, tmp_path, bits,
 
 
 @gpu
+def test_a_model_trains_on_the_gradients_it_accumulates(dev):
+    """README's loop on a model's own parameters: every step sees the gradients
+    of its own backward pass alone."""
+    gen = torch.Generator(device=dev).manual_seed(4)
+    x = torch.randn(9, 131, generator=gen, device=dev).to(BF16)
+
+    class Model(torch.nn.Module):
+        def __init__(self):
+            super().__init__()
+            self.gain = torch.nn.Parameter(torch.full((9, 131), 0.5, device=dev, dtype=BF16))
+            self.bias = torch.nn.Parameter(torch.zeros(131, device=dev, dtype=BF16))
+
+        def forward(self):
+            return (x * self.gain + self.bias).square().sum()
+
+    model, plain = Model(), Model()
+    params = list(model.parameters())
+    for p in params:
+        p.grad = torch.zeros_like(p)
+    grads = [p.grad for p in params]
+    opt = rcs.AdamWList(params, grads, state_bits=8,
+                        wd=[0.01 if p.dim() > 1 else 0.0 for p in params])
+    other = list(plain.parameters())
+    ref_opt = rcs.AdamWList(other, [None] * 2, state_bits=8, wd=[0.01, 0.0])
+    for t in range(1, 5):
+        model().backward()
+        fresh = list(torch.autograd.grad(plain(), other))
+        ref_opt.bind_grads(fresh)
+        assert all(bool((a == b).all()) for a, b in zip(grads, fresh))
+        opt.step(t, lr=3e-3, clip=1.0)
+        ref_opt.step(t, lr=3e-3, clip=1.0)
+        torch._foreach_zero_(grads)
+        torch.cuda.synchronize()
+        assert all(p.grad is g and not bool(g.any()) for p, g in zip(params, grads))
+    for a, b in zip(params, other):
+        assert (raw(a) == raw(b)).all() and not bool((a == 0.5).all())
+
+
+@gpu
 @pytest.mark.parametrize("bits", [32, 8])
 @pytest.mark.parametrize("n", [5000, 8_400_000])
 def test_captured_and_replayed(dev, bits, n):
