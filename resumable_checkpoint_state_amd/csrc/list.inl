@@ -119,9 +119,15 @@ __device__ __forceinline__ uint32_t row_of(Chunk c) { return (uint32_t)c; }
 // gradients and copies, 348 and 338 at 124,356,864 elements, 47.7 and 45.0 at
 // 12.7M of odd sizes; export 328 and 319, import 432 and 426; 32-bit moments
 // 60.6 and 57.5 (12.7M bfloat16, odd sizes), 187 and 185 (37M float32), 247
-// and 245 (50M), but 607 and 624 at 124,356,864 float32: there they stay in
-// order. (16 neighbours: 343 for export; 128 or 256: as 64. Each XCD on an
-// eighth of the list, as in the flat update: 651 for 607.)
+// and 245 (50M). Beside 32-bit moments above 2^26 elements they stay in order:
+// at 124,356,864 elements, on the same arrays, 602 and 612 (float32), 443 and 450
+// (bfloat16), 445 and 449 (float16), 576 and 580 (float32 weights, bfloat16
+// gradients and copies); at 537.6M 2,860 and 2,904, 2,139 and 2,152, 2,111 and
+// 2,177, 2,750 and 2,756. (Odd sizes there: 172.5M float32 878 and 894, but
+// bfloat16 660 and 657, with float32 weights and copies 854 and 838. Why the order
+// that saves lines costs aligned streams of this length is not known. 16
+// neighbours: 343 for export; 128 or 256: as 64. Each XCD on an eighth of the
+// list, as in the flat update: 651 for 607.)
 constexpr uint32_t kNear = 64;
 constexpr int64_t kNearMaxN = 1LL << 26;  // beside 32-bit moments
 constexpr uint32_t kWindow = 8 * kNear;
@@ -615,9 +621,13 @@ __device__ __forceinline__ double squares_of(const void *g, int64_t first, int64
 // one stretch of a tensor at a time; the order depends on the list's chunks
 // alone. The table entries of a run are fetched while the one before it is
 // summed. Bound by HBM; of 16-bit gradients, by the start and end of so short a
-// pass too: 124,356,864 float32 gradients 80 us = 6.2 TB/s, bfloat16 ones 39 us =
-// 6.3 TB/s where the last-level cache holds them, 48 us = 5.2 TB/s behind an
-// update that left other things there.
+// pass too: 124,356,864 float32 gradients 79 us = 6.3 TB/s, bfloat16 ones 39 us =
+// 6.4 TB/s where the last-level cache holds them, 48 us = 5.2 TB/s behind an
+// update that left other things there (right behind kernels that left it full
+// of written lines, which have to go out first, 140 and 103 us). A run is kRun
+// chunks whatever the list's length: up to 16,384 chunks some blocks have no run,
+// at 8 blocks of 32 with 262,144 elements, and above the last turn of runs is
+// not full (12.7M elements: 1.52 turns' work in 2).
 //   The end (unless arrived is null: the update then reduces the partials): the
 // block that finds itself the last to leave its partial reduces them all, in
 // their order, whichever it is. A partial goes out as an exchange whose answer
@@ -884,9 +894,9 @@ __device__ __forceinline__ void update8(const Row &t, int64_t first, int64_t end
 // too (a branch in update8 that left the compiler one order of instructions for
 // both forms: 24.8 and 25.3 us at 8.0M float32 elements).
 //   At 124,356,864 elements, each pass once over its bytes: float32 weights and
-// gradients with 32-bit moments 527 us = 6.6 TB/s, bfloat16 ones 410 us =
+// gradients with 32-bit moments 524 us = 6.6 TB/s, bfloat16 ones 411 us =
 // 6.7 TB/s; with 8-bit moments, float32 weights, bfloat16 gradients and copies
-// 291 us = 6.9 TB/s, bfloat16 weights and gradients 197 us = 6.3 TB/s. Bound by
+// 291 us = 6.9 TB/s, bfloat16 weights and gradients 202 us = 6.2 TB/s. Bound by
 // HBM; the last one, at 397 vector instructions a chunk (49.6 an element), by
 // them as well: 230 us in a run at a lower clock.
 template <class W, class G, bool Q8, bool FOLD, bool WIDE = false>
@@ -950,9 +960,9 @@ __global__ __launch_bounds__(kUpdThreads) void list_update(
 // Flat arrays of the list's elements, in list order: w, m and v, each float32
 // or bfloat16, or null for one that is left out. Bound by HBM: at 124,356,864
 // elements with bfloat16 weights and 8-bit moments, export to float32 takes
-// 328 us = 6.1 TB/s (three quarters of it written), of the moments alone to
-// bfloat16 120 us = 6.3 TB/s (8 elements a lane there, whole lines of it), import
-// from float32 311 us = 6.4 TB/s.
+// 329 us = 6.1 TB/s (three quarters of it written), of the moments alone to
+// bfloat16 119 us = 6.3 TB/s (8 elements a lane there, whole lines of it), import
+// from float32 313 us = 6.4 TB/s.
 struct Flat {
     void *w, *m, *v;
     int wt, mt, vt;
