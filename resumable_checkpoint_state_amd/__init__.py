@@ -413,7 +413,9 @@ class StepFileCheckpointer:
     <dir>/step_NNNNNN.bin when t is a multiple of `every` (0 = never by
     cadence), when SIGUSR1 arrived (write and continue) or when SIGTERM arrived
     (write, then after_step returns True: the caller exits), keeps the newest
-    `keep` files, and resume() loads the newest valid one.
+    `keep` files, and resume() loads the newest valid one. The first save or
+    resume of an AdamWList allocates its flat float32 payload (payload_buffer):
+    12 bytes an element, beside the writer's 12 with async_write.
 
     async_write=True hands each save to the library's CkptWriter (a device
     snapshot on the training stream, the copy on its own stream, the atomic

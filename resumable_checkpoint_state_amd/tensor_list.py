@@ -220,8 +220,8 @@ class AdamWList:
                "rcs_list_import")
 
     def payload_buffer(self) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
-        """Flat float32 w, m and v, one allocation made at the first call: the
-        payload of a step file."""
+        """Flat float32 w, m and v, the payload of a step file: one allocation
+        of 12 bytes an element, made at the first call and kept."""
         if self._payload is None:
             self._payload = torch.empty(3 * self.n, device=self.m.device)
             # the first use may be on another stream than this allocation's
