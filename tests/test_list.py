@@ -573,6 +573,19 @@ def test_denominators_beyond_the_normal_reciprocals(dev, w, g, lr, eps):
 
 
 @gpu
+@pytest.mark.parametrize("w,g", TYPES)
+def test_step_with_a_small_eps_or_lr(dev, w, g):
+    """The kernels of the weight's other form, for each pair of types and both
+    launch forms, on views at odd offsets, copies included."""
+    for sizes in (SIZES, [8_400_001, 515]):
+        case = Case(dev, sizes, w=w, g=g, bits=8, gap=1, copy=F16 if w == F32 else None)
+        if case.c is not None:
+            case.list.import_state(w=torch.cat(case.w))
+        check_step(case, 1, 3e-3, 1.0, eps=1e-20)
+        check_step(case, 2, 1e-19, 1.0)
+
+
+@gpu
 def test_infinite_moments(dev):
     """An infinite 8-bit moment stays infinite, alone in its block; a beta of
     zero forgets it."""
