@@ -491,6 +491,80 @@ int rcs_list_import(rcs_list *list, const void *w, int w_type, const void *m, in
                     const void *v, int v_type, hipStream_t stream);
 
 /*
+ * The two ends of a model at its vocabulary, as a training step meets them: the
+ * loss of the output head with its gradients, and the gradient of the embedding
+ * lookup. With a head that is tied to the token embedding both add to the
+ * gradient of one (vocab, dim) matrix, which an update then reads in the place
+ * where they left it ("k_loss_fwd / k_loss_bwd", "k_embed_bwd" and the
+ * accumulation by += of grow_a_language_model_backprop, section on the pairing
+ * rule). Everything is deterministic: results depend on the arguments alone, so a
+ * resumed run repeats them bit for bit.
+ *
+ * rcs_head. Matrices are row-major with a stride in elements between rows, at
+ * least `dim` and at most 2^20; pointers need the alignment of an element only.
+ *   hidden, weight   (rows, dim) and (vocab, dim), both of `type`. The logits are
+ *                    z = hidden weight^T, with products of float32 values good
+ *                    to 22 bits (relative to the largest magnitude of each
+ *                    matrix where an element is below 2^-17 of it) and sums in
+ *                    float32; they are not kept
+ *   grad_hidden      NULL, or (rows, dim) of `type`: written
+ *   grad_weight      NULL, or (vocab, dim) of grad_weight_type: added to with
+ *                    accumulate, else written
+ *   scale            of both gradients (1/n_micro, a loss scale, or 1): finite
+ *   mean             nonzero: the loss is the mean over the rows that have one,
+ *                    and the gradients are those of the mean; else their sum
+ *   losses           NULL, or float32[rows]: each row's loss, 0 where it has none
+ *   loss             float32[1]: their mean or sum, 0 if no row has a loss
+ *   limit            bytes that the exponentials of the logits may take at a time
+ *                    (16 bits each, 32 with float32). Where they would take more,
+ *                    rows are done in groups; at least 128 rows are done at a time
+ *   workspace        rcs_head_workspace(args) bytes of device memory, aligned to
+ *                    256, used until the call's work is done. It depends on the
+ *                    sizes, the types, which gradients there are, limit and the
+ *                    alignment of weight. Calls that may overlap on the device need one each
+ * What is written must not overlap anything else. Rows without a loss take no
+ * part: what hidden holds there does not matter, and their gradient is zero.
+ * Gradients of 16-bit types go through softmax values of that type (each
+ * rounded once before and once after it is normalized); sums are float32.
+ */
+#define RCS_I32 0
+#define RCS_I64 1
+#define RCS_HEAD_MAX_ENTRIES 1024
+typedef struct rcs_head {
+    const void *hidden, *weight;
+    void *grad_hidden, *grad_weight;
+    int64_t rows, vocab, dim;
+    int64_t hidden_stride, weight_stride, grad_hidden_stride, grad_weight_stride;
+    int32_t type, grad_weight_type;
+    int32_t accumulate, mean;
+    float scale;
+    float *losses, *loss;
+    int64_t limit;
+    void *workspace;
+    int64_t workspace_bytes;
+} rcs_head;
+int64_t rcs_head_workspace(const rcs_head *args);
+
+/*
+ * head_loss: softmax cross entropy, log(sum_v exp z[t][v]) - z[t][targets[t]].
+ * Rows whose target is ignore_index have no loss; any other target outside
+ * [0, vocab) makes the row's loss and the gradients NaN (an update then changes
+ * nothing). targets: int32 or int64[rows] (RCS_I32, RCS_I64).
+ *
+ * head_distill: tau^2 sum_k p_k (log p_k - log softmax(z[t] / tau)[indices[t][k]])
+ * with p the softmax of the row's logits / tau: the divergence from a teacher's
+ * top logits, tau = temperature > 0. indices, logits: (rows, entries), entries at
+ * most RCS_HEAD_MAX_ENTRIES, logits of any of the three types. Entries with a
+ * negative index or a logit of -inf are not there; a row without entries has no
+ * loss; an index that comes twice has both probabilities; one that is not below
+ * vocab makes the row NaN.
+ */
+int head_loss(const rcs_head *args, const void *targets, int index_type, int64_t ignore_index,
+              hipStream_t stream);
+int head_distill(const rcs_head *args, const void *indices, int index_type, const void *logits,
+                 int logits_type, int64_t entries, float temperature, hipStream_t stream);
+
+/*
  * Instrumentation: while enabled, adamw_clip_step has its kernel dispatches
  * stamp HIP events (start of grad_norm_partial, end of the last norm kernel
  * -- grad_norm_partial itself when the update kernel does the final

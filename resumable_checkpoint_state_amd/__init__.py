@@ -24,6 +24,7 @@ __all__ = [
     "ckpt_pack", "ckpt_unpack", "init", "profile_enable", "profile_read",
     "strerror", "lib", "LIB_PATH", "build", "step_file_name", "MAX_N",
     "ckpt_pack_async", "ckpt_pack_wait", "CkptWriter", "StepFileCheckpointer", "AdamWList",
+    "head_loss", "head_distill",
 ]
 
 OK, EINVAL, ESIZE, EHEADER, EHIP, ENOMEM, EIO, ENOENT = 0, -1, -2, -3, -4, -5, -6, -7
@@ -133,6 +134,12 @@ def lib() -> ctypes.CDLL:
         fn = getattr(L, name)
         fn.argtypes = [vp, vp, ctypes.c_int, vp, ctypes.c_int, vp, ctypes.c_int, vp]
         fn.restype = ctypes.c_int
+    L.rcs_head_workspace.argtypes = [vp]
+    L.rcs_head_workspace.restype = i64
+    L.head_loss.argtypes = [vp, vp, ctypes.c_int, i64, vp]
+    L.head_loss.restype = ctypes.c_int
+    L.head_distill.argtypes = [vp, vp, ctypes.c_int, vp, ctypes.c_int, i64, f32, vp]
+    L.head_distill.restype = ctypes.c_int
     _lib = L
     return L
 
@@ -512,3 +519,4 @@ def profile_read():
 
 
 from .tensor_list import AdamWList  # noqa: E402  (uses the helpers above)
+from .head import head_distill, head_loss  # noqa: E402

@@ -1,0 +1,1122 @@
+// head.hip -- losses of a language model's output head and their gradients,
+// without the matrix of logits: softmax cross entropy, and the divergence from
+// a teacher's top logits. gfx950 kernels and their C ABI.
+
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "rcs.h"
+#include "rcs_internal.h"
+
+#pragma clang fp contract(off)
+
+namespace {
+
+// ------------------------------------------------------------------- types
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+struct BF16 {};
+struct F16 {};
+
+__device__ __forceinline__ f32x4 mfma(s16x8 a, s16x8 b, f32x4 c, BF16) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mfma(s16x8 a, s16x8 b, f32x4 c, F16) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
+                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ uint32_t two(float a, float b, BF16) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
+}
+__device__ __forceinline__ uint32_t two(float a, float b, F16) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, f16x2));
+}
+__device__ __forceinline__ float value(uint16_t b, BF16) {
+    return __uint_as_float((uint32_t)b << 16);
+}
+__device__ __forceinline__ float value(uint16_t b, F16) {
+    return (float)__builtin_bit_cast(_Float16, b);
+}
+__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Element i of an array of type t (RCS_F32, RCS_BF16, RCS_F16).
+__device__ __forceinline__ float element(const void *p, int64_t i, int t) {
+    if (t == RCS_F32) return static_cast<const float *>(p)[i];
+    const uint16_t b = static_cast<const uint16_t *>(p)[i];
+    return t == RCS_BF16 ? value(b, BF16{}) : value(b, F16{});
+}
+__device__ __forceinline__ void put(void *p, int64_t i, int t, float x) {
+    if (t == RCS_F32) static_cast<float *>(p)[i] = x;
+    else static_cast<uint16_t *>(p)[i] =
+        (uint16_t)(t == RCS_BF16 ? two(x, 0.f, BF16{}) : two(x, 0.f, F16{}));
+}
+// Four consecutive elements, aligned to one: the hardware's vector accesses need
+// no more.
+typedef u32x4 u32x4_any __attribute__((aligned(4)));
+typedef u32x2 u32x2_any __attribute__((aligned(2)));
+template <class T>
+__device__ __forceinline__ f32x4 four(u32x2 b, T) {
+    return f32x4{value((uint16_t)b[0], T{}), value((uint16_t)(b[0] >> 16), T{}),
+                 value((uint16_t)b[1], T{}), value((uint16_t)(b[1] >> 16), T{})};
+}
+__device__ __forceinline__ f32x4 load4(const void *p, int64_t i, int t) {
+    if (t == RCS_F32)
+        return __builtin_bit_cast(
+            f32x4, *reinterpret_cast<const u32x4_any *>(static_cast<const float *>(p) + i));
+    const u32x2 b = *reinterpret_cast<const u32x2_any *>(static_cast<const uint16_t *>(p) + i);
+    return t == RCS_BF16 ? four(b, BF16{}) : four(b, F16{});
+}
+__device__ __forceinline__ void store4(void *p, int64_t i, int t, f32x4 x) {
+    if (t == RCS_F32) {
+        *reinterpret_cast<u32x4_any *>(static_cast<float *>(p) + i) = __builtin_bit_cast(u32x4, x);
+        return;
+    }
+    const u32x2 b = t == RCS_BF16 ? u32x2{two(x[0], x[1], BF16{}), two(x[2], x[3], BF16{})}
+                                  : u32x2{two(x[0], x[1], F16{}), two(x[2], x[3], F16{})};
+    *reinterpret_cast<u32x2_any *>(static_cast<uint16_t *>(p) + i) = b;
+}
+__device__ __forceinline__ float pick(f32x4 x, int r) {
+    return r == 0 ? x[0] : r == 1 ? x[1] : r == 2 ? x[2] : x[3];
+}
+__device__ __forceinline__ int64_t index_at(const void *p, int64_t i, int t) {
+    return t == RCS_I32 ? (int64_t) static_cast<const int32_t *>(p)[i]
+                        : static_cast<const int64_t *>(p)[i];
+}
+
+constexpr int kWave = 64;
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+// Tiles of a product: kX by kY outputs by a block of four waves, kK at a time.
+constexpr int kX = 256, kY = 128, kK = 32;
+constexpr int kGroup = 128;  // columns of the logits with a reference of their own
+constexpr int kGemmThreads = 256;
+constexpr int kStages = 3;
+constexpr int kXBytes = kX * kK * 2, kYBytes = kY * kK * 2, kStageBytes = kXBytes + kYBytes;
+
+// What the kernels of one call tell each other, in device memory.
+struct Scalars {
+    int32_t count;        // rows that have a loss
+    uint32_t top_h, top_w;  // float32 only: bits of the largest finite magnitudes
+};
+
+// The power of two that brings a largest magnitude of these bits to [2^14, 2^15).
+__device__ __forceinline__ int lift_of(uint32_t top) {
+    const int e = (int)(top >> 23);
+    return e == 0 ? 126 : min(141 - e, 126);
+}
+__device__ __forceinline__ float pow2(int e) { return ldexpf(1.f, e); }
+
+// --------------------------------------------------------------- preparation
+
+// flags[t]: whether row t has a loss.
+__global__ void head_flags(const void *index, int index_type, int64_t entries, int64_t rows,
+                           int64_t ignore, const void *logits, int logits_type, bool distill,
+                           uint8_t *flags) {
+    const int64_t t = blockIdx.x * (int64_t)(blockDim.x / kWave) + threadIdx.x / kWave;
+    const int lane = threadIdx.x % kWave;
+    if (t >= rows) return;
+    bool any = false;
+    if (!distill) any = index_at(index, t, index_type) != ignore;
+    else
+        for (int64_t k = lane; k < entries; k += kWave)
+            any |= index_at(index, t * entries + k, index_type) >= 0 &&
+                   element(logits, t * entries + k, logits_type) != -INFINITY;
+    if (__any(any) && lane == 0) flags[t] = 1;
+    if (!__any(any) && lane == 0) flags[t] = 0;
+}
+
+// rowmap[i]: the i-th row that has a loss; inverse[t]: its i, or -1.
+__global__ __launch_bounds__(1024) void head_scan(const uint8_t *flags, int64_t rows,
+                                                  int32_t *rowmap, int32_t *inverse,
+                                                  Scalars *scalars) {
+    __shared__ int32_t sums[1024 / kWave];
+    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+    int32_t base = 0;
+    for (int64_t at = 0; at < rows; at += 1024) {
+        const int64_t t = at + tid;
+        const bool f = t < rows && flags[t] != 0;
+        const uint64_t m = __ballot(f);
+        if (lane == 0) sums[wave] = __popcll(m);
+        __syncthreads();
+        int32_t before = base, all = 0;
+        for (int w = 0; w < 1024 / kWave; ++w) {
+            if (w < wave) before += sums[w];
+            all += sums[w];
+        }
+        before += __popcll(m & ((1ull << lane) - 1));
+        if (f) rowmap[before] = (int32_t)t;
+        if (t < rows) inverse[t] = f ? before : -1;
+        base += all;
+        __syncthreads();
+    }
+    if (tid == 0) {
+        scalars->count = base;
+        scalars->top_h = 0;
+        scalars->top_w = 0;
+    }
+}
+
+// Largest finite magnitude of the rows (those with a loss, where inverse is given).
+__global__ __launch_bounds__(256) void head_top(const float *p, int64_t ld, int64_t rows,
+                                                int64_t dim, const int32_t *inverse,
+                                                uint32_t *top) {
+    uint32_t best = 0;
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+        if (inverse != nullptr && inverse[r] < 0) continue;
+        for (int64_t k = threadIdx.x; k < dim; k += blockDim.x) {
+            const uint32_t b = __float_as_uint(p[r * ld + k]) & 0x7FFFFFFFu;
+            if (b < 0x7F800000u && b > best) best = b;
+        }
+    }
+#pragma unroll
+    for (int d = 1; d < kWave; d *= 2) best = max(best, (uint32_t)__shfl_xor((int)best, d));
+    if (threadIdx.x % kWave == 0) atomicMax(top, best);
+}
+
+// Rows of src as the products read them: padded with zeros to `pad` columns,
+// float32 as two half-precision planes (x * 2^lift = high + low). With inverse,
+// row t goes to row inverse[t], rows without a loss are left out and their
+// gradient is cleared; the rows behind the last one, up to a whole step of kK,
+// are zero.
+struct PrepArgs {
+    const void *src;
+    void *hi, *lo;
+    int64_t ld, rows, dim, pad;
+    int type;
+    const int32_t *inverse;
+    Scalars *scalars;
+    bool hidden;  // hidden rows, or the weight's
+    void *grad;   // gradient of the hidden rows, or null
+    int64_t grad_ld;
+};
+__global__ __launch_bounds__(256) void head_prep(PrepArgs a) {
+    const int64_t r = blockIdx.x;
+    int64_t to = r;
+    bool zero = false;
+    if (a.inverse != nullptr) {
+        if (r >= a.rows) {  // blocks behind the rows: the padding
+            const int64_t count = a.scalars->count;
+            to = count + (r - a.rows);
+            if (to >= (count + kK - 1) / kK * kK) return;
+            zero = true;
+        } else {
+            to = a.inverse[r];
+            if (to < 0) {
+                if (a.grad != nullptr)
+                    for (int64_t k = threadIdx.x; k < a.dim; k += blockDim.x)
+                        put(a.grad, r * a.grad_ld + k, a.type, 0.f);
+                return;
+            }
+        }
+    }
+    uint16_t *hi = static_cast<uint16_t *>(a.hi) + to * a.pad;
+    if (a.type == RCS_F32) {
+        uint16_t *lo = static_cast<uint16_t *>(a.lo) + to * a.pad;
+        const int lift = lift_of(a.hidden ? a.scalars->top_h : a.scalars->top_w);
+        for (int64_t k = threadIdx.x; k < a.pad; k += blockDim.x) {
+            const float x = zero || k >= a.dim
+                                ? 0.f
+                                : ldexpf(static_cast<const float *>(a.src)[r * a.ld + k], lift);
+            const uint32_t h = two(x, 0.f, F16{});
+            const float rest = x - value((uint16_t)h, F16{});
+            hi[k] = (uint16_t)h;
+            lo[k] = (uint16_t)two(rest, 0.f, F16{});
+        }
+    } else {
+        for (int64_t k = threadIdx.x; k < a.pad; k += blockDim.x)
+            hi[k] = zero || k >= a.dim ? 0 : static_cast<const uint16_t *>(a.src)[r * a.ld + k];
+    }
+}
+
+// ------------------------------------------------------------------ products
+
+enum Op { kLogits, kHidden, kWeight };
+
+struct GemmArgs {
+    const void *x[2], *y[2];  // planes; the second of each only with float32
+    int64_t xld, yld;         // elements
+    int64_t xsize, ysize;     // elements from the first to the last one in memory
+    int64_t nx, ny, nk;       // extent of the product (ny, or nk of kWeight, at most: see count)
+    int64_t kper;             // of nk, for one split
+    int xtiles, ytiles;
+    int64_t row0;             // first row of this group of rows
+    const Scalars *scalars;
+    // kLogits
+    void *e[2];
+    int64_t eld;
+    f32x2 *parts;
+    int64_t groups;
+    float zscale;
+    bool store;
+    // kHidden
+    float *partial;
+    int64_t pld;
+    // kWeight
+    void *out;
+    int64_t old;
+    int out_type;
+    bool add;
+    float scale;
+    bool mean;
+    int gshift;
+};
+
+typedef __attribute__((address_space(3))) char lds_char;
+
+template <bool KCONTIG, int R, bool PERM>
+struct Side;
+
+// Columns of the tile run along memory's rows: R rows of kK consecutive values,
+// four 16-byte chunks each, chunk c of row r at slot c ^ turn(r).
+template <int R, bool PERM>
+struct Side<true, R, PERM> {
+    static constexpr int kCalls = R / 16 / 4;  // of one wave
+    static __device__ __forceinline__ int turn(int r) {
+        return PERM ? ((r >> 3 & 1) << 1 | ((r >> 1 ^ r >> 4) & 1))
+                    : ((r >> 2 & 1) << 1 | ((r >> 1 ^ r >> 3) & 1));
+    }
+    static __device__ __forceinline__ uint32_t source(int call, int lane, int64_t ld) {
+        const int r = call * 16 + lane / 4, c = (lane % 4) ^ turn(r);
+        return (uint32_t)(r * ld * 2 + c * 16);
+    }
+    static __device__ __forceinline__ uint32_t base(int at, int lane) {
+        const int m = lane % 16, g = lane / 16;
+        const int r = PERM ? 8 * (m >> 2) + (m & 3) : m;
+        return (uint32_t)((at + r) * 64 + ((g ^ turn(r)) * 16));
+    }
+    static __device__ __forceinline__ s16x8 read(const lds_char *p, uint32_t base, int i) {
+        const uint32_t at = PERM ? base + (i / 2) * 2048 + (i & 1) * 256 : base + i * 1024;
+        return *(const __attribute__((address_space(3))) s16x8 *)(p + at);
+    }
+};
+
+// Rows of memory run along the product's sum: kK rows of R consecutive values,
+// read back transposed. The R / 16 pairs of chunks of row k are turned by a
+// number that differs between the rows that one read takes.
+template <int R, bool PERM>
+struct Side<false, R, PERM> {
+    static constexpr int kCalls = R / 16 / 4;
+    static constexpr int kPairs = R / 16;
+    static __device__ __forceinline__ int turn(int k) {
+        return ((k & 3) | (k >> 3 & 3) << 2) & (kPairs - 1);
+    }
+    static __device__ __forceinline__ uint32_t source(int call, int lane, int64_t ld) {
+        constexpr int kSlots = R / 8, kRows = 64 / kSlots;
+        const int k = call * kRows + lane / kSlots, slot = lane % kSlots;
+        const int c = (((slot >> 1) ^ turn(k)) << 1) | (slot & 1);
+        return (uint32_t)(k * ld * 2 + c * 16);
+    }
+    static __device__ __forceinline__ uint32_t base(int at, int lane) {
+        const int s = lane % 16, k = 8 * (lane / 16) + s / 4;
+        return (uint32_t)(k * R * 2 + (((at / 16) ^ turn(k)) * 32) + (s % 4) * 8);
+    }
+    static __device__ __forceinline__ s16x8 read(const lds_char *p, uint32_t base, int i) {
+        typedef __attribute__((address_space(3))) s16x4 v;
+        const lds_char *q = p + (base ^ (uint32_t)(i * 32));
+        const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((v *)q);
+        const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((v *)(q + 4 * R * 2));
+        return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+};
+
+// Where a wave's loads of one operand's next step come from.
+struct Source {
+    const char *p;
+    int64_t left;  // bytes from p to the end of the array
+
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc() const {
+        const int64_t n = left < 0 ? 0 : left > 0xFFFFFFFFLL ? 0xFFFFFFFFLL : left;
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(p), 0, (int)(uint32_t)n,
+                                                 0x00020000);
+    }
+    __device__ __forceinline__ void advance(int64_t bytes) {
+        p += bytes;
+        left -= bytes;
+    }
+};
+
+template <class T, int OP, int PLANES>
+__global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
+#ifdef __HIP_DEVICE_COMPILE__  // the host needs the launch stub alone
+    using X = Side<OP == kLogits, kX, OP == kLogits>;
+    using Y = Side<OP != kWeight, kY, false>;
+    __shared__ __attribute__((aligned(1024))) char shared[kStages * kStageBytes];
+    lds_char *lds = (lds_char *)shared;
+    const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int wx = wave & 1, wy = wave >> 1;
+
+    const int64_t count = a.scalars->count - a.row0;
+    const int64_t b = blockIdx.x;
+    const int64_t tiles = (int64_t)a.xtiles * a.ytiles;
+    const int64_t split = b / tiles, tile = b % tiles;
+    const int64_t x0 = tile % a.xtiles * kX, y0 = tile / a.xtiles * kY;
+    const int64_t ny = OP == kWeight ? a.ny : min(a.ny, count);
+    if (y0 >= ny) return;
+    const int64_t nk_all = OP == kWeight ? max((int64_t)0, min(a.nk, count)) : a.nk;
+    const int64_t k0 = split * a.kper;
+    const int64_t nk = max((int64_t)0, min(a.kper, nk_all - k0));
+    if (OP == kWeight && a.add && nk == 0) return;
+    const int per = (int)((nk + kK - 1) / kK);  // steps of one pair of planes
+    constexpr int kPairsOfPlanes = PLANES == 1 ? 1 : 3;
+    const int steps = per * kPairsOfPlanes;
+
+    uint32_t xsrc[X::kCalls], ysrc[Y::kCalls];
+#pragma unroll
+    for (int c = 0; c < X::kCalls; ++c) xsrc[c] = X::source(wave * X::kCalls + c, lane, a.xld);
+#pragma unroll
+    for (int c = 0; c < Y::kCalls; ++c) ysrc[c] = Y::source(wave * Y::kCalls + c, lane, a.yld);
+    const int64_t xat = (OP == kLogits ? x0 * a.xld + k0 : k0 * a.xld + x0) * 2;
+    const int64_t yat = (OP != kWeight ? y0 * a.yld + k0 : k0 * a.yld + y0) * 2;
+    const int64_t xend = a.xsize * 2, yend = a.ysize * 2;
+    const int64_t xstep = OP == kLogits ? kK * 2 : a.xld * kK * 2;
+    const int64_t ystep = OP != kWeight ? kK * 2 : a.yld * kK * 2;
+    Source xs{static_cast<const char *>(a.x[0]) + xat, xend - xat};
+    Source ys{static_cast<const char *>(a.y[0]) + yat, yend - yat};
+    int issued = 0;
+    auto issue = [&](int stage) {
+        lds_char *to = lds + stage * kStageBytes;
+        const __amdgpu_buffer_rsrc_t rx = xs.rsrc(), ry = ys.rsrc();
+#pragma unroll
+        for (int c = 0; c < X::kCalls; ++c)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rx, (__attribute__((address_space(3))) void *)(to + (wave * X::kCalls + c) * 1024),
+                16, xsrc[c], 0, 0, 0);
+#pragma unroll
+        for (int c = 0; c < Y::kCalls; ++c)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                ry,
+                (__attribute__((address_space(3))) void *)(to + kXBytes +
+                                                           (wave * Y::kCalls + c) * 1024),
+                16, ysrc[c], 0, 0, 0);
+        ++issued;
+        if (PLANES > 1 && (issued == per || issued == 2 * per)) {  // low of x, then low of y
+            const int px = issued == per ? 1 : 0, py = issued == per ? 0 : 1;
+            xs = Source{static_cast<const char *>(a.x[px]) + xat, xend - xat};
+            ys = Source{static_cast<const char *>(a.y[py]) + yat, yend - yat};
+        } else {
+            xs.advance(xstep);
+            ys.advance(ystep);
+        }
+    };
+
+    f32x4 acc[8][4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const uint32_t xbase = X::base(wx * 128, lane);
+    const uint32_t ybase = Y::base(wy * 64, lane);
+
+    if (steps > 0) issue(0);
+    if (steps > 1) issue(1);
+    constexpr int kLoads = X::kCalls + Y::kCalls;
+    int stage = 0;
+    for (int it = 0; it < steps; ++it) {
+        // this step's tile has arrived, and the last one's reads are done
+        if (it + 1 < steps) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kLoads) : "memory");
+        else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        if (it + 2 < steps) issue(stage >= 1 ? stage - 1 : kStages - 1);
+        const lds_char *px = lds + stage * kStageBytes, *py = px + kXBytes;
+        s16x8 fx[8], fy[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) fy[j] = Y::read(py, ybase, j);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) fx[i] = X::read(px, xbase, i);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] = mfma(fx[i], fy[j], acc[i][j], T{});
+        stage = stage + 1 == kStages ? 0 : stage + 1;
+    }
+
+    const int g = lane / 16, col = lane % 16;
+    if constexpr (OP == kLogits) {
+        const float c1 = PLANES == 1 ? a.zscale
+                                     : a.zscale * pow2(-lift_of(a.scalars->top_h)) *
+                                           pow2(-lift_of(a.scalars->top_w));
+        const int64_t v0 = x0 + wx * 128;
+        constexpr float kHead = __is_same(T, F16) ? 15.f : 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int64_t i = y0 + wy * 64 + 16 * j + col;
+            float top = -INFINITY;
+#pragma unroll
+            for (int f = 0; f < 8; ++f)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    float z = acc[f][j][r] * c1;
+                    if (x0 + kX > a.nx && v0 + 32 * (f / 2) + 8 * g + 4 * (f & 1) + r >= a.nx)
+                        z = -INFINITY;
+                    acc[f][j][r] = z;
+                    top = fmaxf(top, z);
+                }
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            const float ref = top == -INFINITY ? 0.f : top - kHead;
+            float sum = 0.f;
+#pragma unroll
+            for (int f = 0; f < 8; ++f)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float e = exp2_(acc[f][j][r] - ref);
+                    acc[f][j][r] = e;
+                    sum += e;
+                }
+            sum += __shfl_xor(sum, 16);
+            sum += __shfl_xor(sum, 32);
+            if (i >= ny) continue;
+            if (g == 0 && v0 < a.nx) a.parts[i * a.groups + v0 / kGroup] = f32x2{ref, sum};
+            if (!a.store) continue;
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                float e[8];
+#pragma unroll
+                for (int r = 0; r < 8; ++r) e[r] = acc[2 * p + r / 4][j][r % 4];
+                u32x4 h;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) h[r] = two(e[2 * r], e[2 * r + 1], T{});
+                const int64_t at = i * a.eld + v0 + 32 * p + 8 * g;
+                *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(a.e[0]) + at) = h;
+                if (PLANES > 1) {
+                    u32x4 l;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        l[r] = two(e[2 * r] - value((uint16_t)h[r], T{}),
+                                   e[2 * r + 1] - value((uint16_t)(h[r] >> 16), T{}), T{});
+                    *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(a.e[1]) + at) = l;
+                }
+            }
+        }
+    } else if constexpr (OP == kHidden) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int64_t i = y0 + wy * 64 + 16 * j + col;
+            if (i >= ny) continue;
+#pragma unroll
+            for (int f = 0; f < 8; ++f) {
+                const int64_t n = x0 + wx * 128 + 16 * f + 4 * g;
+                if (n >= a.pld) continue;
+                *reinterpret_cast<f32x4 *>(a.partial + (split * a.ny + i) * a.pld + n) = acc[f][j];
+            }
+        }
+    } else {
+        float s = a.scale * pow2(-a.gshift);
+        if (a.mean) s /= (float)max(a.scalars->count, 1);
+        if (PLANES > 1) s *= pow2(-lift_of(a.scalars->top_h));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int64_t v = y0 + wy * 64 + 16 * j + col;
+            if (v >= a.ny) continue;
+#pragma unroll
+            for (int f = 0; f < 8; ++f) {
+                const int64_t n = x0 + wx * 128 + 16 * f + 4 * g;
+f32x4 x = acc[f][j] * s;
+                const int64_t at = v * a.old + n;
+                if (n + 4 <= a.nx) {
+                    if (a.add) x += load4(a.out, at, a.out_type);
+                    store4(a.out, at, a.out_type, x);
+                } else {
+                    for (int r = 0; r < 4 && n + r < a.nx; ++r)
+                        put(a.out, at + r, a.out_type,
+                            pick(x, r) + (a.add ? element(a.out, at + r, a.out_type) : 0.f));
+                }
+            }
+        }
+    }
+#endif
+}
+
+// ------------------------------------------------------------- rows of logits
+
+constexpr int kRowThreads = 256;
+constexpr int kMaxEntries = RCS_HEAD_MAX_ENTRIES;
+
+__device__ __forceinline__ float wave_sum(float x) {
+#pragma unroll
+    for (int d = 1; d < kWave; d *= 2) x += __shfl_xor(x, d);
+    return x;
+}
+__device__ __forceinline__ float wave_max(float x) {
+#pragma unroll
+    for (int d = 1; d < kWave; d *= 2) x = fmaxf(x, __shfl_xor(x, d));
+    return x;
+}
+struct Sum {
+    static __device__ __forceinline__ float of(float a, float b) { return a + b; }
+    static __device__ __forceinline__ float wave(float a) { return wave_sum(a); }
+};
+struct Max {
+    static __device__ __forceinline__ float of(float a, float b) { return fmaxf(a, b); }
+    static __device__ __forceinline__ float wave(float a) { return wave_max(a); }
+};
+// Over the block, in a fixed order; every lane gets it.
+template <class F>
+__device__ __forceinline__ float block_all(float x, float *shared) {
+    x = F::wave(x);
+    __syncthreads();
+    if (threadIdx.x % kWave == 0) shared[threadIdx.x / kWave] = x;
+    __syncthreads();
+    float y = shared[0];
+#pragma unroll
+    for (int w = 1; w < kRowThreads / kWave; ++w) y = F::of(y, shared[w]);
+    return y;
+}
+
+struct RowArgs {
+    const Scalars *scalars;
+    const int32_t *rowmap;
+    int64_t row0;
+    const f32x2 *parts;
+    int64_t groups, parts_ld, vocab;
+    void *g[2];
+    int64_t gld;
+    bool store;
+    int gshift;
+    const void *hidden, *weight;
+    int64_t hld, wld, dim;
+    int type;
+    const void *index, *logits;
+    int index_type, logits_type;
+    int64_t entries;
+    bool distill;
+    float tau;
+    float *losses;
+};
+
+// Row i of the logits: the sum of its exponentials from those of its groups, the
+// loss, and the exponentials turned into (softmax - target) * 2^gshift.
+template <class T, int PLANES>
+__global__ __launch_bounds__(kRowThreads) void head_rows(RowArgs a) {
+    __shared__ float shared[kRowThreads / kWave];
+    __shared__ float sp[kMaxEntries], sz[kMaxEntries];
+    __shared__ int64_t sv[kMaxEntries];
+    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+    const int64_t local = blockIdx.x, i = a.row0 + local;
+    const int64_t count = a.scalars->count;
+    if (i >= count) {
+        // zeros up to a whole step of the products' sums over the rows
+        if (!a.store || i >= a.row0 + (max((int64_t)0, count - a.row0) + kK - 1) / kK * kK) return;
+        const u32x4 zero = {0, 0, 0, 0};
+        for (int p = 0; p < PLANES; ++p) {
+            u32x4 *g = reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(a.g[p]) + local * a.gld);
+            for (int64_t k = tid; k < a.gld / 8; k += kRowThreads) g[k] = zero;
+        }
+        return;
+    }
+    const int64_t t = a.rowmap[i];
+    const f32x2 *parts = a.parts + local * a.parts_ld;
+    float top = -INFINITY;
+    for (int64_t k = tid; k < a.groups; k += kRowThreads) top = fmaxf(top, parts[k][0]);
+    top = block_all<Max>(top, shared);
+    float sum = 0.f;
+    for (int64_t k = tid; k < a.groups; k += kRowThreads)
+        sum += parts[k][1] * exp2_(parts[k][0] - top);
+    sum = block_all<Sum>(sum, shared);
+    float lse2 = top + __log2f(sum);
+
+    // the targets: their columns, probabilities and logits
+    const float zscale = kLog2e / a.tau;
+    const int entries = (int)a.entries;
+    const int64_t first = a.distill ? t * a.entries : t;
+    bool bad = false;
+    for (int k = tid; k < entries; k += kRowThreads) {
+        int64_t v = index_at(a.index, first + k, a.index_type);
+        float y = 0.f;
+        bool there = true;
+        if (a.distill) {
+            y = element(a.logits, first + k, a.logits_type);
+            there = v >= 0 && y != -INFINITY;
+        }
+        if (there && (v < 0 || v >= a.vocab)) bad = true;
+        sv[k] = there && !bad ? v : -1;
+        sp[k] = there ? y * zscale : -INFINITY;
+    }
+    if (block_all<Max>(bad ? 1.f : 0.f, shared) > 0.f) lse2 = __uint_as_float(0x7FC00000u);
+    for (int k = wave; k < entries; k += kRowThreads / kWave) {
+        const int64_t v = sv[k];
+        float dot = 0.f;
+        if (v >= 0)
+            for (int64_t n = lane; n < a.dim; n += kWave)
+                dot = fmaf(element(a.hidden, t * a.hld + n, a.type),
+                           element(a.weight, v * a.wld + n, a.type), dot);
+        dot = wave_sum(dot);
+        if (lane == 0) sz[k] = dot * zscale;
+    }
+    __syncthreads();
+    float loss;
+    if (!a.distill) {
+        loss = (lse2 - sz[0]) * kLn2;
+        if (loss < 0.f) loss = 0.f;
+        if (tid == 0) sp[0] = 1.f;
+    } else {
+        float m = -INFINITY;
+        for (int k = tid; k < entries; k += kRowThreads) m = fmaxf(m, sp[k]);
+        m = block_all<Max>(m, shared);
+        float s = 0.f;
+        for (int k = tid; k < entries; k += kRowThreads)
+            if (sv[k] >= 0) s += exp2_(sp[k] - m);
+        s = block_all<Sum>(s, shared);
+        const float l2 = m + __log2f(s);
+        float x = 0.f;
+        for (int k = tid; k < entries; k += kRowThreads) {
+            const float y = sp[k] - l2, p = sv[k] >= 0 ? exp2_(y) : 0.f;
+            if (sv[k] >= 0) x += p * (y - (sz[k] - lse2));
+            sp[k] = p;
+        }
+        x = block_all<Sum>(x, shared);
+        loss = x * kLn2 * a.tau * a.tau;
+    }
+    if (lse2 != lse2) loss = lse2;
+    if (tid == 0) a.losses[t] = loss;
+    if (!a.store) return;
+    __syncthreads();
+
+    // the row: exponentials times 2^(reference - lse + gshift)
+    for (int64_t k = tid; k < a.gld / 8; k += kRowThreads) {
+        const int64_t v = 8 * k;
+        u32x4 *gh = reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(a.g[0]) + local * a.gld) + k;
+        u32x4 *gl = reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(a.g[PLANES - 1]) +
+                                              local * a.gld) + k;
+        u32x4 h = {0, 0, 0, 0}, l = {0, 0, 0, 0};
+        if (v < a.vocab) {
+            const float f = exp2_(parts[v / kGroup][0] - lse2 + (float)a.gshift);
+            h = *gh;
+            if (PLANES > 1) l = *gl;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                float x = value((uint16_t)h[r], T{}), y = value((uint16_t)(h[r] >> 16), T{});
+                if (PLANES > 1) {
+                    x += value((uint16_t)l[r], T{});
+                    y += value((uint16_t)(l[r] >> 16), T{});
+                }
+                x = v + 2 * r < a.vocab ? x * f : 0.f;
+                y = v + 2 * r + 1 < a.vocab ? y * f : 0.f;
+                h[r] = two(x, y, T{});
+                if (PLANES > 1)
+                    l[r] = two(x - value((uint16_t)h[r], T{}),
+                               y - value((uint16_t)(h[r] >> 16), T{}), T{});
+            }
+        }
+        *gh = h;
+        if (PLANES > 1) *gl = l;
+    }
+    __syncthreads();
+    // less the targets: an index that comes several times once, with their sum
+    for (int k = tid; k < entries; k += kRowThreads) {
+        const int64_t v = sv[k];
+        if (v < 0) continue;
+        float p = 0.f;
+        bool seen = false;
+        for (int j = 0; j < entries; ++j)
+            if (sv[j] == v) {
+                p += sp[j];
+                seen |= j < k;
+            }
+        if (seen) continue;
+        const float x = (exp2_(sz[k] - lse2) - p) * pow2(a.gshift);
+        const uint32_t h = two(x, 0.f, T{});
+        static_cast<uint16_t *>(a.g[0])[local * a.gld + v] = (uint16_t)h;
+        if (PLANES > 1)
+            static_cast<uint16_t *>(a.g[1])[local * a.gld + v] =
+                (uint16_t)two(x - value((uint16_t)h, T{}), 0.f, T{});
+    }
+}
+
+// ------------------------------------------------------------------- results
+
+struct ReduceArgs {
+    const Scalars *scalars;
+    const int32_t *rowmap;
+    int64_t row0, rows, dim, pld;
+    const float *partial;
+    int splits;
+    void *out;
+    int64_t old;
+    int type;
+    float scale;
+    bool mean;
+    int gshift;
+};
+
+// The gradient of a hidden row: the sum of its splits, in their order.
+__global__ __launch_bounds__(256) void head_hidden(ReduceArgs a) {
+    const int64_t i = blockIdx.x;
+    const int64_t count = a.scalars->count;
+    if (a.row0 + i >= count) return;
+    float s = a.scale * pow2(-a.gshift);
+    if (a.mean) s /= (float)count;
+    if (a.type == RCS_F32) s *= pow2(-lift_of(a.scalars->top_w));
+    const int64_t t = a.rowmap[a.row0 + i];
+    for (int64_t n = threadIdx.x; n < a.dim; n += blockDim.x) {
+        float x = 0.f;
+        for (int k = 0; k < a.splits; ++k) x += a.partial[(k * a.rows + i) * a.pld + n];
+        put(a.out, t * a.old + n, a.type, x * s);
+    }
+}
+
+__global__ __launch_bounds__(256) void head_weight_out(const float *from, int64_t rows,
+                                                       int64_t dim, void *out, int64_t ld,
+                                                       int type, bool add) {
+    const int64_t v = blockIdx.x;
+    for (int64_t n = threadIdx.x; n < dim; n += blockDim.x) {
+        float x = from[v * dim + n];
+        if (add) x += element(out, v * ld + n, type);
+        put(out, v * ld + n, type, x);
+    }
+}
+
+// The loss of the rows that have one, in row order; rows without one are cleared.
+__global__ __launch_bounds__(1024) void head_total(const Scalars *scalars, const int32_t *inverse,
+                                                   float *losses, int64_t rows, bool mean,
+                                                   float *loss) {
+    __shared__ double shared[1024 / kWave];
+    double x = 0.0;
+    for (int64_t t = threadIdx.x; t < rows; t += 1024) {
+        if (inverse[t] >= 0) x += (double)losses[t];
+        else losses[t] = 0.f;
+    }
+#pragma unroll
+    for (int d = 1; d < kWave; d *= 2) x += __shfl_xor(x, d);
+    if (threadIdx.x % kWave == 0) shared[threadIdx.x / kWave] = x;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        x = 0.0;
+        for (int w = 0; w < 1024 / kWave; ++w) x += shared[w];
+        *loss = (float)(mean ? x / (double)max(scalars->count, 1) : x);
+    }
+}
+
+// ----------------------------------------------------------------- host side
+
+constexpr int64_t kMaxWidth = 1 << 20;        // of a row: offsets within a tile fit 32 bits
+constexpr int64_t kMaxRows = 1LL << 30;
+constexpr int64_t kCus = 256;
+
+int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+
+struct Plan {
+    int planes;
+    int64_t rows, vocab, dim, pad;   // pad: columns of the prepared rows
+    int64_t chunk;                   // rows of a group
+    int64_t eld, groups;
+    int splits;
+    int64_t kper;
+    bool copy_w, wide_out;
+    // offsets in the workspace
+    int64_t scalars, flags, rowmap, inverse, losses, h[2], w[2], e[2], parts, partial, acc, bytes;
+};
+
+bool direct_weight(const rcs_head *a) {
+    return a->type != RCS_F32 && a->dim % kK == 0 && a->weight_stride % 8 == 0 &&
+           (reinterpret_cast<uintptr_t>(a->weight) & 15u) == 0;
+}
+
+Plan plan_of(const rcs_head *a, int64_t limit) {
+    Plan p = {};
+    const bool grads = a->grad_hidden != nullptr || a->grad_weight != nullptr;
+    p.planes = a->type == RCS_F32 ? 2 : 1;
+    p.rows = a->rows, p.vocab = a->vocab, p.dim = a->dim;
+    p.pad = up(a->dim, kK);
+    p.eld = up(a->vocab, kX);
+    p.groups = p.eld / kGroup;
+    p.copy_w = !direct_weight(a);
+    // rows of a group: as many as fit the limit, in whole tiles
+    const int64_t row_bytes = (grads ? p.eld * 2 * p.planes : 0) + p.groups * 8;
+    p.chunk = up(a->rows > 0 ? a->rows : 1, kY);
+    const int64_t fit = limit / row_bytes / kY * kY;
+    if (p.chunk > fit) p.chunk = fit < kY ? kY : fit;
+    const int64_t tiles = up(p.dim, kX) / kX * (p.chunk / kY);
+    const int64_t steps = up(a->vocab, kK) / kK;
+    int64_t splits = (2 * kCus * 2 + tiles - 1) / tiles;
+    if (splits > steps / 16) splits = steps / 16;
+    if (splits < 1) splits = 1;
+    p.kper = up((steps + splits - 1) / splits, 1) * kK;
+    p.splits = (int)((steps * kK + p.kper - 1) / p.kper);
+    p.wide_out = a->grad_weight != nullptr && a->grad_weight_type != RCS_F32 && p.chunk < a->rows;
+    int64_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t was = at;
+        at = up(at + bytes, 256);
+        return was;
+    };
+    p.scalars = take(sizeof(Scalars));
+    p.flags = take(a->rows);
+    p.rowmap = take(4 * a->rows);
+    p.inverse = take(4 * a->rows);
+    p.losses = take(4 * a->rows);
+    for (int k = 0; k < p.planes; ++k) p.h[k] = take(2 * (a->rows + kK) * p.pad);
+    if (p.copy_w)
+        for (int k = 0; k < p.planes; ++k) p.w[k] = take(2 * a->vocab * p.pad);
+    p.parts = take(8 * p.chunk * p.groups);
+    if (grads)
+        for (int k = 0; k < p.planes; ++k) p.e[k] = take(2 * p.chunk * p.eld);
+    if (a->grad_hidden != nullptr) p.partial = take(4 * p.splits * p.chunk * p.pad);
+    if (p.wide_out) p.acc = take(4 * a->vocab * a->dim);
+    p.bytes = at;
+    return p;
+}
+
+int64_t size_of(int type) { return type == RCS_F32 ? 4 : 2; }
+bool is_type(int t) { return t == RCS_F32 || t == RCS_BF16 || t == RCS_F16; }
+
+int check_matrix(const void *p, int64_t rows, int64_t cols, int64_t ld, int type) {
+    if (ld < cols || ld > kMaxWidth) return RCS_EINVAL;
+    if (rows == 0) return RCS_OK;
+    const int64_t size = size_of(type);
+    if (p == nullptr || (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(size - 1)) != 0)
+        return RCS_EINVAL;
+    return rcs_check_device_range(p, ((rows - 1) * ld + cols) * size);
+}
+
+int check_array(const void *p, int64_t bytes, int align) {
+    if (bytes == 0) return RCS_OK;
+    if (p == nullptr || (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(align - 1)) != 0)
+        return RCS_EINVAL;
+    return rcs_check_device_range(p, bytes);
+}
+
+struct Targets {
+    const void *index;
+    int index_type;
+    int64_t entries;
+    const void *logits;
+    int logits_type;
+    int64_t ignore;
+    float tau;
+    bool distill;
+};
+
+int check_head(const rcs_head *a) {
+    if (a == nullptr) return RCS_EINVAL;
+    if (a->rows < 0 || a->rows > kMaxRows || a->vocab < 1 || a->vocab > kMaxRows || a->dim < 1 ||
+        a->dim > kMaxWidth || !is_type(a->type))
+        return RCS_EINVAL;
+    if (a->grad_weight != nullptr && !is_type(a->grad_weight_type)) return RCS_EINVAL;
+    return RCS_OK;
+}
+
+template <class T, int PLANES>
+void launch_products(const rcs_head *a, const Targets &tg, const Plan &p, char *ws,
+                     hipStream_t stream) {
+    const bool grads = a->grad_hidden != nullptr || a->grad_weight != nullptr;
+    Scalars *scalars = reinterpret_cast<Scalars *>(ws + p.scalars);
+    const int gshift = __is_same(T, F16) ? 14 : 0;
+    const float scale = a->scale * tg.tau;
+    float *losses = a->losses != nullptr ? a->losses : reinterpret_cast<float *>(ws + p.losses);
+    for (int64_t row0 = 0; row0 == 0 || row0 < a->rows; row0 += p.chunk) {
+        const int64_t rows = a->rows - row0 < p.chunk ? a->rows - row0 : p.chunk;
+        GemmArgs g = {};
+        g.scalars = scalars;
+        g.row0 = row0;
+        g.scale = scale;
+        g.mean = a->mean != 0;
+        g.gshift = gshift;
+        for (int k = 0; k < PLANES; ++k) {
+            g.x[k] = p.copy_w ? ws + p.w[k] : a->weight;
+            g.y[k] = ws + p.h[k] + 2 * row0 * p.pad;
+            g.e[k] = ws + p.e[k];
+        }
+        const int64_t wld = p.copy_w ? p.pad : a->weight_stride;
+        g.xld = wld, g.xsize = (a->vocab - 1) * wld + (p.copy_w ? p.pad : a->dim);
+        g.yld = p.pad, g.ysize = (a->rows + kK - row0) * p.pad;
+        g.nx = a->vocab, g.ny = rows, g.nk = p.pad, g.kper = p.pad;
+        g.xtiles = (int)(p.eld / kX), g.ytiles = (int)(up(rows, kY) / kY);
+        g.eld = p.eld, g.parts = reinterpret_cast<f32x2 *>(ws + p.parts), g.groups = p.groups;
+        g.zscale = kLog2e / tg.tau;
+        g.store = grads;
+        if (rows > 0)
+            head_gemm<T, kLogits, PLANES>
+                <<<dim3((unsigned)(g.xtiles * (int64_t)g.ytiles)), kGemmThreads, 0, stream>>>(g);
+
+        RowArgs r = {};
+        r.scalars = scalars;
+        r.rowmap = reinterpret_cast<int32_t *>(ws + p.rowmap);
+        r.row0 = row0;
+        r.parts = g.parts, r.groups = (a->vocab + kGroup - 1) / kGroup, r.vocab = a->vocab;
+        r.parts_ld = p.groups;
+        for (int k = 0; k < PLANES; ++k) r.g[k] = g.e[k];
+        r.gld = p.eld, r.store = grads, r.gshift = gshift;
+        r.hidden = a->hidden, r.weight = a->weight, r.hld = a->hidden_stride;
+        r.wld = a->weight_stride, r.dim = a->dim, r.type = a->type;
+        r.index = tg.index, r.logits = tg.logits, r.index_type = tg.index_type;
+        r.logits_type = tg.logits_type, r.entries = tg.entries, r.distill = tg.distill;
+        r.tau = tg.tau, r.losses = losses;
+        const int64_t row_blocks = grads ? up(rows, kK) : rows;
+        if (rows > 0)
+            head_rows<T, PLANES><<<dim3((unsigned)row_blocks), kRowThreads, 0, stream>>>(r);
+
+        if (a->grad_hidden != nullptr && rows > 0) {
+            GemmArgs q = g;
+            for (int k = 0; k < PLANES; ++k) q.y[k] = g.e[k];
+            q.yld = p.eld, q.ysize = p.chunk * p.eld;
+            q.nx = a->dim, q.ny = rows, q.nk = up(a->vocab, kK), q.kper = p.kper;
+            q.xtiles = (int)(up(a->dim, kX) / kX);
+            q.partial = reinterpret_cast<float *>(ws + p.partial), q.pld = p.pad;
+            head_gemm<T, kHidden, PLANES>
+                <<<dim3((unsigned)(q.xtiles * (int64_t)q.ytiles * p.splits)), kGemmThreads, 0,
+                   stream>>>(q);
+            ReduceArgs d = {};
+            d.scalars = scalars, d.rowmap = r.rowmap, d.row0 = row0, d.rows = rows;
+            d.dim = a->dim, d.pld = p.pad, d.partial = q.partial, d.splits = p.splits;
+            d.out = a->grad_hidden, d.old = a->grad_hidden_stride, d.type = a->type;
+            d.scale = scale, d.mean = g.mean, d.gshift = gshift;
+            head_hidden<<<dim3((unsigned)rows), 256, 0, stream>>>(d);
+        }
+        if (a->grad_weight != nullptr) {
+            GemmArgs q = g;
+            for (int k = 0; k < PLANES; ++k) q.x[k] = g.y[k], q.y[k] = g.e[k];
+            q.xld = p.pad, q.xsize = g.ysize;
+            q.yld = p.eld, q.ysize = p.chunk * p.eld;
+            q.nx = a->dim, q.ny = a->vocab, q.nk = rows, q.kper = up(rows, kK);
+            q.xtiles = (int)(up(a->dim, kX) / kX), q.ytiles = (int)(up(a->vocab, kY) / kY);
+            q.out = p.wide_out ? ws + p.acc : a->grad_weight;
+            q.old = p.wide_out ? a->dim : a->grad_weight_stride;
+            q.out_type = p.wide_out ? RCS_F32 : a->grad_weight_type;
+            q.add = row0 > 0 || (a->accumulate != 0 && !p.wide_out);
+            head_gemm<T, kWeight, PLANES>
+                <<<dim3((unsigned)(q.xtiles * (int64_t)q.ytiles)), kGemmThreads, 0, stream>>>(q);
+        }
+    }
+    if (p.wide_out)
+        head_weight_out<<<dim3((unsigned)a->vocab), 256, 0, stream>>>(
+            reinterpret_cast<float *>(ws + p.acc), a->vocab, a->dim, a->grad_weight,
+            a->grad_weight_stride, a->grad_weight_type, a->accumulate != 0);
+}
+
+int head_call(const rcs_head *a, const Targets &tg, hipStream_t stream) {
+    int rc = check_head(a);
+    if (rc != RCS_OK) return rc;
+    if (tg.index_type != RCS_I32 && tg.index_type != RCS_I64) return RCS_EINVAL;
+    if (!(std::isfinite(a->scale) && std::isfinite(tg.tau) && tg.tau > 0.f)) return RCS_EINVAL;
+    const int isize = tg.index_type == RCS_I32 ? 4 : 8;
+    const int64_t entries = a->rows * tg.entries;
+    struct {
+        const void *p;
+        int64_t bytes;
+    } reads[4], writes[4];
+    int nr = 0, nw = 0;
+    auto matrix = [&](const void *m, int64_t rows, int64_t ld, int type, bool write) {
+        const int r = check_matrix(m, rows, a->dim, ld, type);
+        if (r == RCS_OK && rows > 0) {
+            const int64_t bytes = ((rows - 1) * ld + a->dim) * size_of(type);
+            if (write) writes[nw++] = {m, bytes};
+            else reads[nr++] = {m, bytes};
+        }
+        return r;
+    };
+    if ((rc = matrix(a->hidden, a->rows, a->hidden_stride, a->type, false)) != RCS_OK) return rc;
+    if ((rc = matrix(a->weight, a->vocab, a->weight_stride, a->type, false)) != RCS_OK) return rc;
+    if ((rc = check_array(tg.index, entries * isize, isize)) != RCS_OK) return rc;
+    if (entries > 0) reads[nr++] = {tg.index, entries * isize};
+    if (tg.distill) {
+        if (!is_type(tg.logits_type)) return RCS_EINVAL;
+        const int64_t size = size_of(tg.logits_type);
+        if ((rc = check_array(tg.logits, entries * size, (int)size)) != RCS_OK) return rc;
+        if (entries > 0) reads[nr++] = {tg.logits, entries * size};
+    }
+    if (a->grad_hidden != nullptr &&
+        (rc = matrix(a->grad_hidden, a->rows, a->grad_hidden_stride, a->type, true)) != RCS_OK)
+        return rc;
+    if (a->grad_weight != nullptr && (rc = matrix(a->grad_weight, a->vocab, a->grad_weight_stride,
+                                                  a->grad_weight_type, true)) != RCS_OK)
+        return rc;
+    if (a->losses != nullptr) {
+        if ((rc = check_array(a->losses, 4 * a->rows, 4)) != RCS_OK) return rc;
+        if (a->rows > 0) writes[nw++] = {a->losses, 4 * a->rows};
+    }
+    if ((rc = check_array(a->loss, 4, 4)) != RCS_OK) return rc;
+    writes[nw++] = {a->loss, 4};
+    const Plan p = plan_of(a, a->limit);
+    if (a->workspace_bytes < p.bytes) return RCS_ESIZE;
+    if ((rc = check_array(a->workspace, p.bytes, 256)) != RCS_OK) return rc;
+    for (int k = 0; k < nw; ++k) {
+        if (rcs_overlaps(writes[k].p, writes[k].bytes, a->workspace, p.bytes)) return RCS_EINVAL;
+        for (int j = 0; j < nr; ++j)
+            if (rcs_overlaps(writes[k].p, writes[k].bytes, reads[j].p, reads[j].bytes))
+                return RCS_EINVAL;
+        for (int j = 0; j < k; ++j)
+            if (rcs_overlaps(writes[k].p, writes[k].bytes, writes[j].p, writes[j].bytes))
+                return RCS_EINVAL;
+    }
+    for (int j = 0; j < nr; ++j)
+        if (rcs_overlaps(a->workspace, p.bytes, reads[j].p, reads[j].bytes)) return RCS_EINVAL;
+
+    char *ws = static_cast<char *>(a->workspace);
+    Scalars *scalars = reinterpret_cast<Scalars *>(ws + p.scalars);
+    uint8_t *flags = reinterpret_cast<uint8_t *>(ws + p.flags);
+    int32_t *rowmap = reinterpret_cast<int32_t *>(ws + p.rowmap);
+    int32_t *inverse = reinterpret_cast<int32_t *>(ws + p.inverse);
+    float *losses = a->losses != nullptr ? a->losses : reinterpret_cast<float *>(ws + p.losses);
+    if (a->rows > 0)
+        head_flags<<<dim3((unsigned)((a->rows + 3) / 4)), 256, 0, stream>>>(
+            tg.index, tg.index_type, tg.entries, a->rows, tg.ignore, tg.logits, tg.logits_type,
+            tg.distill, flags);
+    head_scan<<<1, 1024, 0, stream>>>(flags, a->rows, rowmap, inverse, scalars);
+    if (a->type == RCS_F32) {
+        head_top<<<dim3(1024), 256, 0, stream>>>(static_cast<const float *>(a->hidden),
+                                                 a->hidden_stride, a->rows, a->dim, inverse,
+                                                 &scalars->top_h);
+        head_top<<<dim3(2048), 256, 0, stream>>>(static_cast<const float *>(a->weight),
+                                                 a->weight_stride, a->vocab, a->dim, nullptr,
+                                                 &scalars->top_w);
+    }
+    PrepArgs h = {};
+    h.src = a->hidden, h.hi = ws + p.h[0], h.lo = ws + p.h[p.planes - 1];
+    h.ld = a->hidden_stride, h.rows = a->rows, h.dim = a->dim, h.pad = p.pad, h.type = a->type;
+    h.inverse = inverse, h.scalars = scalars, h.hidden = true;
+    h.grad = a->grad_hidden, h.grad_ld = a->grad_hidden_stride;
+    head_prep<<<dim3((unsigned)(a->rows + kK)), 256, 0, stream>>>(h);
+    if (p.copy_w) {
+        PrepArgs w = {};
+        w.src = a->weight, w.hi = ws + p.w[0], w.lo = ws + p.w[p.planes - 1];
+        w.ld = a->weight_stride, w.rows = a->vocab, w.dim = a->dim, w.pad = p.pad;
+        w.type = a->type, w.scalars = scalars;
+        head_prep<<<dim3((unsigned)a->vocab), 256, 0, stream>>>(w);
+    }
+    if (a->type == RCS_F32) launch_products<F16, 2>(a, tg, p, ws, stream);
+    else if (a->type == RCS_F16) launch_products<F16, 1>(a, tg, p, ws, stream);
+    else launch_products<BF16, 1>(a, tg, p, ws, stream);
+    head_total<<<1, 1024, 0, stream>>>(scalars, inverse, losses, a->rows, a->mean != 0, a->loss);
+    return hipGetLastError() == hipSuccess ? RCS_OK : RCS_EHIP;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t rcs_head_workspace(const rcs_head *a) {
+    const int rc = check_head(a);
+    return rc != RCS_OK ? rc : plan_of(a, a->limit).bytes;
+}
+
+int head_loss(const rcs_head *a, const void *targets, int index_type, int64_t ignore_index,
+              hipStream_t stream) {
+    Targets tg = {targets, index_type, 1, nullptr, 0, ignore_index, 1.f, false};
+    return head_call(a, tg, stream);
+}
+
+int head_distill(const rcs_head *a, const void *indices, int index_type, const void *logits,
+                 int logits_type, int64_t entries, float temperature, hipStream_t stream) {
+    if (entries < 1 || entries > kMaxEntries) return RCS_EINVAL;
+    Targets tg = {indices, index_type, entries, logits, logits_type, 0, temperature, true};
+    return head_call(a, tg, stream);
+}
+
+}  // extern "C"

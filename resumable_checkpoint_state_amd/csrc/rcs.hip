@@ -1244,6 +1244,12 @@ int32_t get_le32(const unsigned char *p) {
 
 }  // namespace
 
+int rcs_check_device_range(const void *p, int64_t bytes) { return check_device_range(p, bytes); }
+
+bool rcs_overlaps(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes) {
+    return overlaps(a, a_bytes, b, b_bytes);
+}
+
 void rcs_snapshot_forget(int dev, const void *snapshot) {
     std::lock_guard<std::mutex> lk(g_mu);
     auto it = g_snap.find(std::make_pair(dev, snapshot));

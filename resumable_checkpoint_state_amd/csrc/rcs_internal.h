@@ -3,8 +3,16 @@
 #ifndef RCS_INTERNAL_H
 #define RCS_INTERNAL_H
 
+#include <cstdint>
+
 // Drops the events ckpt_pack_async keeps for a snapshot buffer of device dev
 // (call before freeing the buffer; no copy out of it may still be pending).
 void rcs_snapshot_forget(int dev, const void *snapshot);
+
+// RCS_OK if [p, p + bytes) is device (or managed) memory of the current device
+// and lies inside one allocation, as far as the runtime can tell.
+int rcs_check_device_range(const void *p, int64_t bytes);
+// Whether [a, a + a_bytes) and [b, b + b_bytes) share a byte.
+bool rcs_overlaps(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes);
 
 #endif
