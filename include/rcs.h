@@ -565,6 +565,22 @@ int head_distill(const rcs_head *args, const void *indices, int index_type, cons
                  int logits_type, int64_t entries, float temperature, hipStream_t stream);
 
 /*
+ * embed_grad: grad[tokens[t]] += scale * rows[t] for t in [0, count), the gradient
+ * of an embedding lookup (of tokens, or of positions). rows: (count, dim), grad:
+ * (vocab, dim), each of any of the three types, strides and alignment as for
+ * rcs_head. tokens: int32 or int64[count]; those outside [0, vocab) add nothing.
+ * The rows of a token are added up in float32, in runs whose bounds depend on
+ * tokens alone, and rounded once to grad's type; scale is finite. workspace:
+ * rcs_embed_workspace bytes of device memory, aligned to 256, used until the
+ * call's work is done; calls that may overlap on the device need one each.
+ */
+int64_t rcs_embed_workspace(int64_t count, int64_t vocab, int64_t dim);
+int embed_grad(const void *rows, int64_t rows_stride, int rows_type, int64_t count,
+               const void *tokens, int index_type, void *grad, int64_t grad_stride, int grad_type,
+               int64_t vocab, int64_t dim, float scale, void *workspace, int64_t workspace_bytes,
+               hipStream_t stream);
+
+/*
  * Instrumentation: while enabled, adamw_clip_step has its kernel dispatches
  * stamp HIP events (start of grad_norm_partial, end of the last norm kernel
  * -- grad_norm_partial itself when the update kernel does the final

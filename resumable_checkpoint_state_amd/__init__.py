@@ -24,7 +24,7 @@ __all__ = [
     "ckpt_pack", "ckpt_unpack", "init", "profile_enable", "profile_read",
     "strerror", "lib", "LIB_PATH", "build", "step_file_name", "MAX_N",
     "ckpt_pack_async", "ckpt_pack_wait", "CkptWriter", "StepFileCheckpointer", "AdamWList",
-    "head_loss", "head_distill",
+    "head_loss", "head_distill", "embed_grad",
 ]
 
 OK, EINVAL, ESIZE, EHEADER, EHIP, ENOMEM, EIO, ENOENT = 0, -1, -2, -3, -4, -5, -6, -7
@@ -140,6 +140,11 @@ def lib() -> ctypes.CDLL:
     L.head_loss.restype = ctypes.c_int
     L.head_distill.argtypes = [vp, vp, ctypes.c_int, vp, ctypes.c_int, i64, f32, vp]
     L.head_distill.restype = ctypes.c_int
+    L.rcs_embed_workspace.argtypes = [i64, i64, i64]
+    L.rcs_embed_workspace.restype = i64
+    L.embed_grad.argtypes = [vp, i64, ctypes.c_int, i64, vp, ctypes.c_int, vp, i64, ctypes.c_int,
+                             i64, i64, f32, vp, i64, vp]
+    L.embed_grad.restype = ctypes.c_int
     _lib = L
     return L
 
@@ -519,4 +524,4 @@ def profile_read():
 
 
 from .tensor_list import AdamWList  # noqa: E402  (uses the helpers above)
-from .head import head_distill, head_loss  # noqa: E402
+from .vocabulary import embed_grad, head_distill, head_loss  # noqa: E402

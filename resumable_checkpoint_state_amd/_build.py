@@ -8,6 +8,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SRC = os.path.join(PKG, "csrc", "rcs.hip")
 SRC_HEAD = os.path.join(PKG, "csrc", "head.hip")
+SRC_EMBED = os.path.join(PKG, "csrc", "embed.hip")
 SRC_IO = os.path.join(PKG, "csrc", "ckpt_io.cpp")
 SRC_WRITER = os.path.join(PKG, "csrc", "ckpt_writer.cpp")
 LIB = os.path.join(PKG, "librcs.so")
@@ -50,7 +51,7 @@ def hipcc_shared(sources: list[str], out: str, extra_flags: list[str] | None = N
 
 
 def build(extra_flags: list[str] | None = None, out: str | None = None) -> str:
-    return hipcc_shared([SRC, SRC_HEAD, SRC_IO, SRC_WRITER], out or LIB, extra_flags)
+    return hipcc_shared([SRC, SRC_HEAD, SRC_EMBED, SRC_IO, SRC_WRITER], out or LIB, extra_flags)
 
 
 def build_ceilings() -> str:

@@ -10,27 +10,18 @@
 
 #include "rcs.h"
 #include "rcs_internal.h"
+#include "vocab.h"
 
 #pragma clang fp contract(off)
 
 namespace {
 
-// ------------------------------------------------------------------- types
-
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-struct BF16 {};
-struct F16 {};
-
+#ifdef __HIP_DEVICE_COMPILE__
 __device__ __forceinline__ f32x4 mfma(s16x8 a, s16x8 b, f32x4 c, BF16) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
@@ -39,65 +30,9 @@ __device__ __forceinline__ f32x4 mfma(s16x8 a, s16x8 b, f32x4 c, F16) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
                                                   __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
-__device__ __forceinline__ uint32_t two(float a, float b, BF16) {
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
-}
-__device__ __forceinline__ uint32_t two(float a, float b, F16) {
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, f16x2));
-}
-__device__ __forceinline__ float value(uint16_t b, BF16) {
-    return __uint_as_float((uint32_t)b << 16);
-}
-__device__ __forceinline__ float value(uint16_t b, F16) {
-    return (float)__builtin_bit_cast(_Float16, b);
-}
+#endif
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// Element i of an array of type t (RCS_F32, RCS_BF16, RCS_F16).
-__device__ __forceinline__ float element(const void *p, int64_t i, int t) {
-    if (t == RCS_F32) return static_cast<const float *>(p)[i];
-    const uint16_t b = static_cast<const uint16_t *>(p)[i];
-    return t == RCS_BF16 ? value(b, BF16{}) : value(b, F16{});
-}
-__device__ __forceinline__ void put(void *p, int64_t i, int t, float x) {
-    if (t == RCS_F32) static_cast<float *>(p)[i] = x;
-    else static_cast<uint16_t *>(p)[i] =
-        (uint16_t)(t == RCS_BF16 ? two(x, 0.f, BF16{}) : two(x, 0.f, F16{}));
-}
-// Four consecutive elements, aligned to one: the hardware's vector accesses need
-// no more.
-typedef u32x4 u32x4_any __attribute__((aligned(4)));
-typedef u32x2 u32x2_any __attribute__((aligned(2)));
-template <class T>
-__device__ __forceinline__ f32x4 four(u32x2 b, T) {
-    return f32x4{value((uint16_t)b[0], T{}), value((uint16_t)(b[0] >> 16), T{}),
-                 value((uint16_t)b[1], T{}), value((uint16_t)(b[1] >> 16), T{})};
-}
-__device__ __forceinline__ f32x4 load4(const void *p, int64_t i, int t) {
-    if (t == RCS_F32)
-        return __builtin_bit_cast(
-            f32x4, *reinterpret_cast<const u32x4_any *>(static_cast<const float *>(p) + i));
-    const u32x2 b = *reinterpret_cast<const u32x2_any *>(static_cast<const uint16_t *>(p) + i);
-    return t == RCS_BF16 ? four(b, BF16{}) : four(b, F16{});
-}
-__device__ __forceinline__ void store4(void *p, int64_t i, int t, f32x4 x) {
-    if (t == RCS_F32) {
-        *reinterpret_cast<u32x4_any *>(static_cast<float *>(p) + i) = __builtin_bit_cast(u32x4, x);
-        return;
-    }
-    const u32x2 b = t == RCS_BF16 ? u32x2{two(x[0], x[1], BF16{}), two(x[2], x[3], BF16{})}
-                                  : u32x2{two(x[0], x[1], F16{}), two(x[2], x[3], F16{})};
-    *reinterpret_cast<u32x2_any *>(static_cast<uint16_t *>(p) + i) = b;
-}
-__device__ __forceinline__ float pick(f32x4 x, int r) {
-    return r == 0 ? x[0] : r == 1 ? x[1] : r == 2 ? x[2] : x[3];
-}
-__device__ __forceinline__ int64_t index_at(const void *p, int64_t i, int t) {
-    return t == RCS_I32 ? (int64_t) static_cast<const int32_t *>(p)[i]
-                        : static_cast<const int64_t *>(p)[i];
-}
-
-constexpr int kWave = 64;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
@@ -805,11 +740,7 @@ __global__ __launch_bounds__(1024) void head_total(const Scalars *scalars, const
 
 // ----------------------------------------------------------------- host side
 
-constexpr int64_t kMaxWidth = 1 << 20;        // of a row: offsets within a tile fit 32 bits
-constexpr int64_t kMaxRows = 1LL << 30;
 constexpr int64_t kCus = 256;
-
-int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
 struct Plan {
     int planes;
@@ -833,27 +764,27 @@ Plan plan_of(const rcs_head *a, int64_t limit) {
     const bool grads = a->grad_hidden != nullptr || a->grad_weight != nullptr;
     p.planes = a->type == RCS_F32 ? 2 : 1;
     p.rows = a->rows, p.vocab = a->vocab, p.dim = a->dim;
-    p.pad = up(a->dim, kK);
-    p.eld = up(a->vocab, kX);
+    p.pad = round_up(a->dim, kK);
+    p.eld = round_up(a->vocab, kX);
     p.groups = p.eld / kGroup;
     p.copy_w = !direct_weight(a);
     // rows of a group: as many as fit the limit, in whole tiles
     const int64_t row_bytes = (grads ? p.eld * 2 * p.planes : 0) + p.groups * 8;
-    p.chunk = up(a->rows > 0 ? a->rows : 1, kY);
+    p.chunk = round_up(a->rows > 0 ? a->rows : 1, kY);
     const int64_t fit = limit / row_bytes / kY * kY;
     if (p.chunk > fit) p.chunk = fit < kY ? kY : fit;
-    const int64_t tiles = up(p.dim, kX) / kX * (p.chunk / kY);
-    const int64_t steps = up(a->vocab, kK) / kK;
+    const int64_t tiles = round_up(p.dim, kX) / kX * (p.chunk / kY);
+    const int64_t steps = round_up(a->vocab, kK) / kK;
     int64_t splits = (2 * kCus * 2 + tiles - 1) / tiles;
     if (splits > steps / 16) splits = steps / 16;
     if (splits < 1) splits = 1;
-    p.kper = up((steps + splits - 1) / splits, 1) * kK;
+    p.kper = round_up((steps + splits - 1) / splits, 1) * kK;
     p.splits = (int)((steps * kK + p.kper - 1) / p.kper);
     p.wide_out = a->grad_weight != nullptr && a->grad_weight_type != RCS_F32 && p.chunk < a->rows;
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
         const int64_t was = at;
-        at = up(at + bytes, 256);
+        at = round_up(at + bytes, 256);
         return was;
     };
     p.scalars = take(sizeof(Scalars));
@@ -871,25 +802,6 @@ Plan plan_of(const rcs_head *a, int64_t limit) {
     if (p.wide_out) p.acc = take(4 * a->vocab * a->dim);
     p.bytes = at;
     return p;
-}
-
-int64_t size_of(int type) { return type == RCS_F32 ? 4 : 2; }
-bool is_type(int t) { return t == RCS_F32 || t == RCS_BF16 || t == RCS_F16; }
-
-int check_matrix(const void *p, int64_t rows, int64_t cols, int64_t ld, int type) {
-    if (ld < cols || ld > kMaxWidth) return RCS_EINVAL;
-    if (rows == 0) return RCS_OK;
-    const int64_t size = size_of(type);
-    if (p == nullptr || (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(size - 1)) != 0)
-        return RCS_EINVAL;
-    return rcs_check_device_range(p, ((rows - 1) * ld + cols) * size);
-}
-
-int check_array(const void *p, int64_t bytes, int align) {
-    if (bytes == 0) return RCS_OK;
-    if (p == nullptr || (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(align - 1)) != 0)
-        return RCS_EINVAL;
-    return rcs_check_device_range(p, bytes);
 }
 
 struct Targets {
@@ -937,7 +849,7 @@ void launch_products(const rcs_head *a, const Targets &tg, const Plan &p, char *
         g.xld = wld, g.xsize = (a->vocab - 1) * wld + (p.copy_w ? p.pad : a->dim);
         g.yld = p.pad, g.ysize = (a->rows + kK - row0) * p.pad;
         g.nx = a->vocab, g.ny = rows, g.nk = p.pad, g.kper = p.pad;
-        g.xtiles = (int)(p.eld / kX), g.ytiles = (int)(up(rows, kY) / kY);
+        g.xtiles = (int)(p.eld / kX), g.ytiles = (int)(round_up(rows, kY) / kY);
         g.eld = p.eld, g.parts = reinterpret_cast<f32x2 *>(ws + p.parts), g.groups = p.groups;
         g.zscale = kLog2e / tg.tau;
         g.store = grads;
@@ -958,7 +870,7 @@ void launch_products(const rcs_head *a, const Targets &tg, const Plan &p, char *
         r.index = tg.index, r.logits = tg.logits, r.index_type = tg.index_type;
         r.logits_type = tg.logits_type, r.entries = tg.entries, r.distill = tg.distill;
         r.tau = tg.tau, r.losses = losses;
-        const int64_t row_blocks = grads ? up(rows, kK) : rows;
+        const int64_t row_blocks = grads ? round_up(rows, kK) : rows;
         if (rows > 0)
             head_rows<T, PLANES><<<dim3((unsigned)row_blocks), kRowThreads, 0, stream>>>(r);
 
@@ -966,8 +878,8 @@ void launch_products(const rcs_head *a, const Targets &tg, const Plan &p, char *
             GemmArgs q = g;
             for (int k = 0; k < PLANES; ++k) q.y[k] = g.e[k];
             q.yld = p.eld, q.ysize = p.chunk * p.eld;
-            q.nx = a->dim, q.ny = rows, q.nk = up(a->vocab, kK), q.kper = p.kper;
-            q.xtiles = (int)(up(a->dim, kX) / kX);
+            q.nx = a->dim, q.ny = rows, q.nk = round_up(a->vocab, kK), q.kper = p.kper;
+            q.xtiles = (int)(round_up(a->dim, kX) / kX);
             q.partial = reinterpret_cast<float *>(ws + p.partial), q.pld = p.pad;
             head_gemm<T, kHidden, PLANES>
                 <<<dim3((unsigned)(q.xtiles * (int64_t)q.ytiles * p.splits)), kGemmThreads, 0,
@@ -984,8 +896,8 @@ void launch_products(const rcs_head *a, const Targets &tg, const Plan &p, char *
             for (int k = 0; k < PLANES; ++k) q.x[k] = g.y[k], q.y[k] = g.e[k];
             q.xld = p.pad, q.xsize = g.ysize;
             q.yld = p.eld, q.ysize = p.chunk * p.eld;
-            q.nx = a->dim, q.ny = a->vocab, q.nk = rows, q.kper = up(rows, kK);
-            q.xtiles = (int)(up(a->dim, kX) / kX), q.ytiles = (int)(up(a->vocab, kY) / kY);
+            q.nx = a->dim, q.ny = a->vocab, q.nk = rows, q.kper = round_up(rows, kK);
+            q.xtiles = (int)(round_up(a->dim, kX) / kX), q.ytiles = (int)(round_up(a->vocab, kY) / kY);
             q.out = p.wide_out ? ws + p.acc : a->grad_weight;
             q.old = p.wide_out ? a->dim : a->grad_weight_stride;
             q.out_type = p.wide_out ? RCS_F32 : a->grad_weight_type;
@@ -1003,60 +915,35 @@ void launch_products(const rcs_head *a, const Targets &tg, const Plan &p, char *
 int head_call(const rcs_head *a, const Targets &tg, hipStream_t stream) {
     int rc = check_head(a);
     if (rc != RCS_OK) return rc;
-    if (tg.index_type != RCS_I32 && tg.index_type != RCS_I64) return RCS_EINVAL;
+    if (!is_index_type(tg.index_type)) return RCS_EINVAL;
     if (!(std::isfinite(a->scale) && std::isfinite(tg.tau) && tg.tau > 0.f)) return RCS_EINVAL;
-    const int isize = tg.index_type == RCS_I32 ? 4 : 8;
+    const int isize = index_size(tg.index_type);
     const int64_t entries = a->rows * tg.entries;
-    struct {
-        const void *p;
-        int64_t bytes;
-    } reads[4], writes[4];
-    int nr = 0, nw = 0;
-    auto matrix = [&](const void *m, int64_t rows, int64_t ld, int type, bool write) {
-        const int r = check_matrix(m, rows, a->dim, ld, type);
-        if (r == RCS_OK && rows > 0) {
-            const int64_t bytes = ((rows - 1) * ld + a->dim) * size_of(type);
-            if (write) writes[nw++] = {m, bytes};
-            else reads[nr++] = {m, bytes};
-        }
-        return r;
-    };
-    if ((rc = matrix(a->hidden, a->rows, a->hidden_stride, a->type, false)) != RCS_OK) return rc;
-    if ((rc = matrix(a->weight, a->vocab, a->weight_stride, a->type, false)) != RCS_OK) return rc;
-    if ((rc = check_array(tg.index, entries * isize, isize)) != RCS_OK) return rc;
-    if (entries > 0) reads[nr++] = {tg.index, entries * isize};
+    Extents reads, writes;
+    if ((rc = reads.matrix(a->hidden, a->rows, a->dim, a->hidden_stride, a->type)) != RCS_OK ||
+        (rc = reads.matrix(a->weight, a->vocab, a->dim, a->weight_stride, a->type)) != RCS_OK ||
+        (rc = reads.array(tg.index, entries * isize, isize)) != RCS_OK)
+        return rc;
     if (tg.distill) {
         if (!is_type(tg.logits_type)) return RCS_EINVAL;
-        const int64_t size = size_of(tg.logits_type);
-        if ((rc = check_array(tg.logits, entries * size, (int)size)) != RCS_OK) return rc;
-        if (entries > 0) reads[nr++] = {tg.logits, entries * size};
+        const int size = type_size(tg.logits_type);
+        if ((rc = reads.array(tg.logits, entries * size, size)) != RCS_OK) return rc;
     }
     if (a->grad_hidden != nullptr &&
-        (rc = matrix(a->grad_hidden, a->rows, a->grad_hidden_stride, a->type, true)) != RCS_OK)
+        (rc = writes.matrix(a->grad_hidden, a->rows, a->dim, a->grad_hidden_stride, a->type)) !=
+            RCS_OK)
         return rc;
-    if (a->grad_weight != nullptr && (rc = matrix(a->grad_weight, a->vocab, a->grad_weight_stride,
-                                                  a->grad_weight_type, true)) != RCS_OK)
+    if (a->grad_weight != nullptr &&
+        (rc = writes.matrix(a->grad_weight, a->vocab, a->dim, a->grad_weight_stride,
+                            a->grad_weight_type)) != RCS_OK)
         return rc;
-    if (a->losses != nullptr) {
-        if ((rc = check_array(a->losses, 4 * a->rows, 4)) != RCS_OK) return rc;
-        if (a->rows > 0) writes[nw++] = {a->losses, 4 * a->rows};
-    }
-    if ((rc = check_array(a->loss, 4, 4)) != RCS_OK) return rc;
-    writes[nw++] = {a->loss, 4};
+    if (a->losses != nullptr && (rc = writes.array(a->losses, 4 * a->rows, 4)) != RCS_OK)
+        return rc;
+    if ((rc = writes.array(a->loss, 4, 4)) != RCS_OK) return rc;
     const Plan p = plan_of(a, a->limit);
     if (a->workspace_bytes < p.bytes) return RCS_ESIZE;
-    if ((rc = check_array(a->workspace, p.bytes, 256)) != RCS_OK) return rc;
-    for (int k = 0; k < nw; ++k) {
-        if (rcs_overlaps(writes[k].p, writes[k].bytes, a->workspace, p.bytes)) return RCS_EINVAL;
-        for (int j = 0; j < nr; ++j)
-            if (rcs_overlaps(writes[k].p, writes[k].bytes, reads[j].p, reads[j].bytes))
-                return RCS_EINVAL;
-        for (int j = 0; j < k; ++j)
-            if (rcs_overlaps(writes[k].p, writes[k].bytes, writes[j].p, writes[j].bytes))
-                return RCS_EINVAL;
-    }
-    for (int j = 0; j < nr; ++j)
-        if (rcs_overlaps(a->workspace, p.bytes, reads[j].p, reads[j].bytes)) return RCS_EINVAL;
+    if ((rc = writes.array(a->workspace, p.bytes, 256)) != RCS_OK) return rc;
+    if (writes.overlap(reads)) return RCS_EINVAL;
 
     char *ws = static_cast<char *>(a->workspace);
     Scalars *scalars = reinterpret_cast<Scalars *>(ws + p.scalars);

@@ -1,7 +1,9 @@
-"""A model's output head in training: a thin binding of head_loss and head_distill.
+"""The two ends of a model at its vocabulary, in training: a thin binding of the
+output head's losses (head_loss, head_distill) and of the embedding's gradient
+(embed_grad).
 
 Argument marshalling only, as in the rest of the package: everything is computed
-in the HIP kernels of csrc/head.hip.
+in the HIP kernels of csrc/head.hip and csrc/embed.hip.
 """
 from __future__ import annotations
 
@@ -110,8 +112,8 @@ def _head(call, name, hidden, weight, grad_hidden, grad_weight, accumulate, redu
     with _stream_context(stream):
         if out is None:
             out = torch.empty(1, dtype=torch.float32, device=h.device)
-        elif _packed(out, "out", dev, (torch.float32,), torch.Size([1])) is None:
-            pass
+        else:
+            _packed(out, "out", dev, (torch.float32,), torch.Size([1]))
         work = torch.empty(need, dtype=torch.uint8, device=h.device)
         a.loss, a.workspace, a.workspace_bytes = out.data_ptr(), work.data_ptr(), need
         _check(call(ctypes.byref(a), _stream(stream)), name)
@@ -179,3 +181,29 @@ def head_distill(hidden, weight, indices, logits, *, temperature: float = 1.0, g
 
     return _head(call, "head_distill", hidden, weight, grad_hidden, grad_weight, accumulate,
                  reduction, scale, losses, out, max_bytes, stream)
+
+
+def embed_grad(rows, tokens, grad, *, scale: float = 1.0, stream=None) -> None:
+    """grad[tokens[...]] += scale * rows[...], the gradient of an embedding lookup,
+    in an order that depends on the arguments alone; asynchronous on stream.
+
+    rows (..., dim): the gradient of what was looked up; grad (vocab, dim): of the
+    matrix (of tokens or of positions); each float32, bfloat16 or float16, with
+    contiguous rows at one stride. tokens (...): int32 or int64; those outside
+    [0, vocab) add nothing. Each token's rows are added up in float32 and rounded
+    once to grad's type."""
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    r, rs = _matrix(rows, "rows", dev, _TYPES)
+    g, gs = _matrix(grad, "grad", dev, _TYPES)
+    if grad.dim() != 2 or g.shape[1] != r.shape[1] or g.shape[0] == 0:
+        raise ValueError(f"grad has shape {tuple(grad.shape)}, expected (vocab, {r.shape[1]})")
+    t = _packed(tokens, "tokens", dev, _INDEX_TYPES, rows.shape[:-1])
+    count, (vocab, dim) = r.shape[0], g.shape
+    need = lib().rcs_embed_workspace(count, vocab, dim)
+    _check(int(need) if need < 0 else 0, "rcs_embed_workspace")
+    with _stream_context(stream):
+        work = torch.empty(need, dtype=torch.uint8, device=g.device)
+        _check(lib().embed_grad(r.data_ptr(), rs, _TYPES[r.dtype], count, t.data_ptr(),
+                                _INDEX_TYPES[t.dtype], g.data_ptr(), gs, _TYPES[g.dtype], vocab,
+                                dim, float(scale), work.data_ptr(), need, _stream(stream)),
+               "embed_grad")
