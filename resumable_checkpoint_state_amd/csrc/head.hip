@@ -36,12 +36,12 @@ __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
-// Tiles of a product: kX by kY outputs by a block of four waves, kK at a time.
-constexpr int kX = 256, kY = 128, kK = 32;
+// Tiles of a product: kX by kY outputs by a block of eight waves, each 128 by 64 of
+// them, kK at a time, from two places in LDS in turn.
+constexpr int kX = 256, kY = 256, kK = 64;
 constexpr int kGroup = 128;  // columns of the logits with a reference of their own
-constexpr int kGemmThreads = 256;
-constexpr int kStages = 3;
-constexpr int kXBytes = kX * kK * 2, kYBytes = kY * kK * 2, kStageBytes = kXBytes + kYBytes;
+constexpr int kGemmThreads = 512, kGemmWaves = kGemmThreads / kWave;
+constexpr int kXBytes = kX * kK * 2, kStageBytes = kXBytes + kY * kK * 2;
 
 // What the kernels of one call tell each other, in device memory.
 struct Scalars {
@@ -212,72 +212,107 @@ struct GemmArgs {
 };
 
 typedef __attribute__((address_space(3))) char lds_char;
+template <int N>
+struct Int {
+    static constexpr int value = N;
+};
 
-template <bool KCONTIG, int R, bool PERM>
+constexpr int kCalls = 256 * kK * 2 / 1024 / kGemmWaves;  // loads of a wave for one operand
+
+// How an operand's tile of 256 by kK lies in LDS: in `kCalls` loads a wave, each of
+// 1,024 consecutive bytes (source: where a lane's 16 come from), and how a wave
+// reads its fragments of 16 by 32 (base: of the first one; read: fragment i of the
+// tile's half `half` of the sum).
+template <bool KCONTIG, bool PERM>
 struct Side;
 
-// Columns of the tile run along memory's rows: R rows of kK consecutive values,
-// four 16-byte chunks each, chunk c of row r at slot c ^ turn(r).
-template <int R, bool PERM>
-struct Side<true, R, PERM> {
-    static constexpr int kCalls = R / 16 / 4;  // of one wave
+// The sum runs along memory's rows: 256 rows of kK consecutive values, eight
+// 16-byte chunks (a line of 128 bytes) each, chunk c of row r at slot c ^ turn(r).
+// A read of 16 rows is served 16 lanes at a time, the lanes of rows 0-3 and 12-15
+// with those of rows 4-11 of the next chunk: turned so, each such group meets all
+// 64 banks once. With PERM, fragments 2i and 2i + 1 take their 32 rows in turns of
+// four, so that a lane's results from both are of eight consecutive rows.
+template <bool PERM>
+struct Side<true, PERM> {
     static __device__ __forceinline__ int turn(int r) {
-        return PERM ? ((r >> 3 & 1) << 1 | ((r >> 1 ^ r >> 4) & 1))
-                    : ((r >> 2 & 1) << 1 | ((r >> 1 ^ r >> 3) & 1));
+        return PERM ? (r >> 2 & 6) | (r >> 1 & 1) : r >> 1 & 7;
     }
     static __device__ __forceinline__ uint32_t source(int call, int lane, int64_t ld) {
-        const int r = call * 16 + lane / 4, c = (lane % 4) ^ turn(r);
+        const int r = call * 8 + lane / 8, c = (lane % 8) ^ turn(r);
         return (uint32_t)(r * ld * 2 + c * 16);
     }
     static __device__ __forceinline__ uint32_t base(int at, int lane) {
         const int m = lane % 16, g = lane / 16;
         const int r = PERM ? 8 * (m >> 2) + (m & 3) : m;
-        return (uint32_t)((at + r) * 64 + ((g ^ turn(r)) * 16));
+        return (uint32_t)((at + r) * 128 + ((g ^ turn(r)) * 16));
     }
-    static __device__ __forceinline__ s16x8 read(const lds_char *p, uint32_t base, int i) {
-        const uint32_t at = PERM ? base + (i / 2) * 2048 + (i & 1) * 256 : base + i * 1024;
+    static __device__ __forceinline__ s16x8 read(const lds_char *p, uint32_t base, int i,
+                                                 int half) {
+        const uint32_t at = (base ^ (uint32_t)(half * 64)) +
+                            (PERM ? (i / 2) * 4096 + (i & 1) * 512 : i * 2048);
         return *(const __attribute__((address_space(3))) s16x8 *)(p + at);
     }
 };
 
-// Rows of memory run along the product's sum: kK rows of R consecutive values,
-// read back transposed. The R / 16 pairs of chunks of row k are turned by a
-// number that differs between the rows that one read takes.
-template <int R, bool PERM>
-struct Side<false, R, PERM> {
-    static constexpr int kCalls = R / 16 / 4;
-    static constexpr int kPairs = R / 16;
-    static __device__ __forceinline__ int turn(int k) {
-        return ((k & 3) | (k >> 3 & 3) << 2) & (kPairs - 1);
-    }
+// The sum runs across memory's rows: kK rows of 256 consecutive values, read back
+// transposed. The 16 pairs of chunks of row k are turned by a number that differs
+// between the rows that one read takes.
+template <bool PERM>
+struct Side<false, PERM> {
+    static __device__ __forceinline__ int turn(int k) { return (k & 3) | (k >> 3 & 3) << 2; }
     static __device__ __forceinline__ uint32_t source(int call, int lane, int64_t ld) {
-        constexpr int kSlots = R / 8, kRows = 64 / kSlots;
-        const int k = call * kRows + lane / kSlots, slot = lane % kSlots;
+        const int k = call * 2 + lane / 32, slot = lane % 32;
         const int c = (((slot >> 1) ^ turn(k)) << 1) | (slot & 1);
         return (uint32_t)(k * ld * 2 + c * 16);
     }
     static __device__ __forceinline__ uint32_t base(int at, int lane) {
         const int s = lane % 16, k = 8 * (lane / 16) + s / 4;
-        return (uint32_t)(k * R * 2 + (((at / 16) ^ turn(k)) * 32) + (s % 4) * 8);
+        return (uint32_t)(k * 512 + (((at / 16) ^ turn(k)) * 32) + (s % 4) * 8);
     }
-    static __device__ __forceinline__ s16x8 read(const lds_char *p, uint32_t base, int i) {
+    static __device__ __forceinline__ s16x8 read(const lds_char *p, uint32_t base, int i,
+                                                 int half) {
         typedef __attribute__((address_space(3))) s16x4 v;
-        const lds_char *q = p + (base ^ (uint32_t)(i * 32));
+        const lds_char *q = p + (base ^ (uint32_t)(i * 32)) + half * 32 * 512;
         const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((v *)q);
-        const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((v *)(q + 4 * R * 2));
+        const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((v *)(q + 4 * 512));
         return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
     }
 };
+
+// The tile of block b of a product. Blocks are dispatched round-robin over the 8
+// XCDs, each with an L2 of its own: an XCD takes a stretch of its own of the
+// order below, in which the 64 blocks that it runs at once share few operand
+// tiles: bands of kBand y tiles, and along a band all y of an x, then the next.
+constexpr int kBand = 8;
+__device__ __forceinline__ void tile_of(int b, int xtiles, int ytiles, int &tx, int &ty) {
+    const int n = xtiles * ytiles, per = n / 8, more = n % 8, xcd = b % 8;
+    const int at = xcd * per + min(xcd, more) + b / 8;
+    const int band = at / (kBand * xtiles), rest = at % (kBand * xtiles);
+    const int high = min(kBand, ytiles - band * kBand);
+    tx = rest / high;
+    ty = band * kBand + rest % high;
+}
+
+// 16 bytes a lane from `at` bytes into the buffer on, to 1,024 consecutive bytes of
+// LDS. (Written out, because the compiler would let each transposing read of LDS
+// wait for all such loads, the ones for later steps too. It has no result
+// register, and `arrive` below waits for it.)
+__device__ __forceinline__ void load_lds(u32x4 buffer, uint32_t at, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to),
+                 "v"(at), "s"(buffer)
+                 : "memory");
+}
 
 // Where a wave's loads of one operand's next step come from.
 struct Source {
     const char *p;
     int64_t left;  // bytes from p to the end of the array
 
-    __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc() const {
+    // A buffer of the bytes that are left: loads behind its end give zeros.
+    __device__ __forceinline__ u32x4 buffer() const {
+        const uint64_t at = reinterpret_cast<uint64_t>(p);
         const int64_t n = left < 0 ? 0 : left > 0xFFFFFFFFLL ? 0xFFFFFFFFLL : left;
-        return __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(p), 0, (int)(uint32_t)n,
-                                                 0x00020000);
+        return u32x4{(uint32_t)at, (uint32_t)(at >> 32) & 0xFFFFu, (uint32_t)n, 0x00020000u};
     }
     __device__ __forceinline__ void advance(int64_t bytes) {
         p += bytes;
@@ -288,33 +323,35 @@ struct Source {
 template <class T, int OP, int PLANES>
 __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
 #ifdef __HIP_DEVICE_COMPILE__  // the host needs the launch stub alone
-    using X = Side<OP == kLogits, kX, OP == kLogits>;
-    using Y = Side<OP != kWeight, kY, false>;
-    __shared__ __attribute__((aligned(1024))) char shared[kStages * kStageBytes];
+    using X = Side<OP == kLogits, OP == kLogits>;
+    using Y = Side<OP != kWeight, false>;
+    __shared__ __attribute__((aligned(1024))) char shared[2 * kStageBytes];
     lds_char *lds = (lds_char *)shared;
+    const uint32_t lds_at = (uint32_t)(uintptr_t)lds;
     const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int wx = wave & 1, wy = wave >> 1;
 
     const int64_t count = a.scalars->count - a.row0;
-    const int64_t b = blockIdx.x;
-    const int64_t tiles = (int64_t)a.xtiles * a.ytiles;
-    const int64_t split = b / tiles, tile = b % tiles;
-    const int64_t x0 = tile % a.xtiles * kX, y0 = tile / a.xtiles * kY;
+    const int tiles = a.xtiles * a.ytiles;
+    const int split = blockIdx.x / tiles;
+    int tx, ty;
+    tile_of(blockIdx.x % tiles, a.xtiles, a.ytiles, tx, ty);
+    const int64_t x0 = (int64_t)tx * kX, y0 = (int64_t)ty * kY;
     const int64_t ny = OP == kWeight ? a.ny : min(a.ny, count);
     if (y0 >= ny) return;
     const int64_t nk_all = OP == kWeight ? max((int64_t)0, min(a.nk, count)) : a.nk;
-    const int64_t k0 = split * a.kper;
+    const int64_t k0 = (int64_t)split * a.kper;
     const int64_t nk = max((int64_t)0, min(a.kper, nk_all - k0));
     if (OP == kWeight && a.add && nk == 0) return;
     const int per = (int)((nk + kK - 1) / kK);  // steps of one pair of planes
     constexpr int kPairsOfPlanes = PLANES == 1 ? 1 : 3;
     const int steps = per * kPairsOfPlanes;
 
-    uint32_t xsrc[X::kCalls], ysrc[Y::kCalls];
+    uint32_t xsrc[kCalls], ysrc[kCalls];
 #pragma unroll
-    for (int c = 0; c < X::kCalls; ++c) xsrc[c] = X::source(wave * X::kCalls + c, lane, a.xld);
+    for (int c = 0; c < kCalls; ++c) xsrc[c] = X::source(wave * kCalls + c, lane, a.xld);
 #pragma unroll
-    for (int c = 0; c < Y::kCalls; ++c) ysrc[c] = Y::source(wave * Y::kCalls + c, lane, a.yld);
+    for (int c = 0; c < kCalls; ++c) ysrc[c] = Y::source(wave * kCalls + c, lane, a.yld);
     const int64_t xat = (OP == kLogits ? x0 * a.xld + k0 : k0 * a.xld + x0) * 2;
     const int64_t yat = (OP != kWeight ? y0 * a.yld + k0 : k0 * a.yld + y0) * 2;
     const int64_t xend = a.xsize * 2, yend = a.ysize * 2;
@@ -324,20 +361,14 @@ __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
     Source ys{static_cast<const char *>(a.y[0]) + yat, yend - yat};
     int issued = 0;
     auto issue = [&](int stage) {
-        lds_char *to = lds + stage * kStageBytes;
-        const __amdgpu_buffer_rsrc_t rx = xs.rsrc(), ry = ys.rsrc();
+        const uint32_t to = lds_at + (uint32_t)(stage * kStageBytes);
+        const u32x4 bx = xs.buffer(), by = ys.buffer();
 #pragma unroll
-        for (int c = 0; c < X::kCalls; ++c)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                rx, (__attribute__((address_space(3))) void *)(to + (wave * X::kCalls + c) * 1024),
-                16, xsrc[c], 0, 0, 0);
+        for (int c = 0; c < kCalls; ++c)
+            load_lds(bx, xsrc[c], to + (wave * kCalls + c) * 1024);
 #pragma unroll
-        for (int c = 0; c < Y::kCalls; ++c)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                ry,
-                (__attribute__((address_space(3))) void *)(to + kXBytes +
-                                                           (wave * Y::kCalls + c) * 1024),
-                16, ysrc[c], 0, 0, 0);
+        for (int c = 0; c < kCalls; ++c)
+            load_lds(by, ysrc[c], to + kXBytes + (wave * kCalls + c) * 1024);
         ++issued;
         if (PLANES > 1 && (issued == per || issued == 2 * per)) {  // low of x, then low of y
             const int px = issued == per ? 1 : 0, py = issued == per ? 0 : 1;
@@ -357,28 +388,60 @@ __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
     const uint32_t xbase = X::base(wx * 128, lane);
     const uint32_t ybase = Y::base(wy * 64, lane);
 
-    if (steps > 0) issue(0);
-    if (steps > 1) issue(1);
-    constexpr int kLoads = X::kCalls + Y::kCalls;
-    int stage = 0;
-    for (int it = 0; it < steps; ++it) {
-        // this step's tile has arrived, and the last one's reads are done
-        if (it + 1 < steps) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kLoads) : "memory");
-        else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
-        if (it + 2 < steps) issue(stage >= 1 ? stage - 1 : kStages - 1);
+    // While one half of a step is multiplied out of registers, the next half is read
+    // into others. Between a step's halves, when every wave has read the whole of its
+    // tile and the next one has arrived, the one after that is loaded in its place.
+    s16x8 fx[2][8], fy[2][4];
+    auto read = [&](int stage, auto half) {
+        constexpr int h = decltype(half)::value;
         const lds_char *px = lds + stage * kStageBytes, *py = px + kXBytes;
-        s16x8 fx[8], fy[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) fy[j] = Y::read(py, ybase, j);
+        for (int j = 0; j < 4; ++j) fy[h][j] = Y::read(py, ybase, j, h);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) fx[i] = X::read(px, xbase, i);
+        for (int i = 0; i < 8; ++i) fx[h][i] = X::read(px, xbase, i, h);
+    };
+    auto multiply = [&](auto half) {
+        constexpr int h = decltype(half)::value;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = mfma(fx[i], fy[j], acc[i][j], T{});
-        stage = stage + 1 == kStages ? 0 : stage + 1;
+            for (int j = 0; j < 4; ++j) acc[i][j] = mfma(fx[h][i], fy[h][j], acc[i][j], T{});
+    };
+    // this wave's reads are done, and all but the last n of its loads; then every wave's
+    auto arrive = [&](auto behind) {
+        constexpr int n = decltype(behind)::value;
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt((n & 15) | (n >> 4) << 14 | 7 << 4);  // vmcnt n, lgkmcnt 0
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    };
+    if (steps > 0) {
+        issue(0);
+        if (steps > 1) {
+            issue(1);
+            arrive(Int<2 * kCalls>{});
+        } else {
+            arrive(Int<0>{});
+        }
+        read(0, Int<0>{});
+    }
+    int it = 0;
+    for (; it + 2 < steps; ++it) {
+        read(it & 1, Int<1>{});
+        multiply(Int<0>{});
+        arrive(Int<0>{});
+        issue(it & 1);
+        read(it + 1 & 1, Int<0>{});
+        multiply(Int<1>{});
+    }
+    for (; it < steps; ++it) {  // the last two steps load nothing
+        read(it & 1, Int<1>{});
+        multiply(Int<0>{});
+        if (it + 1 < steps) {
+            arrive(Int<0>{});
+            read(it + 1 & 1, Int<0>{});
+        }
+        multiply(Int<1>{});
     }
 
     const int g = lane / 16, col = lane % 16;
@@ -388,6 +451,15 @@ __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
                                            pow2(-lift_of(a.scalars->top_w));
         const int64_t v0 = x0 + wx * 128;
         constexpr float kHead = __is_same(T, F16) ? 15.f : 0.f;
+        if (x0 + kX > a.nx) {  // the last tile's columns behind the vocabulary
+#pragma unroll
+            for (int f = 0; f < 8; ++f)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (v0 + 32 * (f / 2) + 8 * g + 4 * (f & 1) + r >= a.nx)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) acc[f][j][r] = -INFINITY;
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int64_t i = y0 + wy * 64 + 16 * j + col;
@@ -396,11 +468,8 @@ __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
             for (int f = 0; f < 8; ++f)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    float z = acc[f][j][r] * c1;
-                    if (x0 + kX > a.nx && v0 + 32 * (f / 2) + 8 * g + 4 * (f & 1) + r >= a.nx)
-                        z = -INFINITY;
-                    acc[f][j][r] = z;
-                    top = fmaxf(top, z);
+                    acc[f][j][r] *= c1;
+                    top = fmaxf(top, acc[f][j][r]);
                 }
             top = fmaxf(top, __shfl_xor(top, 16));
             top = fmaxf(top, __shfl_xor(top, 32));
@@ -448,7 +517,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
             for (int f = 0; f < 8; ++f) {
                 const int64_t n = x0 + wx * 128 + 16 * f + 4 * g;
                 if (n >= a.pld) continue;
-                *reinterpret_cast<f32x4 *>(a.partial + (split * a.ny + i) * a.pld + n) = acc[f][j];
+                *reinterpret_cast<f32x4 *>(a.partial + ((int64_t)split * a.ny + i) * a.pld + n) = acc[f][j];
             }
         }
     } else {
@@ -741,6 +810,7 @@ __global__ __launch_bounds__(1024) void head_total(const Scalars *scalars, const
 // ----------------------------------------------------------------- host side
 
 constexpr int64_t kCus = 256;
+constexpr int64_t kMinChunk = 128;  // rows done at a time at least
 
 struct Plan {
     int planes;
@@ -765,15 +835,18 @@ Plan plan_of(const rcs_head *a, int64_t limit) {
     p.planes = a->type == RCS_F32 ? 2 : 1;
     p.rows = a->rows, p.vocab = a->vocab, p.dim = a->dim;
     p.pad = round_up(a->dim, kK);
+    // a stride of a whole number of kilobytes would put a column's elements into few
+    // of the memory's channels
+    p.groups = round_up(a->vocab, kX) / kGroup;
     p.eld = round_up(a->vocab, kX);
-    p.groups = p.eld / kGroup;
+    if (p.eld % 512 == 0) p.eld += 64;
     p.copy_w = !direct_weight(a);
     // rows of a group: as many as fit the limit, in whole tiles
     const int64_t row_bytes = (grads ? p.eld * 2 * p.planes : 0) + p.groups * 8;
-    p.chunk = round_up(a->rows > 0 ? a->rows : 1, kY);
-    const int64_t fit = limit / row_bytes / kY * kY;
-    if (p.chunk > fit) p.chunk = fit < kY ? kY : fit;
-    const int64_t tiles = round_up(p.dim, kX) / kX * (p.chunk / kY);
+    p.chunk = round_up(a->rows > 0 ? a->rows : 1, kMinChunk);
+    const int64_t fit = limit / row_bytes / kMinChunk * kMinChunk;
+    if (p.chunk > fit) p.chunk = fit < kMinChunk ? kMinChunk : fit;
+    const int64_t tiles = round_up(p.dim, kX) / kX * (round_up(p.chunk, 256) / 256);
     const int64_t steps = round_up(a->vocab, kK) / kK;
     int64_t splits = (2 * kCus * 2 + tiles - 1) / tiles;
     if (splits > steps / 16) splits = steps / 16;
@@ -824,6 +897,14 @@ int check_head(const rcs_head *a) {
     return RCS_OK;
 }
 
+template <class T, int OP, int PLANES>
+void launch_gemm(GemmArgs &g, int splits, hipStream_t stream) {
+    g.xtiles = (int)(round_up(g.nx, kX) / kX);
+    g.ytiles = (int)(round_up(g.ny, kY) / kY);
+    const int64_t blocks = (int64_t)g.xtiles * g.ytiles * splits;
+    head_gemm<T, OP, PLANES><<<dim3((unsigned)blocks), kGemmThreads, 0, stream>>>(g);
+}
+
 template <class T, int PLANES>
 void launch_products(const rcs_head *a, const Targets &tg, const Plan &p, char *ws,
                      hipStream_t stream) {
@@ -849,13 +930,11 @@ void launch_products(const rcs_head *a, const Targets &tg, const Plan &p, char *
         g.xld = wld, g.xsize = (a->vocab - 1) * wld + (p.copy_w ? p.pad : a->dim);
         g.yld = p.pad, g.ysize = (a->rows + kK - row0) * p.pad;
         g.nx = a->vocab, g.ny = rows, g.nk = p.pad, g.kper = p.pad;
-        g.xtiles = (int)(p.eld / kX), g.ytiles = (int)(round_up(rows, kY) / kY);
         g.eld = p.eld, g.parts = reinterpret_cast<f32x2 *>(ws + p.parts), g.groups = p.groups;
         g.zscale = kLog2e / tg.tau;
         g.store = grads;
         if (rows > 0)
-            head_gemm<T, kLogits, PLANES>
-                <<<dim3((unsigned)(g.xtiles * (int64_t)g.ytiles)), kGemmThreads, 0, stream>>>(g);
+            launch_gemm<T, kLogits, PLANES>(g, 1, stream);
 
         RowArgs r = {};
         r.scalars = scalars;
@@ -879,11 +958,8 @@ void launch_products(const rcs_head *a, const Targets &tg, const Plan &p, char *
             for (int k = 0; k < PLANES; ++k) q.y[k] = g.e[k];
             q.yld = p.eld, q.ysize = p.chunk * p.eld;
             q.nx = a->dim, q.ny = rows, q.nk = round_up(a->vocab, kK), q.kper = p.kper;
-            q.xtiles = (int)(round_up(a->dim, kX) / kX);
             q.partial = reinterpret_cast<float *>(ws + p.partial), q.pld = p.pad;
-            head_gemm<T, kHidden, PLANES>
-                <<<dim3((unsigned)(q.xtiles * (int64_t)q.ytiles * p.splits)), kGemmThreads, 0,
-                   stream>>>(q);
+            launch_gemm<T, kHidden, PLANES>(q, p.splits, stream);
             ReduceArgs d = {};
             d.scalars = scalars, d.rowmap = r.rowmap, d.row0 = row0, d.rows = rows;
             d.dim = a->dim, d.pld = p.pad, d.partial = q.partial, d.splits = p.splits;
@@ -897,13 +973,11 @@ void launch_products(const rcs_head *a, const Targets &tg, const Plan &p, char *
             q.xld = p.pad, q.xsize = g.ysize;
             q.yld = p.eld, q.ysize = p.chunk * p.eld;
             q.nx = a->dim, q.ny = a->vocab, q.nk = rows, q.kper = round_up(rows, kK);
-            q.xtiles = (int)(round_up(a->dim, kX) / kX), q.ytiles = (int)(round_up(a->vocab, kY) / kY);
             q.out = p.wide_out ? ws + p.acc : a->grad_weight;
             q.old = p.wide_out ? a->dim : a->grad_weight_stride;
             q.out_type = p.wide_out ? RCS_F32 : a->grad_weight_type;
             q.add = row0 > 0 || (a->accumulate != 0 && !p.wide_out);
-            head_gemm<T, kWeight, PLANES>
-                <<<dim3((unsigned)(q.xtiles * (int64_t)q.ytiles)), kGemmThreads, 0, stream>>>(q);
+            launch_gemm<T, kWeight, PLANES>(q, 1, stream);
         }
     }
     if (p.wide_out)
