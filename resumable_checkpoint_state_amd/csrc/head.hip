@@ -187,8 +187,9 @@ struct GemmArgs {
     int64_t xld, yld;         // elements
     int64_t xsize, ysize;     // elements from the first to the last one in memory
     int64_t nx, ny, nk;       // extent of the product (ny, or nk of kWeight, at most: see count)
-    int64_t kper;             // of nk, for one split
-    int xtiles, ytiles;
+    int64_t kper;             // of nk, for one split of kHidden
+    int xtiles, ytiles, splits;
+    int whole, parts_of_rest;  // kWeight: tiles done whole, and splits of each of the rest
     int64_t row0;             // first row of this group of rows
     const Scalars *scalars;
     // kLogits
@@ -198,7 +199,7 @@ struct GemmArgs {
     int64_t groups;
     float zscale;
     bool store;
-    // kHidden
+    // kHidden, and the rest of kWeight's tiles
     float *partial;
     int64_t pld;
     // kWeight
@@ -279,13 +280,13 @@ struct Side<false, PERM> {
     }
 };
 
-// The tile of block b of a product. Blocks are dispatched round-robin over the 8
+// The tile b of n that are done at a time (a block does b, b + gridDim.x, ...). Blocks are dispatched round-robin over the 8
 // XCDs, each with an L2 of its own: an XCD takes a stretch of its own of the
 // order below, in which the 64 blocks that it runs at once share few operand
 // tiles: bands of kBand y tiles, and along a band all y of an x, then the next.
 constexpr int kBand = 8;
-__device__ __forceinline__ void tile_of(int b, int xtiles, int ytiles, int &tx, int &ty) {
-    const int n = xtiles * ytiles, per = n / 8, more = n % 8, xcd = b % 8;
+__device__ __forceinline__ void tile_of(int b, int n, int xtiles, int ytiles, int &tx, int &ty) {
+    const int per = n / 8, more = n % 8, xcd = b % 8;
     const int at = xcd * per + min(xcd, more) + b / 8;
     const int band = at / (kBand * xtiles), rest = at % (kBand * xtiles);
     const int high = min(kBand, ytiles - band * kBand);
@@ -320,6 +321,14 @@ struct Source {
     }
 };
 
+// Part of a product: an output tile, or a split of its sum.
+struct Item {
+    int64_t x0, y0, k0;
+    int per;  // steps of one pair of planes
+    bool empty;  // a sum over nothing: one step, of zeros
+    int split;  // kHidden: the split; kWeight: place among the partial tiles, or -1
+};
+
 template <class T, int OP, int PLANES>
 __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
 #ifdef __HIP_DEVICE_COMPILE__  // the host needs the launch stub alone
@@ -331,36 +340,74 @@ __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
     const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int wx = wave & 1, wy = wave >> 1;
 
+    // the items of this launch, and this block's first one
     const int64_t count = a.scalars->count - a.row0;
-    const int tiles = a.xtiles * a.ytiles;
-    const int split = blockIdx.x / tiles;
-    int tx, ty;
-    tile_of(blockIdx.x % tiles, a.xtiles, a.ytiles, tx, ty);
-    const int64_t x0 = (int64_t)tx * kX, y0 = (int64_t)ty * kY;
     const int64_t ny = OP == kWeight ? a.ny : min(a.ny, count);
-    if (y0 >= ny) return;
-    const int64_t nk_all = OP == kWeight ? max((int64_t)0, min(a.nk, count)) : a.nk;
-    const int64_t k0 = (int64_t)split * a.kper;
-    const int64_t nk = max((int64_t)0, min(a.kper, nk_all - k0));
-    if (OP == kWeight && a.add && nk == 0) return;
-    const int per = (int)((nk + kK - 1) / kK);  // steps of one pair of planes
+    const int64_t nk = OP == kWeight ? max((int64_t)0, min(a.nk, count)) : a.nk;
+    if (ny <= 0 || (OP == kWeight && a.add && nk == 0)) return;
+    const int ytiles = (int)((ny + kY - 1) / kY), tiles = a.xtiles * ytiles;
+    const int items = OP == kHidden   ? tiles * a.splits
+                      : OP == kWeight ? a.whole + (tiles - a.whole) * a.parts_of_rest
+                                      : tiles;
+    int at = blockIdx.x;
+    if (at >= items) return;
+    auto item_of = [&](int index) {
+        Item m;
+        int tx, ty;
+        int64_t kper = nk;
+        m.k0 = 0;
+        m.split = OP == kWeight ? -1 : 0;
+        if (OP == kHidden) {
+            m.split = index / tiles;
+            index %= tiles;
+            kper = a.kper;
+            m.k0 = m.split * kper;
+        }
+        if (OP == kWeight && index >= a.whole) {
+            m.split = index - a.whole;
+            if (a.parts_of_rest == 1) m.split = -1;
+            index = a.whole + (index - a.whole) / a.parts_of_rest;
+            const int64_t steps = (nk + kK - 1) / kK;
+            kper = (steps + a.parts_of_rest - 1) / a.parts_of_rest * kK;
+            if (m.split >= 0) m.k0 = m.split % a.parts_of_rest * kper;
+        }
+        if (OP == kWeight && index >= a.whole) {
+            tx = index % a.xtiles, ty = index / a.xtiles;
+        } else {
+            tile_of(index, OP == kWeight ? a.whole : tiles, a.xtiles, ytiles, tx, ty);
+        }
+        m.x0 = (int64_t)tx * kX;
+        m.y0 = (int64_t)ty * kY;
+        const int64_t n = max((int64_t)0, min(kper, nk - m.k0));
+        m.per = (int)((n + kK - 1) / kK);
+        m.empty = m.per == 0;
+        if (m.empty) m.per = 1;
+        return m;
+    };
     constexpr int kPairsOfPlanes = PLANES == 1 ? 1 : 3;
-    const int steps = per * kPairsOfPlanes;
 
+    // loads, step after step and item after item
     uint32_t xsrc[kCalls], ysrc[kCalls];
 #pragma unroll
-    for (int c = 0; c < kCalls; ++c) xsrc[c] = X::source(wave * kCalls + c, lane, a.xld);
-#pragma unroll
-    for (int c = 0; c < kCalls; ++c) ysrc[c] = Y::source(wave * kCalls + c, lane, a.yld);
-    const int64_t xat = (OP == kLogits ? x0 * a.xld + k0 : k0 * a.xld + x0) * 2;
-    const int64_t yat = (OP != kWeight ? y0 * a.yld + k0 : k0 * a.yld + y0) * 2;
-    const int64_t xend = a.xsize * 2, yend = a.ysize * 2;
+    for (int c = 0; c < kCalls; ++c) {
+        xsrc[c] = X::source(wave * kCalls + c, lane, a.xld);
+        ysrc[c] = Y::source(wave * kCalls + c, lane, a.yld);
+    }
     const int64_t xstep = OP == kLogits ? kK * 2 : a.xld * kK * 2;
     const int64_t ystep = OP != kWeight ? kK * 2 : a.yld * kK * 2;
-    Source xs{static_cast<const char *>(a.x[0]) + xat, xend - xat};
-    Source ys{static_cast<const char *>(a.y[0]) + yat, yend - yat};
-    int issued = 0;
+    Source xs, ys;
+    Item load = item_of(at);
+    int load_at = at, issued = 0;
+    auto begin_planes = [&](int px, int py) {
+        const int64_t xat = (OP == kLogits ? load.x0 * a.xld + load.k0 : load.k0 * a.xld + load.x0) * 2;
+        const int64_t yat = (OP != kWeight ? load.y0 * a.yld + load.k0 : load.k0 * a.yld + load.y0) * 2;
+        xs = Source{static_cast<const char *>(a.x[px]) + xat, load.empty ? 0 : a.xsize * 2 - xat};
+        ys = Source{static_cast<const char *>(a.y[py]) + yat, load.empty ? 0 : a.ysize * 2 - yat};
+    };
+    begin_planes(0, 0);
+    // loads a step's tiles; false if there is none left
     auto issue = [&](int stage) {
+        if (load_at >= items) return;
         const uint32_t to = lds_at + (uint32_t)(stage * kStageBytes);
         const u32x4 bx = xs.buffer(), by = ys.buffer();
 #pragma unroll
@@ -370,10 +417,16 @@ __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
         for (int c = 0; c < kCalls; ++c)
             load_lds(by, ysrc[c], to + kXBytes + (wave * kCalls + c) * 1024);
         ++issued;
-        if (PLANES > 1 && (issued == per || issued == 2 * per)) {  // low of x, then low of y
-            const int px = issued == per ? 1 : 0, py = issued == per ? 0 : 1;
-            xs = Source{static_cast<const char *>(a.x[px]) + xat, xend - xat};
-            ys = Source{static_cast<const char *>(a.y[py]) + yat, yend - yat};
+        if (issued == load.per * kPairsOfPlanes) {
+            issued = 0;
+            load_at += gridDim.x;
+            if (load_at >= items) return;
+            load = item_of(load_at);
+            begin_planes(0, 0);
+        } else if (PLANES > 1 && issued == load.per) {
+            begin_planes(1, 0);  // low of x
+        } else if (PLANES > 1 && issued == 2 * load.per) {
+            begin_planes(0, 1);  // low of y
         } else {
             xs.advance(xstep);
             ys.advance(ystep);
@@ -381,10 +434,12 @@ __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
     };
 
     f32x4 acc[8][4];
+    auto clear = [&] {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    };
     const uint32_t xbase = X::base(wx * 128, lane);
     const uint32_t ybase = Y::base(wy * 64, lane);
 
@@ -407,144 +462,179 @@ __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[i][j] = mfma(fx[h][i], fy[h][j], acc[i][j], T{});
     };
-    // this wave's reads are done, and all but the last n of its loads; then every wave's
+    // this wave's reads of LDS are done, and all but the last n of its accesses to
+    // memory (which end in their order); then every wave's
     auto arrive = [&](auto behind) {
         constexpr int n = decltype(behind)::value;
+        static_assert(n < 64, "of the counter");
         asm volatile("" ::: "memory");
         __builtin_amdgcn_s_waitcnt((n & 15) | (n >> 4) << 14 | 7 << 4);  // vmcnt n, lgkmcnt 0
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
     };
-    if (steps > 0) {
-        issue(0);
-        if (steps > 1) {
-            issue(1);
-            arrive(Int<2 * kCalls>{});
-        } else {
-            arrive(Int<0>{});
-        }
-        read(0, Int<0>{});
-    }
-    int it = 0;
-    for (; it + 2 < steps; ++it) {
-        read(it & 1, Int<1>{});
-        multiply(Int<0>{});
-        arrive(Int<0>{});
-        issue(it & 1);
-        read(it + 1 & 1, Int<0>{});
-        multiply(Int<1>{});
-    }
-    for (; it < steps; ++it) {  // the last two steps load nothing
-        read(it & 1, Int<1>{});
-        multiply(Int<0>{});
-        if (it + 1 < steps) {
-            arrive(Int<0>{});
-            read(it + 1 & 1, Int<0>{});
-        }
-        multiply(Int<1>{});
-    }
 
-    const int g = lane / 16, col = lane % 16;
+    // The results of an item. kLogits: kStores stores, always, so that the next step's
+    // tile, which was loaded before them, can be waited for without them.
+    constexpr int kStores = OP == kLogits ? 4 + 16 * PLANES : 0;
+    float c1 = 1.f;
     if constexpr (OP == kLogits) {
-        const float c1 = PLANES == 1 ? a.zscale
-                                     : a.zscale * pow2(-lift_of(a.scalars->top_h)) *
-                                           pow2(-lift_of(a.scalars->top_w));
-        const int64_t v0 = x0 + wx * 128;
-        constexpr float kHead = __is_same(T, F16) ? 15.f : 0.f;
-        if (x0 + kX > a.nx) {  // the last tile's columns behind the vocabulary
+        c1 = a.zscale;
+        if (PLANES > 1) c1 = c1 * pow2(-lift_of(a.scalars->top_h)) * pow2(-lift_of(a.scalars->top_w));
+    } else if constexpr (OP == kWeight) {
+        c1 = a.scale * pow2(-a.gshift);
+        if (a.mean) c1 /= (float)max(a.scalars->count, 1);
+        if (PLANES > 1) c1 *= pow2(-lift_of(a.scalars->top_h));
+    }
+    auto finish = [&](const Item &m) {
+        int l = lane;
+        asm volatile("" : "+v"(l));  // addresses are worked out here, not kept through the loop
+        const int g = l / 16, col = l % 16;
+        if constexpr (OP == kLogits) {
+            const int64_t v0 = m.x0 + wx * 128;
+            constexpr float kHead = __is_same(T, F16) ? 15.f : 0.f;
+            if (m.x0 + kX > a.nx) {  // the last tile's columns behind the vocabulary
 #pragma unroll
-            for (int f = 0; f < 8; ++f)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (v0 + 32 * (f / 2) + 8 * g + 4 * (f & 1) + r >= a.nx)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) acc[f][j][r] = -INFINITY;
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t i = y0 + wy * 64 + 16 * j + col;
-            float top = -INFINITY;
-#pragma unroll
-            for (int f = 0; f < 8; ++f)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    acc[f][j][r] *= c1;
-                    top = fmaxf(top, acc[f][j][r]);
-                }
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
-            const float ref = top == -INFINITY ? 0.f : top - kHead;
-            float sum = 0.f;
-#pragma unroll
-            for (int f = 0; f < 8; ++f)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float e = exp2_(acc[f][j][r] - ref);
-                    acc[f][j][r] = e;
-                    sum += e;
-                }
-            sum += __shfl_xor(sum, 16);
-            sum += __shfl_xor(sum, 32);
-            if (i >= ny) continue;
-            if (g == 0 && v0 < a.nx) a.parts[i * a.groups + v0 / kGroup] = f32x2{ref, sum};
-            if (!a.store) continue;
-#pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                float e[8];
-#pragma unroll
-                for (int r = 0; r < 8; ++r) e[r] = acc[2 * p + r / 4][j][r % 4];
-                u32x4 h;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) h[r] = two(e[2 * r], e[2 * r + 1], T{});
-                const int64_t at = i * a.eld + v0 + 32 * p + 8 * g;
-                *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(a.e[0]) + at) = h;
-                if (PLANES > 1) {
-                    u32x4 l;
+                for (int f = 0; f < 8; ++f)
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
-                        l[r] = two(e[2 * r] - value((uint16_t)h[r], T{}),
-                                   e[2 * r + 1] - value((uint16_t)(h[r] >> 16), T{}), T{});
-                    *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(a.e[1]) + at) = l;
+                        if (v0 + 32 * (f / 2) + 8 * g + 4 * (f & 1) + r >= a.nx)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) acc[f][j][r] = -INFINITY;
+            }
+            // rows behind the last one lie behind the buffers' ends, and are not stored
+            const int64_t rows = min((int64_t)kY, ny - m.y0);
+            const auto ebuf = [&](int k) {
+                return __builtin_amdgcn_make_buffer_rsrc(
+                    static_cast<uint16_t *>(a.e[k]) + m.y0 * a.eld, 0,
+                    a.store ? (int)(uint32_t)(rows * a.eld * 2) : 0, 0x00020000);
+            };
+            const __amdgpu_buffer_rsrc_t eh = ebuf(0), el = ebuf(PLANES - 1);
+            const __amdgpu_buffer_rsrc_t pb = __builtin_amdgcn_make_buffer_rsrc(
+                a.parts + m.y0 * a.groups, 0, (int)(uint32_t)(rows * a.groups * 8), 0x00020000);
+            const uint32_t part = g == 0 && v0 < a.nx ? (uint32_t)(v0 / kGroup * 8) : 0xFFFFFF00u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int i = wy * 64 + 16 * j + col;
+                float top = -INFINITY;
+#pragma unroll
+                for (int f = 0; f < 8; ++f)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        acc[f][j][r] *= c1;
+                        top = fmaxf(top, acc[f][j][r]);
+                    }
+                top = fmaxf(top, __shfl_xor(top, 16));
+                top = fmaxf(top, __shfl_xor(top, 32));
+                const float ref = top == -INFINITY ? 0.f : top - kHead;
+                float sum = 0.f;
+#pragma unroll
+                for (int f = 0; f < 8; ++f)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float e = exp2_(acc[f][j][r] - ref);
+                        acc[f][j][r] = e;
+                        sum += e;
+                    }
+                sum += __shfl_xor(sum, 16);
+                sum += __shfl_xor(sum, 32);
+                __builtin_amdgcn_raw_buffer_store_b64(
+                    u32x2{__float_as_uint(ref), __float_as_uint(sum)}, pb,
+                    part == 0xFFFFFF00u ? part : part + (uint32_t)(i * a.groups * 8), 0, 0);
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    float e[8];
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) e[r] = acc[2 * p + r / 4][j][r % 4];
+                    u32x4 h;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) h[r] = two(e[2 * r], e[2 * r + 1], T{});
+                    const uint32_t to = (uint32_t)((i * a.eld + v0 + 32 * p + 8 * g) * 2);
+                    __builtin_amdgcn_raw_buffer_store_b128(h, eh, to, 0, 0);
+                    if (PLANES > 1) {
+                        u32x4 l;
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            l[r] = two(e[2 * r] - value((uint16_t)h[r], T{}),
+                                       e[2 * r + 1] - value((uint16_t)(h[r] >> 16), T{}), T{});
+                        __builtin_amdgcn_raw_buffer_store_b128(l, el, to, 0, 0);
+                    }
+                }
+            }
+        } else if constexpr (OP == kHidden) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int64_t i = m.y0 + wy * 64 + 16 * j + col;
+                if (i >= ny) continue;
+#pragma unroll
+                for (int f = 0; f < 8; ++f) {
+                    const int64_t n = m.x0 + wx * 128 + 16 * f + 4 * g;
+                    if (n >= a.pld) continue;
+                    *reinterpret_cast<f32x4 *>(a.partial + (m.split * a.ny + i) * a.pld + n) =
+                        acc[f][j];
+                }
+            }
+        } else if (m.split >= 0) {
+            float *to = a.partial + (int64_t)m.split * kX * kY;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int f = 0; f < 8; ++f)
+                    *reinterpret_cast<f32x4 *>(to + (wy * 64 + 16 * j + col) * kX + wx * 128 +
+                                               16 * f + 4 * g) = acc[f][j] * c1;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int64_t v = m.y0 + wy * 64 + 16 * j + col;
+                if (v >= a.ny) continue;
+#pragma unroll
+                for (int f = 0; f < 8; ++f) {
+                    const int64_t n = m.x0 + wx * 128 + 16 * f + 4 * g;
+                    put4(a.out, v * a.old + n, a.out_type, acc[f][j] * c1, a.nx - n, a.add);
                 }
             }
         }
-    } else if constexpr (OP == kHidden) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t i = y0 + wy * 64 + 16 * j + col;
-            if (i >= ny) continue;
-#pragma unroll
-            for (int f = 0; f < 8; ++f) {
-                const int64_t n = x0 + wx * 128 + 16 * f + 4 * g;
-                if (n >= a.pld) continue;
-                *reinterpret_cast<f32x4 *>(a.partial + ((int64_t)split * a.ny + i) * a.pld + n) = acc[f][j];
-            }
+    };
+
+    issue(0);
+    issue(1);
+    arrive(Int<0>{});
+    read(0, Int<0>{});
+    int stage = 0;
+    bool stored = false;
+    for (; at < items; at += gridDim.x) {
+        const Item m = item_of(at);
+        clear();
+        for (int left = m.per * kPairsOfPlanes; left > 0; --left) {
+            read(stage, Int<1>{});
+            multiply(Int<0>{});
+            if (kStores > 0 && stored) arrive(Int<kStores>{});
+            else arrive(Int<0>{});
+            stored = false;
+            issue(stage);
+            stage ^= 1;
+            read(stage, Int<0>{});  // of nothing, behind the last step
+            multiply(Int<1>{});
         }
-    } else {
-        float s = a.scale * pow2(-a.gshift);
-        if (a.mean) s /= (float)max(a.scalars->count, 1);
-        if (PLANES > 1) s *= pow2(-lift_of(a.scalars->top_h));
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t v = y0 + wy * 64 + 16 * j + col;
-            if (v >= a.ny) continue;
-#pragma unroll
-            for (int f = 0; f < 8; ++f) {
-                const int64_t n = x0 + wx * 128 + 16 * f + 4 * g;
-f32x4 x = acc[f][j] * s;
-                const int64_t at = v * a.old + n;
-                if (n + 4 <= a.nx) {
-                    if (a.add) x += load4(a.out, at, a.out_type);
-                    store4(a.out, at, a.out_type, x);
-                } else {
-                    for (int r = 0; r < 4 && n + r < a.nx; ++r)
-                        put(a.out, at + r, a.out_type,
-                            pick(x, r) + (a.add ? element(a.out, at + r, a.out_type) : 0.f));
-                }
-            }
-        }
+        finish(m);
+        stored = true;
     }
 #endif
+}
+
+// The tiles of kWeight that were split: sums in the order of the splits.
+__global__ __launch_bounds__(kWave) void head_weight_join(GemmArgs a) {
+    const int64_t count = a.scalars->count - a.row0;
+    if (a.add && count <= 0) return;
+    const int tile = a.whole + (int)(blockIdx.x / kY), row = (int)(blockIdx.x % kY);
+    const int64_t v = (int64_t)(tile / a.xtiles) * kY + row;
+    const int64_t n = (int64_t)(tile % a.xtiles) * kX + 4 * threadIdx.x;
+    if (v >= a.ny || n >= a.nx) return;
+    const float *from = a.partial + (int64_t)(tile - a.whole) * a.parts_of_rest * kX * kY +
+                        row * kX + 4 * threadIdx.x;
+    f32x4 x = {0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < a.parts_of_rest; ++k)
+        x += *reinterpret_cast<const f32x4 *>(from + (int64_t)k * kX * kY);
+    put4(a.out, v * a.old + n, a.out_type, x, a.nx - n, a.add);
 }
 
 // ------------------------------------------------------------- rows of logits
@@ -810,6 +900,7 @@ __global__ __launch_bounds__(1024) void head_total(const Scalars *scalars, const
 // ----------------------------------------------------------------- host side
 
 constexpr int64_t kCus = 256;
+constexpr int64_t kItemSteps = 8;
 constexpr int64_t kMinChunk = 128;  // rows done at a time at least
 
 struct Plan {
@@ -817,11 +908,11 @@ struct Plan {
     int64_t rows, vocab, dim, pad;   // pad: columns of the prepared rows
     int64_t chunk;                   // rows of a group
     int64_t eld, groups;
-    int splits;
+    int splits, whole, parts_of_rest;
     int64_t kper;
     bool copy_w, wide_out;
     // offsets in the workspace
-    int64_t scalars, flags, rowmap, inverse, losses, h[2], w[2], e[2], parts, partial, acc, bytes;
+    int64_t scalars, flags, rowmap, inverse, losses, h[2], w[2], e[2], parts, partial, rest, acc, bytes;
 };
 
 bool direct_weight(const rcs_head *a) {
@@ -846,13 +937,29 @@ Plan plan_of(const rcs_head *a, int64_t limit) {
     p.chunk = round_up(a->rows > 0 ? a->rows : 1, kMinChunk);
     const int64_t fit = limit / row_bytes / kMinChunk * kMinChunk;
     if (p.chunk > fit) p.chunk = fit < kMinChunk ? kMinChunk : fit;
-    const int64_t tiles = round_up(p.dim, kX) / kX * (round_up(p.chunk, 256) / 256);
+    // splits of the hidden gradient's sum over the vocabulary: the number that fills
+    // the chip's rounds best, each item costing about as much as kItemSteps steps more
+    const int64_t xtiles = round_up(p.dim, kX) / kX;
+    const int64_t tiles = xtiles * (round_up(p.chunk < a->rows ? p.chunk : a->rows, kY) / kY);
     const int64_t steps = round_up(a->vocab, kK) / kK;
-    int64_t splits = (2 * kCus * 2 + tiles - 1) / tiles;
-    if (splits > steps / 16) splits = steps / 16;
-    if (splits < 1) splits = 1;
-    p.kper = round_up((steps + splits - 1) / splits, 1) * kK;
+    int64_t best = 0;
+    for (int64_t n = 1; n <= 64 && n <= steps; ++n) {
+        const int64_t rounds = (tiles * n + kCus - 1) / kCus;
+        const int64_t cost = rounds * ((steps + n - 1) / n + kItemSteps);
+        if (n == 1 || cost < best) best = cost, p.splits = (int)n;
+    }
+    p.kper = (steps + p.splits - 1) / p.splits * kK;
     p.splits = (int)((steps * kK + p.kper - 1) / p.kper);
+    // the weight's tiles in whole rounds, and the rest split to fill one more
+    const int64_t wtiles = xtiles * (round_up(a->vocab, kY) / kY);
+    const int64_t rest = wtiles % kCus, wsteps = round_up(p.chunk, kK) / kK;
+    p.parts_of_rest = 1;
+    if (rest > 0) {
+        int64_t n = kCus / rest;
+        if (n > wsteps / kItemSteps) n = wsteps / kItemSteps;
+        if (n > 1) p.parts_of_rest = (int)n;
+    }
+    p.whole = (int)(p.parts_of_rest > 1 ? wtiles - rest : wtiles);
     p.wide_out = a->grad_weight != nullptr && a->grad_weight_type != RCS_F32 && p.chunk < a->rows;
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
@@ -872,6 +979,8 @@ Plan plan_of(const rcs_head *a, int64_t limit) {
     if (grads)
         for (int k = 0; k < p.planes; ++k) p.e[k] = take(2 * p.chunk * p.eld);
     if (a->grad_hidden != nullptr) p.partial = take(4 * p.splits * p.chunk * p.pad);
+    if (a->grad_weight != nullptr && p.parts_of_rest > 1)
+        p.rest = take(4LL * kX * kY * (wtiles - p.whole) * p.parts_of_rest);
     if (p.wide_out) p.acc = take(4 * a->vocab * a->dim);
     p.bytes = at;
     return p;
@@ -898,11 +1007,17 @@ int check_head(const rcs_head *a) {
 }
 
 template <class T, int OP, int PLANES>
-void launch_gemm(GemmArgs &g, int splits, hipStream_t stream) {
+void launch_gemm(GemmArgs &g, hipStream_t stream) {
     g.xtiles = (int)(round_up(g.nx, kX) / kX);
     g.ytiles = (int)(round_up(g.ny, kY) / kY);
-    const int64_t blocks = (int64_t)g.xtiles * g.ytiles * splits;
+    const int64_t tiles = (int64_t)g.xtiles * g.ytiles;
+    int64_t items = tiles;
+    if (OP == kHidden) items *= g.splits;
+    if (OP == kWeight) items = g.whole + (tiles - g.whole) * g.parts_of_rest;
+    const int64_t blocks = items < kCus ? items : kCus;
     head_gemm<T, OP, PLANES><<<dim3((unsigned)blocks), kGemmThreads, 0, stream>>>(g);
+    if (OP == kWeight && g.parts_of_rest > 1)
+        head_weight_join<<<dim3((unsigned)((tiles - g.whole) * kY)), kWave, 0, stream>>>(g);
 }
 
 template <class T, int PLANES>
@@ -934,7 +1049,7 @@ void launch_products(const rcs_head *a, const Targets &tg, const Plan &p, char *
         g.zscale = kLog2e / tg.tau;
         g.store = grads;
         if (rows > 0)
-            launch_gemm<T, kLogits, PLANES>(g, 1, stream);
+            launch_gemm<T, kLogits, PLANES>(g, stream);
 
         RowArgs r = {};
         r.scalars = scalars;
@@ -959,7 +1074,8 @@ void launch_products(const rcs_head *a, const Targets &tg, const Plan &p, char *
             q.yld = p.eld, q.ysize = p.chunk * p.eld;
             q.nx = a->dim, q.ny = rows, q.nk = round_up(a->vocab, kK), q.kper = p.kper;
             q.partial = reinterpret_cast<float *>(ws + p.partial), q.pld = p.pad;
-            launch_gemm<T, kHidden, PLANES>(q, p.splits, stream);
+            q.splits = p.splits;
+            launch_gemm<T, kHidden, PLANES>(q, stream);
             ReduceArgs d = {};
             d.scalars = scalars, d.rowmap = r.rowmap, d.row0 = row0, d.rows = rows;
             d.dim = a->dim, d.pld = p.pad, d.partial = q.partial, d.splits = p.splits;
@@ -977,7 +1093,9 @@ void launch_products(const rcs_head *a, const Targets &tg, const Plan &p, char *
             q.old = p.wide_out ? a->dim : a->grad_weight_stride;
             q.out_type = p.wide_out ? RCS_F32 : a->grad_weight_type;
             q.add = row0 > 0 || (a->accumulate != 0 && !p.wide_out);
-            launch_gemm<T, kWeight, PLANES>(q, 1, stream);
+            q.partial = reinterpret_cast<float *>(ws + p.rest);
+            q.whole = p.whole, q.parts_of_rest = p.parts_of_rest;
+            launch_gemm<T, kWeight, PLANES>(q, stream);
         }
     }
     if (p.wide_out)

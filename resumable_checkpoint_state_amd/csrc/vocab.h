@@ -76,6 +76,17 @@ __device__ __forceinline__ void store4(void *p, int64_t i, int t, f32x4 x) {
 __device__ __forceinline__ float pick(f32x4 x, int r) {
     return r == 0 ? x[0] : r == 1 ? x[1] : r == 2 ? x[2] : x[3];
 }
+// x to elements i to i + 3 of p, or to those of them that there are (`left`); added
+// to what is there, with add.
+__device__ __forceinline__ void put4(void *p, int64_t i, int t, f32x4 x, int64_t left, bool add) {
+    if (left >= 4) {
+        if (add) x += load4(p, i, t);
+        store4(p, i, t, x);
+        return;
+    }
+    for (int r = 0; r < 3; ++r)
+        if (r < left) put(p, i + r, t, add ? pick(x, r) + element(p, i + r, t) : pick(x, r));
+}
 __device__ __forceinline__ int64_t index_at(const void *p, int64_t i, int t) {
     return t == RCS_I32 ? (int64_t) static_cast<const int32_t *>(p)[i]
                         : static_cast<const int64_t *>(p)[i];
