@@ -405,23 +405,20 @@ __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
         ys = Source{static_cast<const char *>(a.y[py]) + yat, load.empty ? 0 : a.ysize * 2 - yat};
     };
     begin_planes(0, 0);
-    // loads a step's tiles; false if there is none left
-    auto issue = [&](int stage) {
-        if (load_at >= items) return;
+    u32x4 bx = xs.buffer(), by = ys.buffer();
+    // the c-th of the loads of a step's tiles (behind the last step: of zeros)
+    auto load_one = [&](int stage, int c) {
         const uint32_t to = lds_at + (uint32_t)(stage * kStageBytes);
-        const u32x4 bx = xs.buffer(), by = ys.buffer();
-#pragma unroll
-        for (int c = 0; c < kCalls; ++c)
-            load_lds(bx, xsrc[c], to + (wave * kCalls + c) * 1024);
-#pragma unroll
-        for (int c = 0; c < kCalls; ++c)
-            load_lds(by, ysrc[c], to + kXBytes + (wave * kCalls + c) * 1024);
+        if (c < kCalls) load_lds(bx, xsrc[c], to + (wave * kCalls + c) * 1024);
+        else load_lds(by, ysrc[c - kCalls], to + kXBytes + (wave * kCalls + c - kCalls) * 1024);
+    };
+    auto next_loads = [&] {
         ++issued;
         if (issued == load.per * kPairsOfPlanes) {
             issued = 0;
             load_at += gridDim.x;
-            if (load_at >= items) return;
-            load = item_of(load_at);
+            if (load_at < items) load = item_of(load_at);
+            else load.empty = true;
             begin_planes(0, 0);
         } else if (PLANES > 1 && issued == load.per) {
             begin_planes(1, 0);  // low of x
@@ -431,6 +428,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
             xs.advance(xstep);
             ys.advance(ystep);
         }
+        bx = xs.buffer(), by = ys.buffer();
     };
 
     f32x4 acc[8][4];
@@ -446,21 +444,26 @@ __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
     // While one half of a step is multiplied out of registers, the next half is read
     // into others. Between a step's halves, when every wave has read the whole of its
     // tile and the next one has arrived, the one after that is loaded in its place.
+    // Each four products come with a read and, in a step's second half, a load: as a
+    // stretch of loads, these would keep the products waiting while they queue (the
+    // order is held by barriers to the compiler's scheduling).
     s16x8 fx[2][8], fy[2][4];
-    auto read = [&](int stage, auto half) {
+    auto read_one = [&](int stage, int i, auto half) {
         constexpr int h = decltype(half)::value;
         const lds_char *px = lds + stage * kStageBytes, *py = px + kXBytes;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) fy[h][j] = Y::read(py, ybase, j, h);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) fx[h][i] = X::read(px, xbase, i, h);
+        if (i < 4) fy[h][i] = Y::read(py, ybase, i, h);
+        fx[h][i] = X::read(px, xbase, i, h);
     };
-    auto multiply = [&](auto half) {
+    auto multiply = [&](auto half, auto between) {
         constexpr int h = decltype(half)::value;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 8; ++i) {
+            between(i);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[i][j] = mfma(fx[h][i], fy[h][j], acc[i][j], T{});
+            __builtin_amdgcn_sched_barrier(0);
+        }
     };
     // this wave's reads of LDS are done, and all but the last n of its accesses to
     // memory (which end in their order); then every wave's
@@ -595,29 +598,36 @@ __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
         }
     };
 
-    issue(0);
-    issue(1);
-    arrive(Int<0>{});
-    read(0, Int<0>{});
+    static_assert(2 * kCalls == 8, "a load for each four products of half a step");
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) load_one(k, c);
+        next_loads();
+    }
+    arrive(Int<8>{});
+#pragma unroll
+    for (int i = 0; i < 8; ++i) read_one(0, i, Int<0>{});
     int stage = 0;
     bool stored = false;
     for (; at < items; at += gridDim.x) {
         const Item m = item_of(at);
         clear();
         for (int left = m.per * kPairsOfPlanes; left > 0; --left) {
-            read(stage, Int<1>{});
-            multiply(Int<0>{});
+            multiply(Int<0>{}, [&](int i) { read_one(stage, i, Int<1>{}); });
             if (kStores > 0 && stored) arrive(Int<kStores>{});
             else arrive(Int<0>{});
             stored = false;
-            issue(stage);
+            multiply(Int<1>{}, [&](int i) {
+                read_one(stage ^ 1, i, Int<0>{});  // of nothing, behind the last step
+                load_one(stage, i);
+            });
+            next_loads();
             stage ^= 1;
-            read(stage, Int<0>{});  // of nothing, behind the last step
-            multiply(Int<1>{});
         }
         finish(m);
         stored = true;
     }
+    arrive(Int<0>{});  // the loads of nothing have ended, too
 #endif
 }
 
