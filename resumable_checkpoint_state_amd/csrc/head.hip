@@ -280,18 +280,21 @@ struct Side<false, PERM> {
     }
 };
 
-// The tile b of n that are done at a time (a block does b, b + gridDim.x, ...). Blocks are dispatched round-robin over the 8
-// XCDs, each with an L2 of its own: an XCD takes a stretch of its own of the
-// order below, in which the 64 blocks that it runs at once share few operand
-// tiles: bands of kBand y tiles, and along a band all y of an x, then the next.
-constexpr int kBand = 8;
-__device__ __forceinline__ void tile_of(int b, int n, int xtiles, int ytiles, int &tx, int &ty) {
+// The b-th of n items in an order that suits the chip's caches. A block does b, b +
+// gridDim.x, ...; blocks are dispatched round-robin over the 8 XCDs, each with an L2
+// of its own: an XCD takes a stretch of its own, so that what its 32 CUs do at once
+// shares operand tiles.
+__device__ __forceinline__ int near_item(int b, int n) {
     const int per = n / 8, more = n % 8, xcd = b % 8;
-    const int at = xcd * per + min(xcd, more) + b / 8;
-    const int band = at / (kBand * xtiles), rest = at % (kBand * xtiles);
-    const int high = min(kBand, ytiles - band * kBand);
+    return xcd * per + min(xcd, more) + b / 8;
+}
+// The tiles in bands of BAND y tiles, and along a band all y of an x, then the next.
+template <int BAND>
+__device__ __forceinline__ void tile_of(int at, int xtiles, int ytiles, int &tx, int &ty) {
+    const int band = at / (BAND * xtiles), rest = at % (BAND * xtiles);
+    const int high = min(BAND, ytiles - band * BAND);
     tx = rest / high;
-    ty = band * kBand + rest % high;
+    ty = band * BAND + rest % high;
 }
 
 // 16 bytes a lane from `at` bytes into the buffer on, to 1,024 consecutive bytes of
@@ -329,6 +332,20 @@ struct Item {
     int split;  // kHidden: the split; kWeight: place among the partial tiles, or -1
 };
 
+// a and b of an even lane and of the odd one after it, as the even lane's a and b in
+// the two lanes' a, and the odd one's in their b.
+__device__ __forceinline__ void swap_rows(u32x4 &a, u32x4 &b, bool odd) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const uint32_t give = odd ? a[r] : b[r];
+        const uint32_t got = (uint32_t)__builtin_amdgcn_mov_dpp((int)give, 0xB1, 0xF, 0xF, true);
+        a[r] = odd ? got : a[r];
+        b[r] = odd ? b[r] : got;
+    }
+}
+
+constexpr int kAux = 0;
+
 template <class T, int OP, int PLANES>
 __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
 #ifdef __HIP_DEVICE_COMPILE__  // the host needs the launch stub alone
@@ -358,24 +375,23 @@ __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
         m.k0 = 0;
         m.split = OP == kWeight ? -1 : 0;
         if (OP == kHidden) {
+            index = near_item(index, items);
             m.split = index / tiles;
             index %= tiles;
             kper = a.kper;
             m.k0 = m.split * kper;
-        }
-        if (OP == kWeight && index >= a.whole) {
-            m.split = index - a.whole;
-            if (a.parts_of_rest == 1) m.split = -1;
-            index = a.whole + (index - a.whole) / a.parts_of_rest;
-            const int64_t steps = (nk + kK - 1) / kK;
-            kper = (steps + a.parts_of_rest - 1) / a.parts_of_rest * kK;
-            if (m.split >= 0) m.k0 = m.split % a.parts_of_rest * kper;
-        }
-        if (OP == kWeight && index >= a.whole) {
-            tx = index % a.xtiles, ty = index / a.xtiles;
+        } else if (OP == kLogits || index < a.whole) {
+            index = near_item(index, OP == kLogits ? tiles : a.whole);
         } else {
-            tile_of(index, OP == kWeight ? a.whole : tiles, a.xtiles, ytiles, tx, ty);
+            if (a.parts_of_rest > 1) {
+                m.split = index - a.whole;
+                const int64_t steps = (nk + kK - 1) / kK;
+                kper = (steps + a.parts_of_rest - 1) / a.parts_of_rest * kK;
+                m.k0 = m.split % a.parts_of_rest * kper;
+            }
+            index = a.whole + (index - a.whole) / a.parts_of_rest;
         }
+        tile_of<OP == kLogits ? 8 : 4>(index, a.xtiles, ytiles, tx, ty);
         m.x0 = (int64_t)tx * kX;
         m.y0 = (int64_t)ty * kY;
         const int64_t n = max((int64_t)0, min(kper, nk - m.k0));
@@ -489,9 +505,9 @@ __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
         if (PLANES > 1) c1 *= pow2(-lift_of(a.scalars->top_h));
     }
     auto finish = [&](const Item &m) {
-        int l = lane;
-        asm volatile("" : "+v"(l));  // addresses are worked out here, not kept through the loop
-        const int g = l / 16, col = l % 16;
+        int at_lane = lane;
+        asm volatile("" : "+v"(at_lane));  // addresses are worked out here, not kept through the loop
+        const int g = at_lane / 16, l16 = at_lane % 16;
         if constexpr (OP == kLogits) {
             const int64_t v0 = m.x0 + wx * 128;
             constexpr float kHead = __is_same(T, F16) ? 15.f : 0.f;
@@ -517,7 +533,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
             const uint32_t part = g == 0 && v0 < a.nx ? (uint32_t)(v0 / kGroup * 8) : 0xFFFFFF00u;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int i = wy * 64 + 16 * j + col;
+                const int i = wy * 64 + 16 * j + l16;
                 float top = -INFINITY;
 #pragma unroll
                 for (int f = 0; f < 8; ++f)
@@ -543,30 +559,38 @@ __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
                 __builtin_amdgcn_raw_buffer_store_b64(
                     u32x2{__float_as_uint(ref), __float_as_uint(sum)}, pb,
                     part == 0xFFFFFF00u ? part : part + (uint32_t)(i * a.groups * 8), 0, 0);
+                u32x4 h[4], l[4];
 #pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    float e[8];
+                for (int p = 0; p < 4; ++p)
 #pragma unroll
-                    for (int r = 0; r < 8; ++r) e[r] = acc[2 * p + r / 4][j][r % 4];
-                    u32x4 h;
+                    for (int r = 0; r < 4; ++r) {
+                        const float x = acc[2 * p + r / 2][j][2 * r % 4];
+                        const float y = acc[2 * p + r / 2][j][2 * r % 4 + 1];
+                        h[p][r] = two(x, y, T{});
+                        if (PLANES > 1)
+                            l[p][r] = two(x - value((uint16_t)h[p][r], T{}),
+                                          y - value((uint16_t)(h[p][r] >> 16), T{}), T{});
+                    }
+                // whole lines: first the even row of a pair of lanes, then the odd one
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) h[r] = two(e[2 * r], e[2 * r + 1], T{});
-                    const uint32_t to = (uint32_t)((i * a.eld + v0 + 32 * p + 8 * g) * 2);
-                    __builtin_amdgcn_raw_buffer_store_b128(h, eh, to, 0, 0);
+                for (int p = 0; p < 4; p += 2) {
+                    const uint32_t to =
+                        (uint32_t)(((i & ~1) * a.eld + v0 + 32 * (p + (l16 & 1)) + 8 * g) * 2);
+                    const uint32_t row = (uint32_t)(a.eld * 2);
+                    swap_rows(h[p], h[p + 1], l16 & 1);
+                    __builtin_amdgcn_raw_buffer_store_b128(h[p], eh, to, 0, kAux);
+                    __builtin_amdgcn_raw_buffer_store_b128(h[p + 1], eh, to + row, 0, kAux);
                     if (PLANES > 1) {
-                        u32x4 l;
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            l[r] = two(e[2 * r] - value((uint16_t)h[r], T{}),
-                                       e[2 * r + 1] - value((uint16_t)(h[r] >> 16), T{}), T{});
-                        __builtin_amdgcn_raw_buffer_store_b128(l, el, to, 0, 0);
+                        swap_rows(l[p], l[p + 1], l16 & 1);
+                        __builtin_amdgcn_raw_buffer_store_b128(l[p], el, to, 0, kAux);
+                        __builtin_amdgcn_raw_buffer_store_b128(l[p + 1], el, to + row, 0, kAux);
                     }
                 }
             }
         } else if constexpr (OP == kHidden) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int64_t i = m.y0 + wy * 64 + 16 * j + col;
+                const int64_t i = m.y0 + wy * 64 + 16 * j + l16;
                 if (i >= ny) continue;
 #pragma unroll
                 for (int f = 0; f < 8; ++f) {
@@ -582,12 +606,12 @@ __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
             for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int f = 0; f < 8; ++f)
-                    *reinterpret_cast<f32x4 *>(to + (wy * 64 + 16 * j + col) * kX + wx * 128 +
+                    *reinterpret_cast<f32x4 *>(to + (wy * 64 + 16 * j + l16) * kX + wx * 128 +
                                                16 * f + 4 * g) = acc[f][j] * c1;
         } else {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int64_t v = m.y0 + wy * 64 + 16 * j + col;
+                const int64_t v = m.y0 + wy * 64 + 16 * j + l16;
                 if (v >= a.ny) continue;
 #pragma unroll
                 for (int f = 0; f < 8; ++f) {
@@ -636,8 +660,9 @@ __global__ __launch_bounds__(kWave) void head_weight_join(GemmArgs a) {
     const int64_t count = a.scalars->count - a.row0;
     if (a.add && count <= 0) return;
     const int tile = a.whole + (int)(blockIdx.x / kY), row = (int)(blockIdx.x % kY);
-    const int64_t v = (int64_t)(tile / a.xtiles) * kY + row;
-    const int64_t n = (int64_t)(tile % a.xtiles) * kX + 4 * threadIdx.x;
+    int tx, ty;
+    tile_of<4>(tile, a.xtiles, a.ytiles, tx, ty);
+    const int64_t v = (int64_t)ty * kY + row, n = (int64_t)tx * kX + 4 * threadIdx.x;
     if (v >= a.ny || n >= a.nx) return;
     const float *from = a.partial + (int64_t)(tile - a.whole) * a.parts_of_rest * kX * kY +
                         row * kX + 4 * threadIdx.x;
