@@ -518,10 +518,11 @@ int rcs_list_import(rcs_list *list, const void *w, int w_type, const void *m, in
  *   limit            bytes that the exponentials of the logits may take at a time
  *                    (16 bits each, 32 with float32). Where they would take more,
  *                    rows are done in groups; at least 128 rows are done at a time
- *   workspace        rcs_head_workspace(args) bytes of device memory, aligned to
- *                    256, used until the call's work is done. It depends on the
- *                    sizes, the types, which gradients there are, limit and the
- *                    alignment of weight. Calls that may overlap on the device need one each
+ *   workspace        rcs_head_workspace(args, entries) bytes of device memory (0
+ *                    entries for head_loss), aligned to 256, used until the call's
+ *                    work is done. It depends on the sizes, the types, which
+ *                    gradients there are, limit and the alignment of weight. Calls
+ *                    that may overlap on the device need one each
  * What is written must not overlap anything else. Rows without a loss take no
  * part: what hidden holds there does not matter, and their gradient is zero.
  * Gradients of 16-bit types go through softmax values of that type (each
@@ -543,7 +544,7 @@ typedef struct rcs_head {
     void *workspace;
     int64_t workspace_bytes;
 } rcs_head;
-int64_t rcs_head_workspace(const rcs_head *args);
+int64_t rcs_head_workspace(const rcs_head *args, int64_t entries);
 
 /*
  * head_loss: softmax cross entropy, log(sum_v exp z[t][v]) - z[t][targets[t]].

@@ -134,7 +134,7 @@ def lib() -> ctypes.CDLL:
         fn = getattr(L, name)
         fn.argtypes = [vp, vp, ctypes.c_int, vp, ctypes.c_int, vp, ctypes.c_int, vp]
         fn.restype = ctypes.c_int
-    L.rcs_head_workspace.argtypes = [vp]
+    L.rcs_head_workspace.argtypes = [vp, i64]
     L.rcs_head_workspace.restype = i64
     L.head_loss.argtypes = [vp, vp, ctypes.c_int, i64, vp]
     L.head_loss.restype = ctypes.c_int

@@ -46,6 +46,7 @@ constexpr int kXBytes = kX * kK * 2, kStageBytes = kXBytes + kY * kK * 2;
 // What the kernels of one call tell each other, in device memory.
 struct Scalars {
     int32_t count;        // rows that have a loss
+    int32_t retries;      // of them, those whose reference was too low
     uint32_t top_h, top_w;  // float32 only: bits of the largest finite magnitudes
 };
 
@@ -101,6 +102,7 @@ __global__ __launch_bounds__(1024) void head_scan(const uint8_t *flags, int64_t 
     }
     if (tid == 0) {
         scalars->count = base;
+        scalars->retries = 0;
         scalars->top_h = 0;
         scalars->top_w = 0;
     }
@@ -198,7 +200,8 @@ struct GemmArgs {
     f32x2 *parts;
     int64_t groups;
     float zscale;
-    bool store;
+    bool store, retry;
+    const float *ref;
     // kHidden, and the rest of kWeight's tiles
     float *partial;
     int64_t pld;
@@ -218,6 +221,7 @@ struct Int {
     static constexpr int value = N;
 };
 
+constexpr int kRefPlaces = 4;  // items whose rows' references are in LDS, at most
 constexpr int kCalls = 256 * kK * 2 / 1024 / kGemmWaves;  // loads of a wave for one operand
 
 // How an operand's tile of 256 by kK lies in LDS: in `kCalls` loads a wave, each of
@@ -300,29 +304,27 @@ __device__ __forceinline__ void tile_of(int at, int xtiles, int ytiles, int &tx,
 // 16 bytes a lane from `at` bytes into the buffer on, to 1,024 consecutive bytes of
 // LDS. (Written out, because the compiler would let each transposing read of LDS
 // wait for all such loads, the ones for later steps too. It has no result
-// register, and `arrive` below waits for it.)
+// register, and `arrive` below waits for it. The wait states: between a vector
+// instruction that wrote one of the scalars and the load.)
 __device__ __forceinline__ void load_lds(u32x4 buffer, uint32_t at, uint32_t to) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to),
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to),
                  "v"(at), "s"(buffer)
                  : "memory");
 }
 
-// Where a wave's loads of one operand's next step come from.
-struct Source {
-    const char *p;
-    int64_t left;  // bytes from p to the end of the array
+__device__ __forceinline__ void load_lds_dword(u32x4 buffer, uint32_t at, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(to),
+                 "v"(at), "s"(buffer)
+                 : "memory");
+}
 
-    // A buffer of the bytes that are left: loads behind its end give zeros.
-    __device__ __forceinline__ u32x4 buffer() const {
-        const uint64_t at = reinterpret_cast<uint64_t>(p);
-        const int64_t n = left < 0 ? 0 : left > 0xFFFFFFFFLL ? 0xFFFFFFFFLL : left;
-        return u32x4{(uint32_t)at, (uint32_t)(at >> 32) & 0xFFFFu, (uint32_t)n, 0x00020000u};
-    }
-    __device__ __forceinline__ void advance(int64_t bytes) {
-        p += bytes;
-        left -= bytes;
-    }
-};
+// The buffer of what an array of `size` bytes has from `at` on: loads behind its end
+// give zeros.
+__device__ __forceinline__ u32x4 buffer_of(const void *p, int64_t at, int64_t size) {
+    const uint64_t from = reinterpret_cast<uint64_t>(p) + (uint64_t)at;
+    const int64_t left = max((int64_t)0, min(size - at, (int64_t)0xFFFFFFFFLL));
+    return u32x4{(uint32_t)from, (uint32_t)(from >> 32) & 0xFFFFu, (uint32_t)left, 0x00020000u};
+}
 
 // Part of a product: an output tile, or a split of its sum.
 struct Item {
@@ -344,14 +346,16 @@ __device__ __forceinline__ void swap_rows(u32x4 &a, u32x4 &b, bool odd) {
     }
 }
 
-constexpr int kAux = 0;
+constexpr int kStreamed = 2;  // a store's cache policy: not kept in L2 (736 -> 700 us)
 
-template <class T, int OP, int PLANES>
+template <class T, int OP, int PLANES, bool DIRECT>
 __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
 #ifdef __HIP_DEVICE_COMPILE__  // the host needs the launch stub alone
     using X = Side<OP == kLogits, OP == kLogits>;
     using Y = Side<OP != kWeight, false>;
-    __shared__ __attribute__((aligned(1024))) char shared[2 * kStageBytes];
+    static_assert(!DIRECT || OP == kLogits, "a form of the logits");
+    __shared__ __attribute__((aligned(1024))) char
+        shared[2 * kStageBytes + (DIRECT ? kRefPlaces * kY * 4 : 0)];
     lds_char *lds = (lds_char *)shared;
     const uint32_t lds_at = (uint32_t)(uintptr_t)lds;
     const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -362,6 +366,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
     const int64_t ny = OP == kWeight ? a.ny : min(a.ny, count);
     const int64_t nk = OP == kWeight ? max((int64_t)0, min(a.nk, count)) : a.nk;
     if (ny <= 0 || (OP == kWeight && a.add && nk == 0)) return;
+    if (OP == kLogits && a.retry && a.scalars->retries == 0) return;
     const int ytiles = (int)((ny + kY - 1) / kY), tiles = a.xtiles * ytiles;
     const int items = OP == kHidden   ? tiles * a.splits
                       : OP == kWeight ? a.whole + (tiles - a.whole) * a.parts_of_rest
@@ -409,42 +414,53 @@ __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
         xsrc[c] = X::source(wave * kCalls + c, lane, a.xld);
         ysrc[c] = Y::source(wave * kCalls + c, lane, a.yld);
     }
-    const int64_t xstep = OP == kLogits ? kK * 2 : a.xld * kK * 2;
-    const int64_t ystep = OP != kWeight ? kK * 2 : a.yld * kK * 2;
-    Source xs, ys;
     Item load = item_of(at);
-    int load_at = at, issued = 0;
-    auto begin_planes = [&](int px, int py) {
-        const int64_t xat = (OP == kLogits ? load.x0 * a.xld + load.k0 : load.k0 * a.xld + load.x0) * 2;
-        const int64_t yat = (OP != kWeight ? load.y0 * a.yld + load.k0 : load.k0 * a.yld + load.y0) * 2;
-        xs = Source{static_cast<const char *>(a.x[px]) + xat, load.empty ? 0 : a.xsize * 2 - xat};
-        ys = Source{static_cast<const char *>(a.y[py]) + yat, load.empty ? 0 : a.ysize * 2 - yat};
+    int load_at = at, load_pair = 0, load_step = 0;
+    u32x4 bx, by;
+    auto place_loads = [&] {
+        const int64_t k = load.k0 + (int64_t)load_step * kK;
+        const int64_t x = OP == kLogits ? load.x0 * a.xld + k : k * a.xld + load.x0;
+        const int64_t y = OP != kWeight ? load.y0 * a.yld + k : k * a.yld + load.y0;
+        const void *px = a.x[0], *py = a.y[0];
+        if (PLANES > 1) {  // high by high, low by high, high by low
+            px = load_pair == 1 ? a.x[1] : px;
+            py = load_pair == 2 ? a.y[1] : py;
+        }
+        bx = buffer_of(px, x * 2, load.empty ? 0 : a.xsize * 2);
+        by = buffer_of(py, y * 2, load.empty ? 0 : a.ysize * 2);
     };
-    begin_planes(0, 0);
-    u32x4 bx = xs.buffer(), by = ys.buffer();
+    place_loads();
     // the c-th of the loads of a step's tiles (behind the last step: of zeros)
     auto load_one = [&](int stage, int c) {
         const uint32_t to = lds_at + (uint32_t)(stage * kStageBytes);
         if (c < kCalls) load_lds(bx, xsrc[c], to + (wave * kCalls + c) * 1024);
         else load_lds(by, ysrc[c - kCalls], to + kXBytes + (wave * kCalls + c - kCalls) * 1024);
     };
-    auto next_loads = [&] {
-        ++issued;
-        if (issued == load.per * kPairsOfPlanes) {
-            issued = 0;
-            load_at += gridDim.x;
-            if (load_at < items) load = item_of(load_at);
-            else load.empty = true;
-            begin_planes(0, 0);
-        } else if (PLANES > 1 && issued == load.per) {
-            begin_planes(1, 0);  // low of x
-        } else if (PLANES > 1 && issued == 2 * load.per) {
-            begin_planes(0, 1);  // low of y
-        } else {
-            xs.advance(xstep);
-            ys.advance(ystep);
+    // the references of the rows of an item
+    int load_place = 0;
+    auto load_refs = [&] {
+        if constexpr (DIRECT) {
+            const int r = (wave & 3) * kWave;
+            const u32x4 rows = buffer_of(a.ref, (load.y0 + r) * 4, load.empty ? 0 : ny * 4);
+            load_lds_dword(rows, (uint32_t)(lane * 4),
+                           lds_at + 2 * kStageBytes + (load_place * kY + r) * 4);
+            load_place = (load_place + 1) % kRefPlaces;
         }
-        bx = xs.buffer(), by = ys.buffer();
+    };
+    auto next_loads = [&] {
+        ++load_step;
+        if (load_step == load.per) {
+            load_step = 0;
+            ++load_pair;
+            if (load_pair == kPairsOfPlanes) {
+                load_pair = 0;
+                load_at += gridDim.x;
+                if (load_at < items) load = item_of(load_at);
+                else load.empty = true;
+                load_refs();
+            }
+        }
+        place_loads();
     };
 
     f32x4 acc[8][4];
@@ -504,7 +520,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
         if (a.mean) c1 /= (float)max(a.scalars->count, 1);
         if (PLANES > 1) c1 *= pow2(-lift_of(a.scalars->top_h));
     }
-    auto finish = [&](const Item &m) {
+    auto finish = [&](const Item &m, int place) {
         int at_lane = lane;
         asm volatile("" : "+v"(at_lane));  // addresses are worked out here, not kept through the loop
         const int g = at_lane / 16, l16 = at_lane % 16;
@@ -534,23 +550,26 @@ __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int i = wy * 64 + 16 * j + l16;
-                float top = -INFINITY;
+                float top = -INFINITY, sum = 0.f;
+                const float less =
+                    DIRECT ? -*(const __attribute__((address_space(3))) float *)(
+                                  lds + 2 * kStageBytes + (place * kY + i) * 4)
+                            : 0.f;
 #pragma unroll
                 for (int f = 0; f < 8; ++f)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        acc[f][j][r] *= c1;
+                        acc[f][j][r] = fmaf(acc[f][j][r], c1, less);
                         top = fmaxf(top, acc[f][j][r]);
                     }
                 top = fmaxf(top, __shfl_xor(top, 16));
                 top = fmaxf(top, __shfl_xor(top, 32));
-                const float ref = top == -INFINITY ? 0.f : top - kHead;
-                float sum = 0.f;
+                const float ref = DIRECT ? top : top == -INFINITY ? 0.f : top - kHead;
 #pragma unroll
                 for (int f = 0; f < 8; ++f)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const float e = exp2_(acc[f][j][r] - ref);
+                        const float e = exp2_(DIRECT ? acc[f][j][r] : acc[f][j][r] - ref);
                         acc[f][j][r] = e;
                         sum += e;
                     }
@@ -578,12 +597,12 @@ __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
                         (uint32_t)(((i & ~1) * a.eld + v0 + 32 * (p + (l16 & 1)) + 8 * g) * 2);
                     const uint32_t row = (uint32_t)(a.eld * 2);
                     swap_rows(h[p], h[p + 1], l16 & 1);
-                    __builtin_amdgcn_raw_buffer_store_b128(h[p], eh, to, 0, kAux);
-                    __builtin_amdgcn_raw_buffer_store_b128(h[p + 1], eh, to + row, 0, kAux);
+                    __builtin_amdgcn_raw_buffer_store_b128(h[p], eh, to, 0, kStreamed);
+                    __builtin_amdgcn_raw_buffer_store_b128(h[p + 1], eh, to + row, 0, kStreamed);
                     if (PLANES > 1) {
                         swap_rows(l[p], l[p + 1], l16 & 1);
-                        __builtin_amdgcn_raw_buffer_store_b128(l[p], el, to, 0, kAux);
-                        __builtin_amdgcn_raw_buffer_store_b128(l[p + 1], el, to + row, 0, kAux);
+                        __builtin_amdgcn_raw_buffer_store_b128(l[p], el, to, 0, kStreamed);
+                        __builtin_amdgcn_raw_buffer_store_b128(l[p + 1], el, to + row, 0, kStreamed);
                     }
                 }
             }
@@ -622,16 +641,17 @@ __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
         }
     };
 
+    load_refs();
     static_assert(2 * kCalls == 8, "a load for each four products of half a step");
     for (int k = 0; k < 2; ++k) {
 #pragma unroll
         for (int c = 0; c < 8; ++c) load_one(k, c);
         next_loads();
     }
-    arrive(Int<8>{});
+    arrive(Int<0>{});
 #pragma unroll
     for (int i = 0; i < 8; ++i) read_one(0, i, Int<0>{});
-    int stage = 0;
+    int stage = 0, place = 0;
     bool stored = false;
     for (; at < items; at += gridDim.x) {
         const Item m = item_of(at);
@@ -648,7 +668,8 @@ __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
             next_loads();
             stage ^= 1;
         }
-        finish(m);
+        finish(m, place);
+        place = (place + 1) % kRefPlaces;
         stored = true;
     }
     arrive(Int<0>{});  // the loads of nothing have ended, too
@@ -709,7 +730,7 @@ __device__ __forceinline__ float block_all(float x, float *shared) {
 }
 
 struct RowArgs {
-    const Scalars *scalars;
+    Scalars *scalars;
     const int32_t *rowmap;
     int64_t row0;
     const f32x2 *parts;
@@ -727,16 +748,101 @@ struct RowArgs {
     bool distill;
     float tau;
     float *losses;
+    float *targets;  // [row][entry]: logits of the targets, in units of log 2
+    // DIRECT only, of each row: its reference, 2^(reference - lse) and the row times that
+    float *ref, *factor;
+    const uint16_t *h;
+    uint16_t *scaled;
+    int64_t pad;
 };
 
-// Row i of the logits: the sum of its exponentials from those of its groups, the
-// loss, and the exponentials turned into (softmax - target) * 2^gshift.
-template <class T, int PLANES>
-__global__ __launch_bounds__(kRowThreads) void head_rows(RowArgs a) {
+// Column of entry k of the row, -1 where there is none; bad is set if it is not one
+// of the vocabulary.
+__device__ __forceinline__ int64_t target_at(const RowArgs &a, int64_t t, int k, bool &bad) {
+    const int64_t at = a.distill ? t * a.entries + k : t;
+    const int64_t v = index_at(a.index, at, a.index_type);
+    if (a.distill && (v < 0 || element(a.logits, at, a.logits_type) == -INFINITY)) return -1;
+    if (v >= 0 && v < a.vocab) return v;
+    bad = true;
+    return -1;
+}
+
+// The logits of the targets (NaN in the first place if one is not a column), and as
+// the row's reference the largest of them: no larger than the row's largest logit.
+// A block does four rows of one entry each, or one row.
+__global__ __launch_bounds__(kRowThreads) void head_targets(RowArgs a) {
     __shared__ float shared[kRowThreads / kWave];
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    constexpr int kWaves = kRowThreads / kWave;
+    const int64_t i = a.row0 + (a.entries == 1 ? blockIdx.x * (int64_t)kWaves + wave : blockIdx.x);
+    if (i >= a.scalars->count) return;  // of the block, or with one entry of the wave
+    const int64_t t = a.rowmap[i];
+    float *to = a.targets + (i - a.row0) * a.entries;
+    float top = -INFINITY;
+    bool bad = false;
+    for (int k = a.entries == 1 ? 0 : wave; k < a.entries; k += kWaves) {
+        const int64_t v = target_at(a, t, k, bad);
+        float dot = 0.f;
+        if (v >= 0) {
+            f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+            for (int64_t n = 4 * lane; n < a.dim; n += 4 * kWave) {
+                if (n + 4 <= a.dim) {
+                    const f32x4 x = load4(a.hidden, t * a.hld + n, a.type);
+                    const f32x4 y = load4(a.weight, v * a.wld + n, a.type);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) sum[r] = fmaf(x[r], y[r], sum[r]);
+                } else {
+                    for (int64_t m = n; m < a.dim; ++m)
+                        sum[0] = fmaf(element(a.hidden, t * a.hld + m, a.type),
+                                      element(a.weight, v * a.wld + m, a.type), sum[0]);
+                }
+            }
+            dot = wave_sum((sum[0] + sum[1]) + (sum[2] + sum[3])) * (kLog2e / a.tau);
+            top = fmaxf(top, dot);
+        }
+        if (lane == 0) to[k] = dot;
+    }
+    if (a.entries > 1) {
+        top = block_all<Max>(top, shared);
+        bad = block_all<Max>(bad ? 1.f : 0.f, shared) > 0.f;
+    }
+    if (lane == 0 && (wave == 0 || a.entries == 1)) {
+        if (bad) to[0] = __uint_as_float(0x7FC00000u);
+        if (a.ref != nullptr) a.ref[i - a.row0] = fabsf(top) < INFINITY ? top : 0.f;
+    }
+}
+
+// Rows whose largest logit is so far above the reference that their exponentials or
+// the products with them might be too large get that logit as their reference.
+constexpr float kReach = 64.f;
+__global__ __launch_bounds__(kRowThreads) void head_reach(RowArgs a) {
+    const int lane = threadIdx.x % kWave;
+    const int64_t local = blockIdx.x * (int64_t)(kRowThreads / kWave) + threadIdx.x / kWave;
+    if (a.row0 + local >= a.scalars->count) return;
+    const f32x2 *parts = a.parts + local * a.parts_ld;
+    float top = -INFINITY;
+    for (int64_t k = lane; k < a.groups; k += kWave) top = fmaxf(top, parts[k][0]);
+    top = wave_max(top);
+    if (lane != 0 || !(top > kReach)) return;
+    a.ref[local] += top;
+    atomicAdd(&a.scalars->retries, 1);
+}
+
+// Row i of the logits: the sum of its exponentials, the loss, and the exponentials
+// made into what the gradients' products take. In general that is (softmax - target)
+// * 2^gshift, from exponentials relative to a reference of each group of columns.
+// DIRECT (bfloat16, whose range is float32's, and one target): they are relative to
+// the row's reference, and so the row's factor is left to the other sides: the hidden
+// gradient's rows are multiplied by it in the end, and the hidden rows for the
+// weight's gradient here. This saves a pass over all exponentials (345 of 2,600 us
+// with 8,192 rows of 50,257), and is one more rounding of what the weight's gradient
+// is made of: with a teacher's many targets, too much of one.
+template <class T, int PLANES, bool DIRECT>
+__global__ __launch_bounds__(kRowThreads) void head_rows(RowArgs a) {
+        __shared__ float shared[kRowThreads / kWave];
     __shared__ float sp[kMaxEntries], sz[kMaxEntries];
     __shared__ int64_t sv[kMaxEntries];
-    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+    const int tid = threadIdx.x;
     const int64_t local = blockIdx.x, i = a.row0 + local;
     const int64_t count = a.scalars->count;
     if (i >= count) {
@@ -747,48 +853,40 @@ __global__ __launch_bounds__(kRowThreads) void head_rows(RowArgs a) {
             u32x4 *g = reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(a.g[p]) + local * a.gld);
             for (int64_t k = tid; k < a.gld / 8; k += kRowThreads) g[k] = zero;
         }
+        if (DIRECT) {
+            u32x4 *h = reinterpret_cast<u32x4 *>(a.scaled + local * a.pad);
+            for (int64_t k = tid; k < a.pad / 8; k += kRowThreads) h[k] = zero;
+        }
         return;
     }
     const int64_t t = a.rowmap[i];
     const f32x2 *parts = a.parts + local * a.parts_ld;
-    float top = -INFINITY;
-    for (int64_t k = tid; k < a.groups; k += kRowThreads) top = fmaxf(top, parts[k][0]);
-    top = block_all<Max>(top, shared);
+    const float ref = DIRECT ? a.ref[local] : 0.f;
+    float top = 0.f;
+    if (!DIRECT) {
+        top = -INFINITY;
+        for (int64_t k = tid; k < a.groups; k += kRowThreads) top = fmaxf(top, parts[k][0]);
+        top = block_all<Max>(top, shared);
+    }
     float sum = 0.f;
     for (int64_t k = tid; k < a.groups; k += kRowThreads)
-        sum += parts[k][1] * exp2_(parts[k][0] - top);
+        sum += DIRECT ? parts[k][1] : parts[k][1] * exp2_(parts[k][0] - top);
     sum = block_all<Sum>(sum, shared);
-    float lse2 = top + __log2f(sum);
+    float lse2 = (DIRECT ? ref : top) + __log2f(sum);
 
     // the targets: their columns, probabilities and logits
-    const float zscale = kLog2e / a.tau;
     const int entries = (int)a.entries;
-    const int64_t first = a.distill ? t * a.entries : t;
-    bool bad = false;
     for (int k = tid; k < entries; k += kRowThreads) {
-        int64_t v = index_at(a.index, first + k, a.index_type);
-        float y = 0.f;
-        bool there = true;
-        if (a.distill) {
-            y = element(a.logits, first + k, a.logits_type);
-            there = v >= 0 && y != -INFINITY;
-        }
-        if (there && (v < 0 || v >= a.vocab)) bad = true;
-        sv[k] = there && !bad ? v : -1;
-        sp[k] = there ? y * zscale : -INFINITY;
-    }
-    if (block_all<Max>(bad ? 1.f : 0.f, shared) > 0.f) lse2 = __uint_as_float(0x7FC00000u);
-    for (int k = wave; k < entries; k += kRowThreads / kWave) {
-        const int64_t v = sv[k];
-        float dot = 0.f;
-        if (v >= 0)
-            for (int64_t n = lane; n < a.dim; n += kWave)
-                dot = fmaf(element(a.hidden, t * a.hld + n, a.type),
-                           element(a.weight, v * a.wld + n, a.type), dot);
-        dot = wave_sum(dot);
-        if (lane == 0) sz[k] = dot * zscale;
+        bool bad = false;
+        sv[k] = target_at(a, t, k, bad);
+        sz[k] = a.targets[local * a.entries + k];
+        sp[k] = !a.distill ? 0.f
+                : sv[k] < 0
+                    ? -INFINITY
+                    : element(a.logits, t * a.entries + k, a.logits_type) * (kLog2e / a.tau);
     }
     __syncthreads();
+    if (sz[0] != sz[0]) lse2 = sz[0];
     float loss;
     if (!a.distill) {
         loss = (lse2 - sz[0]) * kLn2;
@@ -815,36 +913,60 @@ __global__ __launch_bounds__(kRowThreads) void head_rows(RowArgs a) {
     if (lse2 != lse2) loss = lse2;
     if (tid == 0) a.losses[t] = loss;
     if (!a.store) return;
-    __syncthreads();
 
-    // the row: exponentials times 2^(reference - lse + gshift)
-    for (int64_t k = tid; k < a.gld / 8; k += kRowThreads) {
-        const int64_t v = 8 * k;
-        u32x4 *gh = reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(a.g[0]) + local * a.gld) + k;
-        u32x4 *gl = reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(a.g[PLANES - 1]) +
-                                              local * a.gld) + k;
-        u32x4 h = {0, 0, 0, 0}, l = {0, 0, 0, 0};
-        if (v < a.vocab) {
-            const float f = exp2_(parts[v / kGroup][0] - lse2 + (float)a.gshift);
-            h = *gh;
-            if (PLANES > 1) l = *gl;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                float x = value((uint16_t)h[r], T{}), y = value((uint16_t)(h[r] >> 16), T{});
-                if (PLANES > 1) {
-                    x += value((uint16_t)l[r], T{});
-                    y += value((uint16_t)(l[r] >> 16), T{});
-                }
-                x = v + 2 * r < a.vocab ? x * f : 0.f;
-                y = v + 2 * r + 1 < a.vocab ? y * f : 0.f;
-                h[r] = two(x, y, T{});
-                if (PLANES > 1)
-                    l[r] = two(x - value((uint16_t)h[r], T{}),
-                               y - value((uint16_t)(h[r] >> 16), T{}), T{});
-            }
+    if constexpr (DIRECT) {
+        // the factor is moved, by less than half a step of bfloat16, to where the target's
+        // place, which most of the gradients comes from, rounds to no error
+        float f = exp2_(ref - lse2);
+        const float own = exp2_(sz[0] - lse2) - 1.f;
+        const uint16_t held = (uint16_t)two(own / f, 0.f, T{});
+        if (fabsf(own) > 0x1p-10f) f = own / value(held, T{});
+        if (tid == 0) {
+            a.factor[local] = f;
+            static_cast<uint16_t *>(a.g[0])[local * a.gld + sv[0]] = held;
         }
-        *gh = h;
-        if (PLANES > 1) *gl = l;
+        const u32x4 *from = reinterpret_cast<const u32x4 *>(a.h + i * a.pad);
+        u32x4 *to = reinterpret_cast<u32x4 *>(a.scaled + local * a.pad);
+        for (int64_t k = tid; k < a.pad / 8; k += kRowThreads) {
+            u32x4 x = from[k];
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                x[r] = two(value((uint16_t)x[r], T{}) * f, value((uint16_t)(x[r] >> 16), T{}) * f,
+                           T{});
+            to[k] = x;
+        }
+        return;
+    } else {
+        // the row: exponentials times 2^(reference - lse + gshift)
+        for (int64_t k = tid; k < a.gld / 8; k += kRowThreads) {
+            const int64_t v = 8 * k;
+            u32x4 *gh =
+                reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(a.g[0]) + local * a.gld) + k;
+            u32x4 *gl = reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(a.g[PLANES - 1]) +
+                                                  local * a.gld) + k;
+            u32x4 h = {0, 0, 0, 0}, l = {0, 0, 0, 0};
+            if (v < a.vocab) {
+                const float f = exp2_(parts[v / kGroup][0] - lse2 + (float)a.gshift);
+                h = *gh;
+                if (PLANES > 1) l = *gl;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    float x = value((uint16_t)h[r], T{}), y = value((uint16_t)(h[r] >> 16), T{});
+                    if (PLANES > 1) {
+                        x += value((uint16_t)l[r], T{});
+                        y += value((uint16_t)(l[r] >> 16), T{});
+                    }
+                    x = v + 2 * r < a.vocab ? x * f : 0.f;
+                    y = v + 2 * r + 1 < a.vocab ? y * f : 0.f;
+                    h[r] = two(x, y, T{});
+                    if (PLANES > 1)
+                        l[r] = two(x - value((uint16_t)h[r], T{}),
+                                   y - value((uint16_t)(h[r] >> 16), T{}), T{});
+                }
+            }
+            *gh = h;
+            if (PLANES > 1) *gl = l;
+        }
     }
     __syncthreads();
     // less the targets: an index that comes several times once, with their sum
@@ -882,6 +1004,7 @@ struct ReduceArgs {
     float scale;
     bool mean;
     int gshift;
+    const float *factor;  // of each row, or null
 };
 
 // The gradient of a hidden row: the sum of its splits, in their order.
@@ -892,6 +1015,7 @@ __global__ __launch_bounds__(256) void head_hidden(ReduceArgs a) {
     float s = a.scale * pow2(-a.gshift);
     if (a.mean) s /= (float)count;
     if (a.type == RCS_F32) s *= pow2(-lift_of(a.scalars->top_w));
+    if (a.factor != nullptr) s *= a.factor[i];
     const int64_t t = a.rowmap[a.row0 + i];
     for (int64_t n = threadIdx.x; n < a.dim; n += blockDim.x) {
         float x = 0.f;
@@ -945,9 +1069,9 @@ struct Plan {
     int64_t eld, groups;
     int splits, whole, parts_of_rest;
     int64_t kper;
-    bool copy_w, wide_out;
+    bool copy_w, wide_out, direct;
     // offsets in the workspace
-    int64_t scalars, flags, rowmap, inverse, losses, h[2], w[2], e[2], parts, partial, rest, acc, bytes;
+    int64_t scalars, flags, rowmap, inverse, losses, h[2], w[2], e[2], parts, targets, ref, factor, scaled, partial, rest, acc, bytes;
 };
 
 bool direct_weight(const rcs_head *a) {
@@ -955,7 +1079,7 @@ bool direct_weight(const rcs_head *a) {
            (reinterpret_cast<uintptr_t>(a->weight) & 15u) == 0;
 }
 
-Plan plan_of(const rcs_head *a, int64_t limit) {
+Plan plan_of(const rcs_head *a, int64_t entries, bool distill) {
     Plan p = {};
     const bool grads = a->grad_hidden != nullptr || a->grad_weight != nullptr;
     p.planes = a->type == RCS_F32 ? 2 : 1;
@@ -967,10 +1091,11 @@ Plan plan_of(const rcs_head *a, int64_t limit) {
     p.eld = round_up(a->vocab, kX);
     if (p.eld % 512 == 0) p.eld += 64;
     p.copy_w = !direct_weight(a);
+    p.direct = a->type == RCS_BF16 && !distill;
     // rows of a group: as many as fit the limit, in whole tiles
     const int64_t row_bytes = (grads ? p.eld * 2 * p.planes : 0) + p.groups * 8;
     p.chunk = round_up(a->rows > 0 ? a->rows : 1, kMinChunk);
-    const int64_t fit = limit / row_bytes / kMinChunk * kMinChunk;
+    const int64_t fit = a->limit / row_bytes / kMinChunk * kMinChunk;
     if (p.chunk > fit) p.chunk = fit < kMinChunk ? kMinChunk : fit;
     // splits of the hidden gradient's sum over the vocabulary: the number that fills
     // the chip's rounds best, each item costing about as much as kItemSteps steps more
@@ -1011,6 +1136,12 @@ Plan plan_of(const rcs_head *a, int64_t limit) {
     if (p.copy_w)
         for (int k = 0; k < p.planes; ++k) p.w[k] = take(2 * a->vocab * p.pad);
     p.parts = take(8 * p.chunk * p.groups);
+    p.targets = take(4 * p.chunk * entries);
+    if (p.direct) {
+        p.ref = take(4 * p.chunk);
+        p.factor = take(4 * p.chunk);
+        if (grads) p.scaled = take(2 * p.chunk * p.pad);
+    }
     if (grads)
         for (int k = 0; k < p.planes; ++k) p.e[k] = take(2 * p.chunk * p.eld);
     if (a->grad_hidden != nullptr) p.partial = take(4 * p.splits * p.chunk * p.pad);
@@ -1041,7 +1172,7 @@ int check_head(const rcs_head *a) {
     return RCS_OK;
 }
 
-template <class T, int OP, int PLANES>
+template <class T, int OP, int PLANES, bool DIRECT>
 void launch_gemm(GemmArgs &g, hipStream_t stream) {
     g.xtiles = (int)(round_up(g.nx, kX) / kX);
     g.ytiles = (int)(round_up(g.ny, kY) / kY);
@@ -1050,12 +1181,12 @@ void launch_gemm(GemmArgs &g, hipStream_t stream) {
     if (OP == kHidden) items *= g.splits;
     if (OP == kWeight) items = g.whole + (tiles - g.whole) * g.parts_of_rest;
     const int64_t blocks = items < kCus ? items : kCus;
-    head_gemm<T, OP, PLANES><<<dim3((unsigned)blocks), kGemmThreads, 0, stream>>>(g);
+    head_gemm<T, OP, PLANES, DIRECT><<<dim3((unsigned)blocks), kGemmThreads, 0, stream>>>(g);
     if (OP == kWeight && g.parts_of_rest > 1)
         head_weight_join<<<dim3((unsigned)((tiles - g.whole) * kY)), kWave, 0, stream>>>(g);
 }
 
-template <class T, int PLANES>
+template <class T, int PLANES, bool DIRECT>
 void launch_products(const rcs_head *a, const Targets &tg, const Plan &p, char *ws,
                      hipStream_t stream) {
     const bool grads = a->grad_hidden != nullptr || a->grad_weight != nullptr;
@@ -1083,9 +1214,6 @@ void launch_products(const rcs_head *a, const Targets &tg, const Plan &p, char *
         g.eld = p.eld, g.parts = reinterpret_cast<f32x2 *>(ws + p.parts), g.groups = p.groups;
         g.zscale = kLog2e / tg.tau;
         g.store = grads;
-        if (rows > 0)
-            launch_gemm<T, kLogits, PLANES>(g, stream);
-
         RowArgs r = {};
         r.scalars = scalars;
         r.rowmap = reinterpret_cast<int32_t *>(ws + p.rowmap);
@@ -1099,9 +1227,27 @@ void launch_products(const rcs_head *a, const Targets &tg, const Plan &p, char *
         r.index = tg.index, r.logits = tg.logits, r.index_type = tg.index_type;
         r.logits_type = tg.logits_type, r.entries = tg.entries, r.distill = tg.distill;
         r.tau = tg.tau, r.losses = losses;
-        const int64_t row_blocks = grads ? round_up(rows, kK) : rows;
-        if (rows > 0)
-            head_rows<T, PLANES><<<dim3((unsigned)row_blocks), kRowThreads, 0, stream>>>(r);
+        r.targets = reinterpret_cast<float *>(ws + p.targets);
+        r.h = reinterpret_cast<const uint16_t *>(ws + p.h[0]), r.pad = p.pad;
+        if (DIRECT) {
+            r.ref = reinterpret_cast<float *>(ws + p.ref);
+            r.factor = reinterpret_cast<float *>(ws + p.factor);
+            r.scaled = reinterpret_cast<uint16_t *>(ws + p.scaled);
+            g.ref = r.ref;
+        }
+        if (rows > 0) {
+            const unsigned fours = (unsigned)((rows + 3) / 4);
+            head_targets<<<dim3(tg.entries == 1 ? fours : (unsigned)rows), kRowThreads, 0,
+                           stream>>>(r);
+            launch_gemm<T, kLogits, PLANES, DIRECT>(g, stream);
+            if (DIRECT) {
+                head_reach<<<dim3(fours), kRowThreads, 0, stream>>>(r);
+                g.retry = true;
+                launch_gemm<T, kLogits, PLANES, DIRECT>(g, stream);
+            }
+            const int64_t row_blocks = grads ? round_up(rows, kK) : rows;
+            head_rows<T, PLANES, DIRECT><<<dim3((unsigned)row_blocks), kRowThreads, 0, stream>>>(r);
+        }
 
         if (a->grad_hidden != nullptr && rows > 0) {
             GemmArgs q = g;
@@ -1110,18 +1256,21 @@ void launch_products(const rcs_head *a, const Targets &tg, const Plan &p, char *
             q.nx = a->dim, q.ny = rows, q.nk = round_up(a->vocab, kK), q.kper = p.kper;
             q.partial = reinterpret_cast<float *>(ws + p.partial), q.pld = p.pad;
             q.splits = p.splits;
-            launch_gemm<T, kHidden, PLANES>(q, stream);
+            launch_gemm<T, kHidden, PLANES, false>(q, stream);
             ReduceArgs d = {};
             d.scalars = scalars, d.rowmap = r.rowmap, d.row0 = row0, d.rows = rows;
             d.dim = a->dim, d.pld = p.pad, d.partial = q.partial, d.splits = p.splits;
             d.out = a->grad_hidden, d.old = a->grad_hidden_stride, d.type = a->type;
             d.scale = scale, d.mean = g.mean, d.gshift = gshift;
+            d.factor = r.factor;
             head_hidden<<<dim3((unsigned)rows), 256, 0, stream>>>(d);
         }
         if (a->grad_weight != nullptr) {
             GemmArgs q = g;
-            for (int k = 0; k < PLANES; ++k) q.x[k] = g.y[k], q.y[k] = g.e[k];
-            q.xld = p.pad, q.xsize = g.ysize;
+            for (int k = 0; k < PLANES; ++k)
+                q.x[k] = DIRECT ? ws + p.scaled : static_cast<const char *>(g.y[k]),
+                q.y[k] = g.e[k];
+            q.xld = p.pad, q.xsize = DIRECT ? p.chunk * p.pad : g.ysize;
             q.yld = p.eld, q.ysize = p.chunk * p.eld;
             q.nx = a->dim, q.ny = a->vocab, q.nk = rows, q.kper = round_up(rows, kK);
             q.out = p.wide_out ? ws + p.acc : a->grad_weight;
@@ -1130,7 +1279,7 @@ void launch_products(const rcs_head *a, const Targets &tg, const Plan &p, char *
             q.add = row0 > 0 || (a->accumulate != 0 && !p.wide_out);
             q.partial = reinterpret_cast<float *>(ws + p.rest);
             q.whole = p.whole, q.parts_of_rest = p.parts_of_rest;
-            launch_gemm<T, kWeight, PLANES>(q, stream);
+            launch_gemm<T, kWeight, PLANES, false>(q, stream);
         }
     }
     if (p.wide_out)
@@ -1167,7 +1316,7 @@ int head_call(const rcs_head *a, const Targets &tg, hipStream_t stream) {
     if (a->losses != nullptr && (rc = writes.array(a->losses, 4 * a->rows, 4)) != RCS_OK)
         return rc;
     if ((rc = writes.array(a->loss, 4, 4)) != RCS_OK) return rc;
-    const Plan p = plan_of(a, a->limit);
+    const Plan p = plan_of(a, tg.entries, tg.distill);
     if (a->workspace_bytes < p.bytes) return RCS_ESIZE;
     if ((rc = writes.array(a->workspace, p.bytes, 256)) != RCS_OK) return rc;
     if (writes.overlap(reads)) return RCS_EINVAL;
@@ -1204,9 +1353,10 @@ int head_call(const rcs_head *a, const Targets &tg, hipStream_t stream) {
         w.type = a->type, w.scalars = scalars;
         head_prep<<<dim3((unsigned)a->vocab), 256, 0, stream>>>(w);
     }
-    if (a->type == RCS_F32) launch_products<F16, 2>(a, tg, p, ws, stream);
-    else if (a->type == RCS_F16) launch_products<F16, 1>(a, tg, p, ws, stream);
-    else launch_products<BF16, 1>(a, tg, p, ws, stream);
+    if (a->type == RCS_F32) launch_products<F16, 2, false>(a, tg, p, ws, stream);
+    else if (a->type == RCS_F16) launch_products<F16, 1, false>(a, tg, p, ws, stream);
+    else if (p.direct) launch_products<BF16, 1, true>(a, tg, p, ws, stream);
+    else launch_products<BF16, 1, false>(a, tg, p, ws, stream);
     head_total<<<1, 1024, 0, stream>>>(scalars, inverse, losses, a->rows, a->mean != 0, a->loss);
     return hipGetLastError() == hipSuccess ? RCS_OK : RCS_EHIP;
 }
@@ -1215,9 +1365,11 @@ int head_call(const rcs_head *a, const Targets &tg, hipStream_t stream) {
 
 extern "C" {
 
-int64_t rcs_head_workspace(const rcs_head *a) {
+int64_t rcs_head_workspace(const rcs_head *a, int64_t entries) {
     const int rc = check_head(a);
-    return rc != RCS_OK ? rc : plan_of(a, a->limit).bytes;
+    if (rc != RCS_OK) return rc;
+    if (entries < 0 || entries > kMaxEntries) return RCS_EINVAL;
+    return plan_of(a, entries > 0 ? entries : 1, entries > 0).bytes;
 }
 
 int head_loss(const rcs_head *a, const void *targets, int index_type, int64_t ignore_index,

@@ -84,7 +84,7 @@ def _stream_context(stream):
     return torch.cuda.stream(stream)
 
 
-def _head(call, name, hidden, weight, grad_hidden, grad_weight, accumulate, reduction, scale,
+def _head(call, name, entries, hidden, weight, grad_hidden, grad_weight, accumulate, reduction, scale,
           losses, out, max_bytes, stream):
     dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
     h, hs = _matrix(hidden, "hidden", dev, _TYPES)
@@ -107,7 +107,7 @@ def _head(call, name, hidden, weight, grad_hidden, grad_weight, accumulate, redu
         a.grad_weight, a.grad_weight_type = g.data_ptr(), _TYPES[g.dtype]
     if losses is not None:
         a.losses = _packed(losses, "losses", dev, (torch.float32,), lead).data_ptr()
-    need = lib().rcs_head_workspace(ctypes.byref(a))
+    need = lib().rcs_head_workspace(ctypes.byref(a), entries)
     _check(int(need) if need < 0 else 0, "rcs_head_workspace")
     with _stream_context(stream):
         if out is None:
@@ -149,7 +149,7 @@ def head_loss(hidden, weight, targets, *, grad_hidden=None, grad_weight=None,
     def call(a, s):
         return lib().head_loss(a, t.data_ptr(), _INDEX_TYPES[t.dtype], int(ignore_index), s)
 
-    return _head(call, "head_loss", hidden, weight, grad_hidden, grad_weight, accumulate,
+    return _head(call, "head_loss", 0, hidden, weight, grad_hidden, grad_weight, accumulate,
                  reduction, scale, losses, out, max_bytes, stream)
 
 
@@ -179,7 +179,7 @@ def head_distill(hidden, weight, indices, logits, *, temperature: float = 1.0, g
         return lib().head_distill(a, i.data_ptr(), _INDEX_TYPES[i.dtype], g.data_ptr(),
                                   _TYPES[g.dtype], entries, float(temperature), s)
 
-    return _head(call, "head_distill", hidden, weight, grad_hidden, grad_weight, accumulate,
+    return _head(call, "head_distill", entries, hidden, weight, grad_hidden, grad_weight, accumulate,
                  reduction, scale, losses, out, max_bytes, stream)
 
 
