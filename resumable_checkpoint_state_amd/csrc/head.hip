@@ -41,12 +41,12 @@ constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kX = 256, kY = 256, kK = 64;
 constexpr int kGroup = 128;  // columns of the logits with a reference of their own
 constexpr int kGemmThreads = 512, kGemmWaves = kGemmThreads / kWave;
-constexpr int kXBytes = kX * kK * 2, kStageBytes = kXBytes + kY * kK * 2;
+[[maybe_unused]] constexpr int kXBytes = kX * kK * 2, kStageBytes = kXBytes + kY * kK * 2;
 
 // What the kernels of one call tell each other, in device memory.
 struct Scalars {
     int32_t count;        // rows that have a loss
-    int32_t retries;      // of them, those whose reference was too low
+    uint32_t retry;       // not 0: a row's largest logit was beyond its reference's reach
     uint32_t top_h, top_w;  // float32 only: bits of the largest finite magnitudes
 };
 
@@ -59,130 +59,204 @@ __device__ __forceinline__ float pow2(int e) { return ldexpf(1.f, e); }
 
 // --------------------------------------------------------------- preparation
 
-// flags[t]: whether row t has a loss.
-__global__ void head_flags(const void *index, int index_type, int64_t entries, int64_t rows,
-                           int64_t ignore, const void *logits, int logits_type, bool distill,
-                           uint8_t *flags) {
+// flags[t]: whether a row with a teacher's entries has a loss.
+__global__ __launch_bounds__(256) void head_flags(const void *index, int index_type,
+                                                  int64_t entries, int64_t rows,
+                                                  const void *logits, int logits_type,
+                                                  uint8_t *flags) {
     const int64_t t = blockIdx.x * (int64_t)(blockDim.x / kWave) + threadIdx.x / kWave;
     const int lane = threadIdx.x % kWave;
     if (t >= rows) return;
     bool any = false;
-    if (!distill) any = index_at(index, t, index_type) != ignore;
-    else
-        for (int64_t k = lane; k < entries; k += kWave)
-            any |= index_at(index, t * entries + k, index_type) >= 0 &&
-                   element(logits, t * entries + k, logits_type) != -INFINITY;
-    if (__any(any) && lane == 0) flags[t] = 1;
-    if (!__any(any) && lane == 0) flags[t] = 0;
+    for (int64_t k = lane; k < entries; k += kWave)
+        any |= index_at(index, t * entries + k, index_type) >= 0 &&
+               element(logits, t * entries + k, logits_type) != -INFINITY;
+    const bool flag = __any(any);
+    if (lane == 0) flags[t] = flag;
 }
 
-// rowmap[i]: the i-th row that has a loss; inverse[t]: its i, or -1.
-__global__ __launch_bounds__(1024) void head_scan(const uint8_t *flags, int64_t rows,
-                                                  int32_t *rowmap, int32_t *inverse,
-                                                  Scalars *scalars) {
-    __shared__ int32_t sums[1024 / kWave];
+// rowmap[i]: the i-th row that has a loss; inverse[t]: its i, or -1. Without flags,
+// those whose target is not `ignore`.
+constexpr int kScanThreads = 1024, kScanRows = 8;  // consecutive rows of a thread
+__global__ __launch_bounds__(kScanThreads) void head_scan(const uint8_t *flags,
+                                                          const void *index, int index_type,
+                                                          int64_t ignore, int64_t rows,
+                                                          int32_t *rowmap, int32_t *inverse,
+                                                          Scalars *scalars) {
+    __shared__ int32_t sums[kScanThreads / kWave];
+    __shared__ uint8_t found[kScanThreads * kScanRows];
     const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
     int32_t base = 0;
-    for (int64_t at = 0; at < rows; at += 1024) {
-        const int64_t t = at + tid;
-        const bool f = t < rows && flags[t] != 0;
-        const uint64_t m = __ballot(f);
-        if (lane == 0) sums[wave] = __popcll(m);
+    for (int64_t at = 0; at < rows; at += kScanThreads * kScanRows) {
+        bool f[kScanRows];
+#pragma unroll
+        for (int k = 0; k < kScanRows; ++k) {
+            const int64_t t = at + k * kScanThreads + tid;
+            f[k] = false;
+            if (t < rows)
+                f[k] = flags != nullptr ? flags[t] != 0 : index_at(index, t, index_type) != ignore;
+        }
+#pragma unroll
+        for (int k = 0; k < kScanRows; ++k) found[k * kScanThreads + tid] = f[k];
         __syncthreads();
-        int32_t before = base, all = 0;
-        for (int w = 0; w < 1024 / kWave; ++w) {
+        const int64_t first = at + tid * kScanRows;
+        uint32_t mine = 0;
+#pragma unroll
+        for (int k = 0; k < kScanRows; ++k) mine |= (uint32_t)found[tid * kScanRows + k] << k;
+        int32_t run = __popc(mine);  // inclusive over the wave
+#pragma unroll
+        for (int d = 1; d < kWave; d *= 2) {
+            const int32_t up = __shfl_up(run, d);
+            if (lane >= d) run += up;
+        }
+        if (lane == kWave - 1) sums[wave] = run;
+        __syncthreads();
+        int32_t before = base + run - __popc(mine), all = 0;
+#pragma unroll
+        for (int w = 0; w < kScanThreads / kWave; ++w) {
             if (w < wave) before += sums[w];
             all += sums[w];
         }
-        before += __popcll(m & ((1ull << lane) - 1));
-        if (f) rowmap[before] = (int32_t)t;
-        if (t < rows) inverse[t] = f ? before : -1;
+#pragma unroll
+        for (int k = 0; k < kScanRows; ++k) {
+            if (first + k >= rows) break;
+            const bool f = mine >> k & 1;
+            if (f) rowmap[before] = (int32_t)(first + k);
+            inverse[first + k] = f ? before : -1;
+            before += f;
+        }
         base += all;
         __syncthreads();
     }
-    if (tid == 0) {
-        scalars->count = base;
-        scalars->retries = 0;
-        scalars->top_h = 0;
-        scalars->top_w = 0;
-    }
+    if (tid == 0) *scalars = Scalars{base, 0, 0, 0};
 }
 
-// Largest finite magnitude of the rows (those with a loss, where inverse is given).
-__global__ __launch_bounds__(256) void head_top(const float *p, int64_t ld, int64_t rows,
-                                                int64_t dim, const int32_t *inverse,
-                                                uint32_t *top) {
+// Rows of a matrix as the products read them: padded with zeros to `pad` columns,
+// float32 as two half-precision planes (x * 2^lift = high + low).
+struct Rows {
+    const void *src;
+    uint16_t *hi, *lo;
+    int64_t ld, rows;
+};
+struct PrepArgs {
+    Rows hidden, weight;  // weight.rows: 0 if the products read it where it is
+    int64_t dim, pad;
+    int type;
+    const int32_t *inverse;
+    Scalars *scalars;
+    void *grad;  // gradient of the hidden rows, or null
+    int64_t grad_ld;
+    float *losses;
+};
+
+// float32 only: the largest finite magnitudes of the hidden rows that have a loss (the
+// first kTopHidden blocks) and of the weight. One atomic a block: more would queue.
+constexpr int kTopHidden = 64, kTopWeight = 192;
+__global__ __launch_bounds__(1024) void head_top(PrepArgs a) {
+    __shared__ uint32_t shared[1024 / kWave];
+    const bool hidden = blockIdx.x < kTopHidden;
+    const Rows &m = hidden ? a.hidden : a.weight;
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    const int64_t waves = (hidden ? kTopHidden : kTopWeight) * (1024 / kWave);
     uint32_t best = 0;
-    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
-        if (inverse != nullptr && inverse[r] < 0) continue;
-        for (int64_t k = threadIdx.x; k < dim; k += blockDim.x) {
-            const uint32_t b = __float_as_uint(p[r * ld + k]) & 0x7FFFFFFFu;
-            if (b < 0x7F800000u && b > best) best = b;
+    auto take = [&](float x) {
+        const uint32_t b = __float_as_uint(x) & 0x7FFFFFFFu;
+        if (b < 0x7F800000u && b > best) best = b;
+    };
+    for (int64_t r = (blockIdx.x - (hidden ? 0 : kTopHidden)) * (int64_t)(1024 / kWave) + wave;
+         r < m.rows; r += waves) {
+        if (hidden && a.inverse[r] < 0) continue;
+        for (int64_t k = 4 * lane; k < a.dim; k += 4 * kWave) {
+            if (k + 4 <= a.dim) {
+                const f32x4 x = load4(m.src, r * m.ld + k, RCS_F32);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) take(x[j]);
+            } else {
+                for (int64_t j = k; j < a.dim; ++j)
+                    take(static_cast<const float *>(m.src)[r * m.ld + j]);
+            }
         }
     }
 #pragma unroll
     for (int d = 1; d < kWave; d *= 2) best = max(best, (uint32_t)__shfl_xor((int)best, d));
-    if (threadIdx.x % kWave == 0) atomicMax(top, best);
+    if (lane == 0) shared[wave] = best;
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    for (int w = 1; w < 1024 / kWave; ++w) best = max(best, shared[w]);
+    atomicMax(hidden ? &a.scalars->top_h : &a.scalars->top_w, best);
 }
 
-// Rows of src as the products read them: padded with zeros to `pad` columns,
-// float32 as two half-precision planes (x * 2^lift = high + low). With inverse,
-// row t goes to row inverse[t], rows without a loss are left out and their
-// gradient is cleared; the rows behind the last one, up to a whole step of kK,
-// are zero.
-struct PrepArgs {
-    const void *src;
-    void *hi, *lo;
-    int64_t ld, rows, dim, pad;
-    int type;
-    const int32_t *inverse;
-    Scalars *scalars;
-    bool hidden;  // hidden rows, or the weight's
-    void *grad;   // gradient of the hidden rows, or null
-    int64_t grad_ld;
-};
+// A wave does a row. Hidden row t goes to row inverse[t]; a row without a loss is left
+// out, and its gradient and loss are cleared; kK rows more are zeros behind the last
+// one, up to a whole step of the products.
 __global__ __launch_bounds__(256) void head_prep(PrepArgs a) {
-    const int64_t r = blockIdx.x;
+    int64_t r = blockIdx.x * (int64_t)(256 / kWave) + threadIdx.x / kWave;
+    const int lane = threadIdx.x % kWave;
+    const bool hidden = r < a.hidden.rows + kK;
+    const Rows &m = hidden ? a.hidden : a.weight;
+    if (!hidden) r -= a.hidden.rows + kK;
     int64_t to = r;
     bool zero = false;
-    if (a.inverse != nullptr) {
-        if (r >= a.rows) {  // blocks behind the rows: the padding
-            const int64_t count = a.scalars->count;
-            to = count + (r - a.rows);
-            if (to >= (count + kK - 1) / kK * kK) return;
-            zero = true;
-        } else {
-            to = a.inverse[r];
-            if (to < 0) {
-                if (a.grad != nullptr)
-                    for (int64_t k = threadIdx.x; k < a.dim; k += blockDim.x)
-                        put(a.grad, r * a.grad_ld + k, a.type, 0.f);
-                return;
-            }
+    if (hidden && r >= m.rows) {
+        const int64_t count = a.scalars->count;
+        to = count + (r - m.rows);
+        if (to >= (count + kK - 1) / kK * kK) return;
+        zero = true;
+    } else if (hidden) {
+        to = a.inverse[r];
+        if (to < 0) {
+            if (lane == 0) a.losses[r] = 0.f;
+            if (a.grad != nullptr)
+                for (int64_t k = 4 * lane; k < a.dim; k += 4 * kWave)
+                    put4(a.grad, r * a.grad_ld + k, a.type, f32x4{0.f, 0.f, 0.f, 0.f},
+                         a.dim - k, false);
+            return;
         }
     }
-    uint16_t *hi = static_cast<uint16_t *>(a.hi) + to * a.pad;
+    if (r >= m.rows && !zero) return;
+    uint16_t *hi = m.hi + to * a.pad;
     if (a.type == RCS_F32) {
-        uint16_t *lo = static_cast<uint16_t *>(a.lo) + to * a.pad;
-        const int lift = lift_of(a.hidden ? a.scalars->top_h : a.scalars->top_w);
-        for (int64_t k = threadIdx.x; k < a.pad; k += blockDim.x) {
-            const float x = zero || k >= a.dim
-                                ? 0.f
-                                : ldexpf(static_cast<const float *>(a.src)[r * a.ld + k], lift);
-            const uint32_t h = two(x, 0.f, F16{});
-            const float rest = x - value((uint16_t)h, F16{});
-            hi[k] = (uint16_t)h;
-            lo[k] = (uint16_t)two(rest, 0.f, F16{});
+        uint16_t *lo = m.lo + to * a.pad;
+        const float up = pow2(lift_of(hidden ? a.scalars->top_h : a.scalars->top_w));
+        for (int64_t k = 4 * lane; k < a.pad; k += 4 * kWave) {
+            f32x4 x = {0.f, 0.f, 0.f, 0.f};
+            if (!zero && k + 4 <= a.dim) {
+                x = load4(m.src, r * m.ld + k, RCS_F32);
+            } else if (!zero) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (k + j < a.dim) x[j] = static_cast<const float *>(m.src)[r * m.ld + k + j];
+            }
+            x *= up;
+            const u32x2 h = {two(x[0], x[1], F16{}), two(x[2], x[3], F16{})};
+            const f32x4 rest = x - four(h, F16{});
+            *reinterpret_cast<u32x2 *>(hi + k) = h;
+            *reinterpret_cast<u32x2 *>(lo + k) =
+                u32x2{two(rest[0], rest[1], F16{}), two(rest[2], rest[3], F16{})};
         }
-    } else {
-        for (int64_t k = threadIdx.x; k < a.pad; k += blockDim.x)
-            hi[k] = zero || k >= a.dim ? 0 : static_cast<const uint16_t *>(a.src)[r * a.ld + k];
+        return;
+    }
+    const uint16_t *from = static_cast<const uint16_t *>(m.src) + r * m.ld;
+    for (int64_t k = 8 * lane; k < a.pad; k += 8 * kWave) {
+        u32x4 x = {0, 0, 0, 0};
+        if (!zero && k + 8 <= a.dim) {
+            x = *reinterpret_cast<const u32x4_half *>(from + k);
+        } else if (!zero) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (k + j < a.dim) x[j / 2] |= (uint32_t)from[k + j] << (16 * (j & 1));
+        }
+        *reinterpret_cast<u32x4 *>(hi + k) = x;
     }
 }
 
 // ------------------------------------------------------------------ products
 
 enum Op { kLogits, kHidden, kWeight };
+
+// How far, in units of log 2, a logit may be above its row's reference: the
+// exponentials and the products with them then stay within float32's range.
+constexpr float kReach = 64.f;
 
 struct GemmArgs {
     const void *x[2], *y[2];  // planes; the second of each only with float32
@@ -193,7 +267,7 @@ struct GemmArgs {
     int xtiles, ytiles, splits;
     int whole, parts_of_rest;  // kWeight: tiles done whole, and splits of each of the rest
     int64_t row0;             // first row of this group of rows
-    const Scalars *scalars;
+    Scalars *scalars;
     // kLogits
     void *e[2];
     int64_t eld;
@@ -221,8 +295,8 @@ struct Int {
     static constexpr int value = N;
 };
 
-constexpr int kRefPlaces = 4;  // items whose rows' references are in LDS, at most
-constexpr int kCalls = 256 * kK * 2 / 1024 / kGemmWaves;  // loads of a wave for one operand
+[[maybe_unused]] constexpr int kRefPlaces = 4;  // items whose rows' references are in LDS, at most
+[[maybe_unused]] constexpr int kCalls = 256 * kK * 2 / 1024 / kGemmWaves;  // loads of a wave for one operand
 
 // How an operand's tile of 256 by kK lies in LDS: in `kCalls` loads a wave, each of
 // 1,024 consecutive bytes (source: where a lane's 16 come from), and how a wave
@@ -288,7 +362,7 @@ struct Side<false, PERM> {
 // gridDim.x, ...; blocks are dispatched round-robin over the 8 XCDs, each with an L2
 // of its own: an XCD takes a stretch of its own, so that what its 32 CUs do at once
 // shares operand tiles.
-__device__ __forceinline__ int near_item(int b, int n) {
+[[maybe_unused]] __device__ __forceinline__ int near_item(int b, int n) {
     const int per = n / 8, more = n % 8, xcd = b % 8;
     return xcd * per + min(xcd, more) + b / 8;
 }
@@ -306,13 +380,13 @@ __device__ __forceinline__ void tile_of(int at, int xtiles, int ytiles, int &tx,
 // wait for all such loads, the ones for later steps too. It has no result
 // register, and `arrive` below waits for it. The wait states: between a vector
 // instruction that wrote one of the scalars and the load.)
-__device__ __forceinline__ void load_lds(u32x4 buffer, uint32_t at, uint32_t to) {
+[[maybe_unused]] __device__ __forceinline__ void load_lds(u32x4 buffer, uint32_t at, uint32_t to) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to),
                  "v"(at), "s"(buffer)
                  : "memory");
 }
 
-__device__ __forceinline__ void load_lds_dword(u32x4 buffer, uint32_t at, uint32_t to) {
+[[maybe_unused]] __device__ __forceinline__ void load_lds_dword(u32x4 buffer, uint32_t at, uint32_t to) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(to),
                  "v"(at), "s"(buffer)
                  : "memory");
@@ -320,7 +394,7 @@ __device__ __forceinline__ void load_lds_dword(u32x4 buffer, uint32_t at, uint32
 
 // The buffer of what an array of `size` bytes has from `at` on: loads behind its end
 // give zeros.
-__device__ __forceinline__ u32x4 buffer_of(const void *p, int64_t at, int64_t size) {
+[[maybe_unused]] __device__ __forceinline__ u32x4 buffer_of(const void *p, int64_t at, int64_t size) {
     const uint64_t from = reinterpret_cast<uint64_t>(p) + (uint64_t)at;
     const int64_t left = max((int64_t)0, min(size - at, (int64_t)0xFFFFFFFFLL));
     return u32x4{(uint32_t)from, (uint32_t)(from >> 32) & 0xFFFFu, (uint32_t)left, 0x00020000u};
@@ -336,7 +410,7 @@ struct Item {
 
 // a and b of an even lane and of the odd one after it, as the even lane's a and b in
 // the two lanes' a, and the odd one's in their b.
-__device__ __forceinline__ void swap_rows(u32x4 &a, u32x4 &b, bool odd) {
+[[maybe_unused]] __device__ __forceinline__ void swap_rows(u32x4 &a, u32x4 &b, bool odd) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
         const uint32_t give = odd ? a[r] : b[r];
@@ -346,7 +420,7 @@ __device__ __forceinline__ void swap_rows(u32x4 &a, u32x4 &b, bool odd) {
     }
 }
 
-constexpr int kStreamed = 2;  // a store's cache policy: not kept in L2 (736 -> 700 us)
+[[maybe_unused]] constexpr int kStreamed = 2;  // a store's cache policy: not kept in L2 (736 -> 700 us)
 
 template <class T, int OP, int PLANES, bool DIRECT>
 __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
@@ -366,7 +440,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
     const int64_t ny = OP == kWeight ? a.ny : min(a.ny, count);
     const int64_t nk = OP == kWeight ? max((int64_t)0, min(a.nk, count)) : a.nk;
     if (ny <= 0 || (OP == kWeight && a.add && nk == 0)) return;
-    if (OP == kLogits && a.retry && a.scalars->retries == 0) return;
+    if (OP == kLogits && a.retry && a.scalars->retry == 0) return;
     const int ytiles = (int)((ny + kY - 1) / kY), tiles = a.xtiles * ytiles;
     const int items = OP == kHidden   ? tiles * a.splits
                       : OP == kWeight ? a.whole + (tiles - a.whole) * a.parts_of_rest
@@ -564,6 +638,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
                     }
                 top = fmaxf(top, __shfl_xor(top, 16));
                 top = fmaxf(top, __shfl_xor(top, 32));
+                if (DIRECT && top > kReach) atomicOr(&a.scalars->retry, 1u);
                 const float ref = DIRECT ? top : top == -INFINITY ? 0.f : top - kHead;
 #pragma unroll
                 for (int f = 0; f < 8; ++f)
@@ -677,16 +752,17 @@ __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
 }
 
 // The tiles of kWeight that were split: sums in the order of the splits.
-__global__ __launch_bounds__(kWave) void head_weight_join(GemmArgs a) {
+__global__ __launch_bounds__(256) void head_weight_join(GemmArgs a) {
     const int64_t count = a.scalars->count - a.row0;
     if (a.add && count <= 0) return;
-    const int tile = a.whole + (int)(blockIdx.x / kY), row = (int)(blockIdx.x % kY);
+    const int rows = (int)blockIdx.x * (256 / kWave) + threadIdx.x / kWave;
+    const int lane = threadIdx.x % kWave, tile = a.whole + rows / kY, row = rows % kY;
     int tx, ty;
     tile_of<4>(tile, a.xtiles, a.ytiles, tx, ty);
-    const int64_t v = (int64_t)ty * kY + row, n = (int64_t)tx * kX + 4 * threadIdx.x;
+    const int64_t v = (int64_t)ty * kY + row, n = (int64_t)tx * kX + 4 * lane;
     if (v >= a.ny || n >= a.nx) return;
     const float *from = a.partial + (int64_t)(tile - a.whole) * a.parts_of_rest * kX * kY +
-                        row * kX + 4 * threadIdx.x;
+                        row * kX + 4 * lane;
     f32x4 x = {0.f, 0.f, 0.f, 0.f};
     for (int k = 0; k < a.parts_of_rest; ++k)
         x += *reinterpret_cast<const f32x4 *>(from + (int64_t)k * kX * kY);
@@ -747,7 +823,7 @@ struct RowArgs {
     int64_t entries;
     bool distill;
     float tau;
-    float *losses;
+    float *losses, *compact;  // of the rows, and of those that have one
     float *targets;  // [row][entry]: logits of the targets, in units of log 2
     // DIRECT only, of each row: its reference, 2^(reference - lse) and the row times that
     float *ref, *factor;
@@ -770,6 +846,7 @@ __device__ __forceinline__ int64_t target_at(const RowArgs &a, int64_t t, int k,
 // The logits of the targets (NaN in the first place if one is not a column), and as
 // the row's reference the largest of them: no larger than the row's largest logit.
 // A block does four rows of one entry each, or one row.
+template <class T>
 __global__ __launch_bounds__(kRowThreads) void head_targets(RowArgs a) {
     __shared__ float shared[kRowThreads / kWave];
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
@@ -780,52 +857,57 @@ __global__ __launch_bounds__(kRowThreads) void head_targets(RowArgs a) {
     float *to = a.targets + (i - a.row0) * a.entries;
     float top = -INFINITY;
     bool bad = false;
-    for (int k = a.entries == 1 ? 0 : wave; k < a.entries; k += kWaves) {
-        const int64_t v = target_at(a, t, k, bad);
-        float dot = 0.f;
-        if (v >= 0) {
-            f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-            for (int64_t n = 4 * lane; n < a.dim; n += 4 * kWave) {
-                if (n + 4 <= a.dim) {
-                    const f32x4 x = load4(a.hidden, t * a.hld + n, a.type);
-                    const f32x4 y = load4(a.weight, v * a.wld + n, a.type);
+    const int64_t hrow = t * a.hld;
+    constexpr int kFew = 4;  // entries of a wave at a time
+    for (int k0 = a.entries == 1 ? 0 : wave * kFew; k0 < a.entries; k0 += kWaves * kFew) {
+        int64_t v[kFew];
+        float dot[kFew] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) sum[r] = fmaf(x[r], y[r], sum[r]);
-                } else {
-                    for (int64_t m = n; m < a.dim; ++m)
-                        sum[0] = fmaf(element(a.hidden, t * a.hld + m, a.type),
-                                      element(a.weight, v * a.wld + m, a.type), sum[0]);
-                }
-            }
-            dot = wave_sum((sum[0] + sum[1]) + (sum[2] + sum[3])) * (kLog2e / a.tau);
-            top = fmaxf(top, dot);
+        for (int k = 0; k < kFew; ++k)
+            v[k] = k0 + k < a.entries ? target_at(a, t, k0 + k, bad) : -1;
+        const int few = min((int64_t)kFew, a.entries - k0);
+        for (int64_t n = 8 * lane; n < a.dim; n += 8 * kWave) {
+            float x[8], y[kFew][8];
+            const int there = (int)min((int64_t)8, a.dim - n);
+            load8(a.hidden, hrow + n, there, x, T{});
+#pragma unroll
+            for (int k = 0; k < kFew; ++k)  // (of a column that there is, too, where there is none)
+                if (k < few) load8(a.weight, max(v[k], (int64_t)0) * a.wld + n, there, y[k], T{});
+#pragma unroll
+            for (int k = 0; k < kFew; ++k)
+                if (k < few)
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) dot[k] = fmaf(x[r], y[k][r], dot[k]);
         }
-        if (lane == 0) to[k] = dot;
+#pragma unroll
+        for (int k = 0; k < kFew; ++k) {
+            if (k0 + k >= a.entries) continue;
+            dot[k] = v[k] < 0 ? 0.f : wave_sum(dot[k]) * (kLog2e / a.tau);
+            if (v[k] >= 0) top = fmaxf(top, dot[k]);
+            if (lane == 0) to[k0 + k] = dot[k];
+        }
     }
     if (a.entries > 1) {
         top = block_all<Max>(top, shared);
         bad = block_all<Max>(bad ? 1.f : 0.f, shared) > 0.f;
     }
-    if (lane == 0 && (wave == 0 || a.entries == 1)) {
+    if (lane == 0 && (wave == 0 || a.entries == 1)) {  // (wave 0 has written the first one)
         if (bad) to[0] = __uint_as_float(0x7FC00000u);
         if (a.ref != nullptr) a.ref[i - a.row0] = fabsf(top) < INFINITY ? top : 0.f;
     }
 }
 
-// Rows whose largest logit is so far above the reference that their exponentials or
-// the products with them might be too large get that logit as their reference.
-constexpr float kReach = 64.f;
+// Rows whose largest logit is beyond the reach of their reference get that logit as
+// their reference. (Does nothing if there are none, like the product after it.)
 __global__ __launch_bounds__(kRowThreads) void head_reach(RowArgs a) {
     const int lane = threadIdx.x % kWave;
     const int64_t local = blockIdx.x * (int64_t)(kRowThreads / kWave) + threadIdx.x / kWave;
-    if (a.row0 + local >= a.scalars->count) return;
+    if (a.scalars->retry == 0 || a.row0 + local >= a.scalars->count) return;
     const f32x2 *parts = a.parts + local * a.parts_ld;
     float top = -INFINITY;
     for (int64_t k = lane; k < a.groups; k += kWave) top = fmaxf(top, parts[k][0]);
     top = wave_max(top);
-    if (lane != 0 || !(top > kReach)) return;
-    a.ref[local] += top;
-    atomicAdd(&a.scalars->retries, 1);
+    if (lane == 0 && top > kReach) a.ref[local] += top;
 }
 
 // Row i of the logits: the sum of its exponentials, the loss, and the exponentials
@@ -911,7 +993,7 @@ __global__ __launch_bounds__(kRowThreads) void head_rows(RowArgs a) {
         loss = x * kLn2 * a.tau * a.tau;
     }
     if (lse2 != lse2) loss = lse2;
-    if (tid == 0) a.losses[t] = loss;
+    if (tid == 0) a.losses[t] = a.compact[i] = loss;
     if (!a.store) return;
 
     if constexpr (DIRECT) {
@@ -992,6 +1074,35 @@ __global__ __launch_bounds__(kRowThreads) void head_rows(RowArgs a) {
 
 // ------------------------------------------------------------------- results
 
+struct TotalArgs {
+    const Scalars *scalars;
+    const float *losses;  // of the rows that have one
+    bool mean;
+    float *loss;
+};
+
+// The sum or mean of the losses, in an order of its own: each of a block's 256 threads
+// takes every 256th, in four sums.
+__device__ __forceinline__ void total(const TotalArgs &a) {
+    __shared__ double shared[256 / kWave];
+    const int64_t count = a.scalars->count;
+    double x[4] = {0.0, 0.0, 0.0, 0.0};
+    for (int64_t i = threadIdx.x; i < count; i += 1024)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (i + 256 * k < count) x[k] += (double)a.losses[i + 256 * k];
+    double y = (x[0] + x[1]) + (x[2] + x[3]);
+#pragma unroll
+    for (int d = 1; d < kWave; d *= 2) y += __shfl_xor(y, d);
+    if (threadIdx.x % kWave == 0) shared[threadIdx.x / kWave] = y;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        y = (shared[0] + shared[1]) + (shared[2] + shared[3]);
+        *a.loss = (float)(a.mean ? y / (double)max(count, (int64_t)1) : y);
+    }
+}
+__global__ __launch_bounds__(256) void head_total(TotalArgs a) { total(a); }
+
 struct ReduceArgs {
     const Scalars *scalars;
     const int32_t *rowmap;
@@ -1005,61 +1116,49 @@ struct ReduceArgs {
     bool mean;
     int gshift;
     const float *factor;  // of each row, or null
+    TotalArgs total;
 };
 
-// The gradient of a hidden row: the sum of its splits, in their order.
+// The gradients of the hidden rows, a wave a row: the sum of its splits, in their
+// order. The first block of the last group of rows does the loss.
 __global__ __launch_bounds__(256) void head_hidden(ReduceArgs a) {
-    const int64_t i = blockIdx.x;
+    if (a.total.loss != nullptr && blockIdx.x == 0) total(a.total);
+    const int64_t i = (blockIdx.x - (a.total.loss != nullptr ? 1 : 0)) * (int64_t)(256 / kWave) +
+                      threadIdx.x / kWave;
     const int64_t count = a.scalars->count;
-    if (a.row0 + i >= count) return;
+    if (i < 0 || i >= a.rows || a.row0 + i >= count) return;
     float s = a.scale * pow2(-a.gshift);
     if (a.mean) s /= (float)count;
     if (a.type == RCS_F32) s *= pow2(-lift_of(a.scalars->top_w));
     if (a.factor != nullptr) s *= a.factor[i];
     const int64_t t = a.rowmap[a.row0 + i];
-    for (int64_t n = threadIdx.x; n < a.dim; n += blockDim.x) {
-        float x = 0.f;
-        for (int k = 0; k < a.splits; ++k) x += a.partial[(k * a.rows + i) * a.pld + n];
-        put(a.out, t * a.old + n, a.type, x * s);
+    for (int64_t n = 4 * (threadIdx.x % kWave); n < a.dim; n += 4 * kWave) {
+        f32x4 x = {0.f, 0.f, 0.f, 0.f};
+        const float *from = a.partial + i * a.pld + n;
+#pragma unroll 8
+        for (int k = 0; k < a.splits; ++k)
+            x += *reinterpret_cast<const f32x4 *>(from + k * a.rows * a.pld);
+        put4(a.out, t * a.old + n, a.type, x * s, a.dim - n, false);
     }
 }
 
 __global__ __launch_bounds__(256) void head_weight_out(const float *from, int64_t rows,
                                                        int64_t dim, void *out, int64_t ld,
                                                        int type, bool add) {
-    const int64_t v = blockIdx.x;
-    for (int64_t n = threadIdx.x; n < dim; n += blockDim.x) {
-        float x = from[v * dim + n];
-        if (add) x += element(out, v * ld + n, type);
-        put(out, v * ld + n, type, x);
-    }
-}
-
-// The loss of the rows that have one, in row order; rows without one are cleared.
-__global__ __launch_bounds__(1024) void head_total(const Scalars *scalars, const int32_t *inverse,
-                                                   float *losses, int64_t rows, bool mean,
-                                                   float *loss) {
-    __shared__ double shared[1024 / kWave];
-    double x = 0.0;
-    for (int64_t t = threadIdx.x; t < rows; t += 1024) {
-        if (inverse[t] >= 0) x += (double)losses[t];
-        else losses[t] = 0.f;
-    }
-#pragma unroll
-    for (int d = 1; d < kWave; d *= 2) x += __shfl_xor(x, d);
-    if (threadIdx.x % kWave == 0) shared[threadIdx.x / kWave] = x;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        x = 0.0;
-        for (int w = 0; w < 1024 / kWave; ++w) x += shared[w];
-        *loss = (float)(mean ? x / (double)max(scalars->count, 1) : x);
+    const int64_t v = blockIdx.x * (int64_t)(256 / kWave) + threadIdx.x / kWave;
+    if (v >= rows) return;
+    for (int64_t n = 4 * (threadIdx.x % kWave); n < dim; n += 4 * kWave) {
+        f32x4 x = {0.f, 0.f, 0.f, 0.f};
+        for (int r = 0; r < 4; ++r)
+            if (n + r < dim) x[r] = from[v * dim + n + r];
+        put4(out, v * ld + n, type, x, dim - n, add);
     }
 }
 
 // ----------------------------------------------------------------- host side
 
 constexpr int64_t kCus = 256;
-constexpr int64_t kItemSteps = 8;
+constexpr int64_t kItemSteps = 12;
 constexpr int64_t kMinChunk = 128;  // rows done at a time at least
 
 struct Plan {
@@ -1071,7 +1170,7 @@ struct Plan {
     int64_t kper;
     bool copy_w, wide_out, direct;
     // offsets in the workspace
-    int64_t scalars, flags, rowmap, inverse, losses, h[2], w[2], e[2], parts, targets, ref, factor, scaled, partial, rest, acc, bytes;
+    int64_t scalars, flags, rowmap, inverse, losses, compact, h[2], w[2], e[2], parts, targets, ref, factor, scaled, partial, rest, acc, bytes;
 };
 
 bool direct_weight(const rcs_head *a) {
@@ -1091,7 +1190,7 @@ Plan plan_of(const rcs_head *a, int64_t entries, bool distill) {
     p.eld = round_up(a->vocab, kX);
     if (p.eld % 512 == 0) p.eld += 64;
     p.copy_w = !direct_weight(a);
-    p.direct = a->type == RCS_BF16 && !distill;
+    p.direct = a->type == RCS_BF16 && !distill && grads;
     // rows of a group: as many as fit the limit, in whole tiles
     const int64_t row_bytes = (grads ? p.eld * 2 * p.planes : 0) + p.groups * 8;
     p.chunk = round_up(a->rows > 0 ? a->rows : 1, kMinChunk);
@@ -1132,6 +1231,7 @@ Plan plan_of(const rcs_head *a, int64_t entries, bool distill) {
     p.rowmap = take(4 * a->rows);
     p.inverse = take(4 * a->rows);
     p.losses = take(4 * a->rows);
+    p.compact = take(4 * a->rows);
     for (int k = 0; k < p.planes; ++k) p.h[k] = take(2 * (a->rows + kK) * p.pad);
     if (p.copy_w)
         for (int k = 0; k < p.planes; ++k) p.w[k] = take(2 * a->vocab * p.pad);
@@ -1183,7 +1283,12 @@ void launch_gemm(GemmArgs &g, hipStream_t stream) {
     const int64_t blocks = items < kCus ? items : kCus;
     head_gemm<T, OP, PLANES, DIRECT><<<dim3((unsigned)blocks), kGemmThreads, 0, stream>>>(g);
     if (OP == kWeight && g.parts_of_rest > 1)
-        head_weight_join<<<dim3((unsigned)((tiles - g.whole) * kY)), kWave, 0, stream>>>(g);
+        head_weight_join<<<dim3((unsigned)((tiles - g.whole) * (kY / 4))), 256, 0, stream>>>(g);
+}
+
+TotalArgs total_of(const rcs_head *a, const Plan &p, char *ws) {
+    return TotalArgs{reinterpret_cast<Scalars *>(ws + p.scalars),
+                     reinterpret_cast<float *>(ws + p.compact), a->mean != 0, a->loss};
 }
 
 template <class T, int PLANES, bool DIRECT>
@@ -1227,6 +1332,7 @@ void launch_products(const rcs_head *a, const Targets &tg, const Plan &p, char *
         r.index = tg.index, r.logits = tg.logits, r.index_type = tg.index_type;
         r.logits_type = tg.logits_type, r.entries = tg.entries, r.distill = tg.distill;
         r.tau = tg.tau, r.losses = losses;
+        r.compact = reinterpret_cast<float *>(ws + p.compact);
         r.targets = reinterpret_cast<float *>(ws + p.targets);
         r.h = reinterpret_cast<const uint16_t *>(ws + p.h[0]), r.pad = p.pad;
         if (DIRECT) {
@@ -1237,8 +1343,9 @@ void launch_products(const rcs_head *a, const Targets &tg, const Plan &p, char *
         }
         if (rows > 0) {
             const unsigned fours = (unsigned)((rows + 3) / 4);
-            head_targets<<<dim3(tg.entries == 1 ? fours : (unsigned)rows), kRowThreads, 0,
-                           stream>>>(r);
+            const dim3 grid(tg.entries == 1 ? fours : (unsigned)rows);
+            if (PLANES > 1) head_targets<F32><<<grid, kRowThreads, 0, stream>>>(r);
+            else head_targets<T><<<grid, kRowThreads, 0, stream>>>(r);
             launch_gemm<T, kLogits, PLANES, DIRECT>(g, stream);
             if (DIRECT) {
                 head_reach<<<dim3(fours), kRowThreads, 0, stream>>>(r);
@@ -1263,7 +1370,9 @@ void launch_products(const rcs_head *a, const Targets &tg, const Plan &p, char *
             d.out = a->grad_hidden, d.old = a->grad_hidden_stride, d.type = a->type;
             d.scale = scale, d.mean = g.mean, d.gshift = gshift;
             d.factor = r.factor;
-            head_hidden<<<dim3((unsigned)rows), 256, 0, stream>>>(d);
+            const bool last = row0 + p.chunk >= a->rows;
+            if (last) d.total = total_of(a, p, ws);
+            head_hidden<<<dim3((unsigned)((rows + 3) / 4 + (last ? 1 : 0))), 256, 0, stream>>>(d);
         }
         if (a->grad_weight != nullptr) {
             GemmArgs q = g;
@@ -1283,7 +1392,7 @@ void launch_products(const rcs_head *a, const Targets &tg, const Plan &p, char *
         }
     }
     if (p.wide_out)
-        head_weight_out<<<dim3((unsigned)a->vocab), 256, 0, stream>>>(
+        head_weight_out<<<dim3((unsigned)((a->vocab + 3) / 4)), 256, 0, stream>>>(
             reinterpret_cast<float *>(ws + p.acc), a->vocab, a->dim, a->grad_weight,
             a->grad_weight_stride, a->grad_weight_type, a->accumulate != 0);
 }
@@ -1327,37 +1436,28 @@ int head_call(const rcs_head *a, const Targets &tg, hipStream_t stream) {
     int32_t *rowmap = reinterpret_cast<int32_t *>(ws + p.rowmap);
     int32_t *inverse = reinterpret_cast<int32_t *>(ws + p.inverse);
     float *losses = a->losses != nullptr ? a->losses : reinterpret_cast<float *>(ws + p.losses);
-    if (a->rows > 0)
+    if (tg.distill && a->rows > 0)
         head_flags<<<dim3((unsigned)((a->rows + 3) / 4)), 256, 0, stream>>>(
-            tg.index, tg.index_type, tg.entries, a->rows, tg.ignore, tg.logits, tg.logits_type,
-            tg.distill, flags);
-    head_scan<<<1, 1024, 0, stream>>>(flags, a->rows, rowmap, inverse, scalars);
-    if (a->type == RCS_F32) {
-        head_top<<<dim3(1024), 256, 0, stream>>>(static_cast<const float *>(a->hidden),
-                                                 a->hidden_stride, a->rows, a->dim, inverse,
-                                                 &scalars->top_h);
-        head_top<<<dim3(2048), 256, 0, stream>>>(static_cast<const float *>(a->weight),
-                                                 a->weight_stride, a->vocab, a->dim, nullptr,
-                                                 &scalars->top_w);
-    }
+            tg.index, tg.index_type, tg.entries, a->rows, tg.logits, tg.logits_type, flags);
+    head_scan<<<1, kScanThreads, 0, stream>>>(tg.distill ? flags : nullptr, tg.index,
+                                              tg.index_type, tg.ignore, a->rows, rowmap, inverse,
+                                              scalars);
     PrepArgs h = {};
-    h.src = a->hidden, h.hi = ws + p.h[0], h.lo = ws + p.h[p.planes - 1];
-    h.ld = a->hidden_stride, h.rows = a->rows, h.dim = a->dim, h.pad = p.pad, h.type = a->type;
-    h.inverse = inverse, h.scalars = scalars, h.hidden = true;
-    h.grad = a->grad_hidden, h.grad_ld = a->grad_hidden_stride;
-    head_prep<<<dim3((unsigned)(a->rows + kK)), 256, 0, stream>>>(h);
-    if (p.copy_w) {
-        PrepArgs w = {};
-        w.src = a->weight, w.hi = ws + p.w[0], w.lo = ws + p.w[p.planes - 1];
-        w.ld = a->weight_stride, w.rows = a->vocab, w.dim = a->dim, w.pad = p.pad;
-        w.type = a->type, w.scalars = scalars;
-        head_prep<<<dim3((unsigned)a->vocab), 256, 0, stream>>>(w);
-    }
+    const auto plane = [&](int64_t at) { return reinterpret_cast<uint16_t *>(ws + at); };
+    h.hidden = Rows{a->hidden, plane(p.h[0]), plane(p.h[1]), a->hidden_stride, a->rows};
+    h.weight = Rows{a->weight, plane(p.w[0]), plane(p.w[1]), a->weight_stride,
+                    p.copy_w ? a->vocab : 0};
+    h.dim = a->dim, h.pad = p.pad, h.type = a->type, h.inverse = inverse, h.scalars = scalars;
+    h.grad = a->grad_hidden, h.grad_ld = a->grad_hidden_stride, h.losses = losses;
+    if (a->type == RCS_F32) head_top<<<kTopHidden + kTopWeight, 1024, 0, stream>>>(h);
+    head_prep<<<dim3((unsigned)((h.hidden.rows + kK + h.weight.rows + 3) / 4)), 256, 0,
+                stream>>>(h);
     if (a->type == RCS_F32) launch_products<F16, 2, false>(a, tg, p, ws, stream);
     else if (a->type == RCS_F16) launch_products<F16, 1, false>(a, tg, p, ws, stream);
     else if (p.direct) launch_products<BF16, 1, true>(a, tg, p, ws, stream);
     else launch_products<BF16, 1, false>(a, tg, p, ws, stream);
-    head_total<<<1, 1024, 0, stream>>>(scalars, inverse, losses, a->rows, a->mean != 0, a->loss);
+    if (a->grad_hidden == nullptr || a->rows == 0)
+        head_total<<<1, 256, 0, stream>>>(total_of(a, p, ws));
     return hipGetLastError() == hipSuccess ? RCS_OK : RCS_EHIP;
 }
 
