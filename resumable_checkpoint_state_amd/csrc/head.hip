@@ -36,12 +36,19 @@ __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
-// Tiles of a product: kX by kY outputs by a block of eight waves, each 128 by 64 of
-// them, kK at a time, from two places in LDS in turn.
-constexpr int kX = 256, kY = 256, kK = 64;
-constexpr int kGroup = 128;  // columns of the logits with a reference of their own
-constexpr int kGemmThreads = 512, kGemmWaves = kGemmThreads / kWave;
-[[maybe_unused]] constexpr int kXBytes = kX * kK * 2, kStageBytes = kXBytes + kY * kK * 2;
+// Tiles of a product: kX by kY outputs by a block of 2 by kY / 64 waves, each kX / 2
+// by 64 of them, kK at a time, from two places in LDS in turn. The large ones (one
+// block a CU) read least; products that have fewer of them than there are CUs are
+// done in small ones (two blocks a CU).
+constexpr int kK = 64;
+template <bool SMALL>
+struct Shape {
+    static constexpr int kX = SMALL ? 128 : 256, kY = kX;
+    static constexpr int kThreads = 2 * kY, kWaves = kThreads / kWave;
+    static constexpr int kFx = kX / 32, kFy = 4;  // fragments of a wave
+    static constexpr int kGroup = kX / 2;  // columns of the logits with a reference of their own
+    static constexpr int kXBytes = kX * kK * 2, kStageBytes = 2 * kXBytes;
+};
 
 // What the kernels of one call tell each other, in device memory.
 struct Scalars {
@@ -296,23 +303,23 @@ struct Int {
 };
 
 [[maybe_unused]] constexpr int kRefPlaces = 4;  // items whose rows' references are in LDS, at most
-[[maybe_unused]] constexpr int kCalls = 256 * kK * 2 / 1024 / kGemmWaves;  // loads of a wave for one operand
+[[maybe_unused]] constexpr int kCalls = 4;  // loads of a wave for one operand
 
-// How an operand's tile of 256 by kK lies in LDS: in `kCalls` loads a wave, each of
+// How an operand's tile of R by kK lies in LDS: in `kCalls` loads a wave, each of
 // 1,024 consecutive bytes (source: where a lane's 16 come from), and how a wave
 // reads its fragments of 16 by 32 (base: of the first one; read: fragment i of the
 // tile's half `half` of the sum).
-template <bool KCONTIG, bool PERM>
+template <bool KCONTIG, int R, bool PERM>
 struct Side;
 
-// The sum runs along memory's rows: 256 rows of kK consecutive values, eight
+// The sum runs along memory's rows: R rows of kK consecutive values, eight
 // 16-byte chunks (a line of 128 bytes) each, chunk c of row r at slot c ^ turn(r).
 // A read of 16 rows is served 16 lanes at a time, the lanes of rows 0-3 and 12-15
 // with those of rows 4-11 of the next chunk: turned so, each such group meets all
 // 64 banks once. With PERM, fragments 2i and 2i + 1 take their 32 rows in turns of
 // four, so that a lane's results from both are of eight consecutive rows.
-template <bool PERM>
-struct Side<true, PERM> {
+template <int R, bool PERM>
+struct Side<true, R, PERM> {
     static __device__ __forceinline__ int turn(int r) {
         return PERM ? (r >> 2 & 6) | (r >> 1 & 1) : r >> 1 & 7;
     }
@@ -333,27 +340,30 @@ struct Side<true, PERM> {
     }
 };
 
-// The sum runs across memory's rows: kK rows of 256 consecutive values, read back
-// transposed. The 16 pairs of chunks of row k are turned by a number that differs
+// The sum runs across memory's rows: kK rows of R consecutive values, read back
+// transposed. The R / 16 pairs of chunks of row k are turned by a number that differs
 // between the rows that one read takes.
-template <bool PERM>
-struct Side<false, PERM> {
-    static __device__ __forceinline__ int turn(int k) { return (k & 3) | (k >> 3 & 3) << 2; }
+template <int R, bool PERM>
+struct Side<false, R, PERM> {
+    static __device__ __forceinline__ int turn(int k) {
+        return ((k & 3) | (k >> 3 & 3) << 2) & (R / 16 - 1);
+    }
     static __device__ __forceinline__ uint32_t source(int call, int lane, int64_t ld) {
-        const int k = call * 2 + lane / 32, slot = lane % 32;
+        constexpr int kSlots = R / 8;
+        const int k = call * (kWave / kSlots) + lane / kSlots, slot = lane % kSlots;
         const int c = (((slot >> 1) ^ turn(k)) << 1) | (slot & 1);
         return (uint32_t)(k * ld * 2 + c * 16);
     }
     static __device__ __forceinline__ uint32_t base(int at, int lane) {
         const int s = lane % 16, k = 8 * (lane / 16) + s / 4;
-        return (uint32_t)(k * 512 + (((at / 16) ^ turn(k)) * 32) + (s % 4) * 8);
+        return (uint32_t)(k * R * 2 + (((at / 16) ^ turn(k)) * 32) + (s % 4) * 8);
     }
     static __device__ __forceinline__ s16x8 read(const lds_char *p, uint32_t base, int i,
                                                  int half) {
         typedef __attribute__((address_space(3))) s16x4 v;
-        const lds_char *q = p + (base ^ (uint32_t)(i * 32)) + half * 32 * 512;
+        const lds_char *q = p + (base ^ (uint32_t)(i * 32)) + half * 32 * R * 2;
         const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((v *)q);
-        const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((v *)(q + 4 * 512));
+        const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((v *)(q + 4 * R * 2));
         return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
     }
 };
@@ -422,11 +432,15 @@ struct Item {
 
 [[maybe_unused]] constexpr int kStreamed = 2;  // a store's cache policy: not kept in L2 (736 -> 700 us)
 
-template <class T, int OP, int PLANES, bool DIRECT>
-__global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
+template <class T, int OP, int PLANES, bool DIRECT, bool SMALL>
+__global__ __launch_bounds__(Shape<SMALL>::kThreads, 2) void head_gemm(GemmArgs a) {
 #ifdef __HIP_DEVICE_COMPILE__  // the host needs the launch stub alone
-    using X = Side<OP == kLogits, OP == kLogits>;
-    using Y = Side<OP != kWeight, false>;
+    using S = Shape<SMALL>;
+    constexpr int kX = S::kX, kY = S::kY, kXBytes = S::kXBytes, kStageBytes = S::kStageBytes;
+    constexpr int kFx = S::kFx, kFy = S::kFy;
+    using X = Side<OP == kLogits, kX, OP == kLogits>;
+    using Y = Side<OP != kWeight, kY, false>;
+    static_assert(kX / 8 == kCalls * S::kWaves && kY / 8 == kCalls * S::kWaves, "whole tiles");
     static_assert(!DIRECT || OP == kLogits, "a form of the logits");
     __shared__ __attribute__((aligned(1024))) char
         shared[2 * kStageBytes + (DIRECT ? kRefPlaces * kY * 4 : 0)];
@@ -514,7 +528,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
     int load_place = 0;
     auto load_refs = [&] {
         if constexpr (DIRECT) {
-            const int r = (wave & 3) * kWave;
+            const int r = wave % (kY / kWave) * kWave;
             const u32x4 rows = buffer_of(a.ref, (load.y0 + r) * 4, load.empty ? 0 : ny * 4);
             load_lds_dword(rows, (uint32_t)(lane * 4),
                            lds_at + 2 * kStageBytes + (load_place * kY + r) * 4);
@@ -537,14 +551,14 @@ __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
         place_loads();
     };
 
-    f32x4 acc[8][4];
+    f32x4 acc[kFx][kFy];
     auto clear = [&] {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < kFx; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int j = 0; j < kFy; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     };
-    const uint32_t xbase = X::base(wx * 128, lane);
+    const uint32_t xbase = X::base(wx * (kX / 2), lane);
     const uint32_t ybase = Y::base(wy * 64, lane);
 
     // While one half of a step is multiplied out of registers, the next half is read
@@ -553,21 +567,21 @@ __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
     // Each four products come with a read and, in a step's second half, a load: as a
     // stretch of loads, these would keep the products waiting while they queue (the
     // order is held by barriers to the compiler's scheduling).
-    s16x8 fx[2][8], fy[2][4];
+    s16x8 fx[2][kFx], fy[2][kFy];
     auto read_one = [&](int stage, int i, auto half) {
         constexpr int h = decltype(half)::value;
         const lds_char *px = lds + stage * kStageBytes, *py = px + kXBytes;
-        if (i < 4) fy[h][i] = Y::read(py, ybase, i, h);
+        if (i < kFy) fy[h][i] = Y::read(py, ybase, i, h);
         fx[h][i] = X::read(px, xbase, i, h);
     };
     auto multiply = [&](auto half, auto between) {
         constexpr int h = decltype(half)::value;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < kFx; ++i) {
             between(i);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = mfma(fx[h][i], fy[h][j], acc[i][j], T{});
+            for (int j = 0; j < kFy; ++j) acc[i][j] = mfma(fx[h][i], fy[h][j], acc[i][j], T{});
             __builtin_amdgcn_sched_barrier(0);
         }
     };
@@ -584,7 +598,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
 
     // The results of an item. kLogits: kStores stores, always, so that the next step's
     // tile, which was loaded before them, can be waited for without them.
-    constexpr int kStores = OP == kLogits ? 4 + 16 * PLANES : 0;
+    constexpr int kStores = OP == kLogits ? kFy * (1 + kFx / 2 * PLANES) : 0;
     float c1 = 1.f;
     if constexpr (OP == kLogits) {
         c1 = a.zscale;
@@ -599,16 +613,16 @@ __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
         asm volatile("" : "+v"(at_lane));  // addresses are worked out here, not kept through the loop
         const int g = at_lane / 16, l16 = at_lane % 16;
         if constexpr (OP == kLogits) {
-            const int64_t v0 = m.x0 + wx * 128;
+            const int64_t v0 = m.x0 + wx * (kX / 2);
             constexpr float kHead = __is_same(T, F16) ? 15.f : 0.f;
             if (m.x0 + kX > a.nx) {  // the last tile's columns behind the vocabulary
 #pragma unroll
-                for (int f = 0; f < 8; ++f)
+                for (int f = 0; f < kFx; ++f)
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
                         if (v0 + 32 * (f / 2) + 8 * g + 4 * (f & 1) + r >= a.nx)
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) acc[f][j][r] = -INFINITY;
+                            for (int j = 0; j < kFy; ++j) acc[f][j][r] = -INFINITY;
             }
             // rows behind the last one lie behind the buffers' ends, and are not stored
             const int64_t rows = min((int64_t)kY, ny - m.y0);
@@ -620,9 +634,9 @@ __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
             const __amdgpu_buffer_rsrc_t eh = ebuf(0), el = ebuf(PLANES - 1);
             const __amdgpu_buffer_rsrc_t pb = __builtin_amdgcn_make_buffer_rsrc(
                 a.parts + m.y0 * a.groups, 0, (int)(uint32_t)(rows * a.groups * 8), 0x00020000);
-            const uint32_t part = g == 0 && v0 < a.nx ? (uint32_t)(v0 / kGroup * 8) : 0xFFFFFF00u;
+            const uint32_t part = g == 0 && v0 < a.nx ? (uint32_t)(v0 / S::kGroup * 8) : 0xFFFFFF00u;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < kFy; ++j) {
                 const int i = wy * 64 + 16 * j + l16;
                 float top = -INFINITY, sum = 0.f;
                 const float less =
@@ -630,7 +644,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
                                   lds + 2 * kStageBytes + (place * kY + i) * 4)
                             : 0.f;
 #pragma unroll
-                for (int f = 0; f < 8; ++f)
+                for (int f = 0; f < kFx; ++f)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         acc[f][j][r] = fmaf(acc[f][j][r], c1, less);
@@ -641,7 +655,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
                 if (DIRECT && top > kReach) atomicOr(&a.scalars->retry, 1u);
                 const float ref = DIRECT ? top : top == -INFINITY ? 0.f : top - kHead;
 #pragma unroll
-                for (int f = 0; f < 8; ++f)
+                for (int f = 0; f < kFx; ++f)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const float e = exp2_(DIRECT ? acc[f][j][r] : acc[f][j][r] - ref);
@@ -653,9 +667,9 @@ __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
                 __builtin_amdgcn_raw_buffer_store_b64(
                     u32x2{__float_as_uint(ref), __float_as_uint(sum)}, pb,
                     part == 0xFFFFFF00u ? part : part + (uint32_t)(i * a.groups * 8), 0, 0);
-                u32x4 h[4], l[4];
+                u32x4 h[kFx / 2], l[kFx / 2];
 #pragma unroll
-                for (int p = 0; p < 4; ++p)
+                for (int p = 0; p < kFx / 2; ++p)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const float x = acc[2 * p + r / 2][j][2 * r % 4];
@@ -667,7 +681,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
                     }
                 // whole lines: first the even row of a pair of lanes, then the odd one
 #pragma unroll
-                for (int p = 0; p < 4; p += 2) {
+                for (int p = 0; p < kFx / 2; p += 2) {
                     const uint32_t to =
                         (uint32_t)(((i & ~1) * a.eld + v0 + 32 * (p + (l16 & 1)) + 8 * g) * 2);
                     const uint32_t row = (uint32_t)(a.eld * 2);
@@ -683,12 +697,12 @@ __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
             }
         } else if constexpr (OP == kHidden) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < kFy; ++j) {
                 const int64_t i = m.y0 + wy * 64 + 16 * j + l16;
                 if (i >= ny) continue;
 #pragma unroll
-                for (int f = 0; f < 8; ++f) {
-                    const int64_t n = m.x0 + wx * 128 + 16 * f + 4 * g;
+                for (int f = 0; f < kFx; ++f) {
+                    const int64_t n = m.x0 + wx * (kX / 2) + 16 * f + 4 * g;
                     if (n >= a.pld) continue;
                     *reinterpret_cast<f32x4 *>(a.partial + (m.split * a.ny + i) * a.pld + n) =
                         acc[f][j];
@@ -697,19 +711,19 @@ __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
         } else if (m.split >= 0) {
             float *to = a.partial + (int64_t)m.split * kX * kY;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < kFy; ++j)
 #pragma unroll
-                for (int f = 0; f < 8; ++f)
-                    *reinterpret_cast<f32x4 *>(to + (wy * 64 + 16 * j + l16) * kX + wx * 128 +
+                for (int f = 0; f < kFx; ++f)
+                    *reinterpret_cast<f32x4 *>(to + (wy * 64 + 16 * j + l16) * kX + wx * (kX / 2) +
                                                16 * f + 4 * g) = acc[f][j] * c1;
         } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < kFy; ++j) {
                 const int64_t v = m.y0 + wy * 64 + 16 * j + l16;
                 if (v >= a.ny) continue;
 #pragma unroll
-                for (int f = 0; f < 8; ++f) {
-                    const int64_t n = m.x0 + wx * 128 + 16 * f + 4 * g;
+                for (int f = 0; f < kFx; ++f) {
+                    const int64_t n = m.x0 + wx * (kX / 2) + 16 * f + 4 * g;
                     put4(a.out, v * a.old + n, a.out_type, acc[f][j] * c1, a.nx - n, a.add);
                 }
             }
@@ -717,7 +731,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
     };
 
     load_refs();
-    static_assert(2 * kCalls == 8, "a load for each four products of half a step");
+    constexpr int kEach = 2 * kCalls / kFx;  // loads with each read
     for (int k = 0; k < 2; ++k) {
 #pragma unroll
         for (int c = 0; c < 8; ++c) load_one(k, c);
@@ -725,7 +739,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
     }
     arrive(Int<0>{});
 #pragma unroll
-    for (int i = 0; i < 8; ++i) read_one(0, i, Int<0>{});
+    for (int i = 0; i < kFx; ++i) read_one(0, i, Int<0>{});
     int stage = 0, place = 0;
     bool stored = false;
     for (; at < items; at += gridDim.x) {
@@ -738,7 +752,8 @@ __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
             stored = false;
             multiply(Int<1>{}, [&](int i) {
                 read_one(stage ^ 1, i, Int<0>{});  // of nothing, behind the last step
-                load_one(stage, i);
+#pragma unroll
+                for (int c = 0; c < kEach; ++c) load_one(stage, i * kEach + c);
             });
             next_loads();
             stage ^= 1;
@@ -752,7 +767,9 @@ __global__ __launch_bounds__(kGemmThreads, 2) void head_gemm(GemmArgs a) {
 }
 
 // The tiles of kWeight that were split: sums in the order of the splits.
+template <bool SMALL>
 __global__ __launch_bounds__(256) void head_weight_join(GemmArgs a) {
+    constexpr int kX = Shape<SMALL>::kX, kY = Shape<SMALL>::kY;
     const int64_t count = a.scalars->count - a.row0;
     if (a.add && count <= 0) return;
     const int rows = (int)blockIdx.x * (256 / kWave) + threadIdx.x / kWave;
@@ -760,7 +777,7 @@ __global__ __launch_bounds__(256) void head_weight_join(GemmArgs a) {
     int tx, ty;
     tile_of<4>(tile, a.xtiles, a.ytiles, tx, ty);
     const int64_t v = (int64_t)ty * kY + row, n = (int64_t)tx * kX + 4 * lane;
-    if (v >= a.ny || n >= a.nx) return;
+    if (4 * lane >= kX || v >= a.ny || n >= a.nx) return;
     const float *from = a.partial + (int64_t)(tile - a.whole) * a.parts_of_rest * kX * kY +
                         row * kX + 4 * lane;
     f32x4 x = {0.f, 0.f, 0.f, 0.f};
@@ -811,6 +828,7 @@ struct RowArgs {
     int64_t row0;
     const f32x2 *parts;
     int64_t groups, parts_ld, vocab;
+    int group;  // columns
     void *g[2];
     int64_t gld;
     bool store;
@@ -1028,7 +1046,7 @@ __global__ __launch_bounds__(kRowThreads) void head_rows(RowArgs a) {
                                                   local * a.gld) + k;
             u32x4 h = {0, 0, 0, 0}, l = {0, 0, 0, 0};
             if (v < a.vocab) {
-                const float f = exp2_(parts[v / kGroup][0] - lse2 + (float)a.gshift);
+                const float f = exp2_(parts[v / a.group][0] - lse2 + (float)a.gshift);
                 h = *gh;
                 if (PLANES > 1) l = *gl;
 #pragma unroll
@@ -1168,7 +1186,7 @@ struct Plan {
     int64_t eld, groups;
     int splits, whole, parts_of_rest;
     int64_t kper;
-    bool copy_w, wide_out, direct;
+    bool copy_w, wide_out, direct, small_logits, small_hidden, small_weight;
     // offsets in the workspace
     int64_t scalars, flags, rowmap, inverse, losses, compact, h[2], w[2], e[2], parts, targets, ref, factor, scaled, partial, rest, acc, bytes;
 };
@@ -1186,7 +1204,8 @@ Plan plan_of(const rcs_head *a, int64_t entries, bool distill) {
     p.pad = round_up(a->dim, kK);
     // a stride of a whole number of kilobytes would put a column's elements into few
     // of the memory's channels
-    p.groups = round_up(a->vocab, kX) / kGroup;
+    constexpr int kX = Shape<false>::kX, kY = Shape<false>::kY;
+    p.groups = round_up(a->vocab, kX) / Shape<true>::kGroup;  // or half as many
     p.eld = round_up(a->vocab, kX);
     if (p.eld % 512 == 0) p.eld += 64;
     p.copy_w = !direct_weight(a);
@@ -1196,25 +1215,37 @@ Plan plan_of(const rcs_head *a, int64_t entries, bool distill) {
     p.chunk = round_up(a->rows > 0 ? a->rows : 1, kMinChunk);
     const int64_t fit = a->limit / row_bytes / kMinChunk * kMinChunk;
     if (p.chunk > fit) p.chunk = fit < kMinChunk ? kMinChunk : fit;
+    // rows done at a time, and the logits' tiles
+    const int64_t rows = p.chunk < a->rows ? p.chunk : a->rows;
+    const auto tiles_of = [](int64_t x, int64_t y, int64_t tile) {
+        return (x + tile - 1) / tile * ((y + tile - 1) / tile);
+    };
+    p.small_logits = tiles_of(a->vocab, rows, kX) < kCus;
     // splits of the hidden gradient's sum over the vocabulary: the number that fills
-    // the chip's rounds best, each item costing about as much as kItemSteps steps more
-    const int64_t xtiles = round_up(p.dim, kX) / kX;
-    const int64_t tiles = xtiles * (round_up(p.chunk < a->rows ? p.chunk : a->rows, kY) / kY);
+    // the chip's rounds best, each item costing about as much as kItemSteps steps more;
+    // in large tiles unless even small ones have no 64 steps each
     const int64_t steps = round_up(a->vocab, kK) / kK;
+    p.small_hidden = tiles_of(a->dim, rows, kX) * steps < 64 * kCus;
+    const int64_t hidden_tile = p.small_hidden ? Shape<true>::kX : kX;
+    const int64_t slots = p.small_hidden ? 2 * kCus : kCus;
+    const int64_t tiles = tiles_of(a->dim, rows, hidden_tile);
     int64_t best = 0;
     for (int64_t n = 1; n <= 64 && n <= steps; ++n) {
-        const int64_t rounds = (tiles * n + kCus - 1) / kCus;
+        const int64_t rounds = (tiles * n + slots - 1) / slots;
         const int64_t cost = rounds * ((steps + n - 1) / n + kItemSteps);
         if (n == 1 || cost < best) best = cost, p.splits = (int)n;
     }
     p.kper = (steps + p.splits - 1) / p.splits * kK;
     p.splits = (int)((steps * kK + p.kper - 1) / p.kper);
     // the weight's tiles in whole rounds, and the rest split to fill one more
-    const int64_t wtiles = xtiles * (round_up(a->vocab, kY) / kY);
-    const int64_t rest = wtiles % kCus, wsteps = round_up(p.chunk, kK) / kK;
+    p.small_weight = tiles_of(a->dim, a->vocab, kX) < kCus;
+    const int64_t weight_tile = p.small_weight ? Shape<true>::kX : kX;
+    const int64_t weight_slots = p.small_weight ? 2 * kCus : kCus;
+    const int64_t wtiles = tiles_of(a->dim, a->vocab, weight_tile);
+    const int64_t rest = wtiles % weight_slots, wsteps = round_up(p.chunk, kK) / kK;
     p.parts_of_rest = 1;
     if (rest > 0) {
-        int64_t n = kCus / rest;
+        int64_t n = weight_slots / rest;
         if (n > wsteps / kItemSteps) n = wsteps / kItemSteps;
         if (n > 1) p.parts_of_rest = (int)n;
     }
@@ -1246,7 +1277,7 @@ Plan plan_of(const rcs_head *a, int64_t entries, bool distill) {
         for (int k = 0; k < p.planes; ++k) p.e[k] = take(2 * p.chunk * p.eld);
     if (a->grad_hidden != nullptr) p.partial = take(4 * p.splits * p.chunk * p.pad);
     if (a->grad_weight != nullptr && p.parts_of_rest > 1)
-        p.rest = take(4LL * kX * kY * (wtiles - p.whole) * p.parts_of_rest);
+        p.rest = take(4 * weight_tile * weight_tile * (wtiles - p.whole) * p.parts_of_rest);
     if (p.wide_out) p.acc = take(4 * a->vocab * a->dim);
     p.bytes = at;
     return p;
@@ -1272,18 +1303,27 @@ int check_head(const rcs_head *a) {
     return RCS_OK;
 }
 
-template <class T, int OP, int PLANES, bool DIRECT>
-void launch_gemm(GemmArgs &g, hipStream_t stream) {
+template <class T, int OP, int PLANES, bool DIRECT, bool SMALL>
+void launch_shape(GemmArgs &g, hipStream_t stream) {
+    constexpr int kX = Shape<SMALL>::kX, kY = Shape<SMALL>::kY;
     g.xtiles = (int)(round_up(g.nx, kX) / kX);
     g.ytiles = (int)(round_up(g.ny, kY) / kY);
     const int64_t tiles = (int64_t)g.xtiles * g.ytiles;
     int64_t items = tiles;
     if (OP == kHidden) items *= g.splits;
     if (OP == kWeight) items = g.whole + (tiles - g.whole) * g.parts_of_rest;
-    const int64_t blocks = items < kCus ? items : kCus;
-    head_gemm<T, OP, PLANES, DIRECT><<<dim3((unsigned)blocks), kGemmThreads, 0, stream>>>(g);
+    const int64_t slots = SMALL ? 2 * kCus : kCus;
+    const int64_t blocks = items < slots ? items : slots;
+    head_gemm<T, OP, PLANES, DIRECT, SMALL>
+        <<<dim3((unsigned)blocks), Shape<SMALL>::kThreads, 0, stream>>>(g);
     if (OP == kWeight && g.parts_of_rest > 1)
-        head_weight_join<<<dim3((unsigned)((tiles - g.whole) * (kY / 4))), 256, 0, stream>>>(g);
+        head_weight_join<SMALL><<<dim3((unsigned)((tiles - g.whole) * (kY / 4))), 256, 0, stream>>>(g);
+}
+
+template <class T, int OP, int PLANES, bool DIRECT>
+void launch_gemm(GemmArgs &g, bool small, hipStream_t stream) {
+    if (small) launch_shape<T, OP, PLANES, DIRECT, true>(g, stream);
+    else launch_shape<T, OP, PLANES, DIRECT, false>(g, stream);
 }
 
 TotalArgs total_of(const rcs_head *a, const Plan &p, char *ws) {
@@ -1323,7 +1363,9 @@ void launch_products(const rcs_head *a, const Targets &tg, const Plan &p, char *
         r.scalars = scalars;
         r.rowmap = reinterpret_cast<int32_t *>(ws + p.rowmap);
         r.row0 = row0;
-        r.parts = g.parts, r.groups = (a->vocab + kGroup - 1) / kGroup, r.vocab = a->vocab;
+        r.parts = g.parts, r.vocab = a->vocab;
+        r.group = p.small_logits ? Shape<true>::kGroup : Shape<false>::kGroup;
+        r.groups = (a->vocab + r.group - 1) / r.group;
         r.parts_ld = p.groups;
         for (int k = 0; k < PLANES; ++k) r.g[k] = g.e[k];
         r.gld = p.eld, r.store = grads, r.gshift = gshift;
@@ -1346,11 +1388,11 @@ void launch_products(const rcs_head *a, const Targets &tg, const Plan &p, char *
             const dim3 grid(tg.entries == 1 ? fours : (unsigned)rows);
             if (PLANES > 1) head_targets<F32><<<grid, kRowThreads, 0, stream>>>(r);
             else head_targets<T><<<grid, kRowThreads, 0, stream>>>(r);
-            launch_gemm<T, kLogits, PLANES, DIRECT>(g, stream);
+            launch_gemm<T, kLogits, PLANES, DIRECT>(g, p.small_logits, stream);
             if (DIRECT) {
                 head_reach<<<dim3(fours), kRowThreads, 0, stream>>>(r);
                 g.retry = true;
-                launch_gemm<T, kLogits, PLANES, DIRECT>(g, stream);
+                launch_gemm<T, kLogits, PLANES, DIRECT>(g, p.small_logits, stream);
             }
             const int64_t row_blocks = grads ? round_up(rows, kK) : rows;
             head_rows<T, PLANES, DIRECT><<<dim3((unsigned)row_blocks), kRowThreads, 0, stream>>>(r);
@@ -1363,7 +1405,7 @@ void launch_products(const rcs_head *a, const Targets &tg, const Plan &p, char *
             q.nx = a->dim, q.ny = rows, q.nk = round_up(a->vocab, kK), q.kper = p.kper;
             q.partial = reinterpret_cast<float *>(ws + p.partial), q.pld = p.pad;
             q.splits = p.splits;
-            launch_gemm<T, kHidden, PLANES, false>(q, stream);
+            launch_gemm<T, kHidden, PLANES, false>(q, p.small_hidden, stream);
             ReduceArgs d = {};
             d.scalars = scalars, d.rowmap = r.rowmap, d.row0 = row0, d.rows = rows;
             d.dim = a->dim, d.pld = p.pad, d.partial = q.partial, d.splits = p.splits;
@@ -1388,7 +1430,7 @@ void launch_products(const rcs_head *a, const Targets &tg, const Plan &p, char *
             q.add = row0 > 0 || (a->accumulate != 0 && !p.wide_out);
             q.partial = reinterpret_cast<float *>(ws + p.rest);
             q.whole = p.whole, q.parts_of_rest = p.parts_of_rest;
-            launch_gemm<T, kWeight, PLANES, false>(q, stream);
+            launch_gemm<T, kWeight, PLANES, false>(q, p.small_weight, stream);
         }
     }
     if (p.wide_out)
