@@ -1204,7 +1204,7 @@ Plan plan_of(const rcs_head *a, int64_t entries, bool distill) {
     p.pad = round_up(a->dim, kK);
     // a stride of a whole number of kilobytes would put a column's elements into few
     // of the memory's channels
-    constexpr int kX = Shape<false>::kX, kY = Shape<false>::kY;
+    constexpr int kX = Shape<false>::kX;
     p.groups = round_up(a->vocab, kX) / Shape<true>::kGroup;  // or half as many
     p.eld = round_up(a->vocab, kX);
     if (p.eld % 512 == 0) p.eld += 64;

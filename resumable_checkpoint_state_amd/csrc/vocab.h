@@ -116,6 +116,26 @@ __device__ __forceinline__ void put4(void *p, int64_t i, int t, f32x4 x, int64_t
     for (int r = 0; r < 3; ++r)
         if (r < left) put(p, i + r, t, add ? pick(x, r) + element(p, i + r, t) : pick(x, r));
 }
+// Elements i to i + cols - 1 of p, of type T, cols at most 4 (zeros behind them).
+template <class T>
+__device__ __forceinline__ f32x4 load_some(const void *p, int64_t i, int cols, T) {
+    if (cols >= 4) return load4(p, i, T::kType);
+    f32x4 x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int r = 0; r < 3; ++r)
+        if (r < cols) x[r] = element(p, i + r, T::kType);
+    return x;
+}
+template <class T>
+__device__ __forceinline__ void store_some(void *p, int64_t i, int cols, f32x4 x, T) {
+    if (cols >= 4) {
+        store4(p, i, T::kType, x);
+        return;
+    }
+#pragma unroll
+    for (int r = 0; r < 3; ++r)
+        if (r < cols) put(p, i + r, T::kType, pick(x, r));
+}
 __device__ __forceinline__ int64_t index_at(const void *p, int64_t i, int t) {
     return t == RCS_I32 ? (int64_t) static_cast<const int32_t *>(p)[i]
                         : static_cast<const int64_t *>(p)[i];
@@ -133,6 +153,14 @@ inline int type_size(int type) { return type == RCS_F32 ? 4 : 2; }
 inline bool is_type(int t) { return t == RCS_F32 || t == RCS_BF16 || t == RCS_F16; }
 inline int index_size(int type) { return type == RCS_I32 ? 4 : 8; }
 inline bool is_index_type(int t) { return t == RCS_I32 || t == RCS_I64; }
+
+// f(T) for the element type t.
+template <class F>
+void by_type(int t, F f) {
+    if (t == RCS_F32) f(F32{});
+    else if (t == RCS_BF16) f(BF16{});
+    else f(F16{});
+}
 
 // What a call reads, or what it writes: each checked as it is added.
 class Extents {
