@@ -19,6 +19,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "rcs.h"
 #include "rcs_internal.h"
@@ -30,10 +31,10 @@ namespace {
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / kWave;
-constexpr int kKeys = 8;  // of a thread
-constexpr int kTile = kSortThreads * kKeys;  // keys of one block of the sort
-constexpr int kMaxBits = 9, kBins = 1 << kMaxBits;  // of one pass
-constexpr int kSeg = 32;          // sorted places of one wave of the sums
+// Keys of a thread: at most, of the one block that sorts alone, and of one of several.
+constexpr int kAloneKeys = 8, kTileKeys = 2;
+constexpr int kAlone = kSortThreads * kAloneKeys, kTile = kSortThreads * kTileKeys;
+constexpr int kMinBits = 6, kMaxBits = 9;  // of one pass
 constexpr uint32_t kNone = 0xFFFFFFFFu;  // no key
 
 // Keys of a pass: the tokens themselves (first pass), or what the last pass
@@ -57,12 +58,12 @@ __device__ __forceinline__ uint32_t key_at(const SortArgs &a, int64_t t) {
 }
 
 __global__ __launch_bounds__(kSortThreads) void embed_count(SortArgs a) {
-    __shared__ uint32_t bins[kBins];
+    __shared__ uint32_t bins[1 << kMaxBits];
     const int n = 1 << a.bits;
     for (int k = threadIdx.x; k < n; k += kSortThreads) bins[k] = 0;
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < kKeys; ++k) {
+    for (int k = 0; k < kTileKeys; ++k) {
         const int64_t t = (int64_t)blockIdx.x * kTile + k * kSortThreads + threadIdx.x;
         if (t < a.rows) atomicAdd(&bins[key_at(a, t) >> a.shift & (n - 1)], 1u);
     }
@@ -74,15 +75,16 @@ __global__ __launch_bounds__(kSortThreads) void embed_count(SortArgs a) {
 // Each key to its place: those of lower digits first, then equal digits of earlier
 // tiles, waves, turns of a wave and lanes. ALONE: the one block there is does all
 // passes, in LDS; otherwise one pass, with the tiles' counts from embed_count.
-template <bool ALONE>
+template <bool ALONE, int BITS, int KEYS>
 __global__ __launch_bounds__(kSortThreads) void embed_sort(SortArgs a) {
-    __shared__ uint32_t next[kSortWaves][kBins];  // of the wave: where its next key goes
+    constexpr int kKeys = KEYS, kPlaces = kSortThreads * kKeys;
+    constexpr int kBins = 1 << BITS;
+    __shared__ uint32_t next[kSortWaves][kBins];  // of the wave: its keys so far, then where they begin
     __shared__ uint32_t sums[kSortWaves];
-    __shared__ uint32_t keys_at[ALONE ? kTile : 1], ids_at[ALONE ? kTile : 1];
+    __shared__ uint32_t keys_at[ALONE ? kPlaces : 1], ids_at[ALONE ? kPlaces : 1];
     const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
-    const int n = 1 << a.bits;
-    const int first = wave * (kTile / kSortWaves) + lane;  // then every kWave-th
-    const int64_t tile0 = (int64_t)blockIdx.x * kTile;
+    const int first = wave * (kPlaces / kSortWaves) + lane;  // then every kWave-th
+    const int64_t tile0 = (int64_t)blockIdx.x * kPlaces;
     uint32_t keys[kKeys], ids[kKeys];
 #pragma unroll
     for (int k = 0; k < kKeys; ++k) {
@@ -91,29 +93,41 @@ __global__ __launch_bounds__(kSortThreads) void embed_sort(SortArgs a) {
         ids[k] = t < a.rows && a.ids != nullptr ? a.ids[t] : (uint32_t)t;
     }
     for (int pass = 0; pass < (ALONE ? a.passes : 1); ++pass) {
-        const int shift = ALONE ? pass * a.bits : a.shift;
-        for (int k = tid; k < n; k += kSortThreads)
-#pragma unroll
-            for (int w = 0; w < kSortWaves; ++w) next[w][k] = 0;
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kKeys; ++k)
-            if (keys[k] != kNone) atomicAdd(&next[wave][keys[k] >> shift & (n - 1)], 1u);
-        __syncthreads();
-        // of each digit (a thread's): all keys, those of earlier tiles, and those before it
+        const int shift = ALONE ? pass * BITS : a.shift;
+        // of each digit: all keys, and those of earlier tiles
         uint32_t mine = 0, before = 0;
-        if (tid < n) {
-            if (ALONE) {
-#pragma unroll
-                for (int w = 0; w < kSortWaves; ++w) mine += next[w][tid];
-            } else {
+        if (!ALONE && tid < kBins) {
 #pragma unroll 8
-                for (int i = 0; i < a.tiles; ++i) {
-                    const uint32_t c = a.hist[(int64_t)i * n + tid];
-                    mine += c;
-                    before += i < (int)blockIdx.x ? c : 0;
-                }
+            for (int i = 0; i < a.tiles; ++i) {
+                const uint32_t c = a.hist[(int64_t)i * kBins + tid];
+                mine += c;
+                before += i < (int)blockIdx.x ? c : 0;
             }
+        }
+        for (int k = lane; k < kBins; k += kWave) next[wave][k] = 0;
+        // each key's place among the wave's keys of its digit
+        uint32_t place[kKeys];
+#pragma unroll
+        for (int k = 0; k < kKeys; ++k) {
+            const bool in = keys[k] != kNone;
+            const uint32_t digit = keys[k] >> shift & (kBins - 1);
+            uint64_t same = __ballot(in);
+#pragma unroll
+            for (int b = 0; b < BITS; ++b) {
+                const bool bit = digit >> b & 1;
+                const uint64_t set = __ballot(bit);
+                same &= bit ? set : ~set;
+            }
+            const int rank = __popcll(same & ((1ull << lane) - 1));
+            place[k] = (in ? next[wave][digit] : 0) + rank;
+            __builtin_amdgcn_wave_barrier();
+            if (in && rank == 0) next[wave][digit] = place[k] + __popcll(same);
+            __builtin_amdgcn_wave_barrier();
+        }
+        __syncthreads();
+        if (ALONE && tid < kBins) {
+#pragma unroll
+            for (int w = 0; w < kSortWaves; ++w) mine += next[w][tid];
         }
         uint32_t run = mine;  // inclusive over the wave
 #pragma unroll
@@ -123,10 +137,10 @@ __global__ __launch_bounds__(kSortThreads) void embed_sort(SortArgs a) {
         }
         if (lane == kWave - 1) sums[wave] = run;
         __syncthreads();
-        if (tid < n) {
+        if (tid < kBins) {
             uint32_t at = run - mine + before;
 #pragma unroll
-            for (int w = 0; w < kBins / kWave; ++w)
+            for (int w = 0; w < (kBins + kWave - 1) / kWave; ++w)
                 if (w < wave) at += sums[w];
 #pragma unroll
             for (int w = 0; w < kSortWaves; ++w) {
@@ -138,20 +152,8 @@ __global__ __launch_bounds__(kSortThreads) void embed_sort(SortArgs a) {
         __syncthreads();
 #pragma unroll
         for (int k = 0; k < kKeys; ++k) {
-            const bool in = keys[k] != kNone;
-            const uint32_t digit = keys[k] >> shift & (n - 1);
-            uint64_t same = __ballot(in);
-            for (int b = 0; b < a.bits; ++b) {
-                const uint64_t set = __ballot(digit >> b & 1);
-                same &= digit >> b & 1 ? set : ~set;
-            }
-            const int rank = __popcll(same & ((1ull << lane) - 1));
-            uint32_t to = 0;
-            if (in) to = next[wave][digit] + rank;
-            __builtin_amdgcn_wave_barrier();
-            if (in && rank == 0) next[wave][digit] = to + __popcll(same);
-            __builtin_amdgcn_wave_barrier();
-            if (!in) continue;
+            if (keys[k] == kNone) continue;
+            const uint32_t to = next[wave][keys[k] >> shift & (kBins - 1)] + place[k];
             if (ALONE) keys_at[to] = keys[k], ids_at[to] = ids[k];
             else a.keys_out[to] = keys[k], a.ids_out[to] = ids[k];
         }
@@ -186,9 +188,56 @@ struct SumArgs {
 constexpr int kSumThreads = 256;
 constexpr int kCols = 4;    // of a lane
 constexpr int kBatch = 8;   // rows that are under way at a time
+// Sorted places of one wave of the sums: few of them where there are few rows, so that
+// more waves share them (1,023 rows of 321: 25 us with 32 places).
+constexpr int kManySeg = 32, kFewSeg = 8;
+constexpr int64_t kFewRows = 16384;
+
+// A lane's columns n to n + cols - 1 of a row. A row's last few are read as the last of
+// its last four: all loads are then alike, with no branch between them, and are under
+// way together (values are made of them afterwards). NARROW: rows of fewer columns.
+template <class T>
+using Four = typename std::conditional<T::kBytes == 4, u32x4, u32x2>::type;
+template <bool NARROW>
+struct Cols {
+    int64_t n, from;
+    int cols;
+    __device__ __forceinline__ Cols(int64_t at, int64_t dim) {
+        n = at;
+        cols = (int)max((int64_t)0, min((int64_t)kCols, dim - n));
+        from = NARROW ? 0 : min(n, dim - kCols);
+    }
+    template <class T>
+    __device__ __forceinline__ Four<T> load(const void *p, int64_t row, T) const {
+        if constexpr (NARROW) {
+            const f32x4 x = load_some(p, row, cols, T{});
+            if constexpr (T::kBytes == 4) return __builtin_bit_cast(u32x4, x);
+            else return u32x2{two(x[0], x[1], T{}), two(x[2], x[3], T{})};
+        } else if constexpr (T::kBytes == 4) {
+            return *reinterpret_cast<const u32x4_any *>(static_cast<const float *>(p) + row + from);
+        } else {
+            return *reinterpret_cast<const u32x2_any *>(static_cast<const uint16_t *>(p) + row +
+                                                        from);
+        }
+    }
+    template <class T>
+    __device__ __forceinline__ f32x4 values(Four<T> raw, T) const {
+        f32x4 x;
+        if constexpr (T::kBytes == 4) x = __builtin_bit_cast(f32x4, raw);
+        else x = four(raw, T{});
+        if (NARROW || cols == 4) return x;
+        return cols == 3   ? f32x4{x[1], x[2], x[3], 0.f}
+               : cols == 2 ? f32x4{x[2], x[3], 0.f, 0.f}
+                           : f32x4{x[3], 0.f, 0.f, 0.f};
+    }
+    template <class T>
+    __device__ __forceinline__ void store(void *p, int64_t row, f32x4 x, T) const {
+        store_some(p, row + n, cols, x, T{});
+    }
+};
 
 // A wave does a segment of the sorted order and kCols columns a lane.
-template <class R, class G>
+template <class R, class G, int kSeg, bool NARROW>
 __global__ __launch_bounds__(kSumThreads) void embed_sum(SumArgs a) {
     const int64_t item = blockIdx.x * (int64_t)(kSumThreads / kWave) +
                          __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -202,39 +251,37 @@ __global__ __launch_bounds__(kSumThreads) void embed_sum(SumArgs a) {
         const int64_t s = first + lane - 1;
         if (lane < kSeg + 2 && s >= 0 && s < a.count) key = a.keys[s], id = a.ids[s];
     }
-    const int64_t n = (item % a.parts * kWave + lane) * kCols;
-    const int cols = (int)max((int64_t)0, min((int64_t)kCols, a.dim - n));
+    const Cols<NARROW> c((item % a.parts * kWave + lane) * kCols, a.dim);
     const uint32_t vocab = (uint32_t)a.vocab;
     f32x4 sum = {0.f, 0.f, 0.f, 0.f};
     bool begins = __builtin_amdgcn_readlane(key, 0) != __builtin_amdgcn_readlane(key, 1);
     for (int k0 = 0; k0 < kSeg; k0 += kBatch) {
         uint32_t v[kBatch + 1];
-        f32x4 x[kBatch], y[kBatch];
+        Four<R> x[kBatch];
+        Four<G> y[kBatch];  // the gradient: where a token goes on, it is not used
 #pragma unroll
         for (int k = 0; k <= kBatch; ++k) v[k] = __builtin_amdgcn_readlane(key, k0 + k + 1);
         if (v[0] >= vocab) break;  // no more tokens
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            x[k] = y[k] = f32x4{0.f, 0.f, 0.f, 0.f};
-            if (v[k] >= vocab || cols == 0) continue;
             const uint32_t t = __builtin_amdgcn_readlane(id, k0 + k + 1);
-            x[k] = load_some(a.rows, (int64_t)t * a.rows_ld + n, cols, R{});
-            if (v[k + 1] != v[k])  // the gradient, where a token may end
-                y[k] = load_some(a.grad, (int64_t)v[k] * a.grad_ld + n, cols, G{});
+            const uint32_t row = v[k] < vocab ? v[k] : v[0];
+            x[k] = c.load(a.rows, (int64_t)(v[k] < vocab ? t : 0) * a.rows_ld, R{});
+            y[k] = c.load(a.grad, (int64_t)row * a.grad_ld, G{});
         }
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
             if (v[k] >= vocab) break;
-            sum += x[k];
+            sum += c.values(x[k], R{});
             const bool ends = v[k + 1] != v[k];
             if (!ends && k0 + k + 1 < kSeg) continue;
-            if (cols > 0) {
+            if (c.cols > 0) {
                 if (begins && ends) {
-                    store_some(a.grad, (int64_t)v[k] * a.grad_ld + n, cols, y[k] + sum * a.scale,
-                               G{});
+                    c.store(a.grad, (int64_t)v[k] * a.grad_ld, c.values(y[k], G{}) + sum * a.scale,
+                            G{});
                 } else {
                     // 0: a token that came from the segment before, 1: one that begins here
-                    store_some(a.open, (seg * 2 + (begins ? 1 : 0)) * a.dim + n, cols, sum, F32{});
+                    c.store(a.open, (seg * 2 + (begins ? 1 : 0)) * a.dim, sum, F32{});
                 }
             }
             sum = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -243,46 +290,62 @@ __global__ __launch_bounds__(kSumThreads) void embed_sum(SumArgs a) {
     }
 }
 
-// A wave does a segment and kCols columns a lane: if a token begins in the segment and
-// goes on behind its end, the token's sums in the order of the segments.
-template <class G>
+// blockIdx.x: segment; if a token begins in it and goes on behind its end, the token's
+// sums in the order of the segments, kCols columns a lane, the block's four waves a
+// quarter of the segments each. The blocks of a segment share its columns.
+constexpr int kJoinParts = 8;
+template <class G, int kSeg, bool NARROW>
 __global__ __launch_bounds__(kSumThreads) void embed_join(SumArgs a) {
-    const int64_t item = blockIdx.x * (int64_t)(kSumThreads / kWave) +
-                         __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int64_t seg = item / a.parts, last = (seg + 1) * kSeg - 1;
-    if (seg >= a.segments || last + 1 >= a.count) return;
-    const uint32_t v = a.keys[last];
-    if (v >= (uint32_t)a.vocab || a.keys[last + 1] != v) return;
-    if (seg > 0 && a.keys[seg * kSeg] == v && a.keys[seg * kSeg - 1] == v) return;
-    const int64_t n = (item % a.parts * kWave + threadIdx.x % kWave) * kCols;
-    // the segments that it reaches
-    int64_t lo = seg + 1, hi = a.segments - 1;  // the last whose first key is v
-    while (lo < hi) {
-        const int64_t mid = (lo + hi + 1) / 2;
-        if (a.keys[mid * kSeg] == v) lo = mid;
-        else hi = mid - 1;
+    __shared__ f32x4 shared[kSumThreads];
+    const int64_t seg = blockIdx.x, last = (seg + 1) * kSeg - 1;
+    if (last + 1 >= a.count) return;
+    const uint32_t v = a.keys[last], after = a.keys[last + 1], begin = a.keys[seg * kSeg];
+    const uint32_t before = seg > 0 ? a.keys[seg * kSeg - 1] : kNone;
+    if (v >= (uint32_t)a.vocab || after != v || (begin == v && before == v)) return;
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    // the last segment that it reaches: the last whose first key it is
+    int64_t lo = seg;
+    for (bool all = true; all;) {
+        const int64_t s = lo + 1 + lane;
+        const uint64_t here = __ballot(s < a.segments && a.keys[min(s, a.segments - 1) * kSeg] == v);
+        all = here == ~0ull;
+        lo += all ? kWave : __builtin_ctzll(~here);
     }
-    const int cols = (int)max((int64_t)0, min((int64_t)kCols, a.dim - n));
-    if (cols == 0) return;
-    f32x4 sum = load_some(a.open, (seg * 2 + 1) * a.dim + n, cols, F32{});
-    for (int64_t s0 = seg + 1; s0 <= lo; s0 += kBatch) {
-        f32x4 x[kBatch];
+    constexpr int kWaves = kSumThreads / kWave;
+    const int64_t each = (lo - seg + kWaves) / kWaves;  // of lo - seg + 1 segments
+    const int64_t first = seg + wave * each, behind = min(first + each, lo + 1);
+    for (int part = blockIdx.y; part < a.parts; part += gridDim.y) {
+        const Cols<NARROW> c(((int64_t)part * kWave + lane) * kCols, a.dim);
+        const int64_t row = (int64_t)v * a.grad_ld;
+        const Four<G> old = c.load(a.grad, row, G{});
+        f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+        for (int64_t s0 = first; s0 < behind; s0 += kBatch) {
+            u32x4 x[kBatch];
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k)
-            x[k] = s0 + k <= lo ? load_some(a.open, (s0 + k) * 2 * a.dim + n, cols, F32{})
-                                : f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int k = 0; k < kBatch; ++k) {
+                const int64_t s = min(s0 + k, behind - 1);
+                x[k] = c.load(a.open, (s * 2 + (s == seg ? 1 : 0)) * a.dim, F32{});
+            }
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) sum += x[k];
+            for (int k = 0; k < kBatch; ++k)
+                if (s0 + k < behind) sum += c.values(x[k], F32{});
+        }
+        shared[threadIdx.x] = sum;
+        __syncthreads();
+        if (wave == 0 && c.cols > 0) {
+#pragma unroll
+            for (int w = 1; w < kWaves; ++w) sum += shared[w * kWave + lane];
+            c.store(a.grad, row, c.values(old, G{}) + sum * a.scale, G{});
+        }
+        __syncthreads();
     }
-    const int64_t at = (int64_t)v * a.grad_ld + n;
-    store_some(a.grad, at, cols, load_some(a.grad, at, cols, G{}) + sum * a.scale, G{});
 }
 
 // ----------------------------------------------------------------- host side
 
 struct Plan {
     int passes, bits;
-    int tiles;
+    int tiles, seg;
     int64_t segments;
     int64_t keys[2], ids[2], hist, open, bytes;
 };
@@ -292,9 +355,12 @@ Plan plan_of(int64_t rows, int64_t vocab, int64_t dim) {
     int bits = 1;
     while ((vocab >> bits) != 0) ++bits;  // the keys are 0 to vocab
     p.passes = (bits + kMaxBits - 1) / kMaxBits;
-    p.bits = (bits + p.passes - 1) / p.passes;
+    p.bits = kMinBits;
+    while (p.bits * p.passes < bits) ++p.bits;
     p.tiles = (int)((rows + kTile - 1) / kTile);
-    p.segments = (rows + kSeg - 1) / kSeg;
+    if (rows <= kAlone) p.tiles = 1;
+    p.seg = rows <= kFewRows || dim < kCols ? kFewSeg : kManySeg;
+    p.segments = (rows + p.seg - 1) / p.seg;
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
         const int64_t was = at;
@@ -306,6 +372,14 @@ Plan plan_of(int64_t rows, int64_t vocab, int64_t dim) {
     p.open = take(8 * p.segments * dim);
     p.bytes = at;
     return p;
+}
+
+template <class F>
+void by_bits(int bits, F f) {
+    if (bits == 6) f(std::integral_constant<int, 6>{});
+    else if (bits == 7) f(std::integral_constant<int, 7>{});
+    else if (bits == 8) f(std::integral_constant<int, 8>{});
+    else f(std::integral_constant<int, 9>{});
 }
 
 int check_sizes(int64_t rows, int64_t vocab, int64_t dim) {
@@ -356,13 +430,23 @@ int embed_grad(const void *rows, int64_t rows_stride, int rows_type, int64_t cou
     };
     if (p.tiles == 1) {
         to(0);
-        embed_sort<true><<<1, kSortThreads, 0, stream>>>(s);
+        by_bits(p.bits, [&](auto bits) {
+            constexpr int kBits = decltype(bits)::value;
+            if (count <= kSortThreads)
+                embed_sort<true, kBits, 1><<<1, kSortThreads, 0, stream>>>(s);
+            else if (count <= 3 * kSortThreads)
+                embed_sort<true, kBits, 3><<<1, kSortThreads, 0, stream>>>(s);
+            else embed_sort<true, kBits, kAloneKeys><<<1, kSortThreads, 0, stream>>>(s);
+        });
     }
     for (int k = 0; k < p.passes && p.tiles > 1; ++k) {
         to(k & 1);
         s.shift = k * p.bits;
         embed_count<<<dim3((unsigned)p.tiles), kSortThreads, 0, stream>>>(s);
-        embed_sort<false><<<dim3((unsigned)p.tiles), kSortThreads, 0, stream>>>(s);
+        by_bits(p.bits, [&](auto bits) {
+            embed_sort<false, decltype(bits)::value, kTileKeys>
+                <<<dim3((unsigned)p.tiles), kSortThreads, 0, stream>>>(s);
+        });
         s.keys = s.keys_out, s.ids = s.ids_out;
     }
     SumArgs a = {};
@@ -372,12 +456,21 @@ int embed_grad(const void *rows, int64_t rows_stride, int rows_type, int64_t cou
     a.open = reinterpret_cast<float *>(ws + p.open), a.segments = p.segments;
     a.parts = (int)((dim + kCols * kWave - 1) / (kCols * kWave));
     const dim3 grid((unsigned)((p.segments * a.parts + 3) / 4));
+    const dim3 joins((unsigned)p.segments, (unsigned)(a.parts < kJoinParts ? a.parts : kJoinParts));
     by_type(grad_type, [&](auto g) {
         using G = decltype(g);
-        by_type(rows_type, [&](auto r) {
-            embed_sum<decltype(r), G><<<grid, kSumThreads, 0, stream>>>(a);
-        });
-        embed_join<G><<<grid, kSumThreads, 0, stream>>>(a);
+        const auto run = [&](auto seg, auto narrow) {
+            constexpr int kSeg = decltype(seg)::value;
+            constexpr bool kNarrow = decltype(narrow)::value;
+            by_type(rows_type, [&](auto r) {
+                embed_sum<decltype(r), G, kSeg, kNarrow><<<grid, kSumThreads, 0, stream>>>(a);
+            });
+            embed_join<G, kSeg, kNarrow><<<joins, kSumThreads, 0, stream>>>(a);
+        };
+        const std::integral_constant<int, kFewSeg> few{};
+        if (dim < kCols) run(few, std::true_type{});
+        else if (p.seg == kFewSeg) run(few, std::false_type{});
+        else run(std::integral_constant<int, kManySeg>{}, std::false_type{});
     });
     return hipGetLastError() == hipSuccess ? RCS_OK : RCS_EHIP;
 }
