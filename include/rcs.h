@@ -501,7 +501,8 @@ int rcs_list_import(rcs_list *list, const void *w, int w_type, const void *m, in
  * resumed run repeats them bit for bit.
  *
  * rcs_head. Matrices are row-major with a stride in elements between rows, at
- * least `dim` and at most 2^20; pointers need the alignment of an element only.
+ * least `dim` and at most 2^20; pointers need the alignment of an element only. At
+ * most 2^23 rows, 2^22 columns of logits (vocab) and a dim of 2^16.
  *   hidden, weight   (rows, dim) and (vocab, dim), both of `type`. The logits are
  *                    z = hidden weight^T, with products of float32 values good
  *                    to 22 bits (relative to the largest magnitude of each
@@ -515,9 +516,10 @@ int rcs_list_import(rcs_list *list, const void *w, int w_type, const void *m, in
  *                    and the gradients are those of the mean; else their sum
  *   losses           NULL, or float32[rows]: each row's loss, 0 where it has none
  *   loss             float32[1]: their mean or sum, 0 if no row has a loss
- *   limit            bytes that the exponentials of the logits may take at a time
- *                    (16 bits each, 32 with float32). Where they would take more,
- *                    rows are done in groups; at least 128 rows are done at a time
+ *   limit            bytes that the exponentials of the logits (16 bits each, 32 with
+ *                    float32) and what else is held for a row meanwhile may take.
+ *                    Where they would take more, rows are done in groups; at least
+ *                    128 rows are done at a time
  *   workspace        rcs_head_workspace(args, entries) bytes of device memory (0
  *                    entries for head_loss), aligned to 256, used until the call's
  *                    work is done. It depends on the sizes, the types, which
@@ -569,7 +571,8 @@ int head_distill(const rcs_head *args, const void *indices, int index_type, cons
  * embed_grad: grad[tokens[t]] += scale * rows[t] for t in [0, count), the gradient
  * of an embedding lookup (of tokens, or of positions). rows: (count, dim), grad:
  * (vocab, dim), each of any of the three types, strides and alignment as for
- * rcs_head. tokens: int32 or int64[count]; those outside [0, vocab) add nothing.
+ * rcs_head; count at most 2^23, vocab 2^30. tokens: int32 or int64[count]; those
+ * outside [0, vocab) add nothing.
  * The rows of a token are added up in float32, in runs whose bounds depend on
  * tokens alone, and rounded once to grad's type; scale is finite. workspace:
  * rcs_embed_workspace bytes of device memory, aligned to 256, used until the

@@ -343,6 +343,8 @@ __global__ __launch_bounds__(kSumThreads) void embed_join(SumArgs a) {
 
 // ----------------------------------------------------------------- host side
 
+constexpr int64_t kMaxTokens = 1 << 30;
+
 struct Plan {
     int passes, bits;
     int tiles, seg;
@@ -383,8 +385,8 @@ void by_bits(int bits, F f) {
 }
 
 int check_sizes(int64_t rows, int64_t vocab, int64_t dim) {
-    return rows < 0 || rows > kMaxRows || vocab < 1 || vocab > kMaxRows || dim < 1 ||
-                   dim > kMaxWidth
+    return rows < 0 || rows > kMaxRows || vocab < 1 || vocab > kMaxTokens || dim < 1 ||
+                   dim > kMaxDim
                ? RCS_EINVAL
                : RCS_OK;
 }

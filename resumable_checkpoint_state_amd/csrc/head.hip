@@ -1177,6 +1177,7 @@ __global__ __launch_bounds__(256) void head_weight_out(const float *from, int64_
 
 constexpr int64_t kCus = 256;
 constexpr int64_t kItemSteps = 12;
+constexpr int64_t kMaxVocab = 1 << 22;  // a tile's rows of exponentials fit a buffer of 4 GB
 constexpr int64_t kMinChunk = 128;  // rows done at a time at least
 
 struct Plan {
@@ -1211,7 +1212,8 @@ Plan plan_of(const rcs_head *a, int64_t entries, bool distill) {
     p.copy_w = !direct_weight(a);
     p.direct = a->type == RCS_BF16 && !distill && grads;
     // rows of a group: as many as fit the limit, in whole tiles
-    const int64_t row_bytes = (grads ? p.eld * 2 * p.planes : 0) + p.groups * 8;
+    const int64_t row_bytes = (grads ? p.eld * 2 * p.planes : 0) + p.groups * 8 +
+                              (a->grad_hidden != nullptr ? 4 * p.pad : 0);
     p.chunk = round_up(a->rows > 0 ? a->rows : 1, kMinChunk);
     const int64_t fit = a->limit / row_bytes / kMinChunk * kMinChunk;
     if (p.chunk > fit) p.chunk = fit < kMinChunk ? kMinChunk : fit;
@@ -1296,8 +1298,8 @@ struct Targets {
 
 int check_head(const rcs_head *a) {
     if (a == nullptr) return RCS_EINVAL;
-    if (a->rows < 0 || a->rows > kMaxRows || a->vocab < 1 || a->vocab > kMaxRows || a->dim < 1 ||
-        a->dim > kMaxWidth || !is_type(a->type))
+    if (a->rows < 0 || a->rows > kMaxRows || a->vocab < 1 || a->vocab > kMaxVocab || a->dim < 1 ||
+        a->dim > kMaxDim || !is_type(a->type))
         return RCS_EINVAL;
     if (a->grad_weight != nullptr && !is_type(a->grad_weight_type)) return RCS_EINVAL;
     return RCS_OK;

@@ -145,8 +145,8 @@ constexpr int kWave = 64;
 
 // ----------------------------------------------------------------- host side
 
-constexpr int64_t kMaxWidth = 1 << 20;  // of a row: offsets within a tile fit 32 bits
-constexpr int64_t kMaxRows = 1LL << 30;
+constexpr int64_t kMaxStride = 1 << 20;  // of a matrix: offsets within a tile fit 32 bits
+constexpr int64_t kMaxRows = 1 << 23, kMaxDim = 1 << 16;  // the grids' threads do, too
 
 inline int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 inline int type_size(int type) { return type == RCS_F32 ? 4 : 2; }
@@ -174,7 +174,7 @@ public:
         return rc;
     }
     int matrix(const void *p, int64_t rows, int64_t cols, int64_t stride, int type) {
-        if (stride < cols || stride > kMaxWidth) return RCS_EINVAL;
+        if (stride < cols || stride > kMaxStride) return RCS_EINVAL;
         const int size = type_size(type);
         return array(p, rows == 0 ? 0 : ((rows - 1) * stride + cols) * size, size);
     }

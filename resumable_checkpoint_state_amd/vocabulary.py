@@ -63,6 +63,14 @@ def _matrix(t, name: str, dev: int, types, shape=None) -> tuple[torch.Tensor, in
     return t, stride
 
 
+def _table(t, name: str, dev: int, types, dim: int) -> tuple[torch.Tensor, int]:
+    """As _matrix, of a matrix of the vocabulary."""
+    _on_device(t, name, dev, types)
+    if t.dim() != 2 or t.shape[1] != dim or t.shape[0] == 0:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected (vocab, {dim})")
+    return _matrix(t, name, dev, types)
+
+
 def _packed(t, name: str, dev: int, types, shape) -> torch.Tensor:
     _on_device(t, name, dev, types)
     if t.shape != shape:
@@ -88,9 +96,7 @@ def _head(call, name, entries, hidden, weight, grad_hidden, grad_weight, accumul
           losses, out, max_bytes, stream):
     dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
     h, hs = _matrix(hidden, "hidden", dev, _TYPES)
-    w, ws = _matrix(weight, "weight", dev, (hidden.dtype,))
-    if w.dim() != 2 or weight.dim() != 2 or w.shape[1] != h.shape[1] or w.shape[0] == 0:
-        raise ValueError(f"weight has shape {tuple(weight.shape)}, expected (vocab, {h.shape[1]})")
+    w, ws = _table(weight, "weight", dev, (hidden.dtype,), h.shape[1])
     if reduction not in ("mean", "sum"):
         raise ValueError(f"reduction is {reduction!r}, expected 'mean' or 'sum'")
     lead = hidden.shape[:-1]
@@ -194,9 +200,7 @@ def embed_grad(rows, tokens, grad, *, scale: float = 1.0, stream=None) -> None:
     once to grad's type."""
     dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
     r, rs = _matrix(rows, "rows", dev, _TYPES)
-    g, gs = _matrix(grad, "grad", dev, _TYPES)
-    if grad.dim() != 2 or g.shape[1] != r.shape[1] or g.shape[0] == 0:
-        raise ValueError(f"grad has shape {tuple(grad.shape)}, expected (vocab, {r.shape[1]})")
+    g, gs = _table(grad, "grad", dev, _TYPES, r.shape[1])
     t = _packed(tokens, "tokens", dev, _INDEX_TYPES, rows.shape[:-1])
     count, (vocab, dim) = r.shape[0], g.shape
     need = lib().rcs_embed_workspace(count, vocab, dim)
