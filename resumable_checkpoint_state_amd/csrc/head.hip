@@ -66,76 +66,94 @@ __device__ __forceinline__ float pow2(int e) { return ldexpf(1.f, e); }
 
 // --------------------------------------------------------------- preparation
 
-// flags[t]: whether a row with a teacher's entries has a loss.
-__global__ __launch_bounds__(256) void head_flags(const void *index, int index_type,
-                                                  int64_t entries, int64_t rows,
-                                                  const void *logits, int logits_type,
-                                                  uint8_t *flags) {
-    const int64_t t = blockIdx.x * (int64_t)(blockDim.x / kWave) + threadIdx.x / kWave;
-    const int lane = threadIdx.x % kWave;
-    if (t >= rows) return;
-    bool any = false;
-    for (int64_t k = lane; k < entries; k += kWave)
-        any |= index_at(index, t * entries + k, index_type) >= 0 &&
-               element(logits, t * entries + k, logits_type) != -INFINITY;
-    const bool flag = __any(any);
-    if (lane == 0) flags[t] = flag;
+__device__ __forceinline__ float wave_sum(float x) {
+#pragma unroll
+    for (int d = 1; d < kWave; d *= 2) x += __shfl_xor(x, d);
+    return x;
+}
+__device__ __forceinline__ float wave_max(float x) {
+#pragma unroll
+    for (int d = 1; d < kWave; d *= 2) x = fmaxf(x, __shfl_xor(x, d));
+    return x;
 }
 
-// rowmap[i]: the i-th row that has a loss; inverse[t]: its i, or -1. Without flags,
-// those whose target is not `ignore`.
-constexpr int kScanThreads = 1024, kScanRows = 8;  // consecutive rows of a thread
-__global__ __launch_bounds__(kScanThreads) void head_scan(const uint8_t *flags,
-                                                          const void *index, int index_type,
-                                                          int64_t ignore, int64_t rows,
-                                                          int32_t *rowmap, int32_t *inverse,
-                                                          Scalars *scalars) {
-    __shared__ int32_t sums[kScanThreads / kWave];
-    __shared__ uint8_t found[kScanThreads * kScanRows];
-    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
-    int32_t base = 0;
-    for (int64_t at = 0; at < rows; at += kScanThreads * kScanRows) {
-        bool f[kScanRows];
-#pragma unroll
-        for (int k = 0; k < kScanRows; ++k) {
-            const int64_t t = at + k * kScanThreads + tid;
-            f[k] = false;
-            if (t < rows)
-                f[k] = flags != nullptr ? flags[t] != 0 : index_at(index, t, index_type) != ignore;
+// What the rows' kernels read: the rows, their targets and where their results go.
+struct RowArgs {
+    Scalars *scalars;
+    int32_t *rowmap;  // [i]: the i-th row that has a loss
+    int64_t row0;
+    const f32x2 *parts;
+    int64_t groups, parts_ld, vocab;
+    int group;  // columns
+    void *g[2];
+    int64_t gld;
+    bool store;
+    int gshift;
+    const void *hidden, *weight;
+    int64_t hld, wld, dim;
+    int type;
+    const void *index, *logits;
+    int index_type, logits_type;
+    int64_t entries, ignore;
+    bool distill;
+    float tau;
+    float *losses, *compact;  // of the rows, and of those that have one
+    float *targets;  // [i][entry]: logits of the targets, in units of log 2
+    // DIRECT only, of each row: its reference, 2^(reference - lse) and the row times that
+    float *ref, *factor;
+    const uint16_t *h;
+    uint16_t *scaled;
+    int64_t pad;
+    float *only_loss;  // where there is one row, the result too
+};
+
+// Column of entry k of the row, -1 where there is none; bad is set if it is not one
+// of the vocabulary.
+__device__ __forceinline__ int64_t target_at(const RowArgs &a, int64_t t, int k, bool &bad) {
+    const int64_t at = a.distill ? t * a.entries + k : t;
+    const int64_t v = index_at(a.index, at, a.index_type);
+    if (a.distill && (v < 0 || element(a.logits, at, a.logits_type) == -INFINITY)) return -1;
+    if (v >= 0 && v < a.vocab) return v;
+    bad = true;
+    return -1;
+}
+
+// flags[t]: whether row t has a loss; counts[b]: how many of the b-th `chunk` rows.
+struct CountArgs {
+    uint8_t *flags;
+    int32_t *counts;
+    int64_t rows, chunk;
+    int chunks;
+};
+__global__ __launch_bounds__(256) void head_count(RowArgs a, CountArgs c) {
+    __shared__ int32_t shared[256 / kWave];
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    const int64_t first = blockIdx.x * c.chunk, behind = min(first + c.chunk, c.rows);
+    int32_t n = 0;
+    if (a.distill) {
+        for (int64_t t = first + wave; t < behind; t += 256 / kWave) {
+            bool any = false;
+            for (int64_t k = lane; k < a.entries; k += kWave)
+                any |= index_at(a.index, t * a.entries + k, a.index_type) >= 0 &&
+                       element(a.logits, t * a.entries + k, a.logits_type) != -INFINITY;
+            const bool flag = __any(any);
+            if (lane == 0) c.flags[t] = flag;
+            n += flag;
         }
-#pragma unroll
-        for (int k = 0; k < kScanRows; ++k) found[k * kScanThreads + tid] = f[k];
-        __syncthreads();
-        const int64_t first = at + tid * kScanRows;
-        uint32_t mine = 0;
-#pragma unroll
-        for (int k = 0; k < kScanRows; ++k) mine |= (uint32_t)found[tid * kScanRows + k] << k;
-        int32_t run = __popc(mine);  // inclusive over the wave
-#pragma unroll
-        for (int d = 1; d < kWave; d *= 2) {
-            const int32_t up = __shfl_up(run, d);
-            if (lane >= d) run += up;
+    } else {
+        for (int64_t t0 = first + wave * kWave; t0 < behind; t0 += 256) {
+            const int64_t t = t0 + lane;
+            const bool flag = t < behind && index_at(a.index, t, a.index_type) != a.ignore;
+            if (t < behind) c.flags[t] = flag;
+            n += __popcll(__ballot(flag));
         }
-        if (lane == kWave - 1) sums[wave] = run;
-        __syncthreads();
-        int32_t before = base + run - __popc(mine), all = 0;
-#pragma unroll
-        for (int w = 0; w < kScanThreads / kWave; ++w) {
-            if (w < wave) before += sums[w];
-            all += sums[w];
-        }
-#pragma unroll
-        for (int k = 0; k < kScanRows; ++k) {
-            if (first + k >= rows) break;
-            const bool f = mine >> k & 1;
-            if (f) rowmap[before] = (int32_t)(first + k);
-            inverse[first + k] = f ? before : -1;
-            before += f;
-        }
-        base += all;
-        __syncthreads();
     }
-    if (tid == 0) *scalars = Scalars{base, 0, 0, 0};
+    if (lane == 0) shared[wave] = n;
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    for (int w = 1; w < 256 / kWave; ++w) n += shared[w];
+    c.counts[blockIdx.x] = n;
+    if (blockIdx.x == 0) *a.scalars = Scalars{};
 }
 
 // Rows of a matrix as the products read them: padded with zeros to `pad` columns,
@@ -149,17 +167,15 @@ struct PrepArgs {
     Rows hidden, weight;  // weight.rows: 0 if the products read it where it is
     int64_t dim, pad;
     int type;
-    const int32_t *inverse;
-    Scalars *scalars;
     void *grad;  // gradient of the hidden rows, or null
     int64_t grad_ld;
-    float *losses;
 };
 
 // float32 only: the largest finite magnitudes of the hidden rows that have a loss (the
 // first kTopHidden blocks) and of the weight. One atomic a block: more would queue.
 constexpr int kTopHidden = 64, kTopWeight = 192;
-__global__ __launch_bounds__(1024) void head_top(PrepArgs a) {
+__global__ __launch_bounds__(1024) void head_top(PrepArgs a, const uint8_t *flags,
+                                                 Scalars *scalars) {
     __shared__ uint32_t shared[1024 / kWave];
     const bool hidden = blockIdx.x < kTopHidden;
     const Rows &m = hidden ? a.hidden : a.weight;
@@ -172,7 +188,7 @@ __global__ __launch_bounds__(1024) void head_top(PrepArgs a) {
     };
     for (int64_t r = (blockIdx.x - (hidden ? 0 : kTopHidden)) * (int64_t)(1024 / kWave) + wave;
          r < m.rows; r += waves) {
-        if (hidden && a.inverse[r] < 0) continue;
+        if (hidden && flags[r] == 0) continue;
         for (int64_t k = 4 * lane; k < a.dim; k += 4 * kWave) {
             if (k + 4 <= a.dim) {
                 const f32x4 x = load4(m.src, r * m.ld + k, RCS_F32);
@@ -190,41 +206,123 @@ __global__ __launch_bounds__(1024) void head_top(PrepArgs a) {
     __syncthreads();
     if (threadIdx.x != 0) return;
     for (int w = 1; w < 1024 / kWave; ++w) best = max(best, shared[w]);
-    atomicMax(hidden ? &a.scalars->top_h : &a.scalars->top_w, best);
+    atomicMax(hidden ? &scalars->top_h : &scalars->top_w, best);
 }
 
-// A wave does a row. Hidden row t goes to row inverse[t]; a row without a loss is left
-// out, and its gradient and loss are cleared; kK rows more are zeros behind the last
-// one, up to a whole step of the products.
-__global__ __launch_bounds__(256) void head_prep(PrepArgs a) {
-    int64_t r = blockIdx.x * (int64_t)(256 / kWave) + threadIdx.x / kWave;
+// Over a block of 256, every thread gets it.
+__device__ __forceinline__ int32_t block_count(int32_t x, int32_t *shared) {
+#pragma unroll
+    for (int d = 1; d < kWave; d *= 2) x += __shfl_xor(x, d);
+    __syncthreads();
+    if (threadIdx.x % kWave == 0) shared[threadIdx.x / kWave] = x;
+    __syncthreads();
+    return (shared[0] + shared[1]) + (shared[2] + shared[3]);
+}
+
+// The rows' logits of their targets. kFew entries at a time, each lane 8 columns.
+template <class T>
+__device__ __forceinline__ void target_logits(const RowArgs &a, int64_t t, int k0, bool &bad,
+                                              float &top, float *to) {
+    constexpr int kFew = 4;
     const int lane = threadIdx.x % kWave;
-    const bool hidden = r < a.hidden.rows + kK;
+    int64_t v[kFew];
+    float dot[kFew] = {0.f, 0.f, 0.f, 0.f};
+    const int few = (int)min((int64_t)kFew, a.entries - k0);
+#pragma unroll
+    for (int k = 0; k < kFew; ++k) v[k] = k < few ? target_at(a, t, k0 + k, bad) : -1;
+    for (int64_t n = 8 * lane; n < a.dim; n += 8 * kWave) {
+        float x[8], y[kFew][8];
+        const int there = (int)min((int64_t)8, a.dim - n);
+        load8(a.hidden, t * a.hld + n, there, x, T{});
+#pragma unroll
+        for (int k = 0; k < kFew; ++k)  // (of a column that there is, too, where there is none)
+            if (k < few) load8(a.weight, max(v[k], (int64_t)0) * a.wld + n, there, y[k], T{});
+#pragma unroll
+        for (int k = 0; k < kFew; ++k)
+            if (k < few)
+#pragma unroll
+                for (int r = 0; r < 8; ++r) dot[k] = fmaf(x[r], y[k][r], dot[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kFew; ++k) {
+        if (k >= few) continue;
+        dot[k] = v[k] < 0 ? 0.f : wave_sum(dot[k]) * (kLog2e / a.tau);
+        if (v[k] >= 0) top = fmaxf(top, dot[k]);
+        if (lane == 0) to[k0 + k] = dot[k];
+    }
+}
+// As a row's reference, the largest of its targets' logits: no larger than the row's
+// largest. A target that is not a column leaves NaN in the first place.
+__device__ __forceinline__ void target_row(const RowArgs &a, int64_t i, bool bad, float top) {
+    if (bad) a.targets[i * a.entries] = __uint_as_float(0x7FC00000u);
+    if (a.ref != nullptr) a.ref[i] = fabsf(top) < INFINITY ? top : 0.f;
+}
+
+// A wave does a row. A hidden row goes to the place that it has among those with a
+// loss, and with one entry its target's logit is worked out; a row without a loss is
+// left out, and its gradient and loss are cleared; kK rows more are zeros behind the
+// last one, up to a whole step of the products. SOLO: there are no flags and counts of
+// the rows yet: each block looks at all targets before its own.
+template <class T, bool SOLO>
+__global__ __launch_bounds__(256) void head_prep(PrepArgs a, RowArgs rows, CountArgs c) {
+    __shared__ int32_t shared[256 / kWave];
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    const int64_t blocks = (a.hidden.rows + 3) / 4, padding = blocks + kK / 4;
+    const int64_t block = blockIdx.x;
+    const bool hidden = block < padding;
     const Rows &m = hidden ? a.hidden : a.weight;
-    if (!hidden) r -= a.hidden.rows + kK;
-    int64_t to = r;
+    int64_t r = 4 * (hidden ? block : block - padding) + wave, to = r;
     bool zero = false;
-    if (hidden && r >= m.rows) {
-        const int64_t count = a.scalars->count;
-        to = count + (r - m.rows);
-        if (to >= (count + kK - 1) / kK * kK) return;
-        zero = true;
-    } else if (hidden) {
-        to = a.inverse[r];
-        if (to < 0) {
-            if (lane == 0) a.losses[r] = 0.f;
-            if (a.grad != nullptr)
-                for (int64_t k = 4 * lane; k < a.dim; k += 4 * kWave)
-                    put4(a.grad, r * a.grad_ld + k, a.type, f32x4{0.f, 0.f, 0.f, 0.f},
-                         a.dim - k, false);
-            return;
+    if (hidden) {
+        // rows with a loss before the block's first one; before the padding, all
+        const int64_t first = min(4 * block, a.hidden.rows);
+        const auto has = [&](int64_t t) {
+            return SOLO ? index_at(rows.index, t, rows.index_type) != rows.ignore
+                        : c.flags[t] != 0;
+        };
+        const bool all = block >= blocks;
+        const int64_t chunk = SOLO || all ? 0 : first / c.chunk;
+        int32_t n = 0;
+        if (!SOLO)
+            for (int k = threadIdx.x; k < (all ? c.chunks : chunk); k += 256) n += c.counts[k];
+        if (SOLO || !all)
+            for (int64_t t = (SOLO ? 0 : chunk * c.chunk) + threadIdx.x; t < first; t += 256)
+                n += has(t);
+        const int32_t before = block_count(n, shared);
+        if (all) {
+            if (block == blocks && threadIdx.x == 0) {
+                rows.scalars->count = before;
+                rows.scalars->retry = 0;
+            }
+            to = before + (4 * (block - blocks) + wave);
+            if (to >= (before + kK - 1) / kK * kK) return;
+            zero = true;
+        } else {
+            if (r >= a.hidden.rows) return;
+            if (!has(r)) {
+                if (lane == 0) rows.losses[r] = 0.f;
+                if (a.grad != nullptr)
+                    for (int64_t k = 4 * lane; k < a.dim; k += 4 * kWave)
+                        put4(a.grad, r * a.grad_ld + k, a.type, f32x4{0.f, 0.f, 0.f, 0.f},
+                             a.dim - k, false);
+                return;
+            }
+            to = before;
+            for (int64_t t = first; t < r; ++t) to += has(t);
+            if (lane == 0) rows.rowmap[to] = (int32_t)r;
+            if (rows.entries == 1) {
+                bool bad = false;
+                float top = -INFINITY;
+                target_logits<T>(rows, r, 0, bad, top, rows.targets + to);
+                if (lane == 0) target_row(rows, to, bad, top);
+            }
         }
     }
     if (r >= m.rows && !zero) return;
     uint16_t *hi = m.hi + to * a.pad;
     if (a.type == RCS_F32) {
         uint16_t *lo = m.lo + to * a.pad;
-        const float up = pow2(lift_of(hidden ? a.scalars->top_h : a.scalars->top_w));
+        const float up = pow2(lift_of(hidden ? rows.scalars->top_h : rows.scalars->top_w));
         for (int64_t k = 4 * lane; k < a.pad; k += 4 * kWave) {
             f32x4 x = {0.f, 0.f, 0.f, 0.f};
             if (!zero && k + 4 <= a.dim) {
@@ -791,16 +889,6 @@ __global__ __launch_bounds__(256) void head_weight_join(GemmArgs a) {
 constexpr int kRowThreads = 256;
 constexpr int kMaxEntries = RCS_HEAD_MAX_ENTRIES;
 
-__device__ __forceinline__ float wave_sum(float x) {
-#pragma unroll
-    for (int d = 1; d < kWave; d *= 2) x += __shfl_xor(x, d);
-    return x;
-}
-__device__ __forceinline__ float wave_max(float x) {
-#pragma unroll
-    for (int d = 1; d < kWave; d *= 2) x = fmaxf(x, __shfl_xor(x, d));
-    return x;
-}
 struct Sum {
     static __device__ __forceinline__ float of(float a, float b) { return a + b; }
     static __device__ __forceinline__ float wave(float a) { return wave_sum(a); }
@@ -822,97 +910,20 @@ __device__ __forceinline__ float block_all(float x, float *shared) {
     return y;
 }
 
-struct RowArgs {
-    Scalars *scalars;
-    const int32_t *rowmap;
-    int64_t row0;
-    const f32x2 *parts;
-    int64_t groups, parts_ld, vocab;
-    int group;  // columns
-    void *g[2];
-    int64_t gld;
-    bool store;
-    int gshift;
-    const void *hidden, *weight;
-    int64_t hld, wld, dim;
-    int type;
-    const void *index, *logits;
-    int index_type, logits_type;
-    int64_t entries;
-    bool distill;
-    float tau;
-    float *losses, *compact;  // of the rows, and of those that have one
-    float *targets;  // [row][entry]: logits of the targets, in units of log 2
-    // DIRECT only, of each row: its reference, 2^(reference - lse) and the row times that
-    float *ref, *factor;
-    const uint16_t *h;
-    uint16_t *scaled;
-    int64_t pad;
-};
-
-// Column of entry k of the row, -1 where there is none; bad is set if it is not one
-// of the vocabulary.
-__device__ __forceinline__ int64_t target_at(const RowArgs &a, int64_t t, int k, bool &bad) {
-    const int64_t at = a.distill ? t * a.entries + k : t;
-    const int64_t v = index_at(a.index, at, a.index_type);
-    if (a.distill && (v < 0 || element(a.logits, at, a.logits_type) == -INFINITY)) return -1;
-    if (v >= 0 && v < a.vocab) return v;
-    bad = true;
-    return -1;
-}
-
-// The logits of the targets (NaN in the first place if one is not a column), and as
-// the row's reference the largest of them: no larger than the row's largest logit.
-// A block does four rows of one entry each, or one row.
+// The targets' logits where a row has several; a block does a row.
 template <class T>
 __global__ __launch_bounds__(kRowThreads) void head_targets(RowArgs a) {
     __shared__ float shared[kRowThreads / kWave];
-    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-    constexpr int kWaves = kRowThreads / kWave;
-    const int64_t i = a.row0 + (a.entries == 1 ? blockIdx.x * (int64_t)kWaves + wave : blockIdx.x);
-    if (i >= a.scalars->count) return;  // of the block, or with one entry of the wave
+    const int64_t i = a.row0 + blockIdx.x;
+    if (i >= a.scalars->count) return;
     const int64_t t = a.rowmap[i];
-    float *to = a.targets + (i - a.row0) * a.entries;
     float top = -INFINITY;
     bool bad = false;
-    const int64_t hrow = t * a.hld;
-    constexpr int kFew = 4;  // entries of a wave at a time
-    for (int k0 = a.entries == 1 ? 0 : wave * kFew; k0 < a.entries; k0 += kWaves * kFew) {
-        int64_t v[kFew];
-        float dot[kFew] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int k = 0; k < kFew; ++k)
-            v[k] = k0 + k < a.entries ? target_at(a, t, k0 + k, bad) : -1;
-        const int few = min((int64_t)kFew, a.entries - k0);
-        for (int64_t n = 8 * lane; n < a.dim; n += 8 * kWave) {
-            float x[8], y[kFew][8];
-            const int there = (int)min((int64_t)8, a.dim - n);
-            load8(a.hidden, hrow + n, there, x, T{});
-#pragma unroll
-            for (int k = 0; k < kFew; ++k)  // (of a column that there is, too, where there is none)
-                if (k < few) load8(a.weight, max(v[k], (int64_t)0) * a.wld + n, there, y[k], T{});
-#pragma unroll
-            for (int k = 0; k < kFew; ++k)
-                if (k < few)
-#pragma unroll
-                    for (int r = 0; r < 8; ++r) dot[k] = fmaf(x[r], y[k][r], dot[k]);
-        }
-#pragma unroll
-        for (int k = 0; k < kFew; ++k) {
-            if (k0 + k >= a.entries) continue;
-            dot[k] = v[k] < 0 ? 0.f : wave_sum(dot[k]) * (kLog2e / a.tau);
-            if (v[k] >= 0) top = fmaxf(top, dot[k]);
-            if (lane == 0) to[k0 + k] = dot[k];
-        }
-    }
-    if (a.entries > 1) {
-        top = block_all<Max>(top, shared);
-        bad = block_all<Max>(bad ? 1.f : 0.f, shared) > 0.f;
-    }
-    if (lane == 0 && (wave == 0 || a.entries == 1)) {  // (wave 0 has written the first one)
-        if (bad) to[0] = __uint_as_float(0x7FC00000u);
-        if (a.ref != nullptr) a.ref[i - a.row0] = fabsf(top) < INFINITY ? top : 0.f;
-    }
+    for (int k0 = threadIdx.x / kWave * 4; k0 < a.entries; k0 += kRowThreads / kWave * 4)
+        target_logits<T>(a, t, k0, bad, top, a.targets + i * a.entries);
+    top = block_all<Max>(top, shared);
+    bad = block_all<Max>(bad ? 1.f : 0.f, shared) > 0.f;  // (the first place has been written)
+    if (threadIdx.x == 0) target_row(a, i, bad, top);
 }
 
 // Rows whose largest logit is beyond the reach of their reference get that logit as
@@ -925,7 +936,7 @@ __global__ __launch_bounds__(kRowThreads) void head_reach(RowArgs a) {
     float top = -INFINITY;
     for (int64_t k = lane; k < a.groups; k += kWave) top = fmaxf(top, parts[k][0]);
     top = wave_max(top);
-    if (lane == 0 && top > kReach) a.ref[local] += top;
+    if (lane == 0 && top > kReach) a.ref[a.row0 + local] += top;
 }
 
 // Row i of the logits: the sum of its exponentials, the loss, and the exponentials
@@ -946,6 +957,7 @@ __global__ __launch_bounds__(kRowThreads) void head_rows(RowArgs a) {
     const int64_t local = blockIdx.x, i = a.row0 + local;
     const int64_t count = a.scalars->count;
     if (i >= count) {
+        if (a.only_loss != nullptr && tid == 0) *a.only_loss = 0.f;
         // zeros up to a whole step of the products' sums over the rows
         if (!a.store || i >= a.row0 + (max((int64_t)0, count - a.row0) + kK - 1) / kK * kK) return;
         const u32x4 zero = {0, 0, 0, 0};
@@ -961,7 +973,7 @@ __global__ __launch_bounds__(kRowThreads) void head_rows(RowArgs a) {
     }
     const int64_t t = a.rowmap[i];
     const f32x2 *parts = a.parts + local * a.parts_ld;
-    const float ref = DIRECT ? a.ref[local] : 0.f;
+    const float ref = DIRECT ? a.ref[i] : 0.f;
     float top = 0.f;
     if (!DIRECT) {
         top = -INFINITY;
@@ -979,7 +991,7 @@ __global__ __launch_bounds__(kRowThreads) void head_rows(RowArgs a) {
     for (int k = tid; k < entries; k += kRowThreads) {
         bool bad = false;
         sv[k] = target_at(a, t, k, bad);
-        sz[k] = a.targets[local * a.entries + k];
+        sz[k] = a.targets[i * a.entries + k];
         sp[k] = !a.distill ? 0.f
                 : sv[k] < 0
                     ? -INFINITY
@@ -1012,6 +1024,7 @@ __global__ __launch_bounds__(kRowThreads) void head_rows(RowArgs a) {
     }
     if (lse2 != lse2) loss = lse2;
     if (tid == 0) a.losses[t] = a.compact[i] = loss;
+    if (tid == 0 && a.only_loss != nullptr) *a.only_loss = loss;
     if (!a.store) return;
 
     if constexpr (DIRECT) {
@@ -1177,6 +1190,8 @@ __global__ __launch_bounds__(256) void head_weight_out(const float *from, int64_
 
 constexpr int64_t kCus = 256;
 constexpr int64_t kItemSteps = 12;
+constexpr int64_t kSoloRows = 1024;  // of which each block counts those before its own
+constexpr int64_t kChunks = 256;     // that the rows are counted in, at most
 constexpr int64_t kMaxVocab = 1 << 22;  // a tile's rows of exponentials fit a buffer of 4 GB
 constexpr int64_t kMinChunk = 128;  // rows done at a time at least
 
@@ -1187,9 +1202,9 @@ struct Plan {
     int64_t eld, groups;
     int splits, whole, parts_of_rest;
     int64_t kper;
-    bool copy_w, wide_out, direct, small_logits, small_hidden, small_weight;
+    bool copy_w, wide_out, direct, solo, small_logits, small_hidden, small_weight;
     // offsets in the workspace
-    int64_t scalars, flags, rowmap, inverse, losses, compact, h[2], w[2], e[2], parts, targets, ref, factor, scaled, partial, rest, acc, bytes;
+    int64_t scalars, flags, counts, rowmap, losses, compact, h[2], w[2], e[2], parts, targets, ref, factor, scaled, partial, rest, acc, bytes;
 };
 
 bool direct_weight(const rcs_head *a) {
@@ -1210,7 +1225,6 @@ Plan plan_of(const rcs_head *a, int64_t entries, bool distill) {
     p.eld = round_up(a->vocab, kX);
     if (p.eld % 512 == 0) p.eld += 64;
     p.copy_w = !direct_weight(a);
-    p.direct = a->type == RCS_BF16 && !distill && grads;
     // rows of a group: as many as fit the limit, in whole tiles
     const int64_t row_bytes = (grads ? p.eld * 2 * p.planes : 0) + p.groups * 8 +
                               (a->grad_hidden != nullptr ? 4 * p.pad : 0);
@@ -1223,6 +1237,8 @@ Plan plan_of(const rcs_head *a, int64_t entries, bool distill) {
         return (x + tile - 1) / tile * ((y + tile - 1) / tile);
     };
     p.small_logits = tiles_of(a->vocab, rows, kX) < kCus;
+    p.direct = a->type == RCS_BF16 && !distill && grads && !p.small_logits;
+    p.solo = a->type != RCS_F32 && !distill && a->rows <= kSoloRows;
     // splits of the hidden gradient's sum over the vocabulary: the number that fills
     // the chip's rounds best, each item costing about as much as kItemSteps steps more;
     // in large tiles unless even small ones have no 64 steps each
@@ -1261,17 +1277,17 @@ Plan plan_of(const rcs_head *a, int64_t entries, bool distill) {
     };
     p.scalars = take(sizeof(Scalars));
     p.flags = take(a->rows);
+    p.counts = take(4 * kChunks);
     p.rowmap = take(4 * a->rows);
-    p.inverse = take(4 * a->rows);
     p.losses = take(4 * a->rows);
     p.compact = take(4 * a->rows);
     for (int k = 0; k < p.planes; ++k) p.h[k] = take(2 * (a->rows + kK) * p.pad);
     if (p.copy_w)
         for (int k = 0; k < p.planes; ++k) p.w[k] = take(2 * a->vocab * p.pad);
     p.parts = take(8 * p.chunk * p.groups);
-    p.targets = take(4 * p.chunk * entries);
+    p.targets = take(4 * a->rows * entries);
     if (p.direct) {
-        p.ref = take(4 * p.chunk);
+        p.ref = take(4 * a->rows);
         p.factor = take(4 * p.chunk);
         if (grads) p.scaled = take(2 * p.chunk * p.pad);
     }
@@ -1324,8 +1340,13 @@ void launch_shape(GemmArgs &g, hipStream_t stream) {
 
 template <class T, int OP, int PLANES, bool DIRECT>
 void launch_gemm(GemmArgs &g, bool small, hipStream_t stream) {
-    if (small) launch_shape<T, OP, PLANES, DIRECT, true>(g, stream);
-    else launch_shape<T, OP, PLANES, DIRECT, false>(g, stream);
+    if constexpr (!DIRECT) {
+        if (small) {
+            launch_shape<T, OP, PLANES, DIRECT, true>(g, stream);
+            return;
+        }
+    }
+    launch_shape<T, OP, PLANES, DIRECT, false>(g, stream);
 }
 
 TotalArgs total_of(const rcs_head *a, const Plan &p, char *ws) {
@@ -1334,13 +1355,12 @@ TotalArgs total_of(const rcs_head *a, const Plan &p, char *ws) {
 }
 
 template <class T, int PLANES, bool DIRECT>
-void launch_products(const rcs_head *a, const Targets &tg, const Plan &p, char *ws,
-                     hipStream_t stream) {
+void launch_products(const rcs_head *a, const Targets &tg, const Plan &p, const RowArgs &all,
+                     char *ws, hipStream_t stream) {
     const bool grads = a->grad_hidden != nullptr || a->grad_weight != nullptr;
     Scalars *scalars = reinterpret_cast<Scalars *>(ws + p.scalars);
     const int gshift = __is_same(T, F16) ? 14 : 0;
     const float scale = a->scale * tg.tau;
-    float *losses = a->losses != nullptr ? a->losses : reinterpret_cast<float *>(ws + p.losses);
     for (int64_t row0 = 0; row0 == 0 || row0 < a->rows; row0 += p.chunk) {
         const int64_t rows = a->rows - row0 < p.chunk ? a->rows - row0 : p.chunk;
         GemmArgs g = {};
@@ -1361,38 +1381,23 @@ void launch_products(const rcs_head *a, const Targets &tg, const Plan &p, char *
         g.eld = p.eld, g.parts = reinterpret_cast<f32x2 *>(ws + p.parts), g.groups = p.groups;
         g.zscale = kLog2e / tg.tau;
         g.store = grads;
-        RowArgs r = {};
-        r.scalars = scalars;
-        r.rowmap = reinterpret_cast<int32_t *>(ws + p.rowmap);
+        RowArgs r = all;
         r.row0 = row0;
-        r.parts = g.parts, r.vocab = a->vocab;
+        r.parts = g.parts;
         r.group = p.small_logits ? Shape<true>::kGroup : Shape<false>::kGroup;
         r.groups = (a->vocab + r.group - 1) / r.group;
-        r.parts_ld = p.groups;
         for (int k = 0; k < PLANES; ++k) r.g[k] = g.e[k];
-        r.gld = p.eld, r.store = grads, r.gshift = gshift;
-        r.hidden = a->hidden, r.weight = a->weight, r.hld = a->hidden_stride;
-        r.wld = a->weight_stride, r.dim = a->dim, r.type = a->type;
-        r.index = tg.index, r.logits = tg.logits, r.index_type = tg.index_type;
-        r.logits_type = tg.logits_type, r.entries = tg.entries, r.distill = tg.distill;
-        r.tau = tg.tau, r.losses = losses;
-        r.compact = reinterpret_cast<float *>(ws + p.compact);
-        r.targets = reinterpret_cast<float *>(ws + p.targets);
-        r.h = reinterpret_cast<const uint16_t *>(ws + p.h[0]), r.pad = p.pad;
-        if (DIRECT) {
-            r.ref = reinterpret_cast<float *>(ws + p.ref);
-            r.factor = reinterpret_cast<float *>(ws + p.factor);
-            r.scaled = reinterpret_cast<uint16_t *>(ws + p.scaled);
-            g.ref = r.ref;
-        }
+        r.gshift = gshift;
+        if (DIRECT) g.ref = r.ref + row0;
         if (rows > 0) {
-            const unsigned fours = (unsigned)((rows + 3) / 4);
-            const dim3 grid(tg.entries == 1 ? fours : (unsigned)rows);
-            if (PLANES > 1) head_targets<F32><<<grid, kRowThreads, 0, stream>>>(r);
-            else head_targets<T><<<grid, kRowThreads, 0, stream>>>(r);
+            if (tg.entries > 1) {
+                const dim3 grid((unsigned)rows);
+                if (PLANES > 1) head_targets<F32><<<grid, kRowThreads, 0, stream>>>(r);
+                else head_targets<T><<<grid, kRowThreads, 0, stream>>>(r);
+            }
             launch_gemm<T, kLogits, PLANES, DIRECT>(g, p.small_logits, stream);
             if (DIRECT) {
-                head_reach<<<dim3(fours), kRowThreads, 0, stream>>>(r);
+                head_reach<<<dim3((unsigned)((rows + 3) / 4)), kRowThreads, 0, stream>>>(r);
                 g.retry = true;
                 launch_gemm<T, kLogits, PLANES, DIRECT>(g, p.small_logits, stream);
             }
@@ -1476,31 +1481,56 @@ int head_call(const rcs_head *a, const Targets &tg, hipStream_t stream) {
 
     char *ws = static_cast<char *>(a->workspace);
     Scalars *scalars = reinterpret_cast<Scalars *>(ws + p.scalars);
-    uint8_t *flags = reinterpret_cast<uint8_t *>(ws + p.flags);
-    int32_t *rowmap = reinterpret_cast<int32_t *>(ws + p.rowmap);
-    int32_t *inverse = reinterpret_cast<int32_t *>(ws + p.inverse);
-    float *losses = a->losses != nullptr ? a->losses : reinterpret_cast<float *>(ws + p.losses);
-    if (tg.distill && a->rows > 0)
-        head_flags<<<dim3((unsigned)((a->rows + 3) / 4)), 256, 0, stream>>>(
-            tg.index, tg.index_type, tg.entries, a->rows, tg.logits, tg.logits_type, flags);
-    head_scan<<<1, kScanThreads, 0, stream>>>(tg.distill ? flags : nullptr, tg.index,
-                                              tg.index_type, tg.ignore, a->rows, rowmap, inverse,
-                                              scalars);
+    RowArgs r = {};
+    r.scalars = scalars;
+    r.rowmap = reinterpret_cast<int32_t *>(ws + p.rowmap);
+    r.parts_ld = p.groups, r.vocab = a->vocab;
+    r.gld = p.eld, r.store = a->grad_hidden != nullptr || a->grad_weight != nullptr;
+    r.hidden = a->hidden, r.weight = a->weight, r.hld = a->hidden_stride;
+    r.wld = a->weight_stride, r.dim = a->dim, r.type = a->type;
+    r.index = tg.index, r.logits = tg.logits, r.index_type = tg.index_type;
+    r.logits_type = tg.logits_type, r.entries = tg.entries, r.ignore = tg.ignore;
+    r.distill = tg.distill, r.tau = tg.tau;
+    r.losses = a->losses != nullptr ? a->losses : reinterpret_cast<float *>(ws + p.losses);
+    r.compact = reinterpret_cast<float *>(ws + p.compact);
+    r.targets = reinterpret_cast<float *>(ws + p.targets);
+    r.h = reinterpret_cast<const uint16_t *>(ws + p.h[0]), r.pad = p.pad;
+    if (p.direct) {
+        r.ref = reinterpret_cast<float *>(ws + p.ref);
+        r.factor = reinterpret_cast<float *>(ws + p.factor);
+        r.scaled = reinterpret_cast<uint16_t *>(ws + p.scaled);
+    }
+    const bool only = a->rows == 1 && !r.store;
+    if (only) r.only_loss = a->loss;
+    CountArgs c = {};
+    c.flags = reinterpret_cast<uint8_t *>(ws + p.flags);
+    c.counts = reinterpret_cast<int32_t *>(ws + p.counts);
+    c.rows = a->rows;
+    c.chunk = round_up((a->rows + kChunks - 1) / kChunks, 256);
+    if (c.chunk == 0) c.chunk = 256;
+    c.chunks = (int)((a->rows + c.chunk - 1) / c.chunk);
     PrepArgs h = {};
     const auto plane = [&](int64_t at) { return reinterpret_cast<uint16_t *>(ws + at); };
     h.hidden = Rows{a->hidden, plane(p.h[0]), plane(p.h[1]), a->hidden_stride, a->rows};
     h.weight = Rows{a->weight, plane(p.w[0]), plane(p.w[1]), a->weight_stride,
                     p.copy_w ? a->vocab : 0};
-    h.dim = a->dim, h.pad = p.pad, h.type = a->type, h.inverse = inverse, h.scalars = scalars;
-    h.grad = a->grad_hidden, h.grad_ld = a->grad_hidden_stride, h.losses = losses;
-    if (a->type == RCS_F32) head_top<<<kTopHidden + kTopWeight, 1024, 0, stream>>>(h);
-    head_prep<<<dim3((unsigned)((h.hidden.rows + kK + h.weight.rows + 3) / 4)), 256, 0,
-                stream>>>(h);
-    if (a->type == RCS_F32) launch_products<F16, 2, false>(a, tg, p, ws, stream);
-    else if (a->type == RCS_F16) launch_products<F16, 1, false>(a, tg, p, ws, stream);
-    else if (p.direct) launch_products<BF16, 1, true>(a, tg, p, ws, stream);
-    else launch_products<BF16, 1, false>(a, tg, p, ws, stream);
-    if (a->grad_hidden == nullptr || a->rows == 0)
+    h.dim = a->dim, h.pad = p.pad, h.type = a->type;
+    h.grad = a->grad_hidden, h.grad_ld = a->grad_hidden_stride;
+    if (!p.solo)
+        head_count<<<dim3((unsigned)(c.chunks > 0 ? c.chunks : 1)), 256, 0, stream>>>(r, c);
+    if (a->type == RCS_F32)
+        head_top<<<kTopHidden + kTopWeight, 1024, 0, stream>>>(h, c.flags, scalars);
+    const dim3 blocks((unsigned)((a->rows + 3) / 4 + kK / 4 + (h.weight.rows + 3) / 4));
+    by_type(a->type, [&](auto type) {
+        using T = decltype(type);
+        if (p.solo) head_prep<T, true><<<blocks, 256, 0, stream>>>(h, r, c);
+        else head_prep<T, false><<<blocks, 256, 0, stream>>>(h, r, c);
+    });
+    if (a->type == RCS_F32) launch_products<F16, 2, false>(a, tg, p, r, ws, stream);
+    else if (a->type == RCS_F16) launch_products<F16, 1, false>(a, tg, p, r, ws, stream);
+    else if (p.direct) launch_products<BF16, 1, true>(a, tg, p, r, ws, stream);
+    else launch_products<BF16, 1, false>(a, tg, p, r, ws, stream);
+    if ((a->grad_hidden == nullptr || a->rows == 0) && !only)
         head_total<<<1, 256, 0, stream>>>(total_of(a, p, ws));
     return hipGetLastError() == hipSuccess ? RCS_OK : RCS_EHIP;
 }
