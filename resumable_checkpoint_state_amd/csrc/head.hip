@@ -36,6 +36,11 @@ __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
+template <int N>
+struct Int {
+    static constexpr int value = N;
+};
+
 // Tiles of a product: kX by kY outputs by a block of 2 by kY / 64 waves, each kX / 2
 // by 64 of them, kK at a time, from two places in LDS in turn. The large ones (one
 // block a CU) read least; products that have fewer of them than there are CUs are
@@ -66,15 +71,28 @@ __device__ __forceinline__ float pow2(int e) { return ldexpf(1.f, e); }
 
 // --------------------------------------------------------------- preparation
 
+// Over the wave, by permutes within rows of 16 lanes and broadcasts between them.
+template <class F>
+__device__ __forceinline__ float wave_all(float x, float none, F f) {
+    const auto step = [&](auto control, auto rows) {
+        const int y = __builtin_amdgcn_update_dpp(
+            __builtin_bit_cast(int, none), __builtin_bit_cast(int, x), decltype(control)::value,
+            decltype(rows)::value, 0xF, false);
+        x = f(x, __builtin_bit_cast(float, y));
+    };
+    step(Int<0x111>{}, Int<0xF>{});  // from 1, 2, 4 and 8 lanes before in the row
+    step(Int<0x112>{}, Int<0xF>{});
+    step(Int<0x114>{}, Int<0xF>{});
+    step(Int<0x118>{}, Int<0xF>{});
+    step(Int<0x142>{}, Int<0xA>{});  // the row before's last lane, to the second and fourth
+    step(Int<0x143>{}, Int<0xC>{});  // the second row's last lane, to the third and fourth
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 63));
+}
 __device__ __forceinline__ float wave_sum(float x) {
-#pragma unroll
-    for (int d = 1; d < kWave; d *= 2) x += __shfl_xor(x, d);
-    return x;
+    return wave_all(x, 0.f, [](float a, float b) { return a + b; });
 }
 __device__ __forceinline__ float wave_max(float x) {
-#pragma unroll
-    for (int d = 1; d < kWave; d *= 2) x = fmaxf(x, __shfl_xor(x, d));
-    return x;
+    return wave_all(x, -INFINITY, [](float a, float b) { return fmaxf(a, b); });
 }
 
 // What the rows' kernels read: the rows, their targets and where their results go.
@@ -219,14 +237,13 @@ __device__ __forceinline__ int32_t block_count(int32_t x, int32_t *shared) {
     return (shared[0] + shared[1]) + (shared[2] + shared[3]);
 }
 
-// The rows' logits of their targets. kFew entries at a time, each lane 8 columns.
-template <class T>
+// A row's logits of kFew of its targets, each lane 8 columns at a time.
+template <class T, int kFew>
 __device__ __forceinline__ void target_logits(const RowArgs &a, int64_t t, int k0, bool &bad,
                                               float &top, float *to) {
-    constexpr int kFew = 4;
     const int lane = threadIdx.x % kWave;
     int64_t v[kFew];
-    float dot[kFew] = {0.f, 0.f, 0.f, 0.f};
+    float dot[kFew] = {};
     const int few = (int)min((int64_t)kFew, a.entries - k0);
 #pragma unroll
     for (int k = 0; k < kFew; ++k) v[k] = k < few ? target_at(a, t, k0 + k, bad) : -1;
@@ -313,7 +330,7 @@ __global__ __launch_bounds__(256) void head_prep(PrepArgs a, RowArgs rows, Count
             if (rows.entries == 1) {
                 bool bad = false;
                 float top = -INFINITY;
-                target_logits<T>(rows, r, 0, bad, top, rows.targets + to);
+                target_logits<T, 1>(rows, r, 0, bad, top, rows.targets + to);
                 if (lane == 0) target_row(rows, to, bad, top);
             }
         }
@@ -395,10 +412,6 @@ struct GemmArgs {
 };
 
 typedef __attribute__((address_space(3))) char lds_char;
-template <int N>
-struct Int {
-    static constexpr int value = N;
-};
 
 [[maybe_unused]] constexpr int kRefPlaces = 4;  // items whose rows' references are in LDS, at most
 [[maybe_unused]] constexpr int kCalls = 4;  // loads of a wave for one operand
@@ -919,8 +932,9 @@ __global__ __launch_bounds__(kRowThreads) void head_targets(RowArgs a) {
     const int64_t t = a.rowmap[i];
     float top = -INFINITY;
     bool bad = false;
-    for (int k0 = threadIdx.x / kWave * 4; k0 < a.entries; k0 += kRowThreads / kWave * 4)
-        target_logits<T>(a, t, k0, bad, top, a.targets + i * a.entries);
+    constexpr int kFew = 4;
+    for (int k0 = threadIdx.x / kWave * kFew; k0 < a.entries; k0 += kRowThreads / kWave * kFew)
+        target_logits<T, kFew>(a, t, k0, bad, top, a.targets + i * a.entries);
     top = block_all<Max>(top, shared);
     bad = block_all<Max>(bad ? 1.f : 0.f, shared) > 0.f;  // (the first place has been written)
     if (threadIdx.x == 0) target_row(a, i, bad, top);
@@ -1189,7 +1203,7 @@ __global__ __launch_bounds__(256) void head_weight_out(const float *from, int64_
 // ----------------------------------------------------------------- host side
 
 constexpr int64_t kCus = 256;
-constexpr int64_t kItemSteps = 12;
+constexpr int64_t kItemSteps = 24;
 constexpr int64_t kSoloRows = 1024;  // of which each block counts those before its own
 constexpr int64_t kChunks = 256;     // that the rows are counted in, at most
 constexpr int64_t kMaxVocab = 1 << 22;  // a tile's rows of exponentials fit a buffer of 4 GB
@@ -1506,8 +1520,8 @@ int head_call(const rcs_head *a, const Targets &tg, hipStream_t stream) {
     c.flags = reinterpret_cast<uint8_t *>(ws + p.flags);
     c.counts = reinterpret_cast<int32_t *>(ws + p.counts);
     c.rows = a->rows;
-    c.chunk = round_up((a->rows + kChunks - 1) / kChunks, 256);
-    if (c.chunk == 0) c.chunk = 256;
+    c.chunk = round_up((a->rows + kChunks - 1) / kChunks, 32);
+    if (c.chunk == 0) c.chunk = 32;
     c.chunks = (int)((a->rows + c.chunk - 1) / c.chunk);
     PrepArgs h = {};
     const auto plane = [&](int64_t at) { return reinterpret_cast<uint16_t *>(ws + at); };
