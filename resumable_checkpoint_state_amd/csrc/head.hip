@@ -413,7 +413,7 @@ struct GemmArgs {
 
 typedef __attribute__((address_space(3))) char lds_char;
 
-[[maybe_unused]] constexpr int kRefPlaces = 4;  // items whose rows' references are in LDS, at most
+constexpr int kRefPlaces = 4;  // items whose rows' references are in LDS, at most
 [[maybe_unused]] constexpr int kCalls = 4;  // loads of a wave for one operand
 
 // How an operand's tile of R by kK lies in LDS: in `kCalls` loads a wave, each of
@@ -543,9 +543,15 @@ struct Item {
 
 [[maybe_unused]] constexpr int kStreamed = 2;  // a store's cache policy: not kept in L2 (736 -> 700 us)
 
+// LDS of a product's block.
+template <bool DIRECT, bool SMALL>
+constexpr int kSharedBytes =
+    2 * Shape<SMALL>::kStageBytes + (DIRECT ? kRefPlaces * Shape<SMALL>::kY * 4 : 0);
+
+// What the block-th of `blocks` blocks does of a product.
 template <class T, int OP, int PLANES, bool DIRECT, bool SMALL>
-__global__ __launch_bounds__(Shape<SMALL>::kThreads, 2) void head_gemm(GemmArgs a) {
-#ifdef __HIP_DEVICE_COMPILE__  // the host needs the launch stub alone
+__device__ __forceinline__ void product(const GemmArgs &a, char *shared, int block, int blocks) {
+#ifdef __HIP_DEVICE_COMPILE__  // the host needs the kernels' launch stubs alone
     using S = Shape<SMALL>;
     constexpr int kX = S::kX, kY = S::kY, kXBytes = S::kXBytes, kStageBytes = S::kStageBytes;
     constexpr int kFx = S::kFx, kFy = S::kFy;
@@ -553,8 +559,6 @@ __global__ __launch_bounds__(Shape<SMALL>::kThreads, 2) void head_gemm(GemmArgs 
     using Y = Side<OP != kWeight, kY, false>;
     static_assert(kX / 8 == kCalls * S::kWaves && kY / 8 == kCalls * S::kWaves, "whole tiles");
     static_assert(!DIRECT || OP == kLogits, "a form of the logits");
-    __shared__ __attribute__((aligned(1024))) char
-        shared[2 * kStageBytes + (DIRECT ? kRefPlaces * kY * 4 : 0)];
     lds_char *lds = (lds_char *)shared;
     const uint32_t lds_at = (uint32_t)(uintptr_t)lds;
     const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -570,7 +574,7 @@ __global__ __launch_bounds__(Shape<SMALL>::kThreads, 2) void head_gemm(GemmArgs 
     const int items = OP == kHidden   ? tiles * a.splits
                       : OP == kWeight ? a.whole + (tiles - a.whole) * a.parts_of_rest
                                       : tiles;
-    int at = blockIdx.x;
+    int at = block;
     if (at >= items) return;
     auto item_of = [&](int index) {
         Item m;
@@ -653,7 +657,7 @@ __global__ __launch_bounds__(Shape<SMALL>::kThreads, 2) void head_gemm(GemmArgs 
             ++load_pair;
             if (load_pair == kPairsOfPlanes) {
                 load_pair = 0;
-                load_at += gridDim.x;
+                load_at += blocks;
                 if (load_at < items) load = item_of(load_at);
                 else load.empty = true;
                 load_refs();
@@ -853,7 +857,7 @@ __global__ __launch_bounds__(Shape<SMALL>::kThreads, 2) void head_gemm(GemmArgs 
     for (int i = 0; i < kFx; ++i) read_one(0, i, Int<0>{});
     int stage = 0, place = 0;
     bool stored = false;
-    for (; at < items; at += gridDim.x) {
+    for (; at < items; at += blocks) {
         const Item m = item_of(at);
         clear();
         for (int left = m.per * kPairsOfPlanes; left > 0; --left) {
@@ -877,13 +881,32 @@ __global__ __launch_bounds__(Shape<SMALL>::kThreads, 2) void head_gemm(GemmArgs 
 #endif
 }
 
-// The tiles of kWeight that were split: sums in the order of the splits.
+template <class T, int OP, int PLANES, bool DIRECT, bool SMALL>
+__global__ __launch_bounds__(Shape<SMALL>::kThreads, 2) void head_gemm(GemmArgs a) {
+    __shared__ __attribute__((aligned(1024))) char shared[kSharedBytes<DIRECT, SMALL>];
+    product<T, OP, PLANES, DIRECT, SMALL>(a, shared, (int)blockIdx.x, (int)gridDim.x);
+}
+// Both gradients' products, where neither fills the chip.
+template <class T, int PLANES>
+__global__ __launch_bounds__(Shape<true>::kThreads, 2) void head_gemms(GemmArgs hidden,
+                                                                       GemmArgs weight,
+                                                                       int hidden_blocks) {
+    __shared__ __attribute__((aligned(1024))) char shared[kSharedBytes<false, true>];
+    const int block = (int)blockIdx.x;
+    if (block < hidden_blocks)
+        product<T, kHidden, PLANES, false, true>(hidden, shared, block, hidden_blocks);
+    else
+        product<T, kWeight, PLANES, false, true>(weight, shared, block - hidden_blocks,
+                                                 (int)gridDim.x - hidden_blocks);
+}
+
+// The tiles of kWeight that were split: sums in the order of the splits, a wave a row.
 template <bool SMALL>
-__global__ __launch_bounds__(256) void head_weight_join(GemmArgs a) {
+__device__ __forceinline__ void weight_join(const GemmArgs &a, int block) {
     constexpr int kX = Shape<SMALL>::kX, kY = Shape<SMALL>::kY;
     const int64_t count = a.scalars->count - a.row0;
     if (a.add && count <= 0) return;
-    const int rows = (int)blockIdx.x * (256 / kWave) + threadIdx.x / kWave;
+    const int rows = block * (256 / kWave) + threadIdx.x / kWave;
     const int lane = threadIdx.x % kWave, tile = a.whole + rows / kY, row = rows % kY;
     int tx, ty;
     tile_of<4>(tile, a.xtiles, a.ytiles, tx, ty);
@@ -1164,14 +1187,32 @@ struct ReduceArgs {
     TotalArgs total;
 };
 
-// The gradients of the hidden rows, a wave a row: the sum of its splits, in their
-// order. The first block of the last group of rows does the loss.
-__global__ __launch_bounds__(256) void head_hidden(ReduceArgs a) {
-    if (a.total.loss != nullptr && blockIdx.x == 0) total(a.total);
-    const int64_t i = (blockIdx.x - (a.total.loss != nullptr ? 1 : 0)) * (int64_t)(256 / kWave) +
-                      threadIdx.x / kWave;
+// What follows the gradients' products: the gradients of the hidden rows, a wave a row,
+// the sum of its splits in their order; behind them the weight's tiles that were split;
+// and with the last group of rows the loss, by the first block.
+struct FinishArgs {
+    ReduceArgs hidden;
+    GemmArgs weight;
+    int first, hidden_blocks;
+    bool small_weight;
+};
+__global__ __launch_bounds__(256) void head_finish(FinishArgs f) {
+    const ReduceArgs &a = f.hidden;
+    int block = (int)blockIdx.x;
+    if (block < f.first) {
+        total(a.total);
+        return;
+    }
+    block -= f.first;
+    if (block >= f.hidden_blocks) {
+        block -= f.hidden_blocks;
+        if (f.small_weight) weight_join<true>(f.weight, block);
+        else weight_join<false>(f.weight, block);
+        return;
+    }
+    const int64_t i = block * (int64_t)(256 / kWave) + threadIdx.x / kWave;
     const int64_t count = a.scalars->count;
-    if (i < 0 || i >= a.rows || a.row0 + i >= count) return;
+    if (i >= a.rows || a.row0 + i >= count) return;
     float s = a.scale * pow2(-a.gshift);
     if (a.mean) s /= (float)count;
     if (a.type == RCS_F32) s *= pow2(-lift_of(a.scalars->top_w));
@@ -1335,8 +1376,9 @@ int check_head(const rcs_head *a) {
     return RCS_OK;
 }
 
-template <class T, int OP, int PLANES, bool DIRECT, bool SMALL>
-void launch_shape(GemmArgs &g, hipStream_t stream) {
+// Tiles of a product, and the blocks that do it.
+template <int OP, bool SMALL>
+int64_t blocks_of(GemmArgs &g) {
     constexpr int kX = Shape<SMALL>::kX, kY = Shape<SMALL>::kY;
     g.xtiles = (int)(round_up(g.nx, kX) / kX);
     g.ytiles = (int)(round_up(g.ny, kY) / kY);
@@ -1345,11 +1387,14 @@ void launch_shape(GemmArgs &g, hipStream_t stream) {
     if (OP == kHidden) items *= g.splits;
     if (OP == kWeight) items = g.whole + (tiles - g.whole) * g.parts_of_rest;
     const int64_t slots = SMALL ? 2 * kCus : kCus;
-    const int64_t blocks = items < slots ? items : slots;
+    return items < slots ? items : slots;
+}
+
+template <class T, int OP, int PLANES, bool DIRECT, bool SMALL>
+void launch_shape(GemmArgs &g, hipStream_t stream) {
+    const unsigned blocks = (unsigned)blocks_of<OP, SMALL>(g);
     head_gemm<T, OP, PLANES, DIRECT, SMALL>
-        <<<dim3((unsigned)blocks), Shape<SMALL>::kThreads, 0, stream>>>(g);
-    if (OP == kWeight && g.parts_of_rest > 1)
-        head_weight_join<SMALL><<<dim3((unsigned)((tiles - g.whole) * (kY / 4))), 256, 0, stream>>>(g);
+        <<<dim3(blocks), Shape<SMALL>::kThreads, 0, stream>>>(g);
 }
 
 template <class T, int OP, int PLANES, bool DIRECT>
@@ -1419,40 +1464,60 @@ void launch_products(const rcs_head *a, const Targets &tg, const Plan &p, const 
             head_rows<T, PLANES, DIRECT><<<dim3((unsigned)row_blocks), kRowThreads, 0, stream>>>(r);
         }
 
-        if (a->grad_hidden != nullptr && rows > 0) {
-            GemmArgs q = g;
+        const bool hidden = a->grad_hidden != nullptr && rows > 0;
+        const bool weight = a->grad_weight != nullptr;
+        FinishArgs f = {};
+        GemmArgs q = g;
+        if (hidden) {
             for (int k = 0; k < PLANES; ++k) q.y[k] = g.e[k];
             q.yld = p.eld, q.ysize = p.chunk * p.eld;
             q.nx = a->dim, q.ny = rows, q.nk = round_up(a->vocab, kK), q.kper = p.kper;
             q.partial = reinterpret_cast<float *>(ws + p.partial), q.pld = p.pad;
             q.splits = p.splits;
-            launch_gemm<T, kHidden, PLANES, false>(q, p.small_hidden, stream);
-            ReduceArgs d = {};
+            ReduceArgs &d = f.hidden;
             d.scalars = scalars, d.rowmap = r.rowmap, d.row0 = row0, d.rows = rows;
             d.dim = a->dim, d.pld = p.pad, d.partial = q.partial, d.splits = p.splits;
             d.out = a->grad_hidden, d.old = a->grad_hidden_stride, d.type = a->type;
             d.scale = scale, d.mean = g.mean, d.gshift = gshift;
             d.factor = r.factor;
-            const bool last = row0 + p.chunk >= a->rows;
-            if (last) d.total = total_of(a, p, ws);
-            head_hidden<<<dim3((unsigned)((rows + 3) / 4 + (last ? 1 : 0))), 256, 0, stream>>>(d);
+            f.hidden_blocks = (int)((rows + 3) / 4);
+            if (row0 + p.chunk >= a->rows) {
+                d.total = total_of(a, p, ws);
+                f.first = 1;
+            }
         }
-        if (a->grad_weight != nullptr) {
-            GemmArgs q = g;
+        GemmArgs &w = f.weight;
+        int64_t joins = 0;
+        if (weight) {
+            w = g;
             for (int k = 0; k < PLANES; ++k)
-                q.x[k] = DIRECT ? ws + p.scaled : static_cast<const char *>(g.y[k]),
-                q.y[k] = g.e[k];
-            q.xld = p.pad, q.xsize = DIRECT ? p.chunk * p.pad : g.ysize;
-            q.yld = p.eld, q.ysize = p.chunk * p.eld;
-            q.nx = a->dim, q.ny = a->vocab, q.nk = rows, q.kper = round_up(rows, kK);
-            q.out = p.wide_out ? ws + p.acc : a->grad_weight;
-            q.old = p.wide_out ? a->dim : a->grad_weight_stride;
-            q.out_type = p.wide_out ? RCS_F32 : a->grad_weight_type;
-            q.add = row0 > 0 || (a->accumulate != 0 && !p.wide_out);
-            q.partial = reinterpret_cast<float *>(ws + p.rest);
-            q.whole = p.whole, q.parts_of_rest = p.parts_of_rest;
-            launch_gemm<T, kWeight, PLANES, false>(q, p.small_weight, stream);
+                w.x[k] = DIRECT ? ws + p.scaled : static_cast<const char *>(g.y[k]),
+                w.y[k] = g.e[k];
+            w.xld = p.pad, w.xsize = DIRECT ? p.chunk * p.pad : g.ysize;
+            w.yld = p.eld, w.ysize = p.chunk * p.eld;
+            w.nx = a->dim, w.ny = a->vocab, w.nk = rows;
+            w.out = p.wide_out ? ws + p.acc : a->grad_weight;
+            w.old = p.wide_out ? a->dim : a->grad_weight_stride;
+            w.out_type = p.wide_out ? RCS_F32 : a->grad_weight_type;
+            w.add = row0 > 0 || (a->accumulate != 0 && !p.wide_out);
+            w.partial = reinterpret_cast<float *>(ws + p.rest);
+            w.whole = p.whole, w.parts_of_rest = p.parts_of_rest;
+            f.small_weight = p.small_weight;
         }
+        if (hidden && weight && p.small_hidden && p.small_weight) {
+            const int64_t first = blocks_of<kHidden, true>(q), more = blocks_of<kWeight, true>(w);
+            head_gemms<T, PLANES><<<dim3((unsigned)(first + more)), Shape<true>::kThreads, 0,
+                                    stream>>>(q, w, (int)first);
+        } else {
+            if (hidden) launch_gemm<T, kHidden, PLANES, false>(q, p.small_hidden, stream);
+            if (weight) launch_gemm<T, kWeight, PLANES, false>(w, p.small_weight, stream);
+        }
+        if (weight && p.parts_of_rest > 1) {
+            const int tile = p.small_weight ? Shape<true>::kY : Shape<false>::kY;
+            joins = ((int64_t)w.xtiles * w.ytiles - w.whole) * (tile / 4);
+        }
+        const int64_t blocks = f.first + f.hidden_blocks + joins;
+        if (blocks > 0) head_finish<<<dim3((unsigned)blocks), 256, 0, stream>>>(f);
     }
     if (p.wide_out)
         head_weight_out<<<dim3((unsigned)((a->vocab + 3) / 4)), 256, 0, stream>>>(
