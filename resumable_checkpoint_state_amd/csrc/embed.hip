@@ -410,7 +410,8 @@ int embed_grad(const void *rows, int64_t rows_stride, int rows_type, int64_t cou
         !std::isfinite(scale))
         return RCS_EINVAL;
     const int isize = index_size(index_type);
-    Extents reads, writes;
+    Allocations seen;
+    Extents reads(seen), writes(seen);
     if ((rc = reads.matrix(rows, count, dim, rows_stride, rows_type)) != RCS_OK ||
         (rc = reads.array(tokens, count * isize, isize)) != RCS_OK ||
         (rc = writes.matrix(grad, vocab, dim, grad_stride, grad_type)) != RCS_OK)

@@ -1244,7 +1244,20 @@ int32_t get_le32(const unsigned char *p) {
 
 }  // namespace
 
-int rcs_check_device_range(const void *p, int64_t bytes) { return check_device_range(p, bytes); }
+int rcs_device_allocation(const void *p, const char **lo, const char **hi) {
+    const int rc = check_device_range(p, 0);
+    *lo = *hi = nullptr;
+    if (rc != RCS_OK) return rc;
+    hipDeviceptr_t base = nullptr;
+    size_t size = 0;
+    if (hipMemGetAddressRange(&base, &size, const_cast<void *>(p)) == hipSuccess && base) {
+        *lo = static_cast<const char *>(base);
+        *hi = *lo + size;
+    } else {
+        (void)hipGetLastError();
+    }
+    return RCS_OK;
+}
 
 bool rcs_overlaps(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes) {
     return overlaps(a, a_bytes, b, b_bytes);

@@ -9,9 +9,9 @@
 // (call before freeing the buffer; no copy out of it may still be pending).
 void rcs_snapshot_forget(int dev, const void *snapshot);
 
-// RCS_OK if [p, p + bytes) is device (or managed) memory of the current device
-// and lies inside one allocation, as far as the runtime can tell.
-int rcs_check_device_range(const void *p, int64_t bytes);
+// RCS_OK if p is device (or managed) memory of the current device, with the bounds of
+// its allocation (null if the runtime reports none); RCS_EINVAL otherwise.
+int rcs_device_allocation(const void *p, const char **lo, const char **hi);
 // Whether [a, a + a_bytes) and [b, b + b_bytes) share a byte.
 bool rcs_overlaps(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes);
 

@@ -162,14 +162,36 @@ void by_type(int t, F f) {
     else f(F16{});
 }
 
+// The allocations that a call's arrays lie in: often few, and each question to the
+// runtime costs more than the rest of a check.
+class Allocations {
+public:
+    int check(const void *p, int64_t bytes) {
+        const char *q = static_cast<const char *>(p);
+        for (int k = 0; k < n_; ++k)
+            if (lo_[k] <= q && q < hi_[k]) return bytes <= hi_[k] - q ? RCS_OK : RCS_ESIZE;
+        const char *lo, *hi;
+        const int rc = rcs_device_allocation(p, &lo, &hi);
+        if (rc != RCS_OK || lo == nullptr) return rc;
+        if (n_ < kMost) lo_[n_] = lo, hi_[n_++] = hi;
+        return bytes <= hi - q ? RCS_OK : RCS_ESIZE;
+    }
+
+private:
+    static constexpr int kMost = 8;
+    const char *lo_[kMost], *hi_[kMost];
+    int n_ = 0;
+};
+
 // What a call reads, or what it writes: each checked as it is added.
 class Extents {
 public:
+    explicit Extents(Allocations &seen) : seen_(seen) {}
     int array(const void *p, int64_t bytes, int align) {
         if (bytes == 0) return RCS_OK;
         if (p == nullptr || (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(align - 1)) != 0)
             return RCS_EINVAL;
-        const int rc = rcs_check_device_range(p, bytes);
+        const int rc = seen_.check(p, bytes);
         if (rc == RCS_OK) all_[n_++] = Extent{p, bytes};
         return rc;
     }
@@ -195,6 +217,7 @@ private:
         const void *p;
         int64_t bytes;
     };
+    Allocations &seen_;
     Extent all_[6];
     int n_ = 0;
 };
