@@ -1532,7 +1532,8 @@ int head_call(const rcs_head *a, const Targets &tg, hipStream_t stream) {
     if (!(std::isfinite(a->scale) && std::isfinite(tg.tau) && tg.tau > 0.f)) return RCS_EINVAL;
     const int isize = index_size(tg.index_type);
     const int64_t entries = a->rows * tg.entries;
-    Extents reads, writes;
+    Allocations seen;
+    Extents reads(seen), writes(seen);
     if ((rc = reads.matrix(a->hidden, a->rows, a->dim, a->hidden_stride, a->type)) != RCS_OK ||
         (rc = reads.matrix(a->weight, a->vocab, a->dim, a->weight_stride, a->type)) != RCS_OK ||
         (rc = reads.array(tg.index, entries * isize, isize)) != RCS_OK)
