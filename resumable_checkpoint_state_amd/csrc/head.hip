@@ -767,7 +767,7 @@ __device__ __forceinline__ void product(const GemmArgs &a, char *shared, int blo
                     }
                 top = fmaxf(top, __shfl_xor(top, 16));
                 top = fmaxf(top, __shfl_xor(top, 32));
-                if (DIRECT && top > kReach) atomicOr(&a.scalars->retry, 1u);
+                if (DIRECT && top > kReach && i < rows) atomicOr(&a.scalars->retry, 1u);
                 const float ref = DIRECT ? top : top == -INFINITY ? 0.f : top - kHead;
 #pragma unroll
                 for (int f = 0; f < kFx; ++f)
@@ -987,7 +987,7 @@ __global__ __launch_bounds__(kRowThreads) void head_reach(RowArgs a) {
 // is made of: with a teacher's many targets, too much of one.
 template <class T, int PLANES, bool DIRECT>
 __global__ __launch_bounds__(kRowThreads) void head_rows(RowArgs a) {
-        __shared__ float shared[kRowThreads / kWave];
+    __shared__ float shared[kRowThreads / kWave];
     __shared__ float sp[kMaxEntries], sz[kMaxEntries];
     __shared__ int64_t sv[kMaxEntries];
     const int tid = threadIdx.x;
@@ -1073,7 +1073,7 @@ __global__ __launch_bounds__(kRowThreads) void head_rows(RowArgs a) {
         if (fabsf(own) > 0x1p-10f) f = own / value(held, T{});
         if (tid == 0) {
             a.factor[local] = f;
-            static_cast<uint16_t *>(a.g[0])[local * a.gld + sv[0]] = held;
+            if (sv[0] >= 0) static_cast<uint16_t *>(a.g[0])[local * a.gld + sv[0]] = held;
         }
         const u32x4 *from = reinterpret_cast<const u32x4 *>(a.h + i * a.pad);
         u32x4 *to = reinterpret_cast<u32x4 *>(a.scaled + local * a.pad);
@@ -1273,12 +1273,9 @@ Plan plan_of(const rcs_head *a, int64_t entries, bool distill) {
     p.planes = a->type == RCS_F32 ? 2 : 1;
     p.rows = a->rows, p.vocab = a->vocab, p.dim = a->dim;
     p.pad = round_up(a->dim, kK);
-    // a stride of a whole number of kilobytes would put a column's elements into few
-    // of the memory's channels
     constexpr int kX = Shape<false>::kX;
     p.groups = round_up(a->vocab, kX) / Shape<true>::kGroup;  // or half as many
     p.eld = round_up(a->vocab, kX);
-    if (p.eld % 512 == 0) p.eld += 64;
     p.copy_w = !direct_weight(a);
     // rows of a group: as many as fit the limit, in whole tiles
     const int64_t row_bytes = (grads ? p.eld * 2 * p.planes : 0) + p.groups * 8 +
@@ -1529,7 +1526,10 @@ int head_call(const rcs_head *a, const Targets &tg, hipStream_t stream) {
     int rc = check_head(a);
     if (rc != RCS_OK) return rc;
     if (!is_index_type(tg.index_type)) return RCS_EINVAL;
-    if (!(std::isfinite(a->scale) && std::isfinite(tg.tau) && tg.tau > 0.f)) return RCS_EINVAL;
+    // (what is made of the temperature, too)
+    if (!(tg.tau > 0.f && std::isfinite(kLog2e / tg.tau) && std::isfinite(tg.tau * tg.tau) &&
+          std::isfinite(a->scale) && std::isfinite(a->scale * tg.tau)))
+        return RCS_EINVAL;
     const int isize = index_size(tg.index_type);
     const int64_t entries = a->rows * tg.entries;
     Allocations seen;

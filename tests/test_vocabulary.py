@@ -221,6 +221,10 @@ def test_calls_refuse_targets_on_the_host():
     for tau in (0.0, -1.0, math.inf, math.nan):
         assert L.head_distill(a, 128, 1, 128, 0, 2, tau, None) == rcs.EINVAL
     assert L.head_distill(a, 128, 1, 128, 5, 2, 1.0, None) == rcs.EINVAL
+    for tau in (1e-39, 1e20):  # 1 / tau, or its square, is out of float32's range
+        assert L.head_distill(a, 128, 1, 128, 0, 2, tau, None) == rcs.EINVAL
+    big = ctypes.byref(_args(scale=1e38))  # its product with the temperature is
+    assert L.head_distill(big, 128, 1, 128, 0, 2, 10.0, None) == rcs.EINVAL
     e = lambda **m: L.embed_grad(*(dict(  # noqa: E731
         rows=256, rs=16, rt=0, count=4, tokens=128, it=1, grad=512, gs=16, gt=0, vocab=8, dim=16,
         scale=1.0, ws=4096, bytes=1 << 20, stream=None) | m).values())
@@ -488,6 +492,23 @@ def test_loss_bad_targets_and_values_give_nan(dtype):
     x[11, 2] = math.nan
     r = run_loss(h, x, targets)
     assert torch.isnan(r[1]).all() and torch.isnan(r[0]).all()
+
+
+@gpu
+@pytest.mark.parametrize("dtype", TYPES)
+def test_a_bad_target_in_large_tiles_leaves_other_rows(dtype):
+    # a vocabulary of whole tiles: a row's place -1 is the last one of the row before
+    t, v, d = 1030, 13312, 64
+    h, w, targets = data(t, v, d, dtype)
+    good = run_loss(h, w, targets, reduction="sum", scale=scale_of(dtype))
+    for at in (0, 7, t - 1):
+        x = targets.clone()
+        x[at] = -1
+        r = run_loss(h, w, x, reduction="sum", scale=scale_of(dtype))
+        rest = torch.arange(t, device="cuda") != at
+        assert torch.isnan(r[1][at]) and torch.isnan(r[2][at]).all()
+        assert torch.equal(r[1][rest], good[1][rest]) and torch.equal(r[2][rest], good[2][rest])
+        assert torch.isnan(r[3]).any(0).all()
 
 
 @gpu
