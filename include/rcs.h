@@ -527,8 +527,11 @@ int rcs_list_import(rcs_list *list, const void *w, int w_type, const void *m, in
  *                    that may overlap on the device need one each
  * What is written must not overlap anything else. Rows without a loss take no
  * part: what hidden holds there does not matter, and their gradient is zero.
- * Gradients of 16-bit types go through softmax values of that type (each
- * rounded once before and once after it is normalized); sums are float32.
+ * Gradients of 16-bit types go through softmax values of that type, each rounded
+ * as an exponential and again once normalized, or with bfloat16 and one target
+ * a row, once, and for the weight's gradient the hidden value times its row's
+ * factor too; sums are float32. With and without gradients the loss may differ
+ * in its last bits.
  */
 #define RCS_I32 0
 #define RCS_I64 1
@@ -557,7 +560,8 @@ int64_t rcs_head_workspace(const rcs_head *args, int64_t entries);
  * head_distill: tau^2 sum_k p_k (log p_k - log softmax(z[t] / tau)[indices[t][k]])
  * with p the softmax of the row's logits / tau: the divergence from a teacher's
  * top logits, tau = temperature > 0. indices, logits: (rows, entries), entries at
- * most RCS_HEAD_MAX_ENTRIES, logits of any of the three types. Entries with a
+ * most RCS_HEAD_MAX_ENTRIES, logits of any of the three types; tau, 1 / tau, tau^2
+ * and scale tau are within float32's range. Entries with a
  * negative index or a logit of -inf are not there; a row without entries has no
  * loss; an index that comes twice has both probabilities; one that is not below
  * vocab makes the row NaN.

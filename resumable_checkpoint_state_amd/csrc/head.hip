@@ -1,6 +1,38 @@
 // head.hip -- losses of a language model's output head and their gradients,
 // without the matrix of logits: softmax cross entropy, and the divergence from
 // a teacher's top logits. gfx950 kernels and their C ABI.
+//
+// Mathematics. z = h w^T / tau, one row of `vocab` logits for each row of `dim` of h
+// that has a loss, l = log sum_v exp z[v].
+//   cross entropy (tau = 1, q the target's one place): loss = l - z[target]
+//   a teacher's entries, q their softmax at tau:
+//     loss = tau^2 sum_k q[k] (log q[k] - (z[index[k]] - l))
+//   either way, with p = exp(z - l):
+//     d loss / dh = tau (p - q) w,  d loss / dw = tau (p - q)^T h
+// Exponentials are powers of two and logits in units of log 2 throughout.
+//
+// Mapping. The rows that have a loss are counted and placed one after another
+// (head_count, head_prep), so that the rest costs nothing. Three matrix products with
+// one body (`product`): the logits' tiles end as exponentials of 16 bits with a sum of
+// each row's, the only thing of the size of the logits that is kept, and not without
+// gradients; head_rows makes losses of the sums, and of the exponentials what the
+// other two products read; head_finish adds up what was split. Rows are done in groups
+// where their exponentials would exceed the caller's limit. Each sum has one order, and
+// no float is added atomically.
+//
+// Float32 matrices are two half-precision planes, x 2^lift = high + low (22 bits; the
+// low by low products, below 2^-22, are left out): three products of 16 bits are 2.3
+// times as fast as one of float32 on the matrix units, of which 153 TFLOP/s were
+// measured, against 1,400 in half precision.
+//
+// Bounds. The three products of 8,192 x 50,257 x 768 in bfloat16 are 1,897 GFLOP: 1.26
+// ms at the 1,504 TFLOP/s that a product of 16,384^3 reaches on this card. They take
+// 618 us (logits, with their exponentials), 612 (hidden) and 595 (weight), with
+// everything else 1.70 ms; at 131,072 x 4,096 with a tenth of the rows masked 6.16,
+// 6.38 and 5.91 of 18.6 ms, 1,240 to 1,340 TFLOP/s. There, loads with a quarter of the
+// matrix instructions took 5.54, 5.46 and 4.78 ms, and those instructions without loads
+// 5.32, 5.52 and 5.47, at a clock that such work lowers to 2.0 GHz: what is lost is
+// that the two do not overlap wholly.
 
 #include <hip/hip_runtime.h>
 
@@ -43,8 +75,9 @@ struct Int {
 
 // Tiles of a product: kX by kY outputs by a block of 2 by kY / 64 waves, each kX / 2
 // by 64 of them, kK at a time, from two places in LDS in turn. The large ones (one
-// block a CU) read least; products that have fewer of them than there are CUs are
-// done in small ones (two blocks a CU).
+// block a CU) read least: 64 KB for 256 x 256 x 64 products. Products that have fewer
+// of them than there are CUs are done in small ones (two blocks a CU). Four places of
+// 32 columns each instead of two of 64 were slower.
 constexpr int kK = 64;
 template <bool SMALL>
 struct Shape {
@@ -191,6 +224,7 @@ struct PrepArgs {
 
 // float32 only: the largest finite magnitudes of the hidden rows that have a loss (the
 // first kTopHidden blocks) and of the weight. One atomic a block: more would queue.
+// Reads both once: 47 us for 4,096 rows and 50,257, of 768.
 constexpr int kTopHidden = 64, kTopWeight = 192;
 __global__ __launch_bounds__(1024) void head_top(PrepArgs a, const uint8_t *flags,
                                                  Scalars *scalars) {
@@ -237,7 +271,9 @@ __device__ __forceinline__ int32_t block_count(int32_t x, int32_t *shared) {
     return (shared[0] + shared[1]) + (shared[2] + shared[3]);
 }
 
-// A row's logits of kFew of its targets, each lane 8 columns at a time.
+// A row's logits of kFew of its targets, each lane 8 columns at a time. (Four at a time
+// where a row has several: 132 us for 8,192 rows of 32 entries and 768 columns, a
+// gather of 403 MB at 3.1 TB/s; with eight at a time 190.)
 template <class T, int kFew>
 __device__ __forceinline__ void target_logits(const RowArgs &a, int64_t t, int k0, bool &bad,
                                               float &top, float *to) {
@@ -279,7 +315,9 @@ __device__ __forceinline__ void target_row(const RowArgs &a, int64_t i, bool bad
 // loss, and with one entry its target's logit is worked out; a row without a loss is
 // left out, and its gradient and loss are cleared; kK rows more are zeros behind the
 // last one, up to a whole step of the products. SOLO: there are no flags and counts of
-// the rows yet: each block looks at all targets before its own.
+// the rows yet: each block looks at all targets before its own, which saves a launch
+// (5 us) where there are few. Bound by HBM: 42 us for 8,192 rows of 4,096, a tenth
+// masked, which with their copies and their targets' rows are 181 MB.
 template <class T, bool SOLO>
 __global__ __launch_bounds__(256) void head_prep(PrepArgs a, RowArgs rows, CountArgs c) {
     __shared__ int32_t shared[256 / kWave];
@@ -487,7 +525,9 @@ struct Side<false, R, PERM> {
     const int per = n / 8, more = n % 8, xcd = b % 8;
     return xcd * per + min(xcd, more) + b / 8;
 }
-// The tiles in bands of BAND y tiles, and along a band all y of an x, then the next.
+// The tiles in bands of BAND y tiles, and along a band all y of an x, then the next. Of
+// 4, 8 and 16, 8 is best for the logits, and 4 for the others (weight at 131,072 x
+// 4,096: 5,901 us, with 8 6,142; at 50,257 x 768 they are the same).
 template <int BAND>
 __device__ __forceinline__ void tile_of(int at, int xtiles, int ytiles, int &tx, int &ty) {
     const int band = at / (BAND * xtiles), rest = at % (BAND * xtiles);
@@ -541,14 +581,18 @@ struct Item {
     }
 }
 
-[[maybe_unused]] constexpr int kStreamed = 2;  // a store's cache policy: not kept in L2 (736 -> 700 us)
+// A store's cache policy: the exponentials are not kept in L2, where the product's tiles
+// are (then 736 -> 700 us for 8,192 x 50,257 x 768).
+[[maybe_unused]] constexpr int kStreamed = 2;
 
 // LDS of a product's block.
 template <bool DIRECT, bool SMALL>
 constexpr int kSharedBytes =
     2 * Shape<SMALL>::kStageBytes + (DIRECT ? kRefPlaces * Shape<SMALL>::kY * 4 : 0);
 
-// What the block-th of `blocks` blocks does of a product.
+// What the block-th of `blocks` blocks does of a product: items one after another, the
+// loads running two steps ahead of the matrix instructions across their bounds, and an
+// item's results stored while the next one's first step is multiplied.
 template <class T, int OP, int PLANES, bool DIRECT, bool SMALL>
 __device__ __forceinline__ void product(const GemmArgs &a, char *shared, int block, int blocks) {
 #ifdef __HIP_DEVICE_COMPILE__  // the host needs the kernels' launch stubs alone
@@ -886,7 +930,8 @@ __global__ __launch_bounds__(Shape<SMALL>::kThreads, 2) void head_gemm(GemmArgs 
     __shared__ __attribute__((aligned(1024))) char shared[kSharedBytes<DIRECT, SMALL>];
     product<T, OP, PLANES, DIRECT, SMALL>(a, shared, (int)blockIdx.x, (int)gridDim.x);
 }
-// Both gradients' products, where neither fills the chip.
+// Both gradients' products, where neither fills the chip: 21 us for 512 rows by 8,191
+// by 321 in half precision.
 template <class T, int PLANES>
 __global__ __launch_bounds__(Shape<true>::kThreads, 2) void head_gemms(GemmArgs hidden,
                                                                        GemmArgs weight,
@@ -982,9 +1027,9 @@ __global__ __launch_bounds__(kRowThreads) void head_reach(RowArgs a) {
 // DIRECT (bfloat16, whose range is float32's, and one target): they are relative to
 // the row's reference, and so the row's factor is left to the other sides: the hidden
 // gradient's rows are multiplied by it in the end, and the hidden rows for the
-// weight's gradient here. This saves a pass over all exponentials (345 of 2,600 us
-// with 8,192 rows of 50,257), and is one more rounding of what the weight's gradient
-// is made of: with a teacher's many targets, too much of one.
+// weight's gradient here. This saves a pass over all exponentials (20 us instead of
+// 330, which are 5 TB/s, with 8,192 rows of 50,257), and is one more rounding of what
+// the weight's gradient is made of: with a teacher's many targets, too much of one.
 template <class T, int PLANES, bool DIRECT>
 __global__ __launch_bounds__(kRowThreads) void head_rows(RowArgs a) {
     __shared__ float shared[kRowThreads / kWave];
@@ -1189,7 +1234,8 @@ struct ReduceArgs {
 
 // What follows the gradients' products: the gradients of the hidden rows, a wave a row,
 // the sum of its splits in their order; behind them the weight's tiles that were split;
-// and with the last group of rows the loss, by the first block.
+// and with the last group of rows the loss, by the first block. 51 us for 8,192 rows of
+// 768 and 50,257 of the weight, 41 for 4,096 columns, where nothing was split.
 struct FinishArgs {
     ReduceArgs hidden;
     GemmArgs weight;
@@ -1244,7 +1290,7 @@ __global__ __launch_bounds__(256) void head_weight_out(const float *from, int64_
 // ----------------------------------------------------------------- host side
 
 constexpr int64_t kCus = 256;
-constexpr int64_t kItemSteps = 24;
+constexpr int64_t kItemSteps = 24;   // what an item costs beside its steps, in steps
 constexpr int64_t kSoloRows = 1024;  // of which each block counts those before its own
 constexpr int64_t kChunks = 256;     // that the rows are counted in, at most
 constexpr int64_t kMaxVocab = 1 << 22;  // a tile's rows of exponentials fit a buffer of 4 GB
