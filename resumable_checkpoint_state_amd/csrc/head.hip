@@ -26,10 +26,11 @@
 // measured, against 1,400 in half precision.
 //
 // Bounds. The three products of 8,192 x 50,257 x 768 in bfloat16 are 1,897 GFLOP: 1.26
-// ms at the 1,504 TFLOP/s that a product of 16,384^3 reaches on this card. They take
-// 618 us (logits, with their exponentials), 612 (hidden) and 595 (weight), with
-// everything else 1.70 ms; at 131,072 x 4,096 with a tenth of the rows masked 6.16,
-// 6.38 and 5.91 of 18.6 ms, 1,240 to 1,340 TFLOP/s. There, loads with a quarter of the
+// ms at the 1,504 TFLOP/s that a product of 16,384^3 reaches on this card. The whole
+// call takes 1.70 ms; in a trace, where kernels are some 10% longer, the products take
+// 618 us (logits, with their exponentials), 612 (hidden) and 595 (weight). At 131,072 x
+// 4,096 with a tenth of the rows masked 18.6 ms, 6.16, 6.38 and 5.91 of it the
+// products, 1,240 to 1,340 TFLOP/s. There, loads with a quarter of the
 // matrix instructions took 5.54, 5.46 and 4.78 ms, and those instructions without loads
 // 5.32, 5.52 and 5.47, at a clock that such work lowers to 2.0 GHz: what is lost is
 // that the two do not overlap wholly.

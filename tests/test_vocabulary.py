@@ -841,6 +841,40 @@ def test_a_tied_model_trains_and_resumes(state, dtype):
 
 
 @gpu
+def test_a_tied_model_beside_autograd():
+    """The calls around a body that torch differentiates: both ends' gradients in one
+    matrix, and the body's."""
+    b, n, v, d = 3, 50, 700, 64
+    g = torch.Generator(device="cuda").manual_seed(5)
+    emb = torch.randn(v, d, generator=g, device="cuda") * 0.3
+    mix = torch.randn(d, d, generator=g, device="cuda") * d ** -0.5
+    tokens = torch.randint(0, v, (b, n), generator=g, device="cuda")
+    targets = torch.randint(0, v, (b, n), generator=g, device="cuda")
+    targets[1, 30:] = IGNORE
+
+    def body(x, mix):
+        return torch.tanh(x.view(-1, d) @ mix).view(x.shape)
+
+    m = mix.clone().requires_grad_()
+    emb_grad = torch.zeros_like(emb)
+    x = torch.nn.functional.embedding(tokens, emb).requires_grad_()
+    hidden = body(x, m)
+    gh = torch.empty_like(hidden)
+    loss = rcs.head_loss(hidden, emb, targets, grad_hidden=gh, grad_weight=emb_grad)
+    hidden.backward(gh)
+    rcs.embed_grad(x.grad, tokens, emb_grad)
+
+    e, m64 = emb.double().requires_grad_(), mix.double().requires_grad_()
+    z = body(torch.nn.functional.embedding(tokens, e), m64).view(-1, d) @ e.t()
+    want = torch.nn.functional.cross_entropy(z, targets.view(-1))
+    want.backward()
+    assert abs(loss.item() - want.item()) < 1e-5
+    # sums of at most 700 terms, a few roundings of float32 each, in the norm
+    for got, ref in ((emb_grad, e.grad), (m.grad, m64.grad)):
+        assert float((got.double() - ref).norm() / ref.norm()) < 800 * F
+
+
+@gpu
 def test_a_bad_target_leaves_the_weights():
     h, w, targets = data(64, 100, 32, F32)
     grad = torch.zeros_like(w)
