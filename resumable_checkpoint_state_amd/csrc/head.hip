@@ -272,30 +272,67 @@ __device__ __forceinline__ int32_t block_count(int32_t x, int32_t *shared) {
     return (shared[0] + shared[1]) + (shared[2] + shared[3]);
 }
 
-// A row's logits of kFew of its targets, each lane 8 columns at a time. (Four at a time
-// where a row has several: 132 us for 8,192 rows of 32 entries and 768 columns, a
-// gather of 403 MB at 3.1 TB/s; with eight at a time 190.)
+// Eight consecutive elements as they lie in memory.
+template <class T>
+struct Eight {
+    static constexpr int kParts = T::kBytes / 2;
+    u32x4 raw[kParts];
+    __device__ __forceinline__ void load(const void *p, int64_t i) {
+        const u32x4_half *q = reinterpret_cast<const u32x4_half *>(static_cast<const char *>(p) +
+                                                                   i * T::kBytes);
+#pragma unroll
+        for (int k = 0; k < kParts; ++k) raw[k] = q[k];
+    }
+    __device__ __forceinline__ float at(int r) const {
+        if constexpr (T::kBytes == 4) return __uint_as_float(raw[r / 4][r % 4]);
+        else return value((uint16_t)(raw[0][r / 2] >> (16 * (r & 1))), T{});
+    }
+};
+
+// A row's logits of kFew of its targets, each lane 8 columns at a time, two times 512
+// columns of all of them under way together: the loads have no branch between them. A
+// lane at the row's end reads the last eight columns, and leaves out those that are
+// another's. (In head_targets 73 us for 8,192 rows of 32 entries and 768 columns, a
+// gather of 403 MB at 5.5 TB/s; with each load waited for before the next, 132.)
 template <class T, int kFew>
 __device__ __forceinline__ void target_logits(const RowArgs &a, int64_t t, int k0, bool &bad,
                                               float &top, float *to) {
     const int lane = threadIdx.x % kWave;
-    int64_t v[kFew];
-    float dot[kFew] = {};
     const int few = (int)min((int64_t)kFew, a.entries - k0);
+    int column = -1;
+    if (lane < few) column = (int)target_at(a, t, k0 + lane, bad);
+    bad = __any(bad);
+    int v[kFew];
+    float dot[kFew] = {};
 #pragma unroll
-    for (int k = 0; k < kFew; ++k) v[k] = k < few ? target_at(a, t, k0 + k, bad) : -1;
-    for (int64_t n = 8 * lane; n < a.dim; n += 8 * kWave) {
-        float x[8], y[kFew][8];
-        const int there = (int)min((int64_t)8, a.dim - n);
-        load8(a.hidden, t * a.hld + n, there, x, T{});
-#pragma unroll
-        for (int k = 0; k < kFew; ++k)  // (of a column that there is, too, where there is none)
-            if (k < few) load8(a.weight, max(v[k], (int64_t)0) * a.wld + n, there, y[k], T{});
-#pragma unroll
+    for (int k = 0; k < kFew; ++k) v[k] = __builtin_amdgcn_readlane(column, k);
+    if (a.dim < 8) {
         for (int k = 0; k < kFew; ++k)
-            if (k < few)
+            if (lane < a.dim)
+                dot[k] = element(a.hidden, t * a.hld + lane, T::kType) *
+                         element(a.weight, max(v[k], 0) * a.wld + lane, T::kType);
+    } else {
+        constexpr int kTimes = 2;
+        for (int64_t n0 = 0; n0 < a.dim; n0 += kTimes * 8 * kWave) {
+            Eight<T> x[kTimes], y[kTimes][kFew];
+            int64_t skip[kTimes];
 #pragma unroll
-                for (int r = 0; r < 8; ++r) dot[k] = fmaf(x[r], y[k][r], dot[k]);
+            for (int i = 0; i < kTimes; ++i) {
+                const int64_t n = n0 + (i * kWave + lane) * 8, from = min(n, a.dim - 8);
+                skip[i] = n - from;
+                x[i].load(a.hidden, t * a.hld + from);
+#pragma unroll
+                for (int k = 0; k < kFew; ++k)  // (of a column that there is, in any case)
+                    y[i][k].load(a.weight, max(v[k], 0) * a.wld + from);
+            }
+#pragma unroll
+            for (int i = 0; i < kTimes; ++i)
+#pragma unroll
+                for (int k = 0; k < kFew; ++k)
+#pragma unroll
+                    for (int r = 0; r < 8; ++r)
+                        if (r >= skip[i]) dot[k] = fmaf(x[i].at(r), y[i][k].at(r), dot[k]);
+        }
     }
 #pragma unroll
     for (int k = 0; k < kFew; ++k) {
@@ -946,6 +983,29 @@ __global__ __launch_bounds__(Shape<true>::kThreads, 2) void head_gemms(GemmArgs 
                                                  (int)gridDim.x - hidden_blocks);
 }
 
+// Four values of each of n splits, `apart` floats apart, added up in their order, the
+// loads of up to eight splits under way together (16 need more registers and are slower
+// where there are few: 44 us instead of 40 for head_finish with 5).
+template <int N>
+__device__ __forceinline__ void add_some(const float *from, int64_t apart, int n, int &k0,
+                                         f32x4 &sum) {
+    f32x4 x[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+        x[k] = *reinterpret_cast<const f32x4 *>(from + min(k0 + k, n - 1) * apart);
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+        if (k0 + k < n) sum += x[k];
+    k0 += N;
+}
+__device__ __forceinline__ f32x4 add_up(const float *from, int64_t apart, int n) {
+    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+    int k = 0;
+    while (n - k > 4) add_some<8>(from, apart, n, k, sum);
+    if (n - k > 0) add_some<4>(from, apart, n, k, sum);
+    return sum;
+}
+
 // The tiles of kWeight that were split: sums in the order of the splits, a wave a row.
 template <bool SMALL>
 __device__ __forceinline__ void weight_join(const GemmArgs &a, int block) {
@@ -960,9 +1020,7 @@ __device__ __forceinline__ void weight_join(const GemmArgs &a, int block) {
     if (4 * lane >= kX || v >= a.ny || n >= a.nx) return;
     const float *from = a.partial + (int64_t)(tile - a.whole) * a.parts_of_rest * kX * kY +
                         row * kX + 4 * lane;
-    f32x4 x = {0.f, 0.f, 0.f, 0.f};
-    for (int k = 0; k < a.parts_of_rest; ++k)
-        x += *reinterpret_cast<const f32x4 *>(from + (int64_t)k * kX * kY);
+    const f32x4 x = add_up(from, kX * kY, a.parts_of_rest);
     put4(a.out, v * a.old + n, a.out_type, x, a.nx - n, a.add);
 }
 
@@ -1196,16 +1254,20 @@ struct TotalArgs {
 };
 
 // The sum or mean of the losses, in an order of its own: each of a block's 256 threads
-// takes every 256th, in four sums.
+// takes every 256th, in eight sums (whose loads are under way together).
 __device__ __forceinline__ void total(const TotalArgs &a) {
     __shared__ double shared[256 / kWave];
     const int64_t count = a.scalars->count;
-    double x[4] = {0.0, 0.0, 0.0, 0.0};
-    for (int64_t i = threadIdx.x; i < count; i += 1024)
+    constexpr int kSums = 8;
+    double x[kSums] = {};
+    for (int64_t i = threadIdx.x; i < count; i += 256 * kSums) {
+        float loss[kSums];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (i + 256 * k < count) x[k] += (double)a.losses[i + 256 * k];
-    double y = (x[0] + x[1]) + (x[2] + x[3]);
+        for (int k = 0; k < kSums; ++k) loss[k] = a.losses[min(i + 256 * k, count - 1)];
+#pragma unroll
+        for (int k = 0; k < kSums; ++k) x[k] += i + 256 * k < count ? (double)loss[k] : 0.0;
+    }
+    double y = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
 #pragma unroll
     for (int d = 1; d < kWave; d *= 2) y += __shfl_xor(y, d);
     if (threadIdx.x % kWave == 0) shared[threadIdx.x / kWave] = y;
@@ -1235,8 +1297,8 @@ struct ReduceArgs {
 
 // What follows the gradients' products: the gradients of the hidden rows, a wave a row,
 // the sum of its splits in their order; behind them the weight's tiles that were split;
-// and with the last group of rows the loss, by the first block. 51 us for 8,192 rows of
-// 768 and 50,257 of the weight, 41 for 4,096 columns, where nothing was split.
+// and with the last group of rows the loss, by the first block. 40 us for 8,192 rows of
+// 768 in 5 splits with 50,257 of the weight, and 42 for 4,096 columns in one.
 struct FinishArgs {
     ReduceArgs hidden;
     GemmArgs weight;
@@ -1266,11 +1328,8 @@ __global__ __launch_bounds__(256) void head_finish(FinishArgs f) {
     if (a.factor != nullptr) s *= a.factor[i];
     const int64_t t = a.rowmap[a.row0 + i];
     for (int64_t n = 4 * (threadIdx.x % kWave); n < a.dim; n += 4 * kWave) {
-        f32x4 x = {0.f, 0.f, 0.f, 0.f};
         const float *from = a.partial + i * a.pld + n;
-#pragma unroll 8
-        for (int k = 0; k < a.splits; ++k)
-            x += *reinterpret_cast<const f32x4 *>(from + k * a.rows * a.pld);
+        const f32x4 x = add_up(from, a.rows * a.pld, a.splits);
         put4(a.out, t * a.old + n, a.type, x * s, a.dim - n, false);
     }
 }
@@ -1338,22 +1397,6 @@ Plan plan_of(const rcs_head *a, int64_t entries, bool distill) {
     p.small_logits = tiles_of(a->vocab, rows, kX) < kCus;
     p.direct = a->type == RCS_BF16 && !distill && grads && !p.small_logits;
     p.solo = a->type != RCS_F32 && !distill && a->rows <= kSoloRows;
-    // splits of the hidden gradient's sum over the vocabulary: the number that fills
-    // the chip's rounds best, each item costing about as much as kItemSteps steps more;
-    // in large tiles unless even small ones have no 64 steps each
-    const int64_t steps = round_up(a->vocab, kK) / kK;
-    p.small_hidden = tiles_of(a->dim, rows, kX) * steps < 64 * kCus;
-    const int64_t hidden_tile = p.small_hidden ? Shape<true>::kX : kX;
-    const int64_t slots = p.small_hidden ? 2 * kCus : kCus;
-    const int64_t tiles = tiles_of(a->dim, rows, hidden_tile);
-    int64_t best = 0;
-    for (int64_t n = 1; n <= 64 && n <= steps; ++n) {
-        const int64_t rounds = (tiles * n + slots - 1) / slots;
-        const int64_t cost = rounds * ((steps + n - 1) / n + kItemSteps);
-        if (n == 1 || cost < best) best = cost, p.splits = (int)n;
-    }
-    p.kper = (steps + p.splits - 1) / p.splits * kK;
-    p.splits = (int)((steps * kK + p.kper - 1) / p.kper);
     // the weight's tiles in whole rounds, and the rest split to fill one more
     p.small_weight = tiles_of(a->dim, a->vocab, kX) < kCus;
     const int64_t weight_tile = p.small_weight ? Shape<true>::kX : kX;
@@ -1367,6 +1410,27 @@ Plan plan_of(const rcs_head *a, int64_t entries, bool distill) {
         if (n > 1) p.parts_of_rest = (int)n;
     }
     p.whole = (int)(p.parts_of_rest > 1 ? wtiles - rest : wtiles);
+    // splits of the hidden gradient's sum over the vocabulary: the number that fills
+    // the chip's rounds best, each item costing about as much as kItemSteps steps more;
+    // in large tiles unless even small ones have no 64 steps each
+    const int64_t steps = round_up(a->vocab, kK) / kK;
+    p.small_hidden = tiles_of(a->dim, rows, kX) * steps < 64 * kCus;
+    const int64_t hidden_tile = p.small_hidden ? Shape<true>::kX : kX;
+    int64_t slots = p.small_hidden ? 2 * kCus : kCus;
+    if (a->grad_weight != nullptr && p.small_hidden && p.small_weight) {
+        // both in one launch: what the weight's items leave of one round, if half of it
+        const int64_t others = p.whole + (wtiles - p.whole) * p.parts_of_rest;
+        if (others <= slots / 2) slots -= others;
+    }
+    const int64_t tiles = tiles_of(a->dim, rows, hidden_tile);
+    int64_t best = 0;
+    for (int64_t n = 1; n <= 64 && n <= steps; ++n) {
+        const int64_t rounds = (tiles * n + slots - 1) / slots;
+        const int64_t cost = rounds * ((steps + n - 1) / n + kItemSteps);
+        if (n == 1 || cost < best) best = cost, p.splits = (int)n;
+    }
+    p.kper = (steps + p.splits - 1) / p.splits * kK;
+    p.splits = (int)((steps * kK + p.kper - 1) / p.kper);
     p.wide_out = a->grad_weight != nullptr && a->grad_weight_type != RCS_F32 && p.chunk < a->rows;
     int64_t at = 0;
     auto take = [&](int64_t bytes) {

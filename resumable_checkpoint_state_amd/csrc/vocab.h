@@ -71,28 +71,7 @@ __device__ __forceinline__ f32x4 load4(const void *p, int64_t i, int t) {
     const u32x2 b = *reinterpret_cast<const u32x2_any *>(static_cast<const uint16_t *>(p) + i);
     return t == RCS_BF16 ? four(b, BF16{}) : four(b, F16{});
 }
-// Elements i to i + 7 of p, of type T; zeros behind the first `there` of them.
 typedef u32x4 u32x4_half __attribute__((aligned(2)));
-template <class T>
-__device__ __forceinline__ void load8(const void *p, int64_t i, int there, float (&x)[8], T) {
-    if (there >= 8) {
-        if constexpr (T::kBytes == 4) {
-            const u32x4_any *q =
-                reinterpret_cast<const u32x4_any *>(static_cast<const float *>(p) + i);
-            const f32x4 a = __builtin_bit_cast(f32x4, q[0]), b = __builtin_bit_cast(f32x4, q[1]);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) x[r] = a[r], x[4 + r] = b[r];
-        } else {
-            const u32x4 b =
-                *reinterpret_cast<const u32x4_half *>(static_cast<const uint16_t *>(p) + i);
-#pragma unroll
-            for (int r = 0; r < 8; ++r) x[r] = value((uint16_t)(b[r / 2] >> (16 * (r & 1))), T{});
-        }
-        return;
-    }
-#pragma unroll
-    for (int r = 0; r < 8; ++r) x[r] = r < there ? element(p, i + r, T::kType) : 0.f;
-}
 __device__ __forceinline__ void store4(void *p, int64_t i, int t, f32x4 x) {
     if (t == RCS_F32) {
         *reinterpret_cast<u32x4_any *>(static_cast<float *>(p) + i) = __builtin_bit_cast(u32x4, x);
