@@ -707,9 +707,9 @@ __device__ __forceinline__ void product(const GemmArgs &a, char *shared, int blo
         const int64_t x = OP == kLogits ? load.x0 * a.xld + k : k * a.xld + load.x0;
         const int64_t y = OP != kWeight ? load.y0 * a.yld + k : k * a.yld + load.y0;
         const void *px = a.x[0], *py = a.y[0];
-        if (PLANES > 1) {  // high by high, low by high, high by low
-            px = load_pair == 1 ? a.x[1] : px;
-            py = load_pair == 2 ? a.y[1] : py;
+        if (PLANES > 1) {  // low by high, high by low, high by high: the large sums last,
+            px = load_pair == 0 ? a.x[1] : px;  // which the small ones would add roundings to
+            py = load_pair == 1 ? a.y[1] : py;
         }
         bx = buffer_of(px, x * 2, load.empty ? 0 : a.xsize * 2);
         by = buffer_of(py, y * 2, load.empty ? 0 : a.ysize * 2);
