@@ -755,6 +755,22 @@ __device__ __forceinline__ void product(const GemmArgs &a, char *shared, int blo
 #pragma unroll
             for (int j = 0; j < kFy; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     };
+    // Float32 in small tiles, which leave the registers for it: every two steps' sums are
+    // added up apart, a quarter of the roundings at the whole sum's size. (Large ones are
+    // for large vocabularies, whose probabilities are off by more than that.)
+    constexpr bool kPairwise = PLANES > 1 && SMALL;
+    f32x4 whole[kPairwise ? kFx : 1][kPairwise ? kFy : 1];
+    [[maybe_unused]] auto move = [&](auto how) {  // 0: none yet, 1: these too, 2: that is all
+#pragma unroll
+        for (int i = 0; i < kFx; ++i)
+#pragma unroll
+            for (int j = 0; j < kFy; ++j) {
+                if constexpr (!kPairwise) continue;
+                else if constexpr (decltype(how)::value == 0) whole[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+                else if constexpr (decltype(how)::value == 1) whole[i][j] += acc[i][j];
+                else acc[i][j] = whole[i][j];
+            }
+    };
     const uint32_t xbase = X::base(wx * (kX / 2), lane);
     const uint32_t ybase = Y::base(wy * 64, lane);
 
@@ -942,6 +958,7 @@ __device__ __forceinline__ void product(const GemmArgs &a, char *shared, int blo
     for (; at < items; at += blocks) {
         const Item m = item_of(at);
         clear();
+        if constexpr (kPairwise) move(Int<0>{});
         for (int left = m.per * kPairsOfPlanes; left > 0; --left) {
             multiply(Int<0>{}, [&](int i) { read_one(stage, i, Int<1>{}); });
             if (kStores > 0 && stored) arrive(Int<kStores>{});
@@ -954,7 +971,11 @@ __device__ __forceinline__ void product(const GemmArgs &a, char *shared, int blo
             });
             next_loads();
             stage ^= 1;
+            if constexpr (kPairwise) {
+                if (left & 1) move(Int<1>{}), clear();  // every other step, and the last one
+            }
         }
+        if constexpr (kPairwise) move(Int<2>{});
         finish(m, place);
         place = (place + 1) % kRefPlaces;
         stored = true;
