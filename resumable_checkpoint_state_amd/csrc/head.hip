@@ -1256,7 +1256,14 @@ __global__ __launch_bounds__(kRowThreads) void head_rows(RowArgs a) {
                 seen |= j < k;
             }
         if (seen) continue;
-        const float x = (exp2_(sz[k] - lse2) - p) * pow2(a.gshift);
+        // float32: of the softmax value that the others of the row were summed with, so
+        // that one near 1 is off by its own roundings only, not by the logits'
+        float own = exp2_(sz[k] - lse2);
+        if (PLANES > 1)
+            own = (value(static_cast<const uint16_t *>(a.g[0])[local * a.gld + v], T{}) +
+                   value(static_cast<const uint16_t *>(a.g[1])[local * a.gld + v], T{})) *
+                  pow2(-a.gshift);
+        const float x = (own - p) * pow2(a.gshift);
         const uint32_t h = two(x, 0.f, T{});
         static_cast<uint16_t *>(a.g[0])[local * a.gld + v] = (uint16_t)h;
         if (PLANES > 1)
