@@ -21,15 +21,15 @@
 // no float is added atomically.
 //
 // Float32 matrices are two half-precision planes, x 2^lift = high + low (22 bits; the
-// low by low products, below 2^-22, are left out): three products of 16 bits are 2.3
+// low by low products, below 2^-22, are left out): three products of 16 bits are three
 // times as fast as one of float32 on the matrix units, of which 153 TFLOP/s were
 // measured, against 1,400 in half precision.
 //
 // Bounds. The three products of 8,192 x 50,257 x 768 in bfloat16 are 1,897 GFLOP: 1.26
 // ms at the 1,504 TFLOP/s that a product of 16,384^3 reaches on this card. The whole
-// call takes 1.70 ms; in a trace, where kernels are some 10% longer, the products take
+// call takes 1.70 to 1.74 ms; in a trace, where kernels are some 10% longer, the products take
 // 618 us (logits, with their exponentials), 612 (hidden) and 595 (weight). At 131,072 x
-// 4,096 with a tenth of the rows masked 18.6 ms, 6.16, 6.38 and 5.91 of it the
+// 4,096 with a tenth of the rows masked 18.6 to 19.0 ms, 6.16, 6.38 and 5.91 of it the
 // products, 1,240 to 1,340 TFLOP/s. There, loads with a quarter of the
 // matrix instructions took 5.54, 5.46 and 4.78 ms, and those instructions without loads
 // 5.32, 5.52 and 5.47, at a clock that such work lowers to 2.0 GHz: what is lost is
@@ -756,8 +756,8 @@ __device__ __forceinline__ void product(const GemmArgs &a, char *shared, int blo
             for (int j = 0; j < kFy; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     };
     // Float32 in small tiles, which leave the registers for it: every two steps' sums are
-    // added up apart, a quarter of the roundings at the whole sum's size. (Large ones are
-    // for large vocabularies, whose probabilities are off by more than that.)
+    // added up apart, a quarter of the roundings at the whole sum's size (half of the
+    // gradients' error; 3 us of 33 for the products of 65 rows by 8,191 x 321).
     constexpr bool kPairwise = PLANES > 1 && SMALL;
     f32x4 whole[kPairwise ? kFx : 1][kPairwise ? kFy : 1];
     [[maybe_unused]] auto move = [&](auto how) {  // 0: none yet, 1: these too, 2: that is all
@@ -989,7 +989,7 @@ __global__ __launch_bounds__(Shape<SMALL>::kThreads, 2) void head_gemm(GemmArgs 
     __shared__ __attribute__((aligned(1024))) char shared[kSharedBytes<DIRECT, SMALL>];
     product<T, OP, PLANES, DIRECT, SMALL>(a, shared, (int)blockIdx.x, (int)gridDim.x);
 }
-// Both gradients' products, where neither fills the chip: 21 us for 512 rows by 8,191
+// Both gradients' products, where neither fills the chip: 20 us for 512 rows by 8,191
 // by 321 in half precision.
 template <class T, int PLANES>
 __global__ __launch_bounds__(Shape<true>::kThreads, 2) void head_gemms(GemmArgs hidden,
